@@ -192,6 +192,61 @@ int gs_param_list_destroy(gs_param_list* list);
 int gs_master_update_sgd(const gs_param_list* list, float lr, float max_norm,
                          const float* grad_norm, const int32_t* found_inf, void* stream);
 
+/* The AdamW form of the consumer step, with the moments in 32 or in 8 bits.
+ *
+ * Opaque list of parameters for it: per tensor, its fp32 master weights
+ * (updated in place), an optional bf16 copy (master_bf16 NULL or
+ * master_bf16[i] NULL: none), its gradients (grad_dtype GS_F32, GS_BF16 or
+ * GS_F16, unscaled) and its two moments (updated in place; zeros before the
+ * first step):
+ *   GS_MOMENTS_F32   -- m[i] and v[i] hold numels[i] fp32 values each, the
+ *       running means of g and of g^2; the scale arrays are NULL;
+ *   GS_MOMENTS_E4M3  -- m[i] and v[i] hold numels[i] E4M3 codes each, with
+ *       one fp32 scale per 128 consecutive elements of the tensor
+ *       (m_scale[i], v_scale[i]: ceil(numels[i] / 128) values): m = code *
+ *       scale, and v holds the square ROOT of the second moment, whose range
+ *       in powers of two is half the moment's.  fp8_dequant reads either.
+ * decay (n_tensors host floats, or NULL for all 1) multiplies the step's
+ * weight decay per tensor (0: a norm or a bias).  Allocates a device chunk
+ * table and returns once it is on the device (it synchronises the legacy
+ * default stream).  The pointers are captured. */
+typedef enum gs_moments { GS_MOMENTS_F32 = 0, GS_MOMENTS_E4M3 = 1 } gs_moments;
+typedef struct gs_adamw_list gs_adamw_list;
+int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
+                         const void* const* grads, int grad_dtype, int moments, void* const* m,
+                         void* const* v, float* const* m_scale, float* const* v_scale,
+                         const float* decay, const int64_t* numels, int32_t n_tensors,
+                         gs_adamw_list** out);
+int gs_adamw_list_destroy(gs_adamw_list* list);
+
+/* One AdamW step on every parameter of the list, one launch:
+ *   if *found_inf != 0 (device): nothing is written (the skipped step, which
+ *   does not count as one);
+ *   t = *step + 1 (device int64; written back at the end);
+ *   g = coef * g, coef as in gs_master_update_sgd (max_norm, grad_norm);
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + ((1 - beta2) g) g,
+ *   r = sqrt(v)        (each product, sum and root rounded to fp32; 1 - beta
+ *                       formed in double and rounded once);
+ *   w = w (1 - lr weight_decay decay[i])
+ *       - lr / (1 - beta1^t) m / (r / sqrt(1 - beta2^t) + eps);
+ *   bf16 copy = w rounded to nearest even.
+ * With GS_MOMENTS_E4M3 the update uses the new moments before they are
+ * rounded; then, for each block of 128, a = max(max |x|, 1e-30), scale =
+ * a / 448, and x * (448 / a) is rounded to E4M3 up or down at random in
+ * proportion to the distance (so that the mean of many steps keeps what
+ * rounding to nearest would always drop: beta2 near 1 moves v by less than
+ * half a step of the format); a positive r is never stored as zero.  The
+ * random bits are a function of (seed, t, the element's place in the list):
+ * the same inputs give the same bits.  Non-finite gradients are for the
+ * check before this step to find; here they give non-finite states.
+ * beta1, beta2 in [0, 1); lr, weight_decay, eps finite and >= 0.  grad_norm
+ * may be NULL when max_norm <= 0.  Calls on one list must be ordered on one
+ * stream. */
+int gs_master_update_adamw(const gs_adamw_list* list, float lr, float beta1, float beta2,
+                           float eps, float weight_decay, float max_norm,
+                           const float* grad_norm, const int32_t* found_inf, int64_t* step,
+                           uint32_t seed, void* stream);
+
 /* Checkpoint support: the scaler's whole state is {S, growth_tracker}.
  * get: copies the two device scalars to host variables and waits for the
  *      copy on `stream` (this call synchronises that stream).
@@ -360,6 +415,89 @@ int fp8_dequant_mx(const uint8_t* q, const uint8_t* scales, int64_t R, int64_t C
 int fp8_gemm_block_scaled(const uint8_t* qa, const float* sa, const uint8_t* qb, const float* sb,
                           int64_t M, int64_t N, int64_t K, int fmt_a, int fmt_b, int out_dtype,
                           void* d, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The steps that mixed precision keeps in fp32 around the cast path ([P3]
+ * paragraph on autocast: normalisations, softmax and losses run in fp32
+ * whatever the tensors' type): layer norm, and the loss from which the
+ * scaled gradients start.  16-bit or fp32 tensors in and out, every sum and
+ * statistic in fp32.
+ * Rows may lie further apart than their length: ld* is the distance of two
+ * rows in elements (>= the row's length); the elements between are neither
+ * read nor written.
+ * --------------------------------------------------------------------- */
+
+/* Layer norm of each row of x [R, C]:
+ *   mean = sum x / C,  rstd = 1 / sqrt(sum (x - mean)^2 / C + eps),
+ *   y = (x - mean) rstd gamma + beta.
+ * dtype: of x and y; w_dtype: of gamma and beta, GS_F32 or dtype (any may be
+ * NULL: 1 and 0).  mean, rstd: fp32 [R] for the backward pass, or NULL.
+ * R == 0 or C == 0 is a valid no-op. */
+int gs_layernorm_fwd(const void* x, int64_t ldx, int dtype, int64_t R, int64_t C,
+                     const void* gamma, const void* beta, int w_dtype, float eps, void* y,
+                     int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* Bytes of device workspace gs_layernorm_bwd needs for R x C (0 for sizes it
+ * refuses). */
+size_t gs_layernorm_ws_bytes(int64_t R, int64_t C);
+
+/* Its backward pass, with xhat = (x - mean) rstd and d = dy gamma:
+ *   dx = rstd (d - mean over the row of d - xhat * (mean over the row of
+ *        d xhat)),   dgamma = sum over rows of dy xhat,
+ *   dbeta = sum over rows of dy.
+ * dtype: of dy, x and dx; dw_dtype (any of the three): of dgamma and dbeta,
+ * which may be NULL (not computed; with both NULL ws may be NULL too).  GS_F16
+ * gradients of gamma and beta go into a gs_tensor_list like any other.  The
+ * sums over rows are formed in fp32 in an order that depends on the sizes and
+ * the device alone.  R == 0 writes zeros to dgamma and dbeta.
+ * ws: device workspace of gs_layernorm_ws_bytes(R, C) bytes, 16-byte
+ * aligned, any contents; calls sharing one must be ordered on one stream. */
+int gs_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int dtype,
+                     int64_t R, int64_t C, const void* gamma, int w_dtype, const float* mean,
+                     const float* rstd, void* dx, int64_t lddx, void* dgamma, void* dbeta,
+                     int dw_dtype, void* ws, void* stream);
+
+/* Log probabilities of given tokens under the softmax of each row of logits
+ * [R, V] (dtype, row distance ld), with lse = log sum exp x:
+ *   logprob[r] = x[r, targets[r]] - lse[r]       (fp32 [R]; formed as
+ *       (x - max x) - log sum exp(x - max x), so that it keeps its digits
+ *       where lse is large)
+ *   lse[r]                                       (fp32 [R], or NULL)
+ *   entropy[r] = -sum p log p                    (fp32 [R], or NULL)
+ *   top_ids, top_logprob [R, top_k]: the top_k largest logits' indices
+ *       (int32; equal logits in the order of their indices, lowest first)
+ *       and their log probabilities.  top_k 0: none (both NULL);
+ *       top_k <= min(V, GS_MAX_TOP).
+ * targets: device int64 [R]; a negative target (no loss at this token) gives
+ * logprob 0, one >= V gives NaN.  targets and logprob may both be NULL.
+ * Logits of -Inf take no part (p = 0); a row of nothing else has lse -Inf,
+ * entropy 0 and log probabilities -Inf.  A row with NaN or +Inf has NaN
+ * statistics, and NaN counts as the largest logit in top_ids.
+ * R == 0 is a valid no-op; V >= 1, V < 2^31. */
+#define GS_MAX_TOP 32
+int gs_token_logprob(const void* logits, int64_t ld, int dtype, int64_t R, int64_t V,
+                     const int64_t* targets, float* logprob, float* lse, float* entropy,
+                     int32_t top_k, int32_t* top_ids, float* top_logprob, void* stream);
+
+/* The gradient of sum_r (dlogprob[r] logprob[r] + dentropy[r] entropy[r]),
+ * times the loss scale, with respect to the logits:
+ *   p = exp(x - lse),
+ *   dlogits = S (dlogprob (1[j == target] - p) - dentropy p (x - lse +
+ *             entropy)),
+ * rounded to out_dtype (any of the three) to nearest even WITHOUT saturation:
+ * a value beyond the type's range becomes Inf, which the loss scaler's check
+ * then finds.  lse and entropy: as gs_token_logprob wrote them (where |lse| >
+ * 256, so that its own rounding would show in p, the row's sum is formed
+ * anew: a row whose every logit is the type's lowest value has p = 1 / V);
+ * dlogprob, dentropy: fp32 [R]; entropy and dentropy may both be NULL; loss_scale:
+ * device fp32 scalar S, or NULL for 1.  A negative target contributes no
+ * logprob term, one >= V makes its row NaN; a row with lse -Inf has gradient
+ * zero.  dlogits may be the logits themselves (same pointer, type and row
+ * distance); otherwise they must not overlap. */
+int gs_token_logprob_bwd(const void* logits, int64_t ld, int dtype, int64_t R, int64_t V,
+                         const int64_t* targets, const float* lse, const float* dlogprob,
+                         const float* entropy, const float* dentropy, const float* loss_scale,
+                         void* dlogits, int64_t ld_out, int out_dtype, void* stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics.

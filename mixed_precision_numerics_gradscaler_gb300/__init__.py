@@ -23,11 +23,16 @@ __all__ = [
     "gs_unscale_check_update_noalloc", "gs_noalloc_limits", "fp8_quant_mx", "fp8_dequant_mx",
     "gs_unscale_check_update_hysteresis", "fp8_quant_tensor_delayed",
     "gs_unscale_check_update_norm", "ParamList", "gs_param_list_create", "gs_master_update_sgd",
+    "AdamWList", "gs_adamw_list_create", "gs_master_update_adamw", "gs_layernorm_fwd",
+    "gs_layernorm_bwd", "gs_layernorm_ws_bytes", "gs_token_logprob", "gs_token_logprob_bwd",
+    "GS_MAX_TOP", "GS_MOMENTS_F32", "GS_MOMENTS_E4M3",
 ]
 
 GS_OK, GS_ERR_NULL, GS_ERR_SHAPE, GS_ERR_DTYPE, GS_ERR_ARG, GS_ERR_CUDA, GS_ERR_TIMEOUT = range(7)
 GS_F16, GS_BF16, GS_F32 = 0, 1, 2
 GS_E4M3, GS_E5M2 = 0, 1
+GS_MOMENTS_F32, GS_MOMENTS_E4M3 = 0, 1
+GS_MAX_TOP = 32
 
 _DTYPES = {torch.float16: GS_F16, torch.bfloat16: GS_BF16, torch.float32: GS_F32}
 _FMTS = {"e4m3": GS_E4M3, "e5m2": GS_E5M2, GS_E4M3: GS_E4M3, GS_E5M2: GS_E5M2}
@@ -74,6 +79,18 @@ def _load_lib() -> ctypes.CDLL:
         "gs_noalloc_limits": (ci, [ctypes.POINTER(i32), ctypes.POINTER(i64), ctypes.POINTER(i64)]),
         "fp8_gemm_block_scaled": (ci, [vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp, vp]),
         "gs_test_set_stall": (ci, [ci]),
+        "gs_layernorm_fwd": (ci, [vp, i64, ci, i64, i64, vp, vp, ci, f32, vp, i64, vp, vp, vp]),
+        "gs_layernorm_ws_bytes": (ctypes.c_size_t, [i64, i64]),
+        "gs_layernorm_bwd": (ci, [vp, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, i64, vp, vp,
+                                  ci, vp, vp]),
+        "gs_token_logprob": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp]),
+        "gs_token_logprob_bwd": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci,
+                                      vp]),
+        "gs_adamw_list_create": (ci, [vp, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp, i32,
+                                      ctypes.POINTER(vp)]),
+        "gs_adamw_list_destroy": (ci, [vp]),
+        "gs_master_update_adamw": (ci, [vp, f32, f32, f32, f32, f32, f32, vp, vp, vp,
+                                        ctypes.c_uint32, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -274,6 +291,82 @@ def gs_master_update_sgd(plist: ParamList, lr: float, max_norm: float, grad_norm
                                      _stream(stream)), "gs_master_update_sgd")
 
 
+class AdamWList:
+    """Owns a ``gs_adamw_list`` handle: fp32 master weights, gradients (all
+    float32, bfloat16 or float16), both moments and optional bf16 copies,
+    tensor by tensor.  Moments are float32 tensors, or uint8 E4M3 codes with
+    float32 scales of ceil(numel / 128) values each."""
+
+    def __init__(self, master: list[torch.Tensor], grads: list[torch.Tensor], m: list[torch.Tensor],
+                 v: list[torch.Tensor], m_scale: list[torch.Tensor] | None = None,
+                 v_scale: list[torch.Tensor] | None = None,
+                 master_bf16: list[torch.Tensor] | None = None, decay: list[float] | None = None):
+        n = len(master)
+        for other in (grads, m, v, m_scale, v_scale, master_bf16, decay):
+            if other is not None and len(other) != n:
+                raise ValueError("lists differ in length")
+        if (m_scale is None) != (v_scale is None):
+            raise ValueError("m_scale and v_scale go together")
+        mt = torch.float32 if m_scale is None else torch.uint8
+        for i in range(n):
+            k = master[i].numel()
+            blocks = -(-k // 128)
+            for t, name, dtype, numel in (
+                    (master[i], "master", torch.float32, k), (grads[i], "grad", grads[0].dtype, k),
+                    (m[i], "m", mt, k), (v[i], "v", mt, k),
+                    (m_scale and m_scale[i], "m_scale", torch.float32, blocks),
+                    (v_scale and v_scale[i], "v_scale", torch.float32, blocks),
+                    (master_bf16 and master_bf16[i], "master_bf16", torch.bfloat16, k)):
+                if t is None:
+                    continue
+                _contig(t, name)
+                if t.dtype != dtype or t.numel() != numel:
+                    raise ValueError(f"{name} {i} must be {dtype} with {numel} elements")
+        self._keep = [list(t) for t in (master, grads, m, v, m_scale or [], v_scale or [],
+                                        master_bf16 or [])]
+
+        def ptrs(ts):
+            return None if ts is None else (ctypes.c_void_p * max(n, 1))(*[_ptr(t) for t in ts])
+
+        dk = None if decay is None else (ctypes.c_float * max(n, 1))(*decay)
+        ne = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in master])
+        h = ctypes.c_void_p()
+        _check(_lib.gs_adamw_list_create(
+            ptrs(master), ptrs(master_bf16), ptrs(grads),
+            _DTYPES[grads[0].dtype] if n else GS_F32,
+            GS_MOMENTS_F32 if m_scale is None else GS_MOMENTS_E4M3, ptrs(m), ptrs(v),
+            ptrs(m_scale), ptrs(v_scale), dk, ne, n, ctypes.byref(h)), "gs_adamw_list_create")
+        self.handle = h
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            _lib.gs_adamw_list_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def gs_adamw_list_create(master, grads, m, v, m_scale=None, v_scale=None, master_bf16=None,
+                         decay=None) -> AdamWList:
+    return AdamWList(master, grads, m, v, m_scale, v_scale, master_bf16, decay)
+
+
+def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torch.Tensor, lr: float,
+                           beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                           weight_decay: float = 0.01, max_norm: float = 0.0,
+                           grad_norm: torch.Tensor | None = None, seed: int = 0,
+                           stream=None) -> None:
+    """step: int64 [1], the number of updates made so far (advanced on the
+    device unless found_inf is set)."""
+    _check(_lib.gs_master_update_adamw(alist.handle, lr, beta1, beta2, eps, weight_decay, max_norm,
+                                       _ptr(grad_norm), _ptr(found_inf), _ptr(step), seed,
+                                       _stream(stream)), "gs_master_update_adamw")
+
+
 def gs_unscale_check_update_hysteresis(tlist: TensorList, scale: torch.Tensor,
                                        growth_tracker: torch.Tensor, hysteresis_state: torch.Tensor,
                                        found_inf: torch.Tensor, skipped: torch.Tensor | None = None,
@@ -367,6 +460,115 @@ def fp8_gemm_block_scaled(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, 
     _check(_lib.fp8_gemm_block_scaled(_ptr(qa), _ptr(sa), _ptr(qb), _ptr(sb), M, N, K, _FMTS[fmt],
                                       _FMTS[fmt_b], _DTYPES[d.dtype], _ptr(d), _stream(stream)),
            "fp8_gemm_block_scaled")
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """The distance of two rows of a [R, C] tensor, in elements."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [rows, columns] with adjacent columns")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, *dtypes: torch.dtype) -> int | None:
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of {n} elements and one of {dtypes}")
+    return t.data_ptr()
+
+
+def gs_layernorm_fwd(x: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None,
+                     y: torch.Tensor, mean: torch.Tensor | None = None,
+                     rstd: torch.Tensor | None = None, eps: float = 1e-5, stream=None) -> None:
+    """x, y: [R, C] of one type (rows may be apart); gamma, beta: [C], float32
+    or x's type, or None; mean, rstd: float32 [R] or None."""
+    ldx, ldy = _rows(x, "x"), _rows(y, "y", x)
+    R, C = x.shape
+    if y.dtype != x.dtype:
+        raise ValueError("y must have the type of x")
+    w = gamma if gamma is not None else beta
+    wt = torch.float32 if w is None else w.dtype
+    _check(_lib.gs_layernorm_fwd(_ptr(x), ldx, _DTYPES[x.dtype], R, C,
+                                 _vector(gamma, "gamma", C, wt), _vector(beta, "beta", C, wt),
+                                 _DTYPES[wt], eps, _ptr(y), ldy,
+                                 _vector(mean, "mean", R, torch.float32),
+                                 _vector(rstd, "rstd", R, torch.float32), _stream(stream)),
+           "gs_layernorm_fwd")
+
+
+def gs_layernorm_ws_bytes(rows: int, cols: int) -> int:
+    return int(_lib.gs_layernorm_ws_bytes(rows, cols))
+
+
+def gs_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None,
+                     mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                     dgamma: torch.Tensor | None = None, dbeta: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> None:
+    """dy, x, dx: [R, C] of one type; dgamma, dbeta: [C] of one type (float32,
+    bfloat16 or float16) or None; ws: gs_layernorm_ws_bytes(R, C) bytes."""
+    ldx, lddy, lddx = _rows(x, "x"), _rows(dy, "dy", x), _rows(dx, "dx", x)
+    R, C = x.shape
+    if dy.dtype != x.dtype or dx.dtype != x.dtype:
+        raise ValueError("dy and dx must have the type of x")
+    wt = torch.float32 if gamma is None else gamma.dtype
+    d = dgamma if dgamma is not None else dbeta
+    dt = torch.float32 if d is None else d.dtype
+    if ws is not None and ws.numel() * ws.element_size() < gs_layernorm_ws_bytes(R, C):
+        raise ValueError("ws is smaller than gs_layernorm_ws_bytes(R, C)")
+    _check(_lib.gs_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _DTYPES[x.dtype], R, C,
+                                 _vector(gamma, "gamma", C, wt), _DTYPES[wt],
+                                 _vector(mean, "mean", R, torch.float32),
+                                 _vector(rstd, "rstd", R, torch.float32), _ptr(dx), lddx,
+                                 _vector(dgamma, "dgamma", C, dt), _vector(dbeta, "dbeta", C, dt),
+                                 _DTYPES[dt], _ptr(ws), _stream(stream)), "gs_layernorm_bwd")
+
+
+def gs_token_logprob(logits: torch.Tensor, targets: torch.Tensor | None,
+                     logprob: torch.Tensor | None, lse: torch.Tensor | None = None,
+                     entropy: torch.Tensor | None = None, top_ids: torch.Tensor | None = None,
+                     top_logprob: torch.Tensor | None = None, stream=None) -> None:
+    """logits: [R, V] (rows may be apart); targets: int64 [R]; logprob, lse,
+    entropy: float32 [R]; top_ids: int32 [R, k], top_logprob: float32 [R, k].
+    Every output but at least one may be None."""
+    ld = _rows(logits, "logits")
+    R, V = logits.shape
+    if (top_ids is None) != (top_logprob is None):
+        raise ValueError("top_ids and top_logprob go together")
+    k = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] != R:
+            raise ValueError("top_ids must be [rows, k]")
+        k = top_ids.shape[1]
+    f32 = torch.float32
+    _check(_lib.gs_token_logprob(_ptr(logits), ld, _DTYPES[logits.dtype], R, V,
+                                 _vector(targets, "targets", R, torch.int64),
+                                 _vector(logprob, "logprob", R, f32), _vector(lse, "lse", R, f32),
+                                 _vector(entropy, "entropy", R, f32), k,
+                                 _vector(top_ids, "top_ids", R * k, torch.int32),
+                                 _vector(top_logprob, "top_logprob", R * k, f32), _stream(stream)),
+           "gs_token_logprob")
+
+
+def gs_token_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                         dlogprob: torch.Tensor, dlogits: torch.Tensor,
+                         entropy: torch.Tensor | None = None, dentropy: torch.Tensor | None = None,
+                         loss_scale: torch.Tensor | None = None, stream=None) -> None:
+    """dlogits: [R, V], any of the three types, or the logits themselves; lse
+    and entropy as gs_token_logprob wrote them; loss_scale: float32 [1]."""
+    ld, ld_out = _rows(logits, "logits"), _rows(dlogits, "dlogits", logits)
+    R, V = logits.shape
+    f32 = torch.float32
+    _check(_lib.gs_token_logprob_bwd(_ptr(logits), ld, _DTYPES[logits.dtype], R, V,
+                                     _vector(targets, "targets", R, torch.int64),
+                                     _vector(lse, "lse", R, f32),
+                                     _vector(dlogprob, "dlogprob", R, f32),
+                                     _vector(entropy, "entropy", R, f32),
+                                     _vector(dentropy, "dentropy", R, f32),
+                                     _vector(loss_scale, "loss_scale", 1, f32), _ptr(dlogits),
+                                     ld_out, _DTYPES[dlogits.dtype], _stream(stream)),
+           "gs_token_logprob_bwd")
 
 
 def gs_test_set_stall(on: bool) -> None:

@@ -15,6 +15,7 @@
 #include <tuple>
 #include <vector>
 
+#include "gs_args.h"
 #include "gs_internal.h"
 #include "gsfp8.h"
 #include "gsfp8_test.h"
@@ -194,19 +195,6 @@ bool device_reachable(const void* p) {
       return false;
   }
 }
-
-static bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-static bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return na && nb && x < y + nb && y < x + na;
-}
-
-static size_t dtype_size(int dt) { return dt == GS_F32 ? 4 : 2; }
-static bool valid_dtype(int dt) { return dt == GS_F16 || dt == GS_BF16 || dt == GS_F32; }
-static bool valid_fmt(int f) { return f == GS_E4M3 || f == GS_E5M2; }
-
-static bool mul_ok(int64_t a, int64_t b) { return a >= 0 && b >= 0 && (b == 0 || a <= INT64_MAX / b); }
 
 bool spans_conflict(Span* writes, size_t n_writes, const Span* reads, size_t n_reads) {
   size_t k = 0;  // drop empty ranges

@@ -93,6 +93,29 @@ cudaError_t launch_gemm_fp8_block_scaled(const uint8_t* qa, const float* sa, con
                                          const float* sb, int64_t M, int64_t N, int64_t K,
                                          int fmt_a, int fmt_b, int out_dtype, void* d,
                                          int32_t* status, cudaStream_t stream);
+cudaError_t launch_layernorm_fwd(const void* x, int64_t ldx, int dtype, int64_t R, int64_t C,
+                                 const void* gamma, const void* beta, int w_dtype, float eps,
+                                 void* y, int64_t ldy, float* mean, float* rstd,
+                                 cudaStream_t stream);
+// Rows of partial sums the backward pass may write to its workspace.
+int64_t layernorm_partials(int64_t R, int64_t C);
+cudaError_t launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                 int dtype, int64_t R, int64_t C, const void* gamma, int w_dtype,
+                                 const float* mean, const float* rstd, void* dx, int64_t lddx,
+                                 void* dgamma, void* dbeta, int dw_dtype, float* ws,
+                                 cudaStream_t stream);
+cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int64_t R, int64_t V,
+                                 const int64_t* targets, float* logprob, float* lse,
+                                 float* entropy, int top_k, int32_t* top_ids, float* top_logprob,
+                                 cudaStream_t stream);
+cudaError_t launch_token_logprob_bwd(const void* logits, int64_t ld, int dtype, int64_t R,
+                                     int64_t V, const int64_t* targets, const float* lse,
+                                     const float* dlogprob, const float* entropy,
+                                     const float* dentropy, const float* loss_scale,
+                                     void* dlogits, int64_t ld_out, int out_dtype,
+                                     cudaStream_t stream);
+cudaError_t launch_master_update_adamw(const AChunk* d_chunks, int64_t n_chunks, int grad_dtype,
+                                       int moments, const AdamWArgs& args, cudaStream_t stream);
 cudaError_t launch_set_state(float* scale, int32_t* tracker, float h_scale, int32_t h_tracker,
                              cudaStream_t stream);
 

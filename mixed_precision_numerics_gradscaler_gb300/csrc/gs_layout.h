@@ -85,6 +85,36 @@ __host__ __device__ inline int64_t mchunk_head(const float* w, const uint16_t* w
   return h;
 }
 
+// One contiguous run of a parameter tensor for the AdamW step: at most
+// kChunkElems elements, beginning at a multiple of kChunkElems elements of
+// the tensor (so that a block of 128 that shares a moment's scale lies in one
+// chunk).
+struct AChunk {
+  float* w;            // fp32 master weights (updated in place)
+  uint16_t* w_bf16;    // bf16 copy, or nullptr
+  const void* g;       // gradients
+  void* m;             // first moment: fp32, or E4M3 codes
+  void* v;             // second moment: fp32, or E4M3 codes of its root
+  float* m_scale;      // one per 128 elements of this chunk (8-bit moments)
+  float* v_scale;
+  int64_t n;
+  int64_t place;       // the list's elements before this chunk, every tensor
+                       // counted up to a multiple of 128
+  float decay;         // the tensor's factor of the weight decay
+};
+constexpr int kMomentBlock = 128;
+
+struct AdamWArgs {
+  float lr, beta1, beta2, eps, weight_decay, max_norm;
+  float one_beta1, one_beta2;   // fp32(1 - beta), from double
+  float log_beta1, log_beta2;   // fp32(log beta), from double (-Inf for 0)
+  const float* grad_norm;
+  const int32_t* found_inf;
+  int64_t* step;
+  uint32_t seed;
+  unsigned int* arrived;        // the list's arrival count, 0 between calls
+};
+
 // Loss-scale policy applied by the last CTA of the unscale kernel.  With
 // hyst == nullptr it is the GradScaler loop; otherwise the hysteresis
 // policy: an overflow spends one unit of *hyst (S kept) until one is left,

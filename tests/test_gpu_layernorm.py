@@ -1,0 +1,309 @@
+"""Layer norm and its backward pass against 64-bit restatements.
+
+Tolerances.  A sum of n terms added by at least 32 threads has at most
+n / 32 + 16 dependent additions, each with relative error 2^-24: a sum is off
+by at most c = (n / 32 + 16) 2^-24 of the sum of magnitudes.  From there:
+  mean:  c E|x|
+  rstd:  relative c + (2 c E|x| + 2^-22 (|mean| + E|x - mean|))
+         E|x - mean| rstd^2 + (mean error)^2 rstd^2 + 2^-21
+  y:     |gamma| rstd (mean error + 2^-23 (|x| + |mean|)) +
+         |gamma xhat| (rstd error + 2^-21) + 2^-22 |beta|, and half an ulp
+         of the type
+and likewise for the gradients, each term below."""
+import numpy as np
+import pytest
+import torch
+
+import train_refs as tr
+from gpu_helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+HALF_ULP = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+E = tr.EPS24
+
+
+@pytest.fixture(scope="module")
+def gs():
+    import mixed_precision_numerics_gradscaler_gb300 as gs
+    torch.cuda.set_device(0)
+    return gs
+
+
+def rounded(want, dtype):
+    return want.abs() * HALF_ULP[dtype] + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+
+
+def check(got, want, tol, what):
+    got = got.double()
+    ok = (got - want).abs() <= tol
+    assert ok.all(), (what, int((~ok).sum()), float(((got - want).abs() - tol)[~ok].max()))
+
+
+def rows(R, C, pad, dtype, gen, scale=1.0, shift=0.0, offset=0):
+    """A [R, C] view with pad elements between rows, starting `offset`
+    elements into its buffer; the buffer too."""
+    buf = torch.full((offset + R * (C + pad) + 8,), 7.0, dtype=dtype, device=DEV)
+    x = buf.as_strided((R, C), (C + pad, 1), offset)
+    x.copy_(torch.randn(R, C, device=DEV, generator=gen) * scale + shift)
+    return x, buf
+
+
+def gaps_kept(buf, x, offset, fill=7.0):
+    mask = torch.ones_like(buf, dtype=torch.bool)
+    mask.as_strided(x.shape, x.stride(), offset).fill_(False)
+    return bool((buf[mask] == fill).all())
+
+
+def fwd_case(gs, R, C, dtype, wt, pad=0, offset=0, scale=1.0, shift=0.3, eps=1e-5, affine=True):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(R * 1000003 + C)
+    x, _ = rows(R, C, pad, dtype, gen, scale, shift, offset)
+    y, ybuf = rows(R, C, pad, dtype, gen, 0.0, 7.0, offset)
+    gamma = (1 + 0.2 * torch.randn(C, device=DEV, generator=gen)).to(wt) if affine else None
+    beta = (0.2 * torch.randn(C, device=DEV, generator=gen)).to(wt) if affine else None
+    mean, rstd = torch.full((R,), 9.0, device=DEV), torch.full((R,), 9.0, device=DEV)
+    gs.gs_layernorm_fwd(x, gamma, beta, y, mean, rstd, eps)
+    wy, wm, wr = tr.layernorm(x, gamma, beta, eps)
+    c = (C / 32 + 16) * E
+    xd = x.double()
+    ax, dev = xd.abs().mean(1), (xd - wm[:, None]).abs().mean(1)
+    em = c * ax + 2 * E * wm.abs()
+    check(mean, wm, em, "mean")
+    er = c + (2 * em + 4 * E * (wm.abs() + dev)) * dev * wr ** 2 + em ** 2 * wr ** 2 + 8 * E
+    check(rstd, wr, wr * er, "rstd")
+    g = gamma.double().abs() if affine else torch.ones(C, device=DEV, dtype=torch.float64)
+    b = beta.double().abs() if affine else torch.zeros(C, device=DEV, dtype=torch.float64)
+    xh = ((xd - wm[:, None]) * wr[:, None]).abs()
+    tol = g * wr[:, None] * (em[:, None] + 2 * E * (xd.abs() + wm.abs()[:, None])) + \
+        g * xh * (er[:, None] + 8 * E) + 4 * E * b
+    check(y, wy, tol * 1.01 + rounded(wy, dtype), "y")
+    assert gaps_kept(ybuf, y, offset), "written between the rows"
+
+
+@pytest.mark.parametrize("C", [1, 2, 7, 31, 32, 33, 64, 127, 128, 255, 1000, 1023, 1024, 2048, 4096,
+                               4097, 8192, 10000, 16384, 20001, 33000, 70000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_forward_sizes(gs, C, dtype):
+    for R in (1, 3, 37):
+        fwd_case(gs, R, C, TYPES[dtype], torch.float32)
+
+
+@pytest.mark.parametrize("dtype,wt", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (0, 1), (3, 5), (8, 8), (24, 16)])
+def test_forward_strides_and_alignment(gs, dtype, wt, pad, offset):
+    for C in (40, 129, 1024, 4096, 9001):
+        fwd_case(gs, 19, C, TYPES[dtype], TYPES[wt], pad, offset)
+
+
+def test_forward_many_rows(gs):
+    fwd_case(gs, 20011, 96, torch.bfloat16, torch.float32)
+    fwd_case(gs, 70001, 33, torch.float16, torch.float32)
+    fwd_case(gs, 5003, 4096, torch.bfloat16, torch.bfloat16)
+
+
+def test_forward_without_affine_and_with_offset(gs):
+    fwd_case(gs, 64, 1000, torch.float32, torch.float32, affine=False)
+    # rows whose mean is a hundred standard deviations from zero
+    fwd_case(gs, 64, 4096, torch.float32, torch.float32, shift=100.0)
+    # rows of one value: variance zero, y = beta
+    x = torch.full((5, 640), 3.25, device=DEV)
+    y = torch.empty_like(x)
+    beta = torch.randn(640, device=DEV)
+    gs.gs_layernorm_fwd(x, None, beta, y, None, None, 1e-5)
+    assert torch.equal(y, beta.expand(5, -1))
+
+
+def test_forward_nonfinite_rows_stay_apart(gs):
+    x = torch.randn(6, 2048, device=DEV)
+    x[1, 5], x[3, 7], x[4, 2047] = float("nan"), float("inf"), float("-inf")
+    y, y2 = torch.empty_like(x), torch.empty_like(x)
+    gs.gs_layernorm_fwd(x, None, None, y)
+    gs.gs_layernorm_fwd(torch.nan_to_num(x), None, None, y2)
+    for r in range(6):
+        if r in (1, 3, 4):
+            assert torch.isnan(y[r]).any()
+        else:
+            assert torch.equal(y[r], y2[r])
+
+
+def bwd_case(gs, R, C, dtype, wt, pad=0, offset=0, dw=torch.float32, affine=True, sums=(True, True)):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(R * 7919 + C)
+    x, _ = rows(R, C, pad, dtype, gen, 1.5, 0.3, offset)
+    dy, _ = rows(R, C, pad, dtype, gen, 0.5, 0.1, offset)
+    dx, dxbuf = rows(R, C, pad, dtype, gen, 0.0, 7.0, offset)
+    gamma = (1 + 0.2 * torch.randn(C, device=DEV, generator=gen)).to(wt) if affine else None
+    _, mean, rstd = tr.layernorm(x, None, None, 1e-5)
+    mean, rstd = mean.float(), rstd.float()
+    dg = torch.full((C,), 9.0, dtype=dw, device=DEV) if sums[0] else None
+    db = torch.full((C,), 9.0, dtype=dw, device=DEV) if sums[1] else None
+    nbytes = gs.gs_layernorm_ws_bytes(R, C)
+    ws = torch.full((nbytes + 256,), 0xAB, dtype=torch.uint8, device=DEV)
+    gs.gs_layernorm_bwd(dy, x, gamma, mean, rstd, dx, dg, db, ws[:nbytes])
+    wdx, wdg, wdb = tr.layernorm_bwd(dy, x, gamma, mean, rstd)
+    assert (ws[nbytes:] == 0xAB).all()
+    assert gaps_kept(dxbuf, dx, offset), "written between the rows"
+    md, rs = mean.double()[:, None], rstd.double()[:, None]
+    xh = ((x.double() - md) * rs).abs()
+    eh = rs * 2 * E * (x.double().abs() + md.abs()) + 2 * E * xh      # error of xhat
+    d = (dy.double() * (gamma.double() if affine else 1.0)).abs()
+    c = (C / 32 + 16) * E
+    e1 = (c + 2 * E) * d.mean(1, keepdim=True)
+    s2 = (d * xh).mean(1, keepdim=True)
+    e2 = (c + 4 * E) * s2 + (d * eh).mean(1, keepdim=True)
+    s1 = d.mean(1, keepdim=True)
+    tol = rs * (4 * E * (d + s1 + xh * s2) + e1 + xh * e2 + eh * s2)
+    check(dx, wdx, tol * 1.01 + rounded(wdx, dtype), "dx")
+    cr = (R + 16) * E      # a column's rows may be added one after another
+    if sums[0]:
+        tol = cr * (dy.double().abs() * xh).sum(0) + (dy.double().abs() * eh).sum(0)
+        check(dg, wdg, tol * 1.01 + rounded(wdg, dw), "dgamma")
+    if sums[1]:
+        check(db, wdb, cr * dy.double().abs().sum(0) + rounded(wdb, dw), "dbeta")
+
+
+@pytest.mark.parametrize("C", [1, 2, 7, 31, 32, 33, 64, 127, 128, 255, 1000, 1023, 1024, 2048, 4096,
+                               4097, 8192, 10000, 16384, 20001, 33000, 70000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_backward_sizes(gs, C, dtype):
+    for R in (1, 3, 37, 700 if C <= 10000 else 160):
+        bwd_case(gs, R, C, TYPES[dtype], torch.float32)
+
+
+@pytest.mark.parametrize("dtype,wt", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (1, 0), (0, 1), (3, 5), (8, 8), (24, 16)])
+def test_backward_strides_and_alignment(gs, dtype, wt, pad, offset):
+    for C in (40, 129, 1024, 4096, 9001):
+        bwd_case(gs, 203, C, TYPES[dtype], TYPES[wt], pad, offset)
+
+
+@pytest.mark.parametrize("dw", ["f16", "bf16", "f32"])
+def test_backward_gradient_types_and_absent_outputs(gs, dw):
+    bwd_case(gs, 300, 1000, torch.bfloat16, torch.float32, dw=TYPES[dw])
+    bwd_case(gs, 300, 1000, torch.bfloat16, torch.float32, dw=TYPES[dw], sums=(True, False))
+    bwd_case(gs, 300, 1000, torch.bfloat16, torch.float32, dw=TYPES[dw], sums=(False, True))
+    bwd_case(gs, 300, 1000, torch.bfloat16, torch.float32, sums=(False, False), affine=False)
+
+
+def test_backward_many_rows(gs):
+    bwd_case(gs, 20011, 96, torch.bfloat16, torch.float32)
+    bwd_case(gs, 70001, 33, torch.float16, torch.float32)
+    bwd_case(gs, 5003, 4096, torch.bfloat16, torch.bfloat16)
+
+
+def test_backward_without_rows_writes_zero_sums(gs):
+    x = torch.empty(0, 100, device=DEV)
+    none = torch.empty(0, device=DEV)
+    dg, db = torch.full((100,), 9.0, device=DEV), torch.full((100,), 9.0, device=DEV)
+    gs.gs_layernorm_bwd(x, x, None, none, none, torch.empty(0, 100, device=DEV), dg, db, None)
+    assert (dg == 0).all() and (db == 0).all()
+
+
+def test_backward_is_reproducible(gs):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    R, C = 3001, 2056
+    x, dy = (torch.randn(R, C, device=DEV, generator=gen).bfloat16() for _ in range(2))
+    mean, rstd = x.float().mean(1), x.float().var(1).rsqrt()
+    got = []
+    for _ in range(3):
+        dx, dg, db = torch.empty_like(x), torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+        ws = torch.randint(0, 255, (gs.gs_layernorm_ws_bytes(R, C),), dtype=torch.uint8, device=DEV)
+        gs.gs_layernorm_bwd(dy, x, None, mean, rstd, dx, dg, db, ws)
+        got.append((dx, dg, db))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+def test_rows_beyond_32_bit_offsets(gs):
+    C, ld = 4096, (1 << 31) + 4104
+    for off in (0, 1):
+        big = torch.empty(2 * ld + C + 8, dtype=torch.bfloat16, device=DEV)
+        out = torch.empty_like(big)
+        x, y = (b.as_strided((3, C), (ld, 1), off) for b in (big, out))
+        gen = torch.Generator(device=DEV)
+        gen.manual_seed(6)
+        x.copy_(torch.randn(3, C, device=DEV, generator=gen))
+        near, want = x.contiguous(), torch.empty(3, C, dtype=torch.bfloat16, device=DEV)
+        gs.gs_layernorm_fwd(x, None, None, y)
+        gs.gs_layernorm_fwd(near, None, None, want)
+        # bf16 results of sums in another order: one rounding step apart at most
+        assert ((y.float() - want.float()).abs() <= want.float().abs() * 2.0 ** -7).all()
+        mean, rstd = near.float().mean(1), near.float().var(1).rsqrt()
+        wdx, dg, db = torch.empty_like(near), torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+        dg2, db2 = torch.empty_like(dg), torch.empty_like(db)
+        ws = torch.empty(gs.gs_layernorm_ws_bytes(3, C), dtype=torch.uint8, device=DEV)
+        gs.gs_layernorm_bwd(x, x, None, mean, rstd, y, dg, db, ws)
+        gs.gs_layernorm_bwd(near, near, None, mean, rstd, wdx, dg2, db2, ws)
+        bound = wdx.float().abs() * 2.0 ** -7 + 2.0 ** -16
+        assert ((y.float() - wdx.float()).abs() <= bound).all()
+        assert torch.allclose(dg, dg2, rtol=1e-5, atol=1e-5) and torch.allclose(db, db2, rtol=1e-5, atol=1e-5)
+        del big, out, x, y
+        torch.cuda.empty_cache()
+
+
+def test_runs_on_the_given_stream_and_in_a_graph(gs):
+    x = torch.randn(64, 1000, device=DEV)
+    y, want = torch.zeros_like(x), torch.empty_like(x)
+    gs.gs_layernorm_fwd(x, None, None, want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gs.gs_layernorm_fwd(x, None, None, y, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+    mean, rstd = x.mean(1), x.var(1).rsqrt()
+    dx, dg, db = torch.empty_like(x), torch.empty(1000, device=DEV), torch.empty(1000, device=DEV)
+    ws = torch.empty(gs.gs_layernorm_ws_bytes(64, 1000), dtype=torch.uint8, device=DEV)
+    gs.gs_layernorm_bwd(x, x, None, mean, rstd, dx, dg, db, ws)
+    wanted = [t.clone() for t in (dx, dg, db)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gs.gs_layernorm_fwd(x, None, None, y)
+        gs.gs_layernorm_bwd(x, x, None, mean, rstd, dx, dg, db, ws)
+    for t in (y, dx, dg, db):
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and all(torch.equal(a, b) for a, b in zip((dx, dg, db), wanted))
+
+
+def test_refusals(gs):
+    x = torch.randn(8, 64, device=DEV)
+    y = torch.empty_like(x)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(x, None, None, x)                      # in place
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(x, None, None, y, eps=-1.0)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(x, None, None, y, eps=float("nan"))
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(x, torch.ones(64, dtype=torch.float16, device=DEV), None, y)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(x.cpu(), None, None, y)
+    with pytest.raises(ValueError):
+        gs.gs_layernorm_fwd(x, torch.ones(63, device=DEV), None, y)
+    with pytest.raises(ValueError):
+        gs.gs_layernorm_fwd(x, None, None, y.t())
+    with pytest.raises(ValueError):
+        gs.gs_layernorm_fwd(x, None, None, y.half())
+    # columns side by side in one wider buffer do not overlap
+    wide = torch.zeros(8, 128, device=DEV)
+    wide[:, :64] = x
+    gs.gs_layernorm_fwd(wide[:, :64], None, None, wide[:, 64:])
+    gs.gs_layernorm_fwd(x, None, None, y)
+    assert torch.equal(wide[:, 64:], y) and torch.equal(wide[:, :64], x)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_fwd(wide[:, :64], None, None, wide[:, 63:127])
+    s = torch.ones(8, device=DEV)
+    dg = torch.empty(64, device=DEV)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_bwd(x, x, None, s, s, y, dg, None, None)   # sums without a workspace
+    with pytest.raises(ValueError):
+        gs.gs_layernorm_bwd(x, x, None, s, s, y, dg, None, torch.empty(4, dtype=torch.uint8, device=DEV))
+    ws = torch.empty(gs.gs_layernorm_ws_bytes(8, 64) + 4, dtype=torch.uint8, device=DEV)
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_bwd(x, x, None, s, s, y, dg, None, ws[4:])  # not 16-byte aligned
+    with pytest.raises(gs.GsError):
+        gs.gs_layernorm_bwd(x, x, None, s, s, y, s[:1].expand(64).clone()[:64], y[0], ws)
