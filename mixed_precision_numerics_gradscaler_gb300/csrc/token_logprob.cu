@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kLossThreads, 2)
   __shared__ unsigned long long row_list[TOP ? 32 : 1];
   __shared__ int chosen[TOP ? kLossThreads : 1];
   __shared__ int n_chosen;
-  __shared__ uint32_t tau_key;
+  __shared__ unsigned long long tau;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t parts = cluster_size(), rank = cluster_rank();
   constexpr int N = kVec<DT>, U = 4;
@@ -348,12 +348,39 @@ __global__ void __launch_bounds__(kLossThreads, 2)
       if (tid == 0) n_chosen = 0;
       uint32_t* keys = reinterpret_cast<uint32_t*>(lists);
       const uint32_t top = merge_warps<uint32_t>(sort_desc(key, lane), keys, warp, lane);
-      if (warp == 0 && lane == a.top_k - 1) tau_key = top;
+      if (warp == 0 && lane == a.top_k - 1) tau = (unsigned long long)top << 32;
       __syncthreads();
-      const uint32_t tau = tau_key;
-      if (key != 0 && key >= tau) chosen[atomicAdd(&n_chosen, 1)] = tid;
+      unsigned long long bound = tau;
+      if (key != 0 && key >= (uint32_t)(bound >> 32)) chosen[atomicAdd(&n_chosen, 1)] = tid;
       __syncthreads();
-      Best b{0, (unsigned long long)tau << 32, a.top_k};
+      if (n_chosen > 2 * a.top_k + kLossWarps) {
+        // Many equal maxima (a masked part, a row of few values): order them
+        // by where each first occurs, which leaves k threads.
+        unsigned long long first = 0;
+        if (key != 0 && key >= (uint32_t)(bound >> 32)) {
+          for (int64_t i = tid; i < run.nv && first == 0; i += kLossThreads) {
+            float x[N];
+            unpack16<DT>(ld_stream(p + i), x);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+              if (first == 0 && order_key(x[j]) == key)
+                first = order_pair(x[j], (uint32_t)(c0 + run.head + i * N + j));
+          }
+          if (odd >= 0) {
+            const unsigned long long q = order_pair(load1<DT>(row, odd), (uint32_t)(c0 + odd));
+            if (q > first) first = q;
+          }
+        }
+        const unsigned long long best_first =
+            merge_warps<unsigned long long>(sort_desc(first, lane), lists, warp, lane);
+        if (warp == 0 && lane == a.top_k - 1) tau = best_first;
+        if (tid == 0) n_chosen = 0;
+        __syncthreads();
+        bound = tau;
+        if (first != 0 && first >= bound) chosen[atomicAdd(&n_chosen, 1)] = tid;
+        __syncthreads();
+      }
+      Best b{0, bound, a.top_k};
       for (int g = warp; g < n_chosen; g += kLossWarps) {
         const int o = chosen[g];
         for (int64_t i0 = o; i0 < run.nv; i0 += (int64_t)32 * kLossThreads) {
@@ -470,11 +497,17 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
 // ---- backward --------------------------------------------------------------
 // An elementwise pass: each logit is read once, p formed from lse, and the
 // gradient written.  HBM-bound (the two tensors); about five instructions per
-// element.
+// element.  A CTA takes one run of a row and issues its loads before anything
+// that waits for the row's scalars.
 
 constexpr int kBwdThreads = 256;
-constexpr int kBwdVecs = 4;                              // per thread of a run
-constexpr int kBwdRun = kBwdThreads * kBwdVecs * 8;      // columns of a run
+
+// Columns of a thread's granule: 32 bytes of the wider type.
+template <int DT, int OT>
+constexpr int kGranule = (DT == GS_F32 || OT == GS_F32) ? 8 : 16;
+constexpr int kBwdGranules = 2;  // per thread of a run
+template <int DT, int OT>
+constexpr int kBwdRun = kBwdThreads * kBwdGranules * kGranule<DT, OT>;
 
 struct LogprobBwdArgs {
   const void* logits;
@@ -486,57 +519,107 @@ struct LogprobBwdArgs {
   const float* dentropy;
   const float* loss_scale;
   void* dlogits;
-  int64_t ld_out, runs;  // runs per row
+  int64_t ld_out;
+  int runs;  // runs per row
   bool in_place;
 };
 
-// Eight elements as fp32, by 16-byte loads or one by one.  Not through the
-// read-only path: dlogits may be the logits.
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, bool vec, float* x) {
-  const typename Elem<DT>::type* q = static_cast<const typename Elem<DT>::type*>(p) + i;
-  if (vec) {
-    const uint4* v = reinterpret_cast<const uint4*>(q);
-    unpack16<DT>(v[0], x);
-    if constexpr (DT == GS_F32) unpack16<DT>(v[1], x + 4);
-  } else {
+// G elements' bits, loaded 16 or 32 bytes at a time or one by one.  Not
+// through the read-only path: dlogits may be the logits.
+template <int DT, int G>
+struct Granule {
+  static constexpr int kWords = G * (int)sizeof(typename Elem<DT>::type) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* base, int64_t i, bool vec) {
+    const typename Elem<DT>::type* q = static_cast<const typename Elem<DT>::type*>(base) + i;
+    if (vec) {
+      if constexpr (kWords == 8) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(q));
+      } else {
+        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "l"(q));
+      }
+    } else if constexpr (DT == GS_F32) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = Elem<DT>::get(q[j]);
+      for (int j = 0; j < G; ++j) w[j] = __float_as_uint(q[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < G / 2; ++j) w[j] = (uint32_t)q[2 * j] | ((uint32_t)q[2 * j + 1] << 16);
+    }
   }
-}
-// Eight results; p + i is 16-byte aligned.
-template <int OT>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float* x) {
-  uint4* q = reinterpret_cast<uint4*>(static_cast<typename Elem<OT>::type*>(p) + i);
-  if constexpr (OT == GS_F32) {
-    st_stream(q, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                            __float_as_uint(x[3])));
-    st_stream(q + 1, make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]),
-                                __float_as_uint(x[6]), __float_as_uint(x[7])));
-  } else {
-    uint32_t w[4];
+  __device__ __forceinline__ void unpack(float* x) const {
+    if constexpr (DT == GS_F32) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (OT == GS_BF16) {
+      for (int j = 0; j < G; ++j) x[j] = __uint_as_float(w[j]);
+    } else {
+      using Tag = std::conditional_t<DT == GS_BF16, BF16Tag, F16Tag>;
+#pragma unroll
+      for (int j = 0; j < G / 2; ++j) {
+        x[2 * j] = lo16<Tag>(w[j]);
+        x[2 * j + 1] = hi16<Tag>(w[j]);
+      }
+    }
+  }
+  __device__ __forceinline__ void pack(const float* x) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      if constexpr (DT == GS_F32) {
+        w[j] = __float_as_uint(x[j]);
+      } else if constexpr (DT == GS_BF16) {
         w[j] = cvt_f32x2_bf16x2(x[2 * j + 1], x[2 * j]);
       } else {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
       }
     }
-    st_stream(q, make_uint4(w[0], w[1], w[2], w[3]));
   }
-}
+  // base + i is aligned to the granule.
+  __device__ __forceinline__ void store(void* base, int64_t i) const {
+    typename Elem<DT>::type* q = static_cast<typename Elem<DT>::type*>(base) + i;
+    if constexpr (kWords == 8) {
+      V8 v;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v.w[j] = w[j];
+      st_stream8(q, v);
+    } else {
+      st_stream(reinterpret_cast<uint4*>(q), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  }
+};
 
 template <int DT, int OT, bool ENT>
 __global__ void __launch_bounds__(kBwdThreads)
     token_logprob_bwd_kernel(const LogprobBwdArgs a) {
   __shared__ float red[kBwdThreads / 32];
-  const float S = a.loss_scale ? *a.loss_scale : 1.0f;
-  for (int64_t w = blockIdx.x; w < a.R * a.runs; w += gridDim.x) {
-    const int64_t r = w / a.runs, run = w - r * a.runs;
-    const void* in =
-        static_cast<const typename Elem<DT>::type*>(a.logits) + r * a.ld;
+  constexpr int G = kGranule<DT, OT>, U = kBwdGranules;
+  using In = Granule<DT, G>;
+  using Out = Granule<OT, G>;
+  const int run = blockIdx.x;
+  for (int64_t r = blockIdx.y; r < a.R; r += gridDim.y) {
+    const void* in = static_cast<const typename Elem<DT>::type*>(a.logits) + r * a.ld;
     void* out = static_cast<typename Elem<OT>::type*>(a.dlogits) + r * a.ld_out;
+    // `head` columns up to the first granule boundary of the output
+    constexpr uint32_t kAlign = Out::kWords * 4;
+    int64_t head = (int64_t)((kAlign - ((uint32_t)(uintptr_t)out & (kAlign - 1))) & (kAlign - 1)) /
+                   (int64_t)sizeof(typename Elem<OT>::type);
+    if (head > a.V) head = a.V;
+    const int64_t nv = (a.V - head) / G;
+    const bool vec = ((uintptr_t)(static_cast<const typename Elem<DT>::type*>(in) + head) &
+                      (In::kWords * 4 - 1)) == 0;
+    In w[U];
+    const auto fetch = [&](int64_t k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t v = (k * U + u) * kBwdThreads + threadIdx.x;
+        if (v < nv) w[u].load(in, head + v * G, vec);
+      }
+    };
+    fetch(run);
+
+    const float S = a.loss_scale ? *a.loss_scale : 1.0f;
     const float l = a.lse[r];
     const int64_t at = a.targets[r];
     const bool none = l == -CUDART_INF_F;
@@ -548,11 +631,11 @@ __global__ void __launch_bounds__(kBwdThreads)
     // place, the row must not be overwritten by another CTA meanwhile: the
     // first run's CTA then does the whole row.
     float ls = 0.0f;
-    int64_t last_run = run + 1;
+    int runs = 1;
     if (fabsf(l) > kLseExact && !none) {
       if (a.in_place) {
         if (run > 0) continue;
-        last_run = a.runs;
+        runs = a.runs;
       }
       float s = 0.0f;
       for (int64_t c = threadIdx.x; c < a.V; c += kBwdThreads)
@@ -568,45 +651,47 @@ __global__ void __launch_bounds__(kBwdThreads)
       const float p = ex2(d * kLog2e);
       return ENT ? p * __fmaf_rn(-ge, d + eh, -g) : p * -g;
     };
-    // `head` columns up to the first 16-byte boundary of the output
-    int64_t head = (int64_t)((16u - ((uint32_t)(uintptr_t)out & 15u)) & 15u) /
-                   (int64_t)sizeof(typename Elem<OT>::type);
-    if (head > a.V) head = a.V;
-    const int64_t nv = (a.V - head) / 8;
-    const bool vec =
-        ((uintptr_t)(static_cast<const typename Elem<DT>::type*>(in) + head) & 15u) == 0;
-    for (int64_t k = run; k < last_run; ++k) {
-      const int64_t v0 = k * (kBwdRun / 8);
-      float x[kBwdVecs][8];
-  #pragma unroll
-      for (int u = 0; u < kBwdVecs; ++u) {
-        const int64_t v = v0 + u * kBwdThreads + threadIdx.x;
-        if (v < nv) load8<DT>(in, head + v * 8, vec, x[u]);
-      }
-  #pragma unroll
-      for (int u = 0; u < kBwdVecs; ++u) {
-        const int64_t v = v0 + u * kBwdThreads + threadIdx.x;
+    for (int k = run;; ++k) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t v = ((int64_t)k * U + u) * kBwdThreads + threadIdx.x;
         if (v >= nv) continue;
-  #pragma unroll
-        for (int j = 0; j < 8; ++j) x[u][j] = grad(x[u][j]);
-        const uint64_t hot = (uint64_t)(at - (head + v * 8));
-        if (hot < 8) {
-  #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (hot == (uint64_t)j) x[u][j] += g;
+        float x[G];
+        w[u].unpack(x);
+#pragma unroll
+        for (int j = 0; j < G; ++j) x[j] = grad(x[j]);
+        const uint64_t hot = (uint64_t)(at - (head + v * G));
+        if (hot < G) {
+#pragma unroll
+          for (int j = 0; j < G; ++j)
+            if (hot == (uint64_t)j) x[j] += g;
         }
-        store8<OT>(out, head + v * 8, x[u]);
+        Out o;
+        o.pack(x);
+        o.store(out, head + v * G);
       }
+      if (k + 1 >= run + runs) break;
+      fetch(k + 1);
     }
-    if (run == 0) {  // the columns outside the vectors
-      const int64_t odd = a.V - nv * 8;
+    if (run == 0) {  // the columns outside the granules
+      const int64_t odd = a.V - nv * G;
       for (int64_t i = threadIdx.x; i < odd; i += kBwdThreads) {
-        const int64_t c = i < head ? i : nv * 8 + i;
+        const int64_t c = i < head ? i : nv * G + i;
         store1<OT>(out, c, grad(load1<DT>(in, c)) + (c == at ? g : 0.0f));
       }
     }
-    __syncthreads();  // `red` is free for the next run
+    if (gridDim.y < a.R) __syncthreads();  // `red` is free for the next row
   }
+}
+
+template <int DT, int OT>
+static void bwd_launch(LogprobBwdArgs a, cudaStream_t stream) {
+  a.runs = (int)((a.V + kBwdRun<DT, OT> - 1) / kBwdRun<DT, OT>);
+  const dim3 grid((unsigned)a.runs, (unsigned)(a.R < 65535 ? a.R : 65535));
+  if (a.dentropy)
+    token_logprob_bwd_kernel<DT, OT, true><<<grid, kBwdThreads, 0, stream>>>(a);
+  else
+    token_logprob_bwd_kernel<DT, OT, false><<<grid, kBwdThreads, 0, stream>>>(a);
 }
 
 cudaError_t launch_token_logprob_bwd(const void* logits, int64_t ld, int dtype, int64_t R,
@@ -615,25 +700,16 @@ cudaError_t launch_token_logprob_bwd(const void* logits, int64_t ld, int dtype, 
                                      const float* dentropy, const float* loss_scale,
                                      void* dlogits, int64_t ld_out, int out_dtype,
                                      cudaStream_t stream) {
-  const int64_t runs = (V + kBwdRun - 1) / kBwdRun;
-  const LogprobBwdArgs a{logits,  ld,       R,          V,       targets, lse, dlogprob,
-                         entropy, dentropy, loss_scale, dlogits, ld_out,  runs, dlogits == logits};
-  const int64_t most = (int64_t)1 << 30;
-  const unsigned grid = (unsigned)(R < most / runs ? R * runs : most);
-#define GS_F(DT, OT)                                                               \
-  if (dentropy)                                                                    \
-    token_logprob_bwd_kernel<DT, OT, true><<<grid, kBwdThreads, 0, stream>>>(a);   \
-  else                                                                             \
-    token_logprob_bwd_kernel<DT, OT, false><<<grid, kBwdThreads, 0, stream>>>(a)
-#define GS_G(DT)                                     \
-  if (out_dtype == GS_F32) { GS_F(DT, GS_F32); }     \
-  else if (out_dtype == GS_F16) { GS_F(DT, GS_F16); }\
-  else { GS_F(DT, GS_BF16); }
-  if (dtype == GS_F32) { GS_G(GS_F32) }
-  else if (dtype == GS_F16) { GS_G(GS_F16) }
-  else { GS_G(GS_BF16) }
+  const LogprobBwdArgs a{logits,   ld,         R,       V,      targets, lse, dlogprob, entropy,
+                         dentropy, loss_scale, dlogits, ld_out, 0,       dlogits == logits};
+#define GS_G(DT)                                                      \
+  if (out_dtype == GS_F32) bwd_launch<DT, GS_F32>(a, stream);         \
+  else if (out_dtype == GS_F16) bwd_launch<DT, GS_F16>(a, stream);    \
+  else bwd_launch<DT, GS_BF16>(a, stream)
+  if (dtype == GS_F32) { GS_G(GS_F32); }
+  else if (dtype == GS_F16) { GS_G(GS_F16); }
+  else { GS_G(GS_BF16); }
 #undef GS_G
-#undef GS_F
   return cudaGetLastError();
 }
 
