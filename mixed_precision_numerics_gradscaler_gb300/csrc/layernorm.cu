@@ -7,104 +7,243 @@
 //   d = dy gamma,  xhat = (x - mean) rstd
 //   dx = rstd (d - sum d / C - xhat (sum d xhat) / C)
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
+//
+// Both passes are HBM-bound: forward 2 elements moved per element, backward 3.
+//
+// Forward: a row is read once into registers (at most 32 values per thread),
+// the variance formed about the mean from there (two block sums; a one-pass
+// variance would cancel for rows far from zero), and written.  A warp takes a
+// short row by itself, a CTA a long one; several rows per SM overlap.  Longer
+// rows than a CTA's registers hold are read three times, out of L2 after the
+// first.
+//
+// Backward: one pass over dy and x.  A CTA keeps its share of dgamma and
+// dbeta in registers while it walks the rows; every thread owns the same
+// columns of every row and copies its part of the next rows into shared
+// memory itself (cp.async), so that no thread waits for another's copy and
+// the memory stays busy across the one barrier of a row (its two sums).  At
+// the end each CTA writes one row of partial sums, which a second kernel adds
+// in a fixed order: no atomics, the result depends on the sizes and the
+// device alone.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "gs_elem.cuh"
 #include "gs_internal.h"
+#include "gs_quant.cuh"
 
 namespace gs {
 
-constexpr int kNormThreads = 256;
-
-template <int DT, int WT>
-__global__ void __launch_bounds__(kNormThreads)
-    layernorm_fwd_kernel(const void* x, int64_t ldx, int64_t R, int64_t C, const void* gamma,
-                         const void* beta, float eps, void* y, int64_t ldy, float* mean,
-                         float* rstd) {
-  __shared__ float red[kNormThreads / 32];
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const int64_t xo = r * ldx, yo = r * ldy;
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < C; c += kNormThreads) s += load1<DT>(x, xo + c);
-    const float mu = block_sum<kNormThreads>(s, red) / (float)C;
-    s = 0.0f;
-    for (int64_t c = threadIdx.x; c < C; c += kNormThreads) {
-      const float d = load1<DT>(x, xo + c) - mu;
-      s = __fmaf_rn(d, d, s);
-    }
-    const float rs = 1.0f / sqrtf(block_sum<kNormThreads>(s, red) / (float)C + eps);
-    for (int64_t c = threadIdx.x; c < C; c += kNormThreads) {
-      const float h = (load1<DT>(x, xo + c) - mu) * rs;
-      const float g = gamma ? load1<WT>(gamma, c) : 1.0f;
-      const float b = beta ? load1<WT>(beta, c) : 0.0f;
-      store1<DT>(y, yo + c, __fmaf_rn(h, g, b));
-    }
-    if (threadIdx.x == 0) {
-      if (mean) mean[r] = mu;
-      if (rstd) rstd[r] = rs;
-    }
-  }
-}
-
-template <int DT, int WT>
-__global__ void __launch_bounds__(kNormThreads)
-    layernorm_dx_kernel(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t R,
-                        int64_t C, const void* gamma, const float* mean, const float* rstd,
-                        void* dx, int64_t lddx) {
-  __shared__ float red[kNormThreads / 32];
-  for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-    const float mu = mean[r], rs = rstd[r];
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int64_t c = threadIdx.x; c < C; c += kNormThreads) {
-      const float h = (load1<DT>(x, r * ldx + c) - mu) * rs;
-      const float d = load1<DT>(dy, r * lddy + c) * (gamma ? load1<WT>(gamma, c) : 1.0f);
-      s1 += d;
-      s2 = __fmaf_rn(d, h, s2);
-    }
-    s1 = block_sum<kNormThreads>(s1, red) / (float)C;
-    s2 = block_sum<kNormThreads>(s2, red) / (float)C;
-    for (int64_t c = threadIdx.x; c < C; c += kNormThreads) {
-      const float h = (load1<DT>(x, r * ldx + c) - mu) * rs;
-      const float d = load1<DT>(dy, r * lddy + c) * (gamma ? load1<WT>(gamma, c) : 1.0f);
-      store1<DT>(dx, r * lddx + c, rs * (d - s1 - h * s2));
-    }
-  }
-}
-
-// Partial sums of dgamma and dbeta: CTA (i, j) adds rows i, i + P, ... of
-// columns [256 j, 256 j + 256) and writes row i of ws [2, P, C].
+// ---- element vectors --------------------------------------------------------
+// W consecutive elements as fp32: W = 1, or 16 bytes' worth (a whole vector,
+// 16-byte aligned).
 template <int DT>
-__global__ void __launch_bounds__(kNormThreads)
-    layernorm_dw_kernel(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t R,
-                        int64_t C, const float* mean, const float* rstd, float* ws, int64_t P) {
-  const int64_t c = (int64_t)blockIdx.x * kNormThreads + threadIdx.x, i = blockIdx.y;
-  if (c >= C) return;
-  float sg = 0.0f, sb = 0.0f;
-  for (int64_t r = i; r < R; r += P) {
-    const float d = load1<DT>(dy, r * lddy + c);
-    sg = __fmaf_rn(d, (load1<DT>(x, r * ldx + c) - mean[r]) * rstd[r], sg);
-    sb += d;
+constexpr int kVecElems = DT == GS_F32 ? 4 : 8;
+
+template <int DT>
+__device__ __forceinline__ void unpack_vec(const uint4& v, float* f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == GS_F32) {
+      f[i] = __uint_as_float(w[i]);
+    } else {
+      using Tag = std::conditional_t<DT == GS_BF16, BF16Tag, F16Tag>;
+      f[2 * i] = lo16<Tag>(w[i]);
+      f[2 * i + 1] = hi16<Tag>(w[i]);
+    }
   }
-  ws[i * C + c] = sg;
-  ws[(P + i) * C + c] = sb;
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack_vec(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == GS_F32) {
+      w[i] = __float_as_uint(f[i]);
+    } else if constexpr (DT == GS_BF16) {
+      w[i] = cvt_f32x2_bf16x2(f[2 * i + 1], f[2 * i]);
+    } else {
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int OT>
-__global__ void __launch_bounds__(kNormThreads)
-    layernorm_dw_join_kernel(const float* ws, int64_t P, int64_t C, void* dgamma, void* dbeta) {
-  const int64_t c = (int64_t)blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= C) return;
-  float sg = 0.0f, sb = 0.0f;
-  for (int64_t i = 0; i < P; ++i) {
-    sg += ws[i * C + c];
-    sb += ws[(P + i) * C + c];
+// W weights from column c; `missing` where there are none.  `vec`: the array
+// is 16-byte aligned.
+template <int WT, int W>
+__device__ __forceinline__ void load_weights(const void* p, int64_t c, bool vec, float missing,
+                                             float* f) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = missing;
+  } else if (W * sizeof(typename Elem<WT>::type) >= 16 && vec) {
+    const uint4* q =
+        reinterpret_cast<const uint4*>(static_cast<const typename Elem<WT>::type*>(p) + c);
+#pragma unroll
+    for (int i = 0; i < W / kVecElems<WT>; ++i) unpack_vec<WT>(__ldg(q + i), f + i * kVecElems<WT>);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) f[i] = load1<WT>(p, c + i);
   }
-  if (dgamma) store1<OT>(dgamma, c, sg);
-  if (dbeta) store1<OT>(dbeta, c, sb);
 }
 
-int64_t layernorm_partials(int64_t R, int64_t) { return R < 128 ? R : 128; }
+// ---- forward ----------------------------------------------------------------
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx, R, C;
+  const void* gamma;
+  const void* beta;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* mean;
+  float* rstd;
+  bool w_vec;  // gamma and beta are 16-byte aligned (or absent)
+};
+
+// Sum over the NT threads that share a row: a warp's, or the CTA's; `red`
+// holds NT / 32 floats that no thread still reads.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if constexpr (NT > 32) {
+    constexpr int kWarps = NT / 32;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < kWarps ? red[lane] : 0.0f;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if constexpr (kWarps < 32) v = __shfl_sync(0xFFFFFFFFu, v, 0);
+  }
+  return v;
+}
+
+// NT threads per row, each with up to VPT vectors of W columns.
+template <int DT, int WT, int W, int NT, int VPT>
+__global__ void __launch_bounds__(NT < 256 ? 256 : NT)
+    layernorm_fwd_kernel(const NormArgs a) {
+  __shared__ float red[2][NT / 32];
+  const int tid = NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t r = NT >= 256 ? (int64_t)blockIdx.x
+                              : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / NT;
+  if (r >= a.R) return;  // whole warps: NT < 256 has one row per warp
+  static_assert(NT == 32 || NT >= 256, "a row is a warp's or a CTA's");
+  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ldx;
+  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + r * a.ldy;
+  const int C = (int)a.C;
+  float f[VPT][W];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * NT + tid) * W;
+    if (c < C) {
+      if constexpr (W > 1) unpack_vec<DT>(ld_stream(reinterpret_cast<const uint4*>(x + c)), f[i]);
+      else f[i][0] = Elem<DT>::get(x[c]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) f[i][j] = 0.0f;
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < W; ++j) s += f[i][j];
+  const float mu = __fdiv_rn(row_sum<NT>(s, red[0]), (float)C);
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if ((i * NT + tid) * W < C) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        f[i][j] -= mu;
+        s = __fmaf_rn(f[i][j], f[i][j], s);
+      }
+    }
+  const float var = __fdiv_rn(row_sum<NT>(s, red[1]), (float)C);
+  const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = (i * NT + tid) * W;
+    if (c < C) {
+      float g[W], b[W];
+      load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
+      load_weights<WT, W>(a.beta, c, a.w_vec, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < W; ++j) f[i][j] = __fmaf_rn(f[i][j] * rs, g[j], b[j]);
+      if constexpr (W > 1) st_stream(reinterpret_cast<uint4*>(y + c), pack_vec<DT>(f[i]));
+      else y[c] = Elem<DT>::put(f[i][0]);
+    }
+  }
+  if (tid == 0) {
+    if (a.mean) a.mean[r] = mu;
+    if (a.rstd) a.rstd[r] = rs;
+  }
+}
+
+// Rows of any length, read three times.
+constexpr int kLongThreads = 1024;
+template <int DT, int WT>
+__global__ void __launch_bounds__(kLongThreads) layernorm_fwd_long_kernel(const NormArgs a) {
+  __shared__ float red[2][kLongThreads / 32];
+  const int64_t r = blockIdx.x, xo = r * a.ldx, yo = r * a.ldy;
+  float s = 0.0f;
+  for (int64_t c = threadIdx.x; c < a.C; c += kLongThreads) s += load1<DT>(a.x, xo + c);
+  const float mu = __fdiv_rn(row_sum<kLongThreads>(s, red[0]), (float)a.C);
+  s = 0.0f;
+  for (int64_t c = threadIdx.x; c < a.C; c += kLongThreads) {
+    const float d = load1<DT>(a.x, xo + c) - mu;
+    s = __fmaf_rn(d, d, s);
+  }
+  const float var = __fdiv_rn(row_sum<kLongThreads>(s, red[1]), (float)a.C);
+  const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+  for (int64_t c = threadIdx.x; c < a.C; c += kLongThreads) {
+    float g, b;
+    load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g);
+    load_weights<WT, 1>(a.beta, c, false, 0.0f, &b);
+    store1<DT>(a.y, yo + c, __fmaf_rn((load1<DT>(a.x, xo + c) - mu) * rs, g, b));
+  }
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[r] = mu;
+    if (a.rstd) a.rstd[r] = rs;
+  }
+}
+
+static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+template <int DT, int WT>
+static void fwd_launch(const NormArgs& a, cudaStream_t stream) {
+  constexpr int V = kVecElems<DT>;
+  const bool vec = aligned16(a.x) && aligned16(a.y) && a.C % V == 0 && a.ldx % V == 0 &&
+                   a.ldy % V == 0;
+  const unsigned rows = (unsigned)a.R, warps = (unsigned)((a.R + 7) / 8);
+#define GS_L(W, NT, VPT)                                                                      \
+  layernorm_fwd_kernel<DT, WT, W, NT, VPT>                                                    \
+      <<<NT == 32 ? warps : rows, NT == 32 ? 256 : NT, 0, stream>>>(a)
+  if (vec) {
+    const int64_t nv = a.C / V;
+    if (nv <= 32) GS_L(V, 32, 1);
+    else if (nv <= 128) GS_L(V, 32, 4);
+    else if (nv <= 512) GS_L(V, 256, 2);
+    else if (nv <= 1024) GS_L(V, 256, 4);
+    else if (nv <= 2048) GS_L(V, 512, 4);
+    else if (nv <= 4096) GS_L(V, 1024, 4);
+    else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
+  } else {
+    if (a.C <= 128) GS_L(1, 32, 4);
+    else if (a.C <= 1024) GS_L(1, 256, 4);
+    else if (a.C <= 4096) GS_L(1, 512, 8);
+    else if (a.C <= 16384) GS_L(1, 1024, 16);
+    else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
+  }
+#undef GS_L
+}
 
 // Runs `f` with the two type codes as template arguments: w_dtype is GS_F32
 // or dtype.
@@ -122,13 +261,356 @@ cudaError_t launch_layernorm_fwd(const void* x, int64_t ldx, int dtype, int64_t 
                                  const void* gamma, const void* beta, int w_dtype, float eps,
                                  void* y, int64_t ldy, float* mean, float* rstd,
                                  cudaStream_t stream) {
-  const int64_t most = (int64_t)sm_count() * 64;
-  const unsigned grid = (unsigned)(R < most ? R : most);
-#define GS_F(DT, WT)                                                                           \
-  layernorm_fwd_kernel<DT, WT><<<grid, kNormThreads, 0, stream>>>(x, ldx, R, C, gamma, beta,  \
-                                                                  eps, y, ldy, mean, rstd);
-  GS_NORM_TYPES(dtype, w_dtype, GS_F)
+  const int64_t esz = dtype == GS_F32 ? 4 : 2, most = (int64_t)1 << 30;
+  for (int64_t r0 = 0; r0 < R; r0 += most) {  // rows of one grid
+    const NormArgs a{static_cast<const char*>(x) + r0 * ldx * esz, ldx,
+                     std::min(most, R - r0), C, gamma, beta, eps,
+                     static_cast<char*>(y) + r0 * ldy * esz, ldy,
+                     mean ? mean + r0 : nullptr, rstd ? rstd + r0 : nullptr,
+                     aligned16(gamma) && aligned16(beta)};
+#define GS_F(DT, WT) fwd_launch<DT, WT>(a, stream);
+    GS_NORM_TYPES(dtype, w_dtype, GS_F)
 #undef GS_F
+  }
+  return cudaGetLastError();
+}
+
+// ---- backward ---------------------------------------------------------------
+
+struct NormBwdArgs {
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx, R, C;
+  const void* gamma;
+  const float* mean;
+  const float* rstd;
+  void* dx;
+  int64_t lddx;
+  float* ws;  // [2, gridDim.x, C] partial sums, or nullptr
+  bool w_vec;
+};
+
+// The two sums of a row over the CTA, the same in every thread; `red` holds
+// one float2 per warp that no thread still reads.
+__device__ __forceinline__ float2 row_sum2(float s1, float s2, float2* red, int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+    s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+  }
+  if (warps > 1) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(s1, s2);
+    __syncthreads();
+    const float2 p = lane < warps ? red[lane] : make_float2(0.0f, 0.0f);
+    s1 = p.x;
+    s2 = p.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+      s2 += __shfl_xor_sync(0xFFFFFFFFu, s2, o);
+    }
+  }
+  return make_float2(s1, s2);
+}
+
+// Rows 16 bytes at a time: thread t owns vector t of every row.
+constexpr int kBwdSteps = 4;  // rows copied ahead
+template <int DT, int WT>
+__global__ void __launch_bounds__(1024, 1) layernorm_bwd_vec_kernel(const NormBwdArgs a) {
+  constexpr int W = kVecElems<DT>;
+  extern __shared__ uint4 ring[];  // [kBwdSteps][x, dy][blockDim.x]
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, c = tid * W;
+  const bool live = c < a.C;
+  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
+  const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy) + c;
+  typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx) + c;
+  float g[W], ag[W], ab[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) g[j] = ag[j] = ab[j] = 0.0f;
+  if (live) load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
+  const float inv = __fdiv_rn(1.0f, (float)a.C);
+
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
+  const auto copy_row = [&](int64_t r, int slot) {
+    if (r < a.R && live) {
+      const uint32_t to = slot0 + slot * 2 * nt * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(x + r * a.ldx)
+                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + nt * 16),
+                   "l"(dy + r * a.lddy)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kBwdSteps; ++i) copy_row(blockIdx.x + (int64_t)i * gridDim.x, i);
+  int slot = 0, side = 0;
+  float mu = 0.0f, rs = 0.0f;
+  if (blockIdx.x < a.R) {
+    mu = a.mean[blockIdx.x];
+    rs = a.rstd[blockIdx.x];
+  }
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kBwdSteps - 1) : "memory");
+    float h[W], d[W];
+    float s1 = 0.0f, s2 = 0.0f;
+    if (live) {
+      unpack_vec<DT>(ring[slot * 2 * nt + tid], h);
+      unpack_vec<DT>(ring[(slot * 2 + 1) * nt + tid], d);
+    } else {
+#pragma unroll
+      for (int j = 0; j < W; ++j) h[j] = d[j] = 0.0f;
+    }
+    const float this_rs = rs;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      h[j] = (h[j] - mu) * rs;
+      ab[j] += d[j];
+      ag[j] = __fmaf_rn(d[j], h[j], ag[j]);
+      d[j] *= g[j];
+      s1 += d[j];
+      s2 = __fmaf_rn(d[j], h[j], s2);
+    }
+    copy_row(r + (int64_t)kBwdSteps * gridDim.x, slot);
+    slot = slot + 1 < kBwdSteps ? slot + 1 : 0;
+    const int64_t next = r + gridDim.x;
+    if (next < a.R) {
+      mu = a.mean[next];
+      rs = a.rstd[next];
+    }
+    const float2 s = row_sum2(s1, s2, red[side], warps);
+    side ^= 1;  // the other side is free: every thread has passed the barrier after its reads
+    const float c1 = s.x * inv, c2 = s.y * inv;
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) d[j] = this_rs * __fmaf_rn(-h[j], c2, d[j] - c1);
+      st_stream(reinterpret_cast<uint4*>(dx + r * a.lddx), pack_vec<DT>(d));
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;");  // the join may take this SM next
+  if (a.ws && live) {
+    float* pg = a.ws + (int64_t)blockIdx.x * a.C + c;
+    float* pb = pg + (int64_t)gridDim.x * a.C;
+#pragma unroll
+    for (int j = 0; j < W; j += 4) {  // C is a multiple of 4: the rows of ws are aligned
+      *reinterpret_cast<float4*>(pg + j) = make_float4(ag[j], ag[j + 1], ag[j + 2], ag[j + 3]);
+      *reinterpret_cast<float4*>(pb + j) = make_float4(ab[j], ab[j + 1], ab[j + 2], ab[j + 3]);
+    }
+  }
+}
+
+// Rows of any alignment, element by element: thread t owns columns t + i nt.
+// The next row's elements are loaded before this row's barrier.
+template <int DT, int WT, int EPT>
+__global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
+  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x);
+  const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy);
+  typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx);
+  float g[EPT], ag[EPT], ab[EPT];
+  typename Elem<DT>::type nx[EPT], nd[EPT];
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int c = tid + i * nt;
+    ag[i] = ab[i] = 0.0f;
+    g[i] = 0.0f;
+    if (c < C) load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g[i]);
+  }
+  const float inv = __fdiv_rn(1.0f, (float)C);
+  const auto fetch = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = tid + i * nt;
+      nx[i] = c < C ? x[r * a.ldx + c] : 0;
+      nd[i] = c < C ? dy[r * a.lddy + c] : 0;
+    }
+  };
+  float mu = 0.0f, rs = 0.0f;
+  int side = 0;
+  if (blockIdx.x < a.R) {
+    fetch(blockIdx.x);
+    mu = a.mean[blockIdx.x];
+    rs = a.rstd[blockIdx.x];
+  }
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    float h[EPT], d[EPT];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      h[i] = tid + i * nt < C ? (Elem<DT>::get(nx[i]) - mu) * rs : 0.0f;
+      d[i] = Elem<DT>::get(nd[i]);
+      ab[i] += d[i];
+      ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
+      d[i] *= g[i];
+      s1 += d[i];
+      s2 = __fmaf_rn(d[i], h[i], s2);
+    }
+    const float this_rs = rs;
+    const int64_t next = r + gridDim.x;
+    if (next < a.R) {
+      fetch(next);
+      mu = a.mean[next];
+      rs = a.rstd[next];
+    }
+    const float2 s = row_sum2(s1, s2, red[side], warps);
+    side ^= 1;
+    const float c1 = s.x * inv, c2 = s.y * inv;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = tid + i * nt;
+      if (c < C) dx[r * a.lddx + c] = Elem<DT>::put(this_rs * __fmaf_rn(-h[i], c2, d[i] - c1));
+    }
+  }
+  if (a.ws) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const int c = tid + i * nt;
+      if (c < C) {
+        a.ws[(int64_t)blockIdx.x * C + c] = ag[i];
+        a.ws[((int64_t)gridDim.x + blockIdx.x) * C + c] = ab[i];
+      }
+    }
+  }
+}
+
+// Rows of any length: dx alone, the row read twice.
+template <int DT, int WT>
+__global__ void __launch_bounds__(kLongThreads) layernorm_dx_long_kernel(const NormBwdArgs a) {
+  __shared__ float2 red[32];
+  const int64_t r = blockIdx.x;
+  const float mu = a.mean[r], rs = a.rstd[r];
+  float s1 = 0.0f, s2 = 0.0f;
+  for (int64_t c = threadIdx.x; c < a.C; c += kLongThreads) {
+    float g;
+    load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g);
+    const float h = (load1<DT>(a.x, r * a.ldx + c) - mu) * rs;
+    const float d = load1<DT>(a.dy, r * a.lddy + c) * g;
+    s1 += d;
+    s2 = __fmaf_rn(d, h, s2);
+  }
+  const float2 s = row_sum2(s1, s2, red, kLongThreads / 32);
+  const float inv = __fdiv_rn(1.0f, (float)a.C), c1 = s.x * inv, c2 = s.y * inv;
+  for (int64_t c = threadIdx.x; c < a.C; c += kLongThreads) {
+    float g;
+    load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g);
+    const float h = (load1<DT>(a.x, r * a.ldx + c) - mu) * rs;
+    const float d = load1<DT>(a.dy, r * a.lddy + c) * g;
+    store1<DT>(a.dx, r * a.lddx + c, rs * __fmaf_rn(-h, c2, d - c1));
+  }
+}
+
+// Partial sums of dgamma and dbeta for those: CTA (i, j) adds rows i, i + P,
+// ... of columns [256 j, 256 j + 256) and writes row i of ws [2, P, C].
+constexpr int kDwThreads = 256;
+template <int DT>
+__global__ void __launch_bounds__(kDwThreads) layernorm_dw_long_kernel(const NormBwdArgs a) {
+  const int64_t c = (int64_t)blockIdx.x * kDwThreads + threadIdx.x, P = gridDim.y;
+  if (c >= a.C) return;
+  float sg = 0.0f, sb = 0.0f;
+  for (int64_t r = blockIdx.y; r < a.R; r += P) {
+    const float d = load1<DT>(a.dy, r * a.lddy + c);
+    sg = __fmaf_rn(d, (load1<DT>(a.x, r * a.ldx + c) - a.mean[r]) * a.rstd[r], sg);
+    sb += d;
+  }
+  a.ws[blockIdx.y * a.C + c] = sg;
+  a.ws[(P + blockIdx.y) * a.C + c] = sb;
+}
+
+// Adds the P partial sums of each column: 32 columns per CTA, every warp adds
+// each 32nd (of the CTA's 32 warps) and the CTA joins them in order.
+constexpr int kJoinWarps = 32;
+template <int OT>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    layernorm_join_kernel(const float* ws, int64_t P, int64_t C, void* dgamma, void* dbeta) {
+  __shared__ float part[kJoinWarps][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are written
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  void* out = blockIdx.y == 0 ? dgamma : dbeta;
+  if (!out) return;
+  ws += blockIdx.y * P * C;
+  float s = 0.0f;
+  if (c < C)
+    for (int64_t i = warp; i < P; i += kJoinWarps) s += ws[i * C + c];
+  part[warp][lane] = s;
+  __syncthreads();
+  // warp w joins column w
+  s = part[lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  const int64_t oc = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && oc < C) store1<OT>(out, oc, s);
+}
+
+constexpr int kElems = 8;  // columns per thread of the element path
+struct NormBwdPlan {
+  int threads;
+  int64_t ctas;
+};
+// One CTA's threads and the CTAs of the grid, where a thread owns `each`
+// columns: 1024 threads per SM (64 registers each).
+static NormBwdPlan bwd_plan(int64_t R, int64_t C, int64_t each) {
+  const int64_t threads = ((C + each - 1) / each + 31) / 32 * 32;
+  const int64_t per_sm = std::min<int64_t>(32, 1024 / threads);
+  return NormBwdPlan{(int)threads, std::min<int64_t>(R, sm_count() * per_sm)};
+}
+static int64_t long_partials(int64_t R) { return R < 128 ? R : 128; }
+
+// Upper bound over the paths a call with these sizes may take (the alignment
+// decides which).
+int64_t layernorm_partials(int64_t R, int64_t C) {
+  if (C == 0) return 0;
+  int64_t most = long_partials(R);
+  for (int64_t each : {8, 4})
+    if (C <= 1024 * each) most = std::max(most, bwd_plan(R, C, each).ctas);
+  return most;
+}
+
+template <int DT, int WT>
+static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStream_t stream) {
+  constexpr int V = kVecElems<DT>;
+  const bool vec = aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) && a.C % V == 0 &&
+                   a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0;
+  if (vec && a.C <= 1024 * V) {
+    const NormBwdPlan p = bwd_plan(a.R, a.C, V);
+    const auto smem = [](int threads) { return kBwdSteps * 2 * threads * 16; };
+    const auto kernel = layernorm_bwd_vec_kernel<DT, WT>;
+    int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
+    const cudaError_t e =
+        kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
+    *partials = p.ctas;
+  } else if (a.C <= 1024 * kElems) {
+    const bool few = a.C <= 1024 * 4;
+    const NormBwdPlan p = bwd_plan(a.R, a.C, few ? 4 : 8);
+    if (few)
+      layernorm_bwd_elem_kernel<DT, WT, 4><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+    else
+      layernorm_bwd_elem_kernel<DT, WT, 8><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+    *partials = p.ctas;
+  } else {
+    const int64_t most = (int64_t)1 << 30;
+    for (int64_t r0 = 0; r0 < a.R; r0 += most) {
+      NormBwdArgs b = a;
+      b.x = static_cast<const typename Elem<DT>::type*>(a.x) + r0 * a.ldx;
+      b.dy = static_cast<const typename Elem<DT>::type*>(a.dy) + r0 * a.lddy;
+      b.dx = static_cast<typename Elem<DT>::type*>(a.dx) + r0 * a.lddx;
+      b.mean += r0;
+      b.rstd += r0;
+      b.R = std::min(most, a.R - r0);
+      layernorm_dx_long_kernel<DT, WT><<<(unsigned)b.R, kLongThreads, 0, stream>>>(b);
+    }
+    if (a.ws) {
+      *partials = long_partials(a.R);
+      const dim3 grid((unsigned)((a.C + kDwThreads - 1) / kDwThreads), (unsigned)*partials);
+      layernorm_dw_long_kernel<DT><<<grid, kDwThreads, 0, stream>>>(a);
+    }
+  }
   return cudaGetLastError();
 }
 
@@ -137,37 +619,33 @@ cudaError_t launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
                                  const float* mean, const float* rstd, void* dx, int64_t lddx,
                                  void* dgamma, void* dbeta, int dw_dtype, float* ws,
                                  cudaStream_t stream) {
-  const int64_t most = (int64_t)sm_count() * 64;
+  int64_t P = 0;
   if (R > 0) {
-    const unsigned grid = (unsigned)(R < most ? R : most);
-#define GS_F(DT, WT)                                                                        \
-  layernorm_dx_kernel<DT, WT><<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, ldx, R, C,    \
-                                                                 gamma, mean, rstd, dx, lddx);
+    const NormBwdArgs a{dy,   lddy, x,  ldx,  R,  C, gamma, mean, rstd, dx,
+                        lddx, ws,   aligned16(gamma)};
+    cudaError_t e = cudaSuccess;
+#define GS_F(DT, WT) e = bwd_launch<DT, WT>(a, &P, stream);
     GS_NORM_TYPES(dtype, w_dtype, GS_F)
 #undef GS_F
+    if (e != cudaSuccess) return e;
   }
-  if (!dgamma && !dbeta) return cudaGetLastError();
-  const int64_t P = layernorm_partials(R, C);
-  const unsigned cols = (unsigned)((C + kNormThreads - 1) / kNormThreads);
-  if (P > 0) {
-    const dim3 grid(cols, (unsigned)P);
-    if (dtype == GS_F32)
-      layernorm_dw_kernel<GS_F32><<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, ldx, R, C, mean,
-                                                                     rstd, ws, P);
-    else if (dtype == GS_F16)
-      layernorm_dw_kernel<GS_F16><<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, ldx, R, C, mean,
-                                                                     rstd, ws, P);
-    else
-      layernorm_dw_kernel<GS_BF16><<<grid, kNormThreads, 0, stream>>>(dy, lddy, x, ldx, R, C, mean,
-                                                                      rstd, ws, P);
-  }
+  if (!dgamma && !dbeta) return cudaSuccess;
+  // launched while the sums' kernel ends; it waits for them on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((C + 31) / 32), 2);
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const float* cws = ws;
   if (dw_dtype == GS_F32)
-    layernorm_dw_join_kernel<GS_F32><<<cols, kNormThreads, 0, stream>>>(ws, P, C, dgamma, dbeta);
-  else if (dw_dtype == GS_F16)
-    layernorm_dw_join_kernel<GS_F16><<<cols, kNormThreads, 0, stream>>>(ws, P, C, dgamma, dbeta);
-  else
-    layernorm_dw_join_kernel<GS_BF16><<<cols, kNormThreads, 0, stream>>>(ws, P, C, dgamma, dbeta);
-  return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, layernorm_join_kernel<GS_F32>, cws, P, C, dgamma, dbeta);
+  if (dw_dtype == GS_F16)
+    return cudaLaunchKernelEx(&cfg, layernorm_join_kernel<GS_F16>, cws, P, C, dgamma, dbeta);
+  return cudaLaunchKernelEx(&cfg, layernorm_join_kernel<GS_BF16>, cws, P, C, dgamma, dbeta);
 }
 
 }  // namespace gs

@@ -16,11 +16,20 @@
 // distributed shared memory.
 //
 // The alternatives come out of the same pass.  A thread's maximum is the
-// largest of the elements it read, so the k-th largest of the threads' maxima
-// is a lower bound of the k-th largest logit (k elements reach it), and only
-// the elements of threads whose maximum reaches it can be among the first k:
-// about k threads' (a few in a thousand), read again out of L2 by one warp
-// each.  A warp holds its k best in lane order and inserts candidates.
+// largest of the elements it read, so the k-th largest of any 32 of the
+// threads' maxima is a lower bound of the k-th largest logit (k elements reach
+// it), and only the elements of threads whose maximum reaches it can be among
+// the first k: with each warp's largest maxima as the 32, about k threads (a
+// few in a hundred).  Each thread keeps the block (four vectors) in which its
+// maximum first occurred in shared memory, and the maximum of its other
+// blocks: the elements of a chosen thread are at hand, and only where its
+// other blocks reach the bound too is everything it read loaded again.  What
+// reaches the bound, little more than k elements, is sorted by one warp.
+// (Loading the chosen threads' elements again, a microsecond or two under
+// load at the end of every row, cost 4096 x 128256 bf16 with 8 alternatives
+// 204 us, all of them, and 212 us, the one block; collecting candidates while
+// the row is read, against a bound formed on the way, 282 us; as it is 188 us,
+// 164 of them without alternatives.)
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -31,9 +40,9 @@
 
 namespace gs {
 
-constexpr int kLossThreads = 512;
-constexpr int kLossWarps = kLossThreads / 32;
 constexpr int kLossCluster = 8;  // most CTAs of a row
+constexpr int kCandidates = 256; // alternatives' candidates kept for sorting
+constexpr int kLossVecs = 4;     // 16-byte vectors of a thread's block
 
 // Beyond this |lse| its rounding to fp32 (2^-24 |lse|, the relative error it
 // brings to every p) is no longer small beside the rest, and the gradient
@@ -70,14 +79,17 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // ---- running softmax statistics -------------------------------------------
-// m: the maximum (NaN left out); s: sum 2^d, t: sum 2^d d with
-// d = (x - m) log2 e.  A NaN or +Inf logit makes s NaN.
+// s: sum 2^d, t: sum 2^d d with d = (x - m) log2 e, m a logit near the maximum
+// of what was taken: it follows the maximum once that is more than kLag above
+// it (a thread's maximum grows slowly, and in a warp some thread's does at
+// almost every step; 2^d stays below 2^6).  A NaN or +Inf logit makes s NaN.
 struct Stats {
   float m, s, t;
 };
+constexpr float kLag = 4.0f;
 
-// Brings (s, t) from maximum m to the larger M.  m = -Inf (nothing yet, s = 0)
-// must not turn into 0 * Inf: the shift is kept finite.
+// Brings (s, t) from reference m to the larger M.  m = -Inf (nothing yet,
+// s = 0) must not turn into 0 * Inf: the shift is kept finite.
 __device__ __forceinline__ void rescale(float m, float M, float& s, float& t) {
   const float D = fmaxf((m - M) * kLog2e, -1e30f);
   const float f = ex2(D);
@@ -93,39 +105,18 @@ __device__ __forceinline__ Stats join(Stats a, Stats b) {
   return Stats{M, a.s + b.s, a.t + b.t};
 }
 
-// N logits at once (N even).  With ENT, d is kept above -1024, where 2^d is 0
-// all the same, so that a masked logit adds 0 and not 0 * Inf to t.
-template <bool ENT, int N>
-__device__ __forceinline__ void take(Stats& a, const float* x) {
-  float lm = x[0];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const float* x) {
+  float m = x[0];
+  if constexpr (N % 2 == 0) m = fmaxf(m, x[1]);
 #pragma unroll
-  for (int i = 1; i < N; ++i) lm = fmaxf(lm, x[i]);
-  if (lm > a.m) {
-    rescale(a.m, lm, a.s, a.t);
-    a.m = lm;
-  }
-  const float mm = a.m == -CUDART_INF_F ? 0.0f : a.m;
-  const uint64_t nm = pk_f32x2(-mm, -mm), l2e = pk_f32x2(kLog2e, kLog2e);
-  uint64_t s2 = pk_f32x2(a.s, 0.0f), t2 = pk_f32x2(a.t, 0.0f);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    float d0, d1;
-    upk_f32x2(mul_f32x2(add_f32x2(pk_f32x2(x[i], x[i + 1]), nm), l2e), d0, d1);
-    if constexpr (ENT) {
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(d0) : "f"(-1024.0f));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(d1) : "f"(-1024.0f));
-    }
-    const uint64_t e = pk_f32x2(ex2(d0), ex2(d1));
-    s2 = add_f32x2(s2, e);
-    if constexpr (ENT) t2 = fma_f32x2(e, pk_f32x2(d0, d1), t2);
-  }
-  float lo, hi;
-  upk_f32x2(s2, lo, hi);
-  a.s = lo + hi;
-  if constexpr (ENT) {
-    upk_f32x2(t2, lo, hi);
-    a.t = lo + hi;
-  }
+  for (int i = N % 2 ? 1 : 2; i < N; i += 2) m = max3(m, x[i], x[i + 1]);
+  return m;
 }
 
 // 16 bytes of logits as fp32.
@@ -149,19 +140,48 @@ __device__ __forceinline__ void unpack16(const uint4& v, float* x) {
   }
 }
 
+
+// N logits with maximum lm (N even).  d is kept above -1024, where 2^d is 0
+// all the same, so that a masked logit adds 0 and not 0 * Inf to t.
+template <int N>
+__device__ __forceinline__ void take(Stats& a, const float* x, float lm) {
+  if (lm > a.m + kLag) {
+    rescale(a.m, lm, a.s, a.t);
+    a.m = lm;
+  }
+  const float mm = a.m == -CUDART_INF_F ? 0.0f : a.m;
+  const uint64_t nm = pk_f32x2(-mm, -mm), l2e = pk_f32x2(kLog2e, kLog2e);
+  uint64_t s2 = pk_f32x2(a.s, 0.0f), t2 = pk_f32x2(a.t, 0.0f);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float d0, d1;
+    upk_f32x2(mul_f32x2(add_f32x2(pk_f32x2(x[i], x[i + 1]), nm), l2e), d0, d1);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d0) : "f"(-1024.0f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(d1) : "f"(-1024.0f));
+    const uint64_t e = pk_f32x2(ex2(d0), ex2(d1));
+    s2 = add_f32x2(s2, e);
+    t2 = fma_f32x2(e, pk_f32x2(d0, d1), t2);
+  }
+  float lo, hi;
+  upk_f32x2(s2, lo, hi);
+  a.s = lo + hi;
+  upk_f32x2(t2, lo, hi);
+  a.t = lo + hi;
+}
+
 // A run of a row: `head` elements up to the first 16-byte boundary, nv
 // 16-byte vectors, then `tail` elements (head, tail < kVec).
 template <int DT>
 struct Run {
   const char* p;  // first element
   int head, tail;
-  int64_t nv;
+  int nv;
   static constexpr int kSize = sizeof(typename Elem<DT>::type);
   __device__ __forceinline__ Run(const void* base, int64_t n) : p(static_cast<const char*>(base)) {
     const int64_t h = (int64_t)((16u - ((uint32_t)(uintptr_t)p & 15u)) & 15u) / kSize;
     head = (int)(h < n ? h : n);
-    nv = (n - head) / kVec<DT>;
-    tail = (int)(n - head - nv * kVec<DT>);
+    nv = (int)((n - head) / kVec<DT>);
+    tail = (int)(n - head - (int64_t)nv * kVec<DT>);
   }
   __device__ __forceinline__ const uint4* vec() const {
     return reinterpret_cast<const uint4*>(p + head * kSize);
@@ -170,7 +190,7 @@ struct Run {
   // tails), or -1.
   __device__ __forceinline__ int64_t odd(int i) const {
     if (i < head) return i;
-    return i < head + tail ? nv * kVec<DT> + i : -1;
+    return i < head + tail ? (int64_t)nv * kVec<DT> + i : -1;
   }
 };
 
@@ -203,22 +223,6 @@ __device__ __forceinline__ T merge_desc(T a, T b, int lane) {
   }
   return v;
 }
-// Merges the warps' lists; warp 0 returns the result.  `buf` holds
-// kLossWarps * 32 values that no thread still reads.
-template <typename T>
-__device__ __forceinline__ T merge_warps(T v, T* buf, int warp, int lane) {
-  buf[warp * 32 + lane] = v;
-#pragma unroll
-  for (int n = kLossWarps / 2; n > 0; n >>= 1) {
-    __syncthreads();
-    if (warp < n) {
-      v = merge_desc(v, buf[(warp + n) * 32 + lane], lane);
-      buf[warp * 32 + lane] = v;
-    }
-  }
-  return v;
-}
-
 // A warp's k best pairs so far; a pair below `bound` is none of the row's k
 // best.
 struct Best {
@@ -287,19 +291,207 @@ __device__ __forceinline__ unsigned long long remote_u64(const void* p, uint32_t
   return v;
 }
 
-template <int DT, bool ENT, bool TOP>
-__global__ void __launch_bounds__(kLossThreads, 2)
-    token_logprob_kernel(const LogprobArgs a) {
-  __shared__ Stats part_stats[kLossWarps];
+// The k-th largest of 32 of the CTA's keys, each warp's largest ones: a lower
+// bound of the CTA's k-th largest.  `buf` holds 32 values that no thread still
+// reads; every thread returns the same.
+template <int NT, typename T>
+__device__ __forceinline__ T bound_of(T key, int k, T* buf, int warp, int lane) {
+  constexpr int kWarps = NT / 32, kEach = 32 / kWarps;
+  T v = key;
+  if constexpr (sizeof(T) == 4 && kEach <= 4) {  // a few rounds beat a sort
+    T mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const T top = __reduce_max_sync(0xFFFFFFFFu, v);
+      if (lane == i) mine = top;
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, v == top)) - 1) v = 0;
+    }
+    v = mine;
+  } else {
+    v = sort_desc(v, lane);
+  }
+  if constexpr (kWarps > 1) {
+    if (lane < kEach) buf[warp * kEach + lane] = v;
+    __syncthreads();
+    v = sort_desc(buf[lane], lane);
+  }
+  return __shfl_sync(0xFFFFFFFFu, v, k - 1);
+}
+
+// Where a thread's maximum lies: its value, the block in which it first
+// occurred, and the maximum of the other blocks.
+struct Peak {
+  float m, other;
+  int64_t block;
+  // True when the block's maximum lm is the largest so far (or the first).
+  __device__ __forceinline__ bool see(float lm, int64_t blk) {
+    if (lm > m || blk == 0) {
+      other = m;
+      m = lm;
+      block = blk;
+      return true;
+    }
+    other = fmaxf(other, lm);
+    return false;
+  }
+};
+
+// The candidates for the alternatives.
+struct Candidates {
+  unsigned long long* pair;
+  int* n;
+  // Those of a vector's elements (column i0 and on) whose pair reaches `bound`;
+  // low: the logit of the bound's key (an element below it does not reach it;
+  // NaN is not below).
+  template <int DT>
+  __device__ __forceinline__ void offer(const uint4& w, uint32_t i0, unsigned long long bound,
+                                        float low) const {
+    float x[kVec<DT>];
+    unpack16<DT>(w, x);
+#pragma unroll
+    for (int j = 0; j < kVec<DT>; ++j)
+      if (!(x[j] < low)) offer1(order_pair(x[j], i0 + j), bound);
+  }
+  __device__ __forceinline__ void offer1(unsigned long long q, unsigned long long bound) const {
+    if (q < bound) return;
+    const int at = atomicAdd(n, 1);
+    if (at < kCandidates) pair[at] = q;
+  }
+};
+
+// A vector whose logits are all -Inf.
+template <int DT>
+__device__ __forceinline__ uint4 masked16() {
+  const uint32_t w = DT == GS_F32 ? 0xFF800000u : DT == GS_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+  return make_uint4(w, w, w, w);
+}
+
+// The CTA's top_k pairs in order in warp 0 (other warps' result is unused).
+// `nan`: this thread read a NaN or +Inf; kept: the threads' peak blocks.
+template <int DT, int NT>
+__device__ __forceinline__ unsigned long long alternatives(const Run<DT>& run, const char* row,
+                                                           int64_t c0, const Peak& peak, bool nan,
+                                                           int top_k, const uint4* kept,
+                                                           unsigned long long* cand,
+                                                           int* n_cand) {
+  constexpr int N = kVec<DT>, kWarps = NT / 32, U = kLossVecs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint4* p = run.vec();
+  const uint32_t first_col = (uint32_t)(c0 + run.head);
+  const int64_t odd = run.odd(tid);
+  uint32_t key = tid < run.nv || odd >= 0 ? order_key(peak.m) : 0;
+  uint32_t other = order_key(peak.other);
+  if (nan) {  // the keys from the elements: NaN is above all others
+    for (int64_t i = tid; i < run.nv; i += NT) {
+      float x[N];
+      unpack16<DT>(ld_stream(p + i), x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) key = max(key, order_key(x[j]));
+    }
+    if (odd >= 0) key = max(key, order_key(load1<DT>(row, odd)));
+    other = key;  // look at every block
+  }
+  if (tid == 0) *n_cand = 0;
+  unsigned long long bound =
+      (unsigned long long)bound_of<NT>(key, top_k, reinterpret_cast<uint32_t*>(cand), warp, lane)
+      << 32;
+  bool mine = key != 0 && key >= (uint32_t)(bound >> 32);
+  // (the barrier also ends the reads of `cand`)
+  if (__syncthreads_count(mine) > 4 * top_k + 32) {
+    // Many equal maxima (a masked part, a row of few values): order them by
+    // where each first occurs, which leaves about k threads.
+    unsigned long long first = 0;
+    if (mine) {
+      for (int64_t i = tid + (nan ? 0 : peak.block * U * NT); i < run.nv && first == 0; i += NT) {
+        float x[N];
+        unpack16<DT>(ld_stream(p + i), x);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (first == 0 && order_key(x[j]) == key)
+            first = order_pair(x[j], first_col + (uint32_t)(i * N + j));
+      }
+      if (odd >= 0) {
+        const unsigned long long q = order_pair(load1<DT>(row, odd), (uint32_t)(c0 + odd));
+        if (q > first) first = q;
+      }
+    }
+    bound = bound_of<NT>(first, top_k, cand, warp, lane);
+    mine = first != 0 && first >= bound;
+    __syncthreads();
+  }
+  const Candidates list{cand, n_cand};
+  const bool all = mine && other >= (uint32_t)(bound >> 32);
+  const float low = key_value((uint32_t)(bound >> 32));
+  if (mine && !all) {  // the block of the maximum
+    const int64_t v = tid + peak.block * U * NT;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v + u * NT < run.nv)
+        list.offer<DT>(kept[u * NT + tid], first_col + (uint32_t)((v + u * NT) * N), bound, low);
+  }
+  // all blocks of a thread, by its whole warp
+  const unsigned whole = __ballot_sync(0xFFFFFFFFu, all);
+  for (unsigned m = whole; m; m &= m - 1) {
+    const int o = warp * 32 + __ffs(m) - 1;
+    for (int64_t i0 = o + (int64_t)lane * NT; i0 < run.nv; i0 += (int64_t)64 * NT) {
+      const int64_t i1 = i0 + (int64_t)32 * NT;
+      const uint4 w0 = ld_stream(p + i0);
+      const uint4 w1 = i1 < run.nv ? ld_stream(p + i1) : w0;
+      list.offer<DT>(w0, first_col + (uint32_t)(i0 * N), bound, low);
+      if (i1 < run.nv) list.offer<DT>(w1, first_col + (uint32_t)(i1 * N), bound, low);
+    }
+  }
+  if (mine && odd >= 0) list.offer1(order_pair(load1<DT>(row, odd), (uint32_t)(c0 + odd)), bound);
+  const unsigned chosen = __ballot_sync(0xFFFFFFFFu, mine);
+  __syncthreads();
+  const int n = *n_cand;
+  unsigned long long best = 0;
+  if (n <= kCandidates) {
+    if (warp == 0) {
+      best = sort_desc(lane < n ? cand[lane] : 0ull, lane);
+      for (int i = 32; i < n; i += 32)
+        best = merge_desc(best, sort_desc(i + lane < n ? cand[i + lane] : 0ull, lane), lane);
+    }
+    return best;
+  }
+  // A thread held many of the largest: insert them one by one instead.
+  __syncthreads();
+  Best b{0, bound, top_k};
+  for (unsigned m = chosen; m; m &= m - 1) {
+    const int o = warp * 32 + __ffs(m) - 1;
+    for (int64_t i0 = o; i0 < run.nv; i0 += (int64_t)32 * NT) {
+      const int64_t i = i0 + (int64_t)lane * NT;
+      const bool have = i < run.nv;
+      float x[N];
+      unpack16<DT>(have ? ld_stream(p + i) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        b.offer(order_pair(x[j], first_col + (uint32_t)(i * N + j)), have, lane);
+    }
+    const int64_t i = run.odd(o);
+    if (i >= 0) b.offer(order_pair(load1<DT>(row, i), (uint32_t)(c0 + i)), lane == 0, lane);
+  }
+  static_assert(kWarps * 32 <= kCandidates, "the warps' lists must fit");
+  cand[warp * 32 + lane] = b.v;
+  __syncthreads();
+  best = b.v;
+  if (warp == 0)
+    for (int i = 1; i < kWarps; ++i) best = merge_desc(best, cand[i * 32 + lane], lane);
+  return best;
+}
+
+template <int DT, int NT, int CTAS, bool TOP>
+__global__ void __launch_bounds__(NT, CTAS) token_logprob_kernel(const LogprobArgs a) {
+  constexpr int kWarps = NT / 32;
+  __shared__ Stats part_stats[kWarps];
   __shared__ float row_stats[3];
-  __shared__ unsigned long long lists[TOP ? kLossWarps * 32 : 1];
+  __shared__ uint4 kept[TOP ? kLossVecs * NT : 1];
+  __shared__ unsigned long long cand[TOP ? kCandidates : 1];
   __shared__ unsigned long long row_list[TOP ? 32 : 1];
-  __shared__ int chosen[TOP ? kLossThreads : 1];
-  __shared__ int n_chosen;
-  __shared__ unsigned long long tau;
+  __shared__ int n_cand;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t parts = cluster_size(), rank = cluster_rank();
-  constexpr int N = kVec<DT>, U = 4;
+  constexpr int N = kVec<DT>, U = kLossVecs;
 
   for (int64_t r = blockIdx.x / parts; r < a.R; r += gridDim.x / parts) {
     const int64_t c0 = a.part * rank < a.V ? a.part * rank : a.V;
@@ -308,110 +500,63 @@ __global__ void __launch_bounds__(kLossThreads, 2)
                       (r * a.ld + c0) * (int64_t)sizeof(typename Elem<DT>::type);
     const Run<DT> run(row, n);
     Stats st{-CUDART_INF_F, 0.0f, 0.0f};
+    Peak peak{-CUDART_INF_F, -CUDART_INF_F, 0};
     const uint4* p = run.vec();
-    int64_t v = tid;
-    for (; v + (U - 1) * kLossThreads < run.nv; v += U * kLossThreads) {
+    for (int blk = 0; blk * (U * NT) < run.nv; ++blk) {
+      const int v = blk * (U * NT) + tid;
       uint4 w[U];
+      if ((blk + 1) * (U * NT) <= run.nv) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = ld_stream(p + v + u * kLossThreads);
-      float x[U * N];
+        for (int u = 0; u < U; ++u) w[u] = ld_stream(p + v + u * NT);
+      } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) unpack16<DT>(w[u], x + u * N);
-      take<ENT, U * N>(st, x);
-    }
-    for (; v < run.nv; v += kLossThreads) {
-      float x[N];
-      unpack16<DT>(ld_stream(p + v), x);
-      take<ENT, N>(st, x);
+        for (int u = 0; u < U; ++u)
+          w[u] = v + u * NT < run.nv ? ld_stream(p + v + u * NT) : masked16<DT>();
+      }
+      float bm = -CUDART_INF_F;
+#pragma unroll
+      for (int h = 0; h < U; h += 2) {
+        float x[2 * N];
+        unpack16<DT>(w[h], x);
+        unpack16<DT>(w[h + 1], x + N);
+        const float lm = max_of<2 * N>(x);
+        take<2 * N>(st, x, lm);
+        if (TOP) bm = fmaxf(bm, lm);
+      }
+      if (TOP && peak.see(bm, blk)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) kept[u * NT + tid] = w[u];
+      }
     }
     const int64_t odd = run.odd(tid);
     if (odd >= 0) {
       const float x[2] = {load1<DT>(row, odd), -CUDART_INF_F};
-      take<ENT, 2>(st, x);
+      take<2>(st, x, max_of<2>(x));
+      // (a maximum here has no block: every block is looked at if it is chosen)
+      if (TOP && x[0] > peak.m) peak.other = peak.m = x[0];
     }
 
-    unsigned long long best = 0;
-    if constexpr (TOP) {
-      // the threads' maxima, and the k-th largest of them
-      uint32_t key = 0;
-      if (st.s != st.s) {  // a NaN or +Inf was read: its key from the elements
-        for (int64_t i = tid; i < run.nv; i += kLossThreads) {
-          float x[N];
-          unpack16<DT>(ld_stream(p + i), x);
-#pragma unroll
-          for (int j = 0; j < N; ++j) key = max(key, order_key(x[j]));
-        }
-        if (odd >= 0) key = max(key, order_key(load1<DT>(row, odd)));
-      } else if (tid < run.nv || odd >= 0) {
-        key = order_key(st.m);
-      }
-      if (tid == 0) n_chosen = 0;
-      uint32_t* keys = reinterpret_cast<uint32_t*>(lists);
-      const uint32_t top = merge_warps<uint32_t>(sort_desc(key, lane), keys, warp, lane);
-      if (warp == 0 && lane == a.top_k - 1) tau = (unsigned long long)top << 32;
-      __syncthreads();
-      unsigned long long bound = tau;
-      if (key != 0 && key >= (uint32_t)(bound >> 32)) chosen[atomicAdd(&n_chosen, 1)] = tid;
-      __syncthreads();
-      if (n_chosen > 2 * a.top_k + kLossWarps) {
-        // Many equal maxima (a masked part, a row of few values): order them
-        // by where each first occurs, which leaves k threads.
-        unsigned long long first = 0;
-        if (key != 0 && key >= (uint32_t)(bound >> 32)) {
-          for (int64_t i = tid; i < run.nv && first == 0; i += kLossThreads) {
-            float x[N];
-            unpack16<DT>(ld_stream(p + i), x);
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-              if (first == 0 && order_key(x[j]) == key)
-                first = order_pair(x[j], (uint32_t)(c0 + run.head + i * N + j));
-          }
-          if (odd >= 0) {
-            const unsigned long long q = order_pair(load1<DT>(row, odd), (uint32_t)(c0 + odd));
-            if (q > first) first = q;
-          }
-        }
-        const unsigned long long best_first =
-            merge_warps<unsigned long long>(sort_desc(first, lane), lists, warp, lane);
-        if (warp == 0 && lane == a.top_k - 1) tau = best_first;
-        if (tid == 0) n_chosen = 0;
-        __syncthreads();
-        bound = tau;
-        if (first != 0 && first >= bound) chosen[atomicAdd(&n_chosen, 1)] = tid;
-        __syncthreads();
-      }
-      Best b{0, bound, a.top_k};
-      for (int g = warp; g < n_chosen; g += kLossWarps) {
-        const int o = chosen[g];
-        for (int64_t i0 = o; i0 < run.nv; i0 += (int64_t)32 * kLossThreads) {
-          const int64_t i = i0 + (int64_t)lane * kLossThreads;
-          const bool have = i < run.nv;
-          float x[N];
-          unpack16<DT>(have ? ld_stream(p + i) : make_uint4(0, 0, 0, 0), x);
-#pragma unroll
-          for (int j = 0; j < N; ++j)
-            b.offer(order_pair(x[j], (uint32_t)(c0 + run.head + i * N + j)), have, lane);
-        }
-        const int64_t i = run.odd(o);
-        if (i >= 0) b.offer(order_pair(load1<DT>(row, i), (uint32_t)(c0 + i)), lane == 0, lane);
-      }
-      best = merge_warps<unsigned long long>(b.v, lists, warp, lane);
-    }
-
+    const bool nan = st.s != st.s;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
       st = join(st, Stats{__shfl_xor_sync(0xFFFFFFFFu, st.m, o),
                           __shfl_xor_sync(0xFFFFFFFFu, st.s, o),
                           __shfl_xor_sync(0xFFFFFFFFu, st.t, o)});
-    if (lane == 0) part_stats[warp] = st;
-    __syncthreads();
-    if (warp == 0) {
-      st = lane < kLossWarps ? part_stats[lane] : Stats{-CUDART_INF_F, 0.0f, 0.0f};
+    unsigned long long best = 0;
+    if constexpr (TOP)
+      best = alternatives<DT, NT>(run, row, c0, peak, nan, a.top_k, kept, cand, &n_cand);
+
+    if constexpr (kWarps > 1) {
+      if (lane == 0) part_stats[warp] = st;
+      __syncthreads();
+      if (warp == 0) {
+        st = lane < kWarps ? part_stats[lane] : Stats{-CUDART_INF_F, 0.0f, 0.0f};
 #pragma unroll
-      for (int o = kLossWarps / 2; o > 0; o >>= 1)
-        st = join(st, Stats{__shfl_xor_sync(0xFFFFFFFFu, st.m, o),
-                            __shfl_xor_sync(0xFFFFFFFFu, st.s, o),
-                            __shfl_xor_sync(0xFFFFFFFFu, st.t, o)});
+        for (int o = kWarps / 2; o > 0; o >>= 1)
+          st = join(st, Stats{__shfl_xor_sync(0xFFFFFFFFu, st.m, o),
+                              __shfl_xor_sync(0xFFFFFFFFu, st.s, o),
+                              __shfl_xor_sync(0xFFFFFFFFu, st.t, o)});
+      }
     }
     if (parts > 1) {  // the row's other parts, through their shared memory
       if (warp == 0) {
@@ -432,16 +577,18 @@ __global__ void __launch_bounds__(kLossThreads, 2)
       cluster_barrier();
     }
     if (rank == 0 && warp == 0) {
-      const float m = __shfl_sync(0xFFFFFFFFu, st.m, 0), s = __shfl_sync(0xFFFFFFFFu, st.s, 0);
+      st.m = __shfl_sync(0xFFFFFFFFu, st.m, 0);
+      st.s = __shfl_sync(0xFFFFFFFFu, st.s, 0);
+      const float m = st.m, s = st.s;
       const bool bad = s != s, none = !bad && m == -CUDART_INF_F;
-      const float ls = logf(s);
+      const float ls = logf(s);  // log sum e^(x - m)
       // log probability of a logit
       const auto lp = [&](float x) {
         return bad ? CUDART_NAN_F : none ? -CUDART_INF_F : (x - m) - ls;
       };
       if (lane == 0) {
         if (a.lse) a.lse[r] = bad ? CUDART_NAN_F : none ? m : m + ls;
-        if (ENT) a.entropy[r] = bad ? CUDART_NAN_F : none ? 0.0f : ls - kLn2 * (st.t / s);
+        if (a.entropy) a.entropy[r] = bad ? CUDART_NAN_F : none ? 0.0f : ls - kLn2 * (st.t / s);
         if (a.logprob) {
           const int64_t at = a.targets[r];
           a.logprob[r] = at >= a.V ? CUDART_NAN_F
@@ -464,9 +611,10 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
                                  const int64_t* targets, float* logprob, float* lse,
                                  float* entropy, int top_k, int32_t* top_ids, float* top_logprob,
                                  cudaStream_t stream) {
-  // CTAs of a row: as few as fill the device several times over, none with
-  // less than 4096 columns
-  const int64_t want = (int64_t)sm_count() * 8;
+  // CTAs of a row: as few as fill the device once (five CTAs per SM), none
+  // with less than 4096 columns.  512 rows of 128256 bf16 with 8 alternatives
+  // take 43 us so, 51 us with the device filled twice over.
+  const int64_t want = (int64_t)sm_count() * 5;
   int parts = 1;
   while (parts < kLossCluster && R * parts < want && V / (2 * parts) >= 4096) parts *= 2;
   const int64_t part = ((V + parts - 1) / parts + 7) / 8 * 8;
@@ -475,7 +623,6 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
   const int64_t most = (int64_t)1 << 27;  // clusters of a grid; more rows go round
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((R < most ? R : most) * parts));
-  cfg.blockDim = dim3(kLossThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -483,15 +630,21 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-#define GS_F(DT)                                                                               \
-  (entropy ? (top_k ? cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, true, true>, a)        \
-                    : cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, true, false>, a))      \
-           : (top_k ? cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, false, true>, a)       \
-                    : cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, false, false>, a)))
-  if (dtype == GS_F32) return GS_F(GS_F32);
-  if (dtype == GS_F16) return GS_F(GS_F16);
-  return GS_F(GS_BF16);
+  // Threads of a CTA: short rows leave most of a wide CTA's time to its
+  // joins (16000 rows of 8000 bf16, lse alone: 76 us with 64 threads, 101 with
+  // 256); long ones want few joins (4096 x 128256 with 8 alternatives: 188 us
+  // with 256, 250 with 128).
+#define GS_N(DT, NT, CTAS)                                                     \
+  (cfg.blockDim = dim3(NT),                                                    \
+   top_k ? cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, NT, CTAS, true>, a) \
+         : cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, NT, CTAS, false>, a))
+#define GS_F(DT)                                                               \
+  return part > 12288 ? GS_N(DT, 256, 5) : part > 1536 ? GS_N(DT, 64, 16) : GS_N(DT, 32, 32)
+  if (dtype == GS_F32) GS_F(GS_F32);
+  if (dtype == GS_F16) GS_F(GS_F16);
+  GS_F(GS_BF16);
 #undef GS_F
+#undef GS_N
 }
 
 // ---- backward --------------------------------------------------------------
