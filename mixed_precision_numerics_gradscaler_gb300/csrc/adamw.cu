@@ -28,13 +28,6 @@ namespace gs {
 
 constexpr int kAdamThreads = 256;
 
-// Maximum that keeps a NaN.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // The smallest magnitude a block's scale is formed from: 448 / a stays
 // finite.
 constexpr float kMomentFloor = 1e-30f;
@@ -49,24 +42,21 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// |t| rounded up or down to a multiple of E4M3's step at |t|, up with
-// probability equal to the fraction (r16: 16 random bits): the bits are
+// The E4M3 code (without sign) of t >= 0 rounded up or down, up with
+// probability equal to the fraction of the way (r16: 16 random bits): they are
 // added below the three kept significand bits and the rest cut off.  Below
 // 2^-6 E4M3's step stays 2^-9; adding 2^-6 moves the value into the binade
-// with that step.
-__device__ __forceinline__ float round_e4m3_random(float t, uint32_t r16) {
-  const float a = fabsf(t);
-  const bool low = a < 0.015625f;
-  const uint32_t b = __float_as_uint(low ? a + 0.015625f : a) + (r16 << 4);
-  const float c = __uint_as_float(b & 0xFFF00000u);
-  return copysignf(fminf(low ? c - 0.015625f : c, 448.0f), t);
+// with that step.  Codes count steps, so they are the fp32 word's upper twelve
+// bits less the exponents' difference; 126 is 448.
+__device__ __forceinline__ uint32_t round_e4m3_random(float t, uint32_t r16) {
+  const bool low = t < 0.015625f;
+  const uint32_t b = __float_as_uint(low ? t + 0.015625f : t) + (r16 << 4);
+  const int c = (int)(b >> 20) - (low ? 968 : 960);
+  return (uint32_t)(c < 126 ? c : 126);
 }
 
 __device__ __forceinline__ float decode_e4m3(uint8_t q) {
   return lo_f16(cvt_fp8x2_f16x2<GS_E4M3>(q));
-}
-__device__ __forceinline__ uint8_t encode_e4m3(float f) {
-  return (uint8_t)cvt_f32x2_fp8x2<GS_E4M3>(0.0f, f);
 }
 
 struct AdamWStep {
@@ -117,6 +107,55 @@ __device__ __forceinline__ void count_step(const AdamWArgs& a) {
   }
 }
 
+// N gradients (N a multiple of 4), 16 bytes at a time or 8.
+template <int GT, int N>
+__device__ __forceinline__ void load_grads(const void* g, int64_t i, float* f) {
+  if constexpr (GT == GS_F32) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const uint4 w = ld_stream(reinterpret_cast<const uint4*>(static_cast<const float*>(g) + i + j));
+      f[j] = __uint_as_float(w.x);
+      f[j + 1] = __uint_as_float(w.y);
+      f[j + 2] = __uint_as_float(w.z);
+      f[j + 3] = __uint_as_float(w.w);
+    }
+  } else {
+    using Tag = std::conditional_t<GT == GS_BF16, BF16Tag, F16Tag>;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      uint2 w;
+      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(w.x), "=r"(w.y)
+                   : "l"(static_cast<const uint16_t*>(g) + i + j));
+      f[j] = lo16<Tag>(w.x);
+      f[j + 1] = hi16<Tag>(w.x);
+      f[j + 2] = lo16<Tag>(w.y);
+      f[j + 3] = hi16<Tag>(w.y);
+    }
+  }
+}
+// State arrays are read and written in place: not through the read-only path.
+__device__ __forceinline__ V8 ld_state8(const float* p) {
+  V8 a;
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.w[0]), "=r"(a.w[1]), "=r"(a.w[2]), "=r"(a.w[3]), "=r"(a.w[4]),
+                 "=r"(a.w[5]), "=r"(a.w[6]), "=r"(a.w[7])
+               : "l"(p));
+  return a;
+}
+__device__ __forceinline__ float4 ld_state4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ bool aligned_to(const void* p, uint32_t n) {
+  return ((uint32_t)(uintptr_t)p & (n - 1)) == 0;
+}
+
+// fp32 moments: 4 x 4 bytes read, 3 x 4 and the copy's 2 written per
+// parameter; 32-byte accesses where the chunk's arrays allow them.
 template <int GT>
 __global__ void __launch_bounds__(kAdamThreads)
     adamw_f32_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
@@ -127,7 +166,32 @@ __global__ void __launch_bounds__(kAdamThreads)
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
     float* m = static_cast<float*>(ch.m);
     float* v = static_cast<float*>(ch.v);
-    for (int64_t i = threadIdx.x; i < ch.n; i += kAdamThreads) {
+    const bool vec = aligned_to(ch.w, 32) && aligned_to(m, 32) && aligned_to(v, 32) &&
+                     aligned_to(ch.g, 16) && aligned_to(ch.w_bf16, 16);
+    const int n8 = vec ? (int)(ch.n >> 3) : 0;
+    for (int i = threadIdx.x; i < n8; i += kAdamThreads) {
+      V8 w8 = ld_state8(ch.w + 8 * i), m8 = ld_state8(m + 8 * i), v8 = ld_state8(v + 8 * i);
+      float g[8];
+      load_grads<GT, 8>(ch.g, 8 * i, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const Adam1 o = adam1(a, s, keep, __uint_as_float(w8.w[j]), g[j], __uint_as_float(m8.w[j]),
+                              __uint_as_float(v8.w[j]));
+        w8.w[j] = __float_as_uint(o.w);
+        m8.w[j] = __float_as_uint(o.m);
+        v8.w[j] = __float_as_uint(o.v);
+      }
+      st_stream8(ch.w + 8 * i, w8);
+      st_stream8(m + 8 * i, m8);
+      st_stream8(v + 8 * i, v8);
+      if (ch.w_bf16) {
+        const float* f = reinterpret_cast<const float*>(w8.w);
+        st_stream(reinterpret_cast<uint4*>(ch.w_bf16 + 8 * i),
+                  make_uint4(cvt_f32x2_bf16x2(f[1], f[0]), cvt_f32x2_bf16x2(f[3], f[2]),
+                             cvt_f32x2_bf16x2(f[5], f[4]), cvt_f32x2_bf16x2(f[7], f[6])));
+      }
+    }
+    for (int64_t i = n8 * 8 + threadIdx.x; i < ch.n; i += kAdamThreads) {
       const Adam1 o = adam1(a, s, keep, ch.w[i], load1<GT>(ch.g, i), m[i], v[i]);
       m[i] = o.m;
       v[i] = o.v;
@@ -138,57 +202,151 @@ __global__ void __launch_bounds__(kAdamThreads)
   count_step(a);
 }
 
+// 8-bit moments.  One warp per block of 128: the new moments stay in
+// registers until the block's two maxima are known (as integer maxima of the
+// magnitudes' bits: a NaN is above everything and makes the scale NaN).
+struct BlockScales {
+  float m, r, im, ir;  // scale and 448 / maximum of both moments
+};
+__device__ __forceinline__ BlockScales block_scales(uint32_t am, uint32_t ar) {
+  am = __reduce_max_sync(0xFFFFFFFFu, am);
+  ar = __reduce_max_sync(0xFFFFFFFFu, ar);
+  const uint32_t floor_bits = __float_as_uint(kMomentFloor);
+  const float fm = __uint_as_float(am > floor_bits ? am : floor_bits);
+  const float fr = __uint_as_float(ar > floor_bits ? ar : floor_bits);
+  BlockScales b;
+  b.m = __fdiv_rn(fm, 448.0f);
+  b.r = __fdiv_rn(fr, 448.0f);
+  b.im = __fdiv_rn(448.0f, fm);
+  b.ir = __fdiv_rn(448.0f, fr);
+  return b;
+}
+// Codes of one element's moments: m's in the low byte, the root's in the next.
+__device__ __forceinline__ uint32_t encode_moments(float m, float r, const BlockScales& b,
+                                                   uint32_t h) {
+  const float tm = __fmul_rn(m, b.im);
+  const uint32_t qm = round_e4m3_random(fabsf(tm), h & 0xFFFFu) |
+                      ((__float_as_uint(tm) >> 24) & 0x80u);
+  uint32_t qr = round_e4m3_random(__fmul_rn(r, b.ir), h >> 16);
+  if (qr == 0 && r > 0.0f) qr = 1;
+  return qm | (qr << 8);
+}
+
+constexpr int kAdamBlocks = 2;  // blocks of 128 that a warp has in flight
+
 template <int GT>
 __global__ void __launch_bounds__(kAdamThreads)
     adamw_e4m3_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
   if (*a.found_inf) return;
   const AdamWStep s = step_of(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kWarps = kAdamThreads / 32, U = kAdamBlocks;
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     const AChunk ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
     uint8_t* mq = static_cast<uint8_t*>(ch.m);
     uint8_t* vq = static_cast<uint8_t*>(ch.v);
-    // one warp per block of 128, four elements per lane
-    for (int64_t b = warp; b * kMomentBlock < ch.n; b += kAdamThreads / 32) {
+    const bool vec = aligned_to(ch.w, 16) && aligned_to(ch.g, 16) && aligned_to(mq, 4) &&
+                     aligned_to(vq, 4) && aligned_to(ch.w_bf16, 8);
+    const int whole = vec ? (int)(ch.n / kMomentBlock) : 0;  // blocks of the vector path
+    for (int b0 = warp * U; b0 < whole; b0 += kWarps * U) {
+      float w[U][4], g[U][4], m[U][4], r[U][4];
+      uint32_t q[U][2];
+      float sc[U][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b0 + u >= whole) continue;
+        const int i = (b0 + u) * kMomentBlock + lane * 4;
+        const float4 f = ld_state4(ch.w + i);
+        w[u][0] = f.x;
+        w[u][1] = f.y;
+        w[u][2] = f.z;
+        w[u][3] = f.w;
+        load_grads<GT, 4>(ch.g, i, g[u]);
+        q[u][0] = *reinterpret_cast<const uint32_t*>(mq + i);
+        q[u][1] = *reinterpret_cast<const uint32_t*>(vq + i);
+        sc[u][0] = ch.m_scale[b0 + u];
+        sc[u][1] = ch.v_scale[b0 + u];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (b0 + u >= whole) continue;
+        const int i = (b0 + u) * kMomentBlock + lane * 4;
+        uint32_t am = 0, ar = 0;
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          const uint32_t hm = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][0] >> (8 * j)));
+          const uint32_t hv = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][1] >> (8 * j)));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float rv = __fmul_rn(k ? hi_f16(hv) : lo_f16(hv), sc[u][1]);
+            const Adam1 o = adam1(a, s, keep, w[u][j + k], g[u][j + k],
+                                  __fmul_rn(k ? hi_f16(hm) : lo_f16(hm), sc[u][0]),
+                                  __fmul_rn(rv, rv));
+            w[u][j + k] = o.w;
+            m[u][j + k] = o.m;
+            r[u][j + k] = o.r;
+            am = max(am, __float_as_uint(o.m) & 0x7FFFFFFFu);
+            ar = max(ar, __float_as_uint(o.r) & 0x7FFFFFFFu);
+          }
+        }
+        *reinterpret_cast<float4*>(ch.w + i) = make_float4(w[u][0], w[u][1], w[u][2], w[u][3]);
+        if (ch.w_bf16)
+          st_stream(reinterpret_cast<uint2*>(ch.w_bf16 + i),
+                    make_uint2(cvt_f32x2_bf16x2(w[u][1], w[u][0]),
+                               cvt_f32x2_bf16x2(w[u][3], w[u][2])));
+        const int64_t place = ch.place + (int64_t)(b0 + u) * kMomentBlock;  // one high word
+        const uint32_t key = mix32(s.key + 0x85EBCA6Bu * (uint32_t)(place >> 32));
+        const BlockScales b = block_scales(am, ar);
+        uint32_t qm = 0, qr = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t e =
+              encode_moments(m[u][j], r[u][j], b, mix32((uint32_t)(place + lane * 4 + j) ^ key));
+          qm |= (e & 0xFFu) << (8 * j);
+          qr |= (e >> 8) << (8 * j);
+        }
+        *reinterpret_cast<uint32_t*>(mq + i) = qm;
+        *reinterpret_cast<uint32_t*>(vq + i) = qr;
+        if (lane == 0) {
+          ch.m_scale[b0 + u] = b.m;
+          ch.v_scale[b0 + u] = b.r;
+        }
+      }
+    }
+    // a tensor's last, short block, and chunks off alignment
+    for (int b = whole + warp; (int64_t)b * kMomentBlock < ch.n; b += kWarps) {
       const float sm = ch.m_scale[b], sv = ch.v_scale[b];
-      const int64_t place = ch.place + b * kMomentBlock;  // one high word per block
+      const int64_t place = ch.place + (int64_t)b * kMomentBlock;
       const uint32_t key = mix32(s.key + 0x85EBCA6Bu * (uint32_t)(place >> 32));
       Adam1 o[4];
-      float am = 0.0f, ar = 0.0f;
+      uint32_t am = 0, ar = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t i = b * kMomentBlock + j * 32 + lane;
+        const int k = j * 32 + lane;
+        const int64_t i = (int64_t)b * kMomentBlock + k;
         if (i >= ch.n) continue;
         const float rv = __fmul_rn(decode_e4m3(vq[i]), sv);
         o[j] = adam1(a, s, keep, ch.w[i], load1<GT>(ch.g, i), __fmul_rn(decode_e4m3(mq[i]), sm),
                      __fmul_rn(rv, rv));
         ch.w[i] = o[j].w;
         if (ch.w_bf16) ch.w_bf16[i] = Elem<GS_BF16>::put(o[j].w);
-        am = max_nan(am, fabsf(o[j].m));
-        ar = max_nan(ar, o[j].r);
+        am = max(am, __float_as_uint(o[j].m) & 0x7FFFFFFFu);
+        ar = max(ar, __float_as_uint(o[j].r) & 0x7FFFFFFFu);
       }
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) {
-        am = max_nan(am, __shfl_xor_sync(0xFFFFFFFFu, am, k));
-        ar = max_nan(ar, __shfl_xor_sync(0xFFFFFFFFu, ar, k));
-      }
-      am = am < kMomentFloor ? kMomentFloor : am;  // a NaN stays: it makes the scale NaN
-      ar = ar < kMomentFloor ? kMomentFloor : ar;
-      const float im = __fdiv_rn(448.0f, am), ir = __fdiv_rn(448.0f, ar);
+      const BlockScales bs = block_scales(am, ar);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t i = b * kMomentBlock + j * 32 + lane;
+        const int k = j * 32 + lane;
+        const int64_t i = (int64_t)b * kMomentBlock + k;
         if (i >= ch.n) continue;
-        const uint32_t h = mix32((uint32_t)(ch.place + i) ^ key);
-        mq[i] = encode_e4m3(round_e4m3_random(__fmul_rn(o[j].m, im), h & 0xFFFFu));
-        uint8_t q = encode_e4m3(round_e4m3_random(__fmul_rn(o[j].r, ir), h >> 16));
-        if (q == 0 && o[j].r > 0.0f) q = 1;
-        vq[i] = q;
+        const uint32_t e = encode_moments(o[j].m, o[j].r, bs, mix32((uint32_t)(place + k) ^ key));
+        mq[i] = (uint8_t)(e & 0xFFu);
+        vq[i] = (uint8_t)(e >> 8);
       }
       if (lane == 0) {
-        ch.m_scale[b] = __fdiv_rn(am, 448.0f);
-        ch.v_scale[b] = __fdiv_rn(ar, 448.0f);
+        ch.m_scale[b] = bs.m;
+        ch.v_scale[b] = bs.r;
       }
     }
   }

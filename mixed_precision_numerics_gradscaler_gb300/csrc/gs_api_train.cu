@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -269,14 +270,19 @@ int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
       range(written, m[i], n * msz);
       range(written, v[i], n * msz);
       range(read, grads[i], n * gsz);
-      for (int64_t off = 0; off < n; off += kChunkElems) {
+      // fp32 moments: a short first chunk up to where the vector path's
+      // alignments hold (E4M3 blocks begin with the tensor)
+      const int64_t head = e4m3 ? 0 : achunk_head(master[i], wb, grads[i], m[i], v[i], gsz, n);
+      for (int64_t off = 0; off < n;) {
         const int64_t b = off / kMomentBlock;
+        const int64_t len = off == 0 && head > 0 ? head : std::min(n - off, kChunkElems);
         chunks.push_back(AChunk{master[i] + off, wb ? wb + off : nullptr,
                                 static_cast<const char*>(grads[i]) + off * gsz,
                                 static_cast<char*>(m[i]) + off * msz,
                                 static_cast<char*>(v[i]) + off * msz,
                                 e4m3 ? m_scale[i] + b : nullptr, e4m3 ? v_scale[i] + b : nullptr,
-                                n - off < kChunkElems ? n - off : kChunkElems, place + off, dk});
+                                len, place + off, dk});
+        off += len;
       }
       place += blocks * kMomentBlock;
     }

@@ -86,9 +86,9 @@ __host__ __device__ inline int64_t mchunk_head(const float* w, const uint16_t* w
 }
 
 // One contiguous run of a parameter tensor for the AdamW step: at most
-// kChunkElems elements, beginning at a multiple of kChunkElems elements of
-// the tensor (so that a block of 128 that shares a moment's scale lies in one
-// chunk).
+// kChunkElems elements; with 8-bit moments beginning at a multiple of
+// kChunkElems elements of the tensor (so that a block of 128 that shares a
+// moment's scale lies in one chunk).
 struct AChunk {
   float* w;            // fp32 master weights (updated in place)
   uint16_t* w_bf16;    // bf16 copy, or nullptr
@@ -103,6 +103,22 @@ struct AChunk {
   float decay;         // the tensor's factor of the weight decay
 };
 constexpr int kMomentBlock = 128;
+
+// Elements of a tensor with fp32 moments before the first one at which w, m
+// and v are 32-byte aligned and the gradients (gsz bytes each) and the bf16
+// copy 16-byte aligned, or 0 when there is no such element before the end (or
+// the tensor starts aligned): a tensor at any place of flat buffers still gets
+// full chunks the 32-byte path takes.
+__host__ __device__ inline int64_t achunk_head(const float* w, const uint16_t* wb, const void* g,
+                                               const void* m, const void* v, int64_t gsz,
+                                               int64_t n) {
+  const int64_t h = (int64_t)(((32u - ((uint32_t)(uintptr_t)w & 31u)) & 31u) >> 2);
+  if (h == 0 || h >= n) return 0;
+  const bool ok = (((uintptr_t)m + 4 * h) & 31u) == 0 && (((uintptr_t)v + 4 * h) & 31u) == 0 &&
+                  (((uintptr_t)g + gsz * h) & 15u) == 0 &&
+                  (!wb || (((uintptr_t)(wb + h)) & 15u) == 0);
+  return ok ? h : 0;
+}
 
 struct AdamWArgs {
   float lr, beta1, beta2, eps, weight_decay, max_norm;
