@@ -23,6 +23,7 @@
 
 #include "gs_elem.cuh"
 #include "gs_internal.h"
+#include "gs_quant.cuh"
 
 namespace gs {
 
@@ -64,19 +65,26 @@ struct AdamWStep {
   uint32_t key;        // of the random bits, without the place's high word
 };
 
-// 1 - b^t = -expm1(t log b); b = 0 gives 1.
+// The step's factors, by the CTA's first thread for all of them (the
+// exponentials are a few hundred instructions).  1 - b^t = -expm1(t log b);
+// b = 0 gives 1.
 __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
-  AdamWStep s;
-  s.coef = 1.0f;
-  if (a.max_norm > 0.0f) {
-    const float nrm = *a.grad_norm;
-    if (nrm > a.max_norm) s.coef = __fdiv_rn(a.max_norm, nrm);
+  __shared__ AdamWStep shared;
+  if (threadIdx.x == 0) {
+    AdamWStep s;
+    s.coef = 1.0f;
+    if (a.max_norm > 0.0f) {
+      const float nrm = *a.grad_norm;
+      if (nrm > a.max_norm) s.coef = __fdiv_rn(a.max_norm, nrm);
+    }
+    const int64_t t = *a.step + 1;
+    s.c1 = __fdiv_rn(a.lr, -expm1f((float)t * a.log_beta1));
+    s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
+    s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
+    shared = s;
   }
-  const int64_t t = *a.step + 1;
-  s.c1 = __fdiv_rn(a.lr, -expm1f((float)t * a.log_beta1));
-  s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
-  s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
-  return s;
+  __syncthreads();
+  return shared;
 }
 
 // One element's new moments and weight.
@@ -202,40 +210,96 @@ __global__ void __launch_bounds__(kAdamThreads)
   count_step(a);
 }
 
-// 8-bit moments.  One warp per block of 128: the new moments stay in
-// registers until the block's two maxima are known (as integer maxima of the
-// magnitudes' bits: a NaN is above everything and makes the scale NaN).
-struct BlockScales {
-  float m, r, im, ir;  // scale and 448 / maximum of both moments
+// Two elements' new moments and weights: adam1, both at once (f32x2
+// operations round each half like the single ones).
+__device__ __forceinline__ uint64_t pk1(float f) { return pk_f32x2(f, f); }
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// A product that is rounded by itself: the compiler fuses a packed product
+// with the sum it goes into (whatever -fmad and .rn say), but not this one,
+// whose addend, -0, changes nothing and is not known to it.
+__device__ __forceinline__ uint64_t product_f32x2(const AdamWArgs& a, uint64_t x, uint64_t y) {
+  return fma_f32x2(x, y, pk_f32x2(a.minus_zero, a.minus_zero));
+}
+struct Adam2 {
+  float m[2], r[2], w[2];
 };
-__device__ __forceinline__ BlockScales block_scales(uint32_t am, uint32_t ar) {
-  am = __reduce_max_sync(0xFFFFFFFFu, am);
-  ar = __reduce_max_sync(0xFFFFFFFFu, ar);
-  const uint32_t floor_bits = __float_as_uint(kMomentFloor);
-  const float fm = __uint_as_float(am > floor_bits ? am : floor_bits);
-  const float fr = __uint_as_float(ar > floor_bits ? ar : floor_bits);
+__device__ __forceinline__ Adam2 adam2(const AdamWArgs& a, const AdamWStep& s, float keep,
+                                       uint64_t w, uint64_t g, uint64_t m, uint64_t v) {
+  g = mul_f32x2(g, pk1(s.coef));
+  m = add_f32x2(product_f32x2(a, m, pk1(a.beta1)), product_f32x2(a, g, pk1(a.one_beta1)));
+  v = add_f32x2(product_f32x2(a, v, pk1(a.beta2)),
+                product_f32x2(a, mul_f32x2(g, pk1(a.one_beta2)), g));
+  Adam2 o;
+  upk_f32x2(m, o.m[0], o.m[1]);
+  float v0, v1;
+  upk_f32x2(v, v0, v1);
+  o.r[0] = __fsqrt_rn(v0);
+  o.r[1] = __fsqrt_rn(v1);
+  const uint64_t num = mul_f32x2(m, pk1(s.c1));
+  const uint64_t den = fma_f32x2(pk_f32x2(o.r[0], o.r[1]), pk1(s.c2), pk1(a.eps));
+  float n0, n1, d0, d1;
+  upk_f32x2(num, n0, n1);
+  upk_f32x2(den, d0, d1);
+  const uint64_t upd = pk_f32x2(-__fdividef(n0, d0), -__fdividef(n1, d1));
+  upk_f32x2(fma_f32x2(w, pk1(keep), upd), o.w[0], o.w[1]);
+  return o;
+}
+
+// 8-bit moments.  A warp takes blocks of 128 two at a time, four consecutive
+// elements per lane; the new moments stay in registers until the blocks'
+// maxima are known (as integer maxima of the magnitudes' bits: a NaN is above
+// everything and makes the scale NaN).
+constexpr int kAdamBlocks = 2;
+
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// A moment's scale a / 448 and factor 448 / a of up to four maxima (two
+// blocks' m and root), lane i of a group of eight dividing for one of the
+// eight: four divisions of every lane's own cost more than all else here.
+struct BlockScales {
+  float scale;  // of this lane: its block's and moment's (lanes 0-3 of eight)
+  float inv[2 * kAdamBlocks];
+};
+__device__ __forceinline__ BlockScales block_scales(const float* mx, int lane) {
+  float a[2 * kAdamBlocks];
+#pragma unroll
+  for (int i = 0; i < 2 * kAdamBlocks; ++i) {
+    const uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx[i]));
+    const uint32_t least = __float_as_uint(kMomentFloor);
+    a[i] = __uint_as_float(bits > least ? bits : least);
+  }
+  const float x = (lane & 2) ? ((lane & 1) ? a[3] : a[2]) : ((lane & 1) ? a[1] : a[0]);
+  const bool inverse = lane & 4;
   BlockScales b;
-  b.m = __fdiv_rn(fm, 448.0f);
-  b.r = __fdiv_rn(fr, 448.0f);
-  b.im = __fdiv_rn(448.0f, fm);
-  b.ir = __fdiv_rn(448.0f, fr);
+  b.scale = __fdiv_rn(inverse ? 448.0f : x, inverse ? x : 448.0f);
+#pragma unroll
+  for (int i = 0; i < 2 * kAdamBlocks; ++i) b.inv[i] = __shfl_sync(0xFFFFFFFFu, b.scale, 4 + i);
   return b;
 }
-// Codes of one element's moments: m's in the low byte, the root's in the next.
-__device__ __forceinline__ uint32_t encode_moments(float m, float r, const BlockScales& b,
-                                                   uint32_t h) {
-  const float tm = __fmul_rn(m, b.im);
-  const uint32_t qm = round_e4m3_random(fabsf(tm), h & 0xFFFFu) |
-                      ((__float_as_uint(tm) >> 24) & 0x80u);
-  uint32_t qr = round_e4m3_random(__fmul_rn(r, b.ir), h >> 16);
-  if (qr == 0 && r > 0.0f) qr = 1;
-  return qm | (qr << 8);
+
+__device__ __forceinline__ uint32_t encode_m(float m, float inv, uint32_t h) {
+  const float t = __fmul_rn(m, inv);
+  return round_e4m3_random(fabsf(t), h & 0xFFFFu) | ((__float_as_uint(t) >> 24) & 0x80u);
+}
+__device__ __forceinline__ uint32_t encode_r(float r, float inv, uint32_t h) {
+  const uint32_t q = round_e4m3_random(__fmul_rn(r, inv), h >> 16);
+  return q == 0 && r > 0.0f ? 1u : q;
+}
+__device__ __forceinline__ uint32_t pack4(const uint32_t* q) {
+  return __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
 }
 
-constexpr int kAdamBlocks = 2;  // blocks of 128 that a warp has in flight
-
 template <int GT>
-__global__ void __launch_bounds__(kAdamThreads)
+__global__ void __launch_bounds__(kAdamThreads, 4)
     adamw_e4m3_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
   if (*a.found_inf) return;
   const AdamWStep s = step_of(a);
@@ -248,105 +312,99 @@ __global__ void __launch_bounds__(kAdamThreads)
     uint8_t* vq = static_cast<uint8_t*>(ch.v);
     const bool vec = aligned_to(ch.w, 16) && aligned_to(ch.g, 16) && aligned_to(mq, 4) &&
                      aligned_to(vq, 4) && aligned_to(ch.w_bf16, 8);
-    const int whole = vec ? (int)(ch.n / kMomentBlock) : 0;  // blocks of the vector path
+    // blocks of the vector path, whole ones in pairs
+    const int whole = vec ? (int)(ch.n / kMomentBlock) / U * U : 0;
     for (int b0 = warp * U; b0 < whole; b0 += kWarps * U) {
-      float w[U][4], g[U][4], m[U][4], r[U][4];
+      float4 w[U];
+      float g[U][4];
       uint32_t q[U][2];
       float sc[U][2];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (b0 + u >= whole) continue;
         const int i = (b0 + u) * kMomentBlock + lane * 4;
-        const float4 f = ld_state4(ch.w + i);
-        w[u][0] = f.x;
-        w[u][1] = f.y;
-        w[u][2] = f.z;
-        w[u][3] = f.w;
+        w[u] = ld_state4(ch.w + i);
         load_grads<GT, 4>(ch.g, i, g[u]);
         q[u][0] = *reinterpret_cast<const uint32_t*>(mq + i);
         q[u][1] = *reinterpret_cast<const uint32_t*>(vq + i);
         sc[u][0] = ch.m_scale[b0 + u];
         sc[u][1] = ch.v_scale[b0 + u];
       }
+      float m[U][4], r[U][4], mx[2 * U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (b0 + u >= whole) continue;
         const int i = (b0 + u) * kMomentBlock + lane * 4;
-        uint32_t am = 0, ar = 0;
+        const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float nw[4];
+        mx[2 * u] = mx[2 * u + 1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
           const uint32_t hm = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][0] >> (8 * j)));
           const uint32_t hv = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][1] >> (8 * j)));
+          const uint64_t m2 = mul_f32x2(pk_f32x2(lo_f16(hm), hi_f16(hm)), pk1(sc[u][0]));
+          const uint64_t r2 = mul_f32x2(pk_f32x2(lo_f16(hv), hi_f16(hv)), pk1(sc[u][1]));
+          const Adam2 o = adam2(a, s, keep, pk_f32x2(wf[j], wf[j + 1]),
+                                pk_f32x2(g[u][j], g[u][j + 1]), m2, mul_f32x2(r2, r2));
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float rv = __fmul_rn(k ? hi_f16(hv) : lo_f16(hv), sc[u][1]);
-            const Adam1 o = adam1(a, s, keep, w[u][j + k], g[u][j + k],
-                                  __fmul_rn(k ? hi_f16(hm) : lo_f16(hm), sc[u][0]),
-                                  __fmul_rn(rv, rv));
-            w[u][j + k] = o.w;
-            m[u][j + k] = o.m;
-            r[u][j + k] = o.r;
-            am = max(am, __float_as_uint(o.m) & 0x7FFFFFFFu);
-            ar = max(ar, __float_as_uint(o.r) & 0x7FFFFFFFu);
+            nw[j + k] = o.w[k];
+            m[u][j + k] = o.m[k];
+            r[u][j + k] = o.r[k];
+            mx[2 * u] = max_nan(mx[2 * u], fabsf(o.m[k]));
+            mx[2 * u + 1] = max_nan(mx[2 * u + 1], o.r[k]);
           }
         }
-        *reinterpret_cast<float4*>(ch.w + i) = make_float4(w[u][0], w[u][1], w[u][2], w[u][3]);
+        *reinterpret_cast<float4*>(ch.w + i) = make_float4(nw[0], nw[1], nw[2], nw[3]);
         if (ch.w_bf16)
           st_stream(reinterpret_cast<uint2*>(ch.w_bf16 + i),
-                    make_uint2(cvt_f32x2_bf16x2(w[u][1], w[u][0]),
-                               cvt_f32x2_bf16x2(w[u][3], w[u][2])));
+                    make_uint2(cvt_f32x2_bf16x2(nw[1], nw[0]), cvt_f32x2_bf16x2(nw[3], nw[2])));
+      }
+      const BlockScales b = block_scales(mx, lane);
+      if (lane < 2 * U)
+        ((lane & 1) ? ch.v_scale : ch.m_scale)[b0 + (lane >> 1)] = b.scale;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = (b0 + u) * kMomentBlock + lane * 4;
         const int64_t place = ch.place + (int64_t)(b0 + u) * kMomentBlock;  // one high word
         const uint32_t key = mix32(s.key + 0x85EBCA6Bu * (uint32_t)(place >> 32));
-        const BlockScales b = block_scales(am, ar);
-        uint32_t qm = 0, qr = 0;
+        uint32_t qm[4], qr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t e =
-              encode_moments(m[u][j], r[u][j], b, mix32((uint32_t)(place + lane * 4 + j) ^ key));
-          qm |= (e & 0xFFu) << (8 * j);
-          qr |= (e >> 8) << (8 * j);
+          const uint32_t h = mix32((uint32_t)(place + lane * 4 + j) ^ key);
+          qm[j] = encode_m(m[u][j], b.inv[2 * u], h);
+          qr[j] = encode_r(r[u][j], b.inv[2 * u + 1], h);
         }
-        *reinterpret_cast<uint32_t*>(mq + i) = qm;
-        *reinterpret_cast<uint32_t*>(vq + i) = qr;
-        if (lane == 0) {
-          ch.m_scale[b0 + u] = b.m;
-          ch.v_scale[b0 + u] = b.r;
-        }
+        *reinterpret_cast<uint32_t*>(mq + i) = pack4(qm);
+        *reinterpret_cast<uint32_t*>(vq + i) = pack4(qr);
       }
     }
-    // a tensor's last, short block, and chunks off alignment
-    for (int b = whole + warp; (int64_t)b * kMomentBlock < ch.n; b += kWarps) {
-      const float sm = ch.m_scale[b], sv = ch.v_scale[b];
-      const int64_t place = ch.place + (int64_t)b * kMomentBlock;
+    // a tensor's last blocks, and chunks off alignment: one block at a time
+    for (int b0 = whole + warp; (int64_t)b0 * kMomentBlock < ch.n; b0 += kWarps) {
+      const float sm = ch.m_scale[b0], sv = ch.v_scale[b0];
+      const int64_t place = ch.place + (int64_t)b0 * kMomentBlock;
       const uint32_t key = mix32(s.key + 0x85EBCA6Bu * (uint32_t)(place >> 32));
       Adam1 o[4];
-      uint32_t am = 0, ar = 0;
+      float mx[2 * U] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = j * 32 + lane;
-        const int64_t i = (int64_t)b * kMomentBlock + k;
+        const int64_t i = (int64_t)b0 * kMomentBlock + j * 32 + lane;
         if (i >= ch.n) continue;
         const float rv = __fmul_rn(decode_e4m3(vq[i]), sv);
         o[j] = adam1(a, s, keep, ch.w[i], load1<GT>(ch.g, i), __fmul_rn(decode_e4m3(mq[i]), sm),
                      __fmul_rn(rv, rv));
         ch.w[i] = o[j].w;
         if (ch.w_bf16) ch.w_bf16[i] = Elem<GS_BF16>::put(o[j].w);
-        am = max(am, __float_as_uint(o[j].m) & 0x7FFFFFFFu);
-        ar = max(ar, __float_as_uint(o[j].r) & 0x7FFFFFFFu);
+        mx[0] = max_nan(mx[0], fabsf(o[j].m));
+        mx[1] = max_nan(mx[1], o[j].r);
       }
-      const BlockScales bs = block_scales(am, ar);
+      const BlockScales b = block_scales(mx, lane);
+      if (lane < 2) ((lane & 1) ? ch.v_scale : ch.m_scale)[b0] = b.scale;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = j * 32 + lane;
-        const int64_t i = (int64_t)b * kMomentBlock + k;
+        const int64_t i = (int64_t)b0 * kMomentBlock + j * 32 + lane;
         if (i >= ch.n) continue;
-        const uint32_t e = encode_moments(o[j].m, o[j].r, bs, mix32((uint32_t)(place + k) ^ key));
-        mq[i] = (uint8_t)(e & 0xFFu);
-        vq[i] = (uint8_t)(e >> 8);
-      }
-      if (lane == 0) {
-        ch.m_scale[b] = bs.m;
-        ch.v_scale[b] = bs.r;
+        const uint32_t h = mix32((uint32_t)(place + j * 32 + lane) ^ key);
+        mq[i] = (uint8_t)encode_m(o[j].m, b.inv[0], h);
+        vq[i] = (uint8_t)encode_r(o[j].r, b.inv[1], h);
       }
     }
   }

@@ -357,6 +357,7 @@ int gs_master_update_adamw(const gs_adamw_list* list, float lr, float beta1, flo
   a.found_inf = found_inf;
   a.step = step;
   a.seed = seed;
+  a.minus_zero = -0.0f;
   a.arrived = list->d_arrived;
   const cudaError_t e = launch_master_update_adamw(list->d_chunks, list->n_chunks,
                                                    list->grad_dtype, list->moments, a,

@@ -128,6 +128,7 @@ struct AdamWArgs {
   const int32_t* found_inf;
   int64_t* step;
   uint32_t seed;
+  float minus_zero;             // -0, where the compiler must not know it
   unsigned int* arrived;        // the list's arrival count, 0 between calls
 };
 
