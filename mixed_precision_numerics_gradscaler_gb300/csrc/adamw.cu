@@ -87,6 +87,30 @@ __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
   return shared;
 }
 
+// n / d, off by 2 ulp at most, for a normal d (here at least eps + the root of
+// the smallest fp32 number, or 0: a quotient of NaN or Inf).
+__device__ __forceinline__ float quotient(float n, float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return n * r;
+}
+
+// sqrt(v) rounded to nearest for v in [2^-96, 2^96], two at once: s = v y and
+// h = y / 2 with y near 1 / sqrt(v), then s + h (v - s^2), the residual exact by
+// a fused multiply-add (Markstein, "IA-64 and Elementary Functions", 2000,
+// chapter 9: one such step from an estimate within an ulp rounds correctly
+// but where y is too coarse; all significands of both binades were compared
+// with the IEEE root on the device, and a test does so again).
+__device__ __forceinline__ uint64_t sqrt_f32x2(uint64_t v) {
+  float v0, v1, y0, y1;
+  upk_f32x2(v, v0, v1);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v0));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v1));
+  const uint64_t y = pk_f32x2(y0, y1), s = mul_f32x2(v, y);
+  const uint64_t e = fma_f32x2(s ^ 0x8000000080000000ull, s, v);
+  return fma_f32x2(e, mul_f32x2(y, pk_f32x2(0.5f, 0.5f)), s);
+}
+
 // One element's new moments and weight.
 struct Adam1 {
   float m, v, r, w;
@@ -99,7 +123,7 @@ __device__ __forceinline__ Adam1 adam1(const AdamWArgs& a, const AdamWStep& s, f
   o.v = __fadd_rn(__fmul_rn(v, a.beta2), __fmul_rn(__fmul_rn(g, a.one_beta2), g));
   o.r = __fsqrt_rn(o.v);
   o.w = __fsub_rn(__fmul_rn(w, keep),
-                  __fdividef(__fmul_rn(o.m, s.c1), __fmaf_rn(o.r, s.c2, a.eps)));
+                  quotient(__fmul_rn(o.m, s.c1), __fmaf_rn(o.r, s.c2, a.eps)));
   return o;
 }
 
@@ -115,12 +139,12 @@ __device__ __forceinline__ void count_step(const AdamWArgs& a) {
   }
 }
 
-// N gradients (N a multiple of 4), 16 bytes at a time or 8.
-template <int GT, int N>
-__device__ __forceinline__ void load_grads(const void* g, int64_t i, float* f) {
+// Eight gradients, 16 bytes at a time.
+template <int GT>
+__device__ __forceinline__ void load_grads8(const void* g, int64_t i, float* f) {
   if constexpr (GT == GS_F32) {
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
+    for (int j = 0; j < 8; j += 4) {
       const uint4 w = ld_stream(reinterpret_cast<const uint4*>(static_cast<const float*>(g) + i + j));
       f[j] = __uint_as_float(w.x);
       f[j + 1] = __uint_as_float(w.y);
@@ -129,16 +153,12 @@ __device__ __forceinline__ void load_grads(const void* g, int64_t i, float* f) {
     }
   } else {
     using Tag = std::conditional_t<GT == GS_BF16, BF16Tag, F16Tag>;
+    const uint4 w = ld_stream(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i));
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      uint2 w;
-      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                   : "=r"(w.x), "=r"(w.y)
-                   : "l"(static_cast<const uint16_t*>(g) + i + j));
-      f[j] = lo16<Tag>(w.x);
-      f[j + 1] = hi16<Tag>(w.x);
-      f[j + 2] = lo16<Tag>(w.y);
-      f[j + 3] = hi16<Tag>(w.y);
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = lo16<Tag>(q[j]);
+      f[2 * j + 1] = hi16<Tag>(q[j]);
     }
   }
 }
@@ -180,7 +200,7 @@ __global__ void __launch_bounds__(kAdamThreads)
     for (int i = threadIdx.x; i < n8; i += kAdamThreads) {
       V8 w8 = ld_state8(ch.w + 8 * i), m8 = ld_state8(m + 8 * i), v8 = ld_state8(v + 8 * i);
       float g[8];
-      load_grads<GT, 8>(ch.g, 8 * i, g);
+      load_grads8<GT>(ch.g, 8 * i, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const Adam1 o = adam1(a, s, keep, __uint_as_float(w8.w[j]), g[j], __uint_as_float(m8.w[j]),
@@ -237,14 +257,18 @@ __device__ __forceinline__ Adam2 adam2(const AdamWArgs& a, const AdamWStep& s, f
   upk_f32x2(m, o.m[0], o.m[1]);
   float v0, v1;
   upk_f32x2(v, v0, v1);
-  o.r[0] = __fsqrt_rn(v0);
-  o.r[1] = __fsqrt_rn(v1);
+  if (fminf(v0, v1) >= 0x1p-96f && fmaxf(v0, v1) <= 0x1p96f) {
+    upk_f32x2(sqrt_f32x2(v), o.r[0], o.r[1]);
+  } else {
+    o.r[0] = __fsqrt_rn(v0);
+    o.r[1] = __fsqrt_rn(v1);
+  }
   const uint64_t num = mul_f32x2(m, pk1(s.c1));
   const uint64_t den = fma_f32x2(pk_f32x2(o.r[0], o.r[1]), pk1(s.c2), pk1(a.eps));
   float n0, n1, d0, d1;
   upk_f32x2(num, n0, n1);
   upk_f32x2(den, d0, d1);
-  const uint64_t upd = pk_f32x2(-__fdividef(n0, d0), -__fdividef(n1, d1));
+  const uint64_t upd = pk_f32x2(-quotient(n0, d0), -quotient(n1, d1));
   upk_f32x2(fma_f32x2(w, pk1(keep), upd), o.w[0], o.w[1]);
   return o;
 }
@@ -261,6 +285,43 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+
+// Four gradients as they are in memory.
+template <int GT>
+__device__ __forceinline__ void load_raw(const void* g, int64_t i, uint32_t* w) {
+  if constexpr (GT == GS_F32) {
+    const uint4 v = ld_stream(reinterpret_cast<const uint4*>(static_cast<const float*>(g) + i));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "l"(static_cast<const uint16_t*>(g) + i));
+  }
+}
+template <int GT>
+__device__ __forceinline__ void unpack_raw(const uint32_t* w, float* f) {
+  if constexpr (GT == GS_F32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(w[j]);
+  } else {
+    using Tag = std::conditional_t<GT == GS_BF16, BF16Tag, F16Tag>;
+    f[0] = lo16<Tag>(w[0]);
+    f[1] = hi16<Tag>(w[0]);
+    f[2] = lo16<Tag>(w[1]);
+    f[3] = hi16<Tag>(w[1]);
+  }
+}
+// A lane's part of a block as it is in memory.
+template <int GT>
+struct RawBlock {
+  float4 w;
+  uint32_t g[GT == GS_F32 ? 4 : 2];
+  uint32_t m, v;
+  float sm, sv;
+};
 
 // A moment's scale a / 448 and factor 448 / a of up to four maxima (two
 // blocks' m and root), lane i of a group of eight dividing for one of the
@@ -302,9 +363,9 @@ template <int GT>
 __global__ void __launch_bounds__(kAdamThreads, 4)
     adamw_e4m3_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
   if (*a.found_inf) return;
-  const AdamWStep s = step_of(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kWarps = kAdamThreads / 32, U = kAdamBlocks;
+  const AdamWStep s = step_of(a);
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     const AChunk ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
@@ -315,35 +376,34 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
     // blocks of the vector path, whole ones in pairs
     const int whole = vec ? (int)(ch.n / kMomentBlock) / U * U : 0;
     for (int b0 = warp * U; b0 < whole; b0 += kWarps * U) {
-      float4 w[U];
-      float g[U][4];
-      uint32_t q[U][2];
-      float sc[U][2];
+      RawBlock<GT> now[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = (b0 + u) * kMomentBlock + lane * 4;
-        w[u] = ld_state4(ch.w + i);
-        load_grads<GT, 4>(ch.g, i, g[u]);
-        q[u][0] = *reinterpret_cast<const uint32_t*>(mq + i);
-        q[u][1] = *reinterpret_cast<const uint32_t*>(vq + i);
-        sc[u][0] = ch.m_scale[b0 + u];
-        sc[u][1] = ch.v_scale[b0 + u];
+        now[u].w = ld_state4(ch.w + i);
+        load_raw<GT>(ch.g, i, now[u].g);
+        now[u].m = *reinterpret_cast<const uint32_t*>(mq + i);
+        now[u].v = *reinterpret_cast<const uint32_t*>(vq + i);
+        now[u].sm = ch.m_scale[b0 + u];
+        now[u].sv = ch.v_scale[b0 + u];
       }
       float m[U][4], r[U][4], mx[2 * U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = (b0 + u) * kMomentBlock + lane * 4;
-        const float wf[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        const float wf[4] = {now[u].w.x, now[u].w.y, now[u].w.z, now[u].w.w};
+        float g[4];
+        unpack_raw<GT>(now[u].g, g);
         float nw[4];
         mx[2 * u] = mx[2 * u + 1] = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          const uint32_t hm = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][0] >> (8 * j)));
-          const uint32_t hv = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(q[u][1] >> (8 * j)));
-          const uint64_t m2 = mul_f32x2(pk_f32x2(lo_f16(hm), hi_f16(hm)), pk1(sc[u][0]));
-          const uint64_t r2 = mul_f32x2(pk_f32x2(lo_f16(hv), hi_f16(hv)), pk1(sc[u][1]));
+          const uint32_t hm = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(now[u].m >> (8 * j)));
+          const uint32_t hv = cvt_fp8x2_f16x2<GS_E4M3>((uint16_t)(now[u].v >> (8 * j)));
+          const uint64_t m2 = mul_f32x2(pk_f32x2(lo_f16(hm), hi_f16(hm)), pk1(now[u].sm));
+          const uint64_t r2 = mul_f32x2(pk_f32x2(lo_f16(hv), hi_f16(hv)), pk1(now[u].sv));
           const Adam2 o = adam2(a, s, keep, pk_f32x2(wf[j], wf[j + 1]),
-                                pk_f32x2(g[u][j], g[u][j + 1]), m2, mul_f32x2(r2, r2));
+                                pk_f32x2(g[j], g[j + 1]), m2, mul_f32x2(r2, r2));
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             nw[j + k] = o.w[k];
@@ -369,7 +429,8 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
         uint32_t qm[4], qr[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t h = mix32((uint32_t)(place + lane * 4 + j) ^ key);
+          // (place is a multiple of 128: the sum of place and j is their xor)
+          const uint32_t h = mix32(((uint32_t)place + lane * 4) ^ key ^ (uint32_t)j);
           qm[j] = encode_m(m[u][j], b.inv[2 * u], h);
           qr[j] = encode_r(r[u][j], b.inv[2 * u + 1], h);
         }

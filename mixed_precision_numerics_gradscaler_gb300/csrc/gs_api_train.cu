@@ -242,7 +242,14 @@ int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
     const auto range = [](std::vector<Span>& to, const void* p, int64_t bytes) {
       to.push_back(Span{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes});
     };
-    int64_t place = 0;
+    // A chunk is four passes of a CTA; one in lists that would leave SMs
+    // without work.
+    int64_t place = 0, total = 0;
+    for (int32_t i = 0; i < n_tensors; ++i)
+      if (numels[i] > 0 && numels[i] <= (INT64_MAX >> 4) && total <= (INT64_MAX >> 1))
+        total += numels[i];
+    const int64_t chunk = total / kChunkElems < (int64_t)sm_count() * 4 ? kChunkElems / 4
+                                                                       : kChunkElems;
     for (int32_t i = 0; i < n_tensors; ++i) {
       const int64_t n = numels[i];
       if (n < 0 || n > (INT64_MAX >> 4) || place > (INT64_MAX >> 1) - n) return GS_ERR_SHAPE;
@@ -275,7 +282,7 @@ int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
       const int64_t head = e4m3 ? 0 : achunk_head(master[i], wb, grads[i], m[i], v[i], gsz, n);
       for (int64_t off = 0; off < n;) {
         const int64_t b = off / kMomentBlock;
-        const int64_t len = off == 0 && head > 0 ? head : std::min(n - off, kChunkElems);
+        const int64_t len = off == 0 && head > 0 ? head : std::min(n - off, chunk);
         chunks.push_back(AChunk{master[i] + off, wb ? wb + off : nullptr,
                                 static_cast<const char*>(grads[i]) + off * gsz,
                                 static_cast<char*>(m[i]) + off * msz,

@@ -233,6 +233,29 @@ def test_nonfinite_gradients_show_in_the_states(gs, bad):
             assert not torch.isfinite(p.m[0][200]) and torch.isfinite(p.m[0][:200]).all()
 
 
+def test_root_of_every_significand(gs):
+    """The step's square root is its own: beta2 = 0 and gradients g make v the
+    rounded product g * g, whose root must be the IEEE one (numpy's).  With
+    g = s * 2^k, s every 2^-12th significand, over the whole range of v, in
+    both element types' kernels."""
+    s = (1 + np.arange(4096) / 4096).astype(np.float32)
+    g = np.concatenate([s * np.float32(2.0 ** k) for k in (-60, -49, -48, -47, -20, -1, 0, 7, 47, 48, 49, 60)])
+    rng = np.random.default_rng(2)
+    g = np.concatenate([g, np.exp2(rng.uniform(-62, 62, 1 << 20)).astype(np.float32)])
+    hp = dict(lr=0.0, beta1=0.0, beta2=0.0, eps=f32(1e-8), weight_decay=0.0)
+    for e4m3 in (False, True):
+        p = Params(gs, [g.size], e4m3, "f32", False, zero=True)
+        p.g[0].copy_(torch.from_numpy(g))
+        gs.gs_master_update_adamw(p.list, p.step, p.found, seed=5, **hp)
+        _, v, r = tr.moments_f32(g, 0 * g, 0 * g, 0.0, 0.0)
+        if e4m3:
+            code, scale = tr.round_block(r, tr.random_bits(0, g.size, 5, 1) >> np.uint32(16), True)
+            assert np.array_equal(p.vs[0].cpu().numpy(), scale)
+            assert np.array_equal(p.v[0].cpu().numpy(), code)
+        else:
+            assert np.array_equal(p.v[0].cpu().numpy(), v)
+
+
 def test_codes_read_back_through_fp8_dequant(gs):
     p = Params(gs, [1024], True)
     gs.gs_master_update_adamw(p.list, p.step, p.found, **HP)
