@@ -187,6 +187,154 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
   }
 }
 
+// ---- rows through a copy ring ----------------------------------------------
+// Thread t owns vector t of every row (its weights stay in registers) and
+// copies its part of the next rows into shared memory itself (cp.async), so
+// that no thread waits for another's copy and the memory stays busy across
+// the barriers.  Two rows share a barrier: the sums' latency, some 800 cycles
+// of shuffles and barrier, would take half the time of a row otherwise.
+// 1024 threads per SM with 64 registers each, one CTA of them for the widest
+// rows, up to 32 for the narrowest.
+
+// Sums of four values over the warp: lane 8 q and its seven neighbours return
+// the sum of s[q].
+__device__ __forceinline__ float warp_sum4(const float* s, int lane) {
+  const bool hi = lane & 16, mid = lane & 8;
+  const float u0 = (hi ? s[2] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s[0] : s[2], 16);
+  const float u1 = (hi ? s[3] : s[1]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s[1] : s[3], 16);
+  float v = (mid ? u1 : u0) + __shfl_xor_sync(0xFFFFFFFFu, mid ? u0 : u1, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+// Sums of two values: lane 16 q and its neighbours return the sum of s[q].
+__device__ __forceinline__ float warp_sum2(float s0, float s1, int lane) {
+  const bool hi = lane & 16;
+  float v = (hi ? s1 : s0) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s0 : s1, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+constexpr int kRingRows = 2;  // rows that share a barrier
+constexpr int kFwdGroups = 4, kBwdGroups = 3;  // pairs of rows in the ring
+
+template <int DT, int WT>
+__global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormArgs a) {
+  constexpr int W = kVecElems<DT>, D = kFwdGroups;
+  extern __shared__ uint4 ring[];  // [D][2][blockDim.x]
+  // per row of the pair: the warps' means and squared deviations from them
+  __shared__ float2 part[2][2][32];
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
+  const int c = tid * W;
+  const bool live = c < a.C;
+  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
+  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + c;
+  float g[W], b[W];
+#pragma unroll
+  for (int j = 0; j < W; ++j) g[j] = b[j] = 0.0f;
+  if (live) {
+    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
+    load_weights<WT, W>(a.beta, c, a.w_vec, 0.0f, b);
+  }
+  // columns of this warp and of warp i
+  const auto columns = [&](int i) {
+    const int n = (int)a.C - i * 32 * W;
+    return (float)(n < 0 ? 0 : n < 32 * W ? n : 32 * W);
+  };
+  const float inv = __fdiv_rn(1.0f, (float)a.C);
+  const float inv_warp = __fdiv_rn(1.0f, fmaxf(columns(warp), 1.0f));
+  // the two warps whose partial sums this lane joins, and their columns
+  const int w0 = (lane & 15) * 2, pair = lane >> 4;
+  const float n0 = columns(w0), n1 = columns(w0 + 1);
+
+  const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
+  const int64_t stride = (int64_t)gridDim.x * 2;
+  const auto copy_pair = [&](int64_t r, int slot) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (live && r + q < a.R)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot0 +
+                                                                       (slot * 2 + q) * nt * 16),
+                     "l"(x + (r + q) * a.ldx)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int64_t first = (int64_t)blockIdx.x * 2;
+#pragma unroll
+  for (int i = 0; i < D; ++i) copy_pair(first + i * stride, i);
+  int slot = 0, side = 0;
+  for (int64_t r = first; r < a.R; r += stride) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    float f[2][W], s[2], q[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (live && r + i < a.R) {
+        unpack_vec<DT>(ring[(slot * 2 + i) * nt + tid], f[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[i][j] = 0.0f;
+      }
+      s[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < W; ++j) s[i] += f[i][j];
+    }
+    copy_pair(r + D * stride, slot);
+    slot = slot + 1 < D ? slot + 1 : 0;
+    // this warp's means, and the deviations from them
+    const float ws = warp_sum2(s[0], s[1], lane) * inv_warp;
+    const float wm[2] = {__shfl_sync(0xFFFFFFFFu, ws, 0), __shfl_sync(0xFFFFFFFFu, ws, 16)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      q[i] = 0.0f;
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          f[i][j] -= wm[i];
+          q[i] = __fmaf_rn(f[i][j], f[i][j], q[i]);
+        }
+      }
+    }
+    const float wq = warp_sum2(q[0], q[1], lane);
+    float mu, var;  // of row `pair` of the two, in this lane
+    if (warps > 1) {
+      if ((lane & 15) == 0) part[side][pair][warp] = make_float2(ws, wq);
+      __syncthreads();
+      const float2 none = make_float2(0.0f, 0.0f);
+      const float2 p0 = w0 < warps ? part[side][pair][w0] : none;
+      const float2 p1 = w0 + 1 < warps ? part[side][pair][w0 + 1] : none;
+      side ^= 1;  // free again: every thread passes the next barrier after these reads
+      float t = __fmaf_rn(n0, p0.x, n1 * p1.x);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      mu = t * inv;
+      const float d0 = p0.x - mu, d1 = p1.x - mu;
+      t = __fmaf_rn(n0 * d0, d0, p0.y) + __fmaf_rn(n1 * d1, d1, p1.y);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      var = t * inv;
+    } else {
+      mu = ws;
+      var = wq * inv;
+    }
+    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+    if (warp == 0 && (lane & 15) == 0 && r + pair < a.R) {
+      if (a.mean) a.mean[r + pair] = mu;
+      if (a.rstd) a.rstd[r + pair] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float shift = wm[i] - __shfl_sync(0xFFFFFFFFu, mu, 16 * i);
+      const float scale = __shfl_sync(0xFFFFFFFFu, rs, 16 * i);
+      if (live && r + i < a.R) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[i][j] = __fmaf_rn((f[i][j] + shift) * scale, g[j], b[j]);
+        st_stream(reinterpret_cast<uint4*>(y + (r + i) * a.ldy), pack_vec<DT>(f[i]));
+      }
+    }
+  }
+}
+
 // Rows of any length, read three times.
 constexpr int kLongThreads = 1024;
 template <int DT, int WT>
@@ -218,7 +366,7 @@ __global__ void __launch_bounds__(kLongThreads) layernorm_fwd_long_kernel(const 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 template <int DT, int WT>
-static void fwd_launch(const NormArgs& a, cudaStream_t stream) {
+static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
   constexpr int V = kVecElems<DT>;
   const bool vec = aligned16(a.x) && aligned16(a.y) && a.C % V == 0 && a.ldx % V == 0 &&
                    a.ldy % V == 0;
@@ -226,7 +374,17 @@ static void fwd_launch(const NormArgs& a, cudaStream_t stream) {
 #define GS_L(W, NT, VPT)                                                                      \
   layernorm_fwd_kernel<DT, WT, W, NT, VPT>                                                    \
       <<<NT == 32 ? warps : rows, NT == 32 ? 256 : NT, 0, stream>>>(a)
-  if (vec) {
+  const int threads = (int)((a.C / V + 31) / 32 * 32);
+  const int64_t ctas = (int64_t)sm_count() * (threads <= 1024 ? 1024 / std::max(threads, 32) : 0);
+  if (vec && ctas > 0 && a.R >= ctas * 2 * kRingRows) {
+    const auto smem = [](int n) { return kFwdGroups * 2 * n * 16; };
+    const auto kernel = layernorm_fwd_ring_kernel<DT, WT>;
+    int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
+    const cudaError_t e =
+        kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)ctas, threads, smem(threads), stream>>>(a);
+  } else if (vec) {
     const int64_t nv = a.C / V;
     if (nv <= 32) GS_L(V, 32, 1);
     else if (nv <= 128) GS_L(V, 32, 4);
@@ -243,6 +401,7 @@ static void fwd_launch(const NormArgs& a, cudaStream_t stream) {
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   }
 #undef GS_L
+  return cudaGetLastError();
 }
 
 // Runs `f` with the two type codes as template arguments: w_dtype is GS_F32
@@ -268,11 +427,13 @@ cudaError_t launch_layernorm_fwd(const void* x, int64_t ldx, int dtype, int64_t 
                      static_cast<char*>(y) + r0 * ldy * esz, ldy,
                      mean ? mean + r0 : nullptr, rstd ? rstd + r0 : nullptr,
                      aligned16(gamma) && aligned16(beta)};
-#define GS_F(DT, WT) fwd_launch<DT, WT>(a, stream);
+    cudaError_t e = cudaSuccess;
+#define GS_F(DT, WT) e = fwd_launch<DT, WT>(a, stream);
     GS_NORM_TYPES(dtype, w_dtype, GS_F)
 #undef GS_F
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -315,14 +476,16 @@ __device__ __forceinline__ float2 row_sum2(float s1, float s2, float2* red, int 
   return make_float2(s1, s2);
 }
 
-// Rows 16 bytes at a time: thread t owns vector t of every row.
-constexpr int kBwdSteps = 4;  // rows copied ahead
+// Rows 16 bytes at a time, two per barrier.  The rows are read from the ring
+// again after it (registers hold the weights and both sums' accumulators).
 template <int DT, int WT>
-__global__ void __launch_bounds__(1024, 1) layernorm_bwd_vec_kernel(const NormBwdArgs a) {
-  constexpr int W = kVecElems<DT>;
-  extern __shared__ uint4 ring[];  // [kBwdSteps][x, dy][blockDim.x]
-  __shared__ float2 red[2][32];
-  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, c = tid * W;
+__global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormBwdArgs a) {
+  constexpr int W = kVecElems<DT>, D = kBwdGroups;
+  extern __shared__ uint4 ring[];  // [D][2][x, dy][blockDim.x]
+  __shared__ float4 part4[2][32];  // per value of the pair's four: eight warps' sums a float4
+  float* const part = reinterpret_cast<float*>(part4);  // [2][4][32]
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
+  const int c = tid * W;
   const bool live = c < a.C;
   const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
   const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy) + c;
@@ -332,63 +495,87 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_vec_kernel(const NormBw
   for (int j = 0; j < W; ++j) g[j] = ag[j] = ab[j] = 0.0f;
   if (live) load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
   const float inv = __fdiv_rn(1.0f, (float)a.C);
+  for (int i = tid; i < 256; i += nt) part[i] = 0.0f;  // of warps that do not exist
+  __syncthreads();
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
-  const auto copy_row = [&](int64_t r, int slot) {
-    if (r < a.R && live) {
-      const uint32_t to = slot0 + slot * 2 * nt * 16;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(x + r * a.ldx)
-                   : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + nt * 16),
-                   "l"(dy + r * a.lddy)
-                   : "memory");
-    }
+  const int64_t stride = (int64_t)gridDim.x * 2;
+  const auto copy_pair = [&](int64_t r, int slot) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (live && r + q < a.R) {
+        const uint32_t to = slot0 + (slot * 2 + q) * 2 * nt * 16;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(x + (r + q) * a.ldx)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + nt * 16),
+                     "l"(dy + (r + q) * a.lddy)
+                     : "memory");
+      }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  const int64_t first = (int64_t)blockIdx.x * 2;
 #pragma unroll
-  for (int i = 0; i < kBwdSteps; ++i) copy_row(blockIdx.x + (int64_t)i * gridDim.x, i);
+  for (int i = 0; i < D; ++i) copy_pair(first + i * stride, i);
   int slot = 0, side = 0;
-  float mu = 0.0f, rs = 0.0f;
-  if (blockIdx.x < a.R) {
-    mu = a.mean[blockIdx.x];
-    rs = a.rstd[blockIdx.x];
-  }
-  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kBwdSteps - 1) : "memory");
-    float h[W], d[W];
-    float s1 = 0.0f, s2 = 0.0f;
-    if (live) {
-      unpack_vec<DT>(ring[slot * 2 * nt + tid], h);
-      unpack_vec<DT>(ring[(slot * 2 + 1) * nt + tid], d);
-    } else {
+  float mu[2] = {0.0f, 0.0f}, rs[2] = {0.0f, 0.0f};  // of the pair in hand
+  const auto stats = [&](int64_t r) {
 #pragma unroll
-      for (int j = 0; j < W; ++j) h[j] = d[j] = 0.0f;
-    }
-    const float this_rs = rs;
+    for (int q = 0; q < 2; ++q)
+      if (r + q < a.R) {
+        mu[q] = a.mean[r + q];
+        rs[q] = a.rstd[r + q];
+      }
+  };
+  stats(first);
+  for (int64_t r = first; r < a.R; r += stride) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    const uint4* mine = ring + slot * 4 * nt + tid;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < W; ++j) {
-      h[j] = (h[j] - mu) * rs;
-      ab[j] += d[j];
-      ag[j] = __fmaf_rn(d[j], h[j], ag[j]);
-      d[j] *= g[j];
-      s1 += d[j];
-      s2 = __fmaf_rn(d[j], h[j], s2);
-    }
-    copy_row(r + (int64_t)kBwdSteps * gridDim.x, slot);
-    slot = slot + 1 < kBwdSteps ? slot + 1 : 0;
-    const int64_t next = r + gridDim.x;
-    if (next < a.R) {
-      mu = a.mean[next];
-      rs = a.rstd[next];
-    }
-    const float2 s = row_sum2(s1, s2, red[side], warps);
-    side ^= 1;  // the other side is free: every thread has passed the barrier after its reads
-    const float c1 = s.x * inv, c2 = s.y * inv;
-    if (live) {
+    for (int q = 0; q < 2; ++q) {
+      if (!(live && r + q < a.R)) continue;
+      float h[W], d[W];
+      unpack_vec<DT>(mine[2 * q * nt], h);
+      unpack_vec<DT>(mine[(2 * q + 1) * nt], d);
 #pragma unroll
-      for (int j = 0; j < W; ++j) d[j] = this_rs * __fmaf_rn(-h[j], c2, d[j] - c1);
-      st_stream(reinterpret_cast<uint4*>(dx + r * a.lddx), pack_vec<DT>(d));
+      for (int j = 0; j < W; ++j) {
+        h[j] = (h[j] - mu[q]) * rs[q];
+        ab[j] += d[j];
+        ag[j] = __fmaf_rn(d[j], h[j], ag[j]);
+        d[j] *= g[j];
+        s[2 * q] += d[j];
+        s[2 * q + 1] = __fmaf_rn(d[j], h[j], s[2 * q + 1]);
+      }
     }
+    float t = warp_sum4(s, lane);
+    if (warps > 1) {
+      if ((lane & 7) == 0) part[side * 128 + (lane >> 3) * 32 + warp] = t;
+      __syncthreads();
+      const float4 p = part4[side][lane];  // value lane / 8, four warps of it
+      side ^= 1;  // free again: every thread passes the next barrier after these reads
+      t = (p.x + p.y) + (p.z + p.w);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    }
+    t *= inv;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float c1 = __shfl_sync(0xFFFFFFFFu, t, 16 * q);
+      const float c2 = __shfl_sync(0xFFFFFFFFu, t, 16 * q + 8);
+      if (!(live && r + q < a.R)) continue;
+      float h[W], d[W];
+      unpack_vec<DT>(mine[2 * q * nt], h);
+      unpack_vec<DT>(mine[(2 * q + 1) * nt], d);
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        h[j] = (h[j] - mu[q]) * rs[q];
+        d[j] = rs[q] * __fmaf_rn(-h[j], c2, __fmaf_rn(d[j], g[j], -c1));
+      }
+      st_stream(reinterpret_cast<uint4*>(dx + (r + q) * a.lddx), pack_vec<DT>(d));
+    }
+    copy_pair(r + D * stride, slot);
+    slot = slot + 1 < D ? slot + 1 : 0;
+    stats(r + stride);
   }
   asm volatile("griddepcontrol.launch_dependents;");  // the join may take this SM next
   if (a.ws && live) {
@@ -577,8 +764,8 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
                    a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0;
   if (vec && a.C <= 1024 * V) {
     const NormBwdPlan p = bwd_plan(a.R, a.C, V);
-    const auto smem = [](int threads) { return kBwdSteps * 2 * threads * 16; };
-    const auto kernel = layernorm_bwd_vec_kernel<DT, WT>;
+    const auto smem = [](int threads) { return kBwdGroups * 4 * threads * 16; };
+    const auto kernel = layernorm_bwd_ring_kernel<DT, WT>;
     int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
     const cudaError_t e =
         kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
