@@ -72,6 +72,33 @@ __device__ __forceinline__ uint4 pack_vec(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 16 bytes of elements as pairs of fp32 for the packed operations.
+template <int DT>
+__device__ __forceinline__ void unpack_pairs(const uint4& v, uint64_t* p) {
+  float f[kVecElems<DT>];
+  unpack_vec<DT>(v, f);
+#pragma unroll
+  for (int i = 0; i < kVecElems<DT> / 2; ++i) p[i] = pk_f32x2(f[2 * i], f[2 * i + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack_pairs(const uint64_t* p) {
+  float f[kVecElems<DT>];
+#pragma unroll
+  for (int i = 0; i < kVecElems<DT> / 2; ++i) upk_f32x2(p[i], f[2 * i], f[2 * i + 1]);
+  return pack_vec<DT>(f);
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float f) { return pk_f32x2(f, f); }
+__device__ __forceinline__ float sum_of(uint64_t p) {
+  float lo, hi;
+  upk_f32x2(p, lo, hi);
+  return lo + hi;
+}
+
 // W weights from column c; `missing` where there are none.  `vec`: the array
 // is 16-byte aligned.
 template <int WT, int W>
@@ -230,12 +257,18 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   const bool live = c < a.C;
   const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
   typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + c;
-  float g[W], b[W];
+  constexpr int P = W / 2;  // pairs of columns
+  uint64_t g[P], b[P];
 #pragma unroll
-  for (int j = 0; j < W; ++j) g[j] = b[j] = 0.0f;
+  for (int j = 0; j < P; ++j) g[j] = b[j] = 0;
   if (live) {
-    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
-    load_weights<WT, W>(a.beta, c, a.w_vec, 0.0f, b);
+    float f[W];
+    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, f);
+#pragma unroll
+    for (int j = 0; j < P; ++j) g[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
+    load_weights<WT, W>(a.beta, c, a.w_vec, 0.0f, f);
+#pragma unroll
+    for (int j = 0; j < P; ++j) b[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
   }
   // columns of this warp and of warp i
   const auto columns = [&](int i) {
@@ -249,51 +282,57 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   const float n0 = columns(w0), n1 = columns(w0 + 1);
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
-  const int64_t stride = (int64_t)gridDim.x * 2;
-  const auto copy_pair = [&](int64_t r, int slot) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if (live && r + q < a.R)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot0 +
-                                                                       (slot * 2 + q) * nt * 16),
-                     "l"(x + (r + q) * a.ldx)
-                     : "memory");
+  const int64_t stride = (int64_t)gridDim.x * 2, first = (int64_t)blockIdx.x * 2;
+  // the rows left from the pair to copy next, and from the pair in hand
+  int64_t ahead = a.R - first, rows = a.R - first;
+  const typename Elem<DT>::type* from = x + first * a.ldx;
+  typename Elem<DT>::type* to = y + first * a.ldy;
+  const auto copy_pair = [&](int slot) {
+    const uint32_t at = slot0 + slot * 2 * nt * 16;
+    if (live && ahead > 0)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    if (live && ahead > 1)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 16),
+                   "l"(from + a.ldx)
+                   : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead -= stride;
+    from += stride * a.ldx;
   };
-  const int64_t first = (int64_t)blockIdx.x * 2;
 #pragma unroll
-  for (int i = 0; i < D; ++i) copy_pair(first + i * stride, i);
+  for (int i = 0; i < D; ++i) copy_pair(i);
   int slot = 0, side = 0;
-  for (int64_t r = first; r < a.R; r += stride) {
+  for (; rows > 0; rows -= stride, to += stride * a.ldy) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    float f[2][W], s[2], q[2];
+    uint64_t f[2][P];
+    float s[2], q[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (live && r + i < a.R) {
-        unpack_vec<DT>(ring[(slot * 2 + i) * nt + tid], f[i]);
+      if (live && rows > i) {
+        unpack_pairs<DT>(ring[(slot * 2 + i) * nt + tid], f[i]);
       } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[i][j] = 0.0f;
+        for (int j = 0; j < P; ++j) f[i][j] = 0;
       }
-      s[i] = 0.0f;
+      uint64_t t = f[i][0];
 #pragma unroll
-      for (int j = 0; j < W; ++j) s[i] += f[i][j];
+      for (int j = 1; j < P; ++j) t = add_f32x2(t, f[i][j]);
+      s[i] = sum_of(t);
     }
-    copy_pair(r + D * stride, slot);
+    copy_pair(slot);
     slot = slot + 1 < D ? slot + 1 : 0;
     // this warp's means, and the deviations from them
     const float ws = warp_sum2(s[0], s[1], lane) * inv_warp;
     const float wm[2] = {__shfl_sync(0xFFFFFFFFu, ws, 0), __shfl_sync(0xFFFFFFFFu, ws, 16)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      q[i] = 0.0f;
-      if (live) {
+      uint64_t t = 0;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          f[i][j] -= wm[i];
-          q[i] = __fmaf_rn(f[i][j], f[i][j], q[i]);
-        }
+      for (int j = 0; j < P; ++j) {
+        f[i][j] = add_f32x2(f[i][j], both(-wm[i]));
+        t = fma_f32x2(f[i][j], f[i][j], t);
       }
+      q[i] = live ? sum_of(t) : 0.0f;
     }
     const float wq = warp_sum2(q[0], q[1], lane);
     float mu, var;  // of row `pair` of the two, in this lane
@@ -318,19 +357,21 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
       var = wq * inv;
     }
     const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-    if (warp == 0 && (lane & 15) == 0 && r + pair < a.R) {
-      if (a.mean) a.mean[r + pair] = mu;
-      if (a.rstd) a.rstd[r + pair] = rs;
+    if (warp == 0 && (lane & 15) == 0 && rows > pair) {
+      if (a.mean) a.mean[a.R - rows + pair] = mu;
+      if (a.rstd) a.rstd[a.R - rows + pair] = rs;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float shift = wm[i] - __shfl_sync(0xFFFFFFFFu, mu, 16 * i);
       const float scale = __shfl_sync(0xFFFFFFFFu, rs, 16 * i);
-      if (live && r + i < a.R) {
+      const float shift = (wm[i] - __shfl_sync(0xFFFFFFFFu, mu, 16 * i)) * scale;
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[i][j] = __fmaf_rn((f[i][j] + shift) * scale, g[j], b[j]);
-        st_stream(reinterpret_cast<uint4*>(y + (r + i) * a.ldy), pack_vec<DT>(f[i]));
-      }
+      for (int j = 0; j < P; ++j)
+        f[i][j] = fma_f32x2(fma_f32x2(f[i][j], both(scale), both(shift)), g[j], b[j]);
+    }
+    if (live) {
+      st_stream(reinterpret_cast<uint4*>(to), pack_pairs<DT>(f[0]));
+      if (rows > 1) st_stream(reinterpret_cast<uint4*>(to + a.ldy), pack_pairs<DT>(f[1]));
     }
   }
 }
@@ -484,68 +525,88 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
   extern __shared__ uint4 ring[];  // [D][2][x, dy][blockDim.x]
   __shared__ float4 part4[2][32];  // per value of the pair's four: eight warps' sums a float4
   float* const part = reinterpret_cast<float*>(part4);  // [2][4][32]
+  __shared__ float4 stats[D][32];  // a pair's means and rstd, one copy per warp
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
   const int c = tid * W;
   const bool live = c < a.C;
   const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
   const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy) + c;
   typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx) + c;
-  float g[W], ag[W], ab[W];
+  constexpr int P = W / 2;  // pairs of columns
+  uint64_t g[P], ag[P], ab[P];
 #pragma unroll
-  for (int j = 0; j < W; ++j) g[j] = ag[j] = ab[j] = 0.0f;
-  if (live) load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, g);
+  for (int j = 0; j < P; ++j) g[j] = ag[j] = ab[j] = 0;
+  if (live) {
+    float f[W];
+    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, f);
+#pragma unroll
+    for (int j = 0; j < P; ++j) g[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
+  }
   const float inv = __fdiv_rn(1.0f, (float)a.C);
   for (int i = tid; i < 256; i += nt) part[i] = 0.0f;  // of warps that do not exist
   __syncthreads();
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
-  const int64_t stride = (int64_t)gridDim.x * 2;
-  const auto copy_pair = [&](int64_t r, int slot) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if (live && r + q < a.R) {
-        const uint32_t to = slot0 + (slot * 2 + q) * 2 * nt * 16;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(x + (r + q) * a.ldx)
-                     : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + nt * 16),
-                     "l"(dy + (r + q) * a.lddy)
-                     : "memory");
-      }
+  const uint32_t stat0 = (uint32_t)__cvta_generic_to_shared(&stats[0][warp]);
+  const int64_t stride = (int64_t)gridDim.x * 2, first = (int64_t)blockIdx.x * 2;
+  // the rows left from the pair to copy next, and from the pair in hand
+  int64_t ahead = a.R - first, rows = a.R - first;
+  const typename Elem<DT>::type* from_x = x + first * a.ldx;
+  const typename Elem<DT>::type* from_dy = dy + first * a.lddy;
+  typename Elem<DT>::type* to_dx = dx + first * a.lddx;
+  const auto copy_pair = [&](int slot) {
+    const uint32_t at = slot0 + slot * 4 * nt * 16;
+    if (live && ahead > 0) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from_x) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 16), "l"(from_dy)
+                   : "memory");
+    }
+    if (live && ahead > 1) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 32),
+                   "l"(from_x + a.ldx)
+                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 48),
+                   "l"(from_dy + a.lddy)
+                   : "memory");
+    }
+    // the rows' statistics, for the warp: lanes 0, 1 the means, 2, 3 rstd
+    if (lane < 4 && ahead > (lane & 1))
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stat0 + slot * 512 + lane * 4),
+                   "l"((lane < 2 ? a.mean : a.rstd) + (a.R - ahead) + (lane & 1))
+                   : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead -= stride;
+    from_x += stride * a.ldx;
+    from_dy += stride * a.lddy;
   };
-  const int64_t first = (int64_t)blockIdx.x * 2;
 #pragma unroll
-  for (int i = 0; i < D; ++i) copy_pair(first + i * stride, i);
+  for (int i = 0; i < D; ++i) copy_pair(i);
   int slot = 0, side = 0;
-  float mu[2] = {0.0f, 0.0f}, rs[2] = {0.0f, 0.0f};  // of the pair in hand
-  const auto stats = [&](int64_t r) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      if (r + q < a.R) {
-        mu[q] = a.mean[r + q];
-        rs[q] = a.rstd[r + q];
-      }
-  };
-  stats(first);
-  for (int64_t r = first; r < a.R; r += stride) {
+  for (; rows > 0; rows -= stride, to_dx += stride * a.lddx) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    __syncwarp();  // the statistics are other lanes' copies
+    const float4 st = stats[slot][warp];
+    const float mu[2] = {st.x, st.y}, rs[2] = {st.z, st.w};
     const uint4* mine = ring + slot * 4 * nt + tid;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      if (!(live && r + q < a.R)) continue;
-      float h[W], d[W];
-      unpack_vec<DT>(mine[2 * q * nt], h);
-      unpack_vec<DT>(mine[(2 * q + 1) * nt], d);
+      if (!(live && rows > q)) continue;
+      uint64_t h[P], d[P], s1 = 0, s2 = 0;
+      unpack_pairs<DT>(mine[2 * q * nt], h);
+      unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
+      const uint64_t scale = both(rs[q]), shift = both(-mu[q] * rs[q]);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        h[j] = (h[j] - mu[q]) * rs[q];
-        ab[j] += d[j];
-        ag[j] = __fmaf_rn(d[j], h[j], ag[j]);
-        d[j] *= g[j];
-        s[2 * q] += d[j];
-        s[2 * q + 1] = __fmaf_rn(d[j], h[j], s[2 * q + 1]);
+      for (int j = 0; j < P; ++j) {
+        h[j] = fma_f32x2(h[j], scale, shift);
+        ab[j] = add_f32x2(ab[j], d[j]);
+        ag[j] = fma_f32x2(d[j], h[j], ag[j]);
+        d[j] = mul_f32x2(d[j], g[j]);
+        s1 = add_f32x2(s1, d[j]);
+        s2 = fma_f32x2(d[j], h[j], s2);
       }
+      s[2 * q] = sum_of(s1);
+      s[2 * q + 1] = sum_of(s2);
     }
     float t = warp_sum4(s, lane);
     if (warps > 1) {
@@ -562,29 +623,30 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
     for (int q = 0; q < 2; ++q) {
       const float c1 = __shfl_sync(0xFFFFFFFFu, t, 16 * q);
       const float c2 = __shfl_sync(0xFFFFFFFFu, t, 16 * q + 8);
-      if (!(live && r + q < a.R)) continue;
-      float h[W], d[W];
-      unpack_vec<DT>(mine[2 * q * nt], h);
-      unpack_vec<DT>(mine[(2 * q + 1) * nt], d);
+      if (!(live && rows > q)) continue;
+      uint64_t h[P], d[P];
+      unpack_pairs<DT>(mine[2 * q * nt], h);
+      unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
+      const uint64_t scale = both(rs[q]), shift = both(-mu[q] * rs[q]);
+      const uint64_t n1 = both(-c1), n2 = both(-c2);
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        h[j] = (h[j] - mu[q]) * rs[q];
-        d[j] = rs[q] * __fmaf_rn(-h[j], c2, __fmaf_rn(d[j], g[j], -c1));
+      for (int j = 0; j < P; ++j) {
+        h[j] = fma_f32x2(h[j], scale, shift);
+        d[j] = mul_f32x2(fma_f32x2(h[j], n2, fma_f32x2(d[j], g[j], n1)), scale);
       }
-      st_stream(reinterpret_cast<uint4*>(dx + (r + q) * a.lddx), pack_vec<DT>(d));
+      st_stream(reinterpret_cast<uint4*>(to_dx + (q ? a.lddx : 0)), pack_pairs<DT>(d));
     }
-    copy_pair(r + D * stride, slot);
+    copy_pair(slot);
     slot = slot + 1 < D ? slot + 1 : 0;
-    stats(r + stride);
   }
   asm volatile("griddepcontrol.launch_dependents;");  // the join may take this SM next
   if (a.ws && live) {
     float* pg = a.ws + (int64_t)blockIdx.x * a.C + c;
     float* pb = pg + (int64_t)gridDim.x * a.C;
 #pragma unroll
-    for (int j = 0; j < W; j += 4) {  // C is a multiple of 4: the rows of ws are aligned
-      *reinterpret_cast<float4*>(pg + j) = make_float4(ag[j], ag[j + 1], ag[j + 2], ag[j + 3]);
-      *reinterpret_cast<float4*>(pb + j) = make_float4(ab[j], ab[j + 1], ab[j + 2], ab[j + 3]);
+    for (int j = 0; j < P; j += 2) {  // C is a multiple of 4: the rows of ws are aligned
+      *reinterpret_cast<ulonglong2*>(pg + 2 * j) = make_ulonglong2(ag[j], ag[j + 1]);
+      *reinterpret_cast<ulonglong2*>(pb + 2 * j) = make_ulonglong2(ab[j], ab[j + 1]);
     }
   }
 }
