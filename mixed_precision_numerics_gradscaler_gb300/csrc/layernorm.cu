@@ -218,8 +218,9 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 // Thread t owns vector t of every row (its weights stay in registers) and
 // copies its part of the next rows into shared memory itself (cp.async), so
 // that no thread waits for another's copy and the memory stays busy across
-// the barriers.  Two rows share a barrier: the sums' latency, some 800 cycles
-// of shuffles and barrier, would take half the time of a row otherwise.
+// the barriers.  Two rows (backward) or four (forward) share a barrier: the
+// sums' latency, some 800 cycles of shuffles and barrier, would take half the
+// time of a row otherwise.
 // 1024 threads per SM with 64 registers each, one CTA of them for the widest
 // rows, up to 32 for the narrowest.
 
@@ -234,30 +235,21 @@ __device__ __forceinline__ float warp_sum4(const float* s, int lane) {
   for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-// Sums of two values: lane 16 q and its neighbours return the sum of s[q].
-__device__ __forceinline__ float warp_sum2(float s0, float s1, int lane) {
-  const bool hi = lane & 16;
-  float v = (hi ? s1 : s0) + __shfl_xor_sync(0xFFFFFFFFu, hi ? s0 : s1, 16);
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
-
-constexpr int kRingRows = 2;  // rows that share a barrier
-constexpr int kFwdGroups = 4, kBwdGroups = 3;  // pairs of rows in the ring
+constexpr int kFwdRows = 4, kFwdGroups = 3;  // forward: rows that share a barrier, groups in the ring
+constexpr int kBwdGroups = 3;                // backward: pairs of rows in the ring
 
 template <int DT, int WT>
 __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormArgs a) {
-  constexpr int W = kVecElems<DT>, D = kFwdGroups;
-  extern __shared__ uint4 ring[];  // [D][2][blockDim.x]
-  // per row of the pair: the warps' means and squared deviations from them
-  __shared__ float2 part[2][2][32];
+  constexpr int W = kVecElems<DT>, P = W / 2, D = kFwdGroups, Q = kFwdRows;
+  static_assert(Q == 4, "the joins below are of four rows");
+  extern __shared__ uint4 ring[];  // [D][Q][blockDim.x]
+  // per row of the group: the warps' means, and their squared deviations
+  __shared__ float4 part_mean[2][Q][8], part_dev[2][Q][8];
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const int c = tid * W;
+  const int c = tid * W, row8 = lane >> 3;  // the group's row that this lane joins
   const bool live = c < a.C;
   const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
   typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + c;
-  constexpr int P = W / 2;  // pairs of columns
   uint64_t g[P], b[P];
 #pragma unroll
   for (int j = 0; j < P; ++j) g[j] = b[j] = 0;
@@ -270,109 +262,162 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
 #pragma unroll
     for (int j = 0; j < P; ++j) b[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
   }
-  // columns of this warp and of warp i
+  // columns of warp i
   const auto columns = [&](int i) {
     const int n = (int)a.C - i * 32 * W;
     return (float)(n < 0 ? 0 : n < 32 * W ? n : 32 * W);
   };
   const float inv = __fdiv_rn(1.0f, (float)a.C);
   const float inv_warp = __fdiv_rn(1.0f, fmaxf(columns(warp), 1.0f));
-  // the two warps whose partial sums this lane joins, and their columns
-  const int w0 = (lane & 15) * 2, pair = lane >> 4;
-  const float n0 = columns(w0), n1 = columns(w0 + 1);
+  for (int i = tid; i < 2 * Q * 8; i += nt)  // of warps that do not exist
+    (&part_mean[0][0][0])[i] = (&part_dev[0][0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  __syncthreads();
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
-  const int64_t stride = (int64_t)gridDim.x * 2, first = (int64_t)blockIdx.x * 2;
-  // the rows left from the pair to copy next, and from the pair in hand
+  const int64_t stride = (int64_t)gridDim.x * Q, first = (int64_t)blockIdx.x * Q;
+  // the rows left from the group to copy next, and from the group in hand
   int64_t ahead = a.R - first, rows = a.R - first;
   const typename Elem<DT>::type* from = x + first * a.ldx;
   typename Elem<DT>::type* to = y + first * a.ldy;
-  const auto copy_pair = [&](int slot) {
-    const uint32_t at = slot0 + slot * 2 * nt * 16;
-    if (live && ahead > 0)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
-    if (live && ahead > 1)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 16),
-                   "l"(from + a.ldx)
-                   : "memory");
+  const auto copy_group = [&](int slot) {
+    const uint32_t at = slot0 + slot * Q * nt * 16;
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      if (live && ahead > i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * nt * 16),
+                     "l"(from + i * a.ldx)
+                     : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead -= stride;
     from += stride * a.ldx;
   };
 #pragma unroll
-  for (int i = 0; i < D; ++i) copy_pair(i);
+  for (int i = 0; i < D; ++i) copy_group(i);
   int slot = 0, side = 0;
   for (; rows > 0; rows -= stride, to += stride * a.ldy) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    uint64_t f[2][P];
-    float s[2], q[2];
+    uint4 raw[Q];
+    float s[Q];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (live && rows > i) {
-        unpack_pairs<DT>(ring[(slot * 2 + i) * nt + tid], f[i]);
-      } else {
+    for (int i = 0; i < Q; ++i) {
+      raw[i] = live && rows > i ? ring[(slot * Q + i) * nt + tid] : make_uint4(0, 0, 0, 0);
+      uint64_t f[P];
+      unpack_pairs<DT>(raw[i], f);
 #pragma unroll
-        for (int j = 0; j < P; ++j) f[i][j] = 0;
-      }
-      uint64_t t = f[i][0];
-#pragma unroll
-      for (int j = 1; j < P; ++j) t = add_f32x2(t, f[i][j]);
-      s[i] = sum_of(t);
+      for (int j = 1; j < P; ++j) f[0] = add_f32x2(f[0], f[j]);
+      s[i] = sum_of(f[0]);
     }
-    copy_pair(slot);
+    copy_group(slot);
     slot = slot + 1 < D ? slot + 1 : 0;
-    // this warp's means, and the deviations from them
-    const float ws = warp_sum2(s[0], s[1], lane) * inv_warp;
-    const float wm[2] = {__shfl_sync(0xFFFFFFFFu, ws, 0), __shfl_sync(0xFFFFFFFFu, ws, 16)};
+    // this warp's means, and the squared deviations from them
+    const float wm = warp_sum4(s, lane) * inv_warp;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint64_t t = 0;
+    for (int i = 0; i < Q; ++i) {
+      const uint64_t m2 = both(-__shfl_sync(0xFFFFFFFFu, wm, 8 * i));
+      uint64_t f[P], t = 0;
+      unpack_pairs<DT>(raw[i], f);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        f[i][j] = add_f32x2(f[i][j], both(-wm[i]));
-        t = fma_f32x2(f[i][j], f[i][j], t);
+        f[j] = add_f32x2(f[j], m2);
+        t = fma_f32x2(f[j], f[j], t);
       }
-      q[i] = live ? sum_of(t) : 0.0f;
+      s[i] = live ? sum_of(t) : 0.0f;
     }
-    const float wq = warp_sum2(q[0], q[1], lane);
-    float mu, var;  // of row `pair` of the two, in this lane
+    const float wq = warp_sum4(s, lane);
+    float mu, var;  // of row `row8` of the group, in this lane
     if (warps > 1) {
-      if ((lane & 15) == 0) part[side][pair][warp] = make_float2(ws, wq);
+      if ((lane & 7) == 0) {
+        reinterpret_cast<float*>(part_mean[side][row8])[warp] = wm;
+        reinterpret_cast<float*>(part_dev[side][row8])[warp] = wq;
+      }
       __syncthreads();
-      const float2 none = make_float2(0.0f, 0.0f);
-      const float2 p0 = w0 < warps ? part[side][pair][w0] : none;
-      const float2 p1 = w0 + 1 < warps ? part[side][pair][w0 + 1] : none;
+      const float4 m = part_mean[side][row8][lane & 7], q = part_dev[side][row8][lane & 7];
       side ^= 1;  // free again: every thread passes the next barrier after these reads
-      float t = __fmaf_rn(n0, p0.x, n1 * p1.x);
+      // four warps' sums, each with its columns (fewer in the last one)
+      const int w0 = (lane & 7) * 4;
+      const float n0 = columns(w0), n1 = columns(w0 + 1), n2 = columns(w0 + 2), n3 = columns(w0 + 3);
+      float t = __fmaf_rn(n0, m.x, n1 * m.y) + __fmaf_rn(n2, m.z, n3 * m.w);
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       mu = t * inv;
-      const float d0 = p0.x - mu, d1 = p1.x - mu;
-      t = __fmaf_rn(n0 * d0, d0, p0.y) + __fmaf_rn(n1 * d1, d1, p1.y);
+      const float d0 = m.x - mu, d1 = m.y - mu, d2 = m.z - mu, d3 = m.w - mu;
+      t = (__fmaf_rn(n0 * d0, d0, q.x) + __fmaf_rn(n1 * d1, d1, q.y)) +
+          (__fmaf_rn(n2 * d2, d2, q.z) + __fmaf_rn(n3 * d3, d3, q.w));
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+      for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       var = t * inv;
     } else {
-      mu = ws;
+      mu = wm;
       var = wq * inv;
     }
     const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-    if (warp == 0 && (lane & 15) == 0 && rows > pair) {
-      if (a.mean) a.mean[a.R - rows + pair] = mu;
-      if (a.rstd) a.rstd[a.R - rows + pair] = rs;
+    if (warp == 0 && (lane & 7) == 0 && rows > row8) {
+      if (a.mean) a.mean[a.R - rows + row8] = mu;
+      if (a.rstd) a.rstd[a.R - rows + row8] = rs;
     }
+    const float shift = -mu * rs;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float scale = __shfl_sync(0xFFFFFFFFu, rs, 16 * i);
-      const float shift = (wm[i] - __shfl_sync(0xFFFFFFFFu, mu, 16 * i)) * scale;
+    for (int i = 0; i < Q; ++i) {
+      const uint64_t scale2 = both(__shfl_sync(0xFFFFFFFFu, rs, 8 * i));
+      const uint64_t shift2 = both(__shfl_sync(0xFFFFFFFFu, shift, 8 * i));
+      uint64_t f[P];
+      unpack_pairs<DT>(raw[i], f);
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-        f[i][j] = fma_f32x2(fma_f32x2(f[i][j], both(scale), both(shift)), g[j], b[j]);
+      for (int j = 0; j < P; ++j) f[j] = fma_f32x2(fma_f32x2(f[j], scale2, shift2), g[j], b[j]);
+      if (live && rows > i) st_stream(reinterpret_cast<uint4*>(to + i * a.ldy), pack_pairs<DT>(f));
     }
-    if (live) {
-      st_stream(reinterpret_cast<uint4*>(to), pack_pairs<DT>(f[0]));
-      if (rows > 1) st_stream(reinterpret_cast<uint4*>(to + a.ldy), pack_pairs<DT>(f[1]));
+  }
+}
+
+// Rows of any alignment, element by element: thread t of a CTA just wide
+// enough holds columns t + i blockDim.x.
+template <int DT, int WT, int EPT>
+__global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs a) {
+  __shared__ float red[2][32];
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
+  const int64_t r = blockIdx.x;
+  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ldx;
+  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + r * a.ldy;
+  const auto row_sum = [&](float v, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (warps > 1) {
+      const int lane = tid & 31;
+      if (lane == 0) part[tid >> 5] = v;
+      __syncthreads();
+      v = lane < warps ? part[lane] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     }
+    return v;
+  };
+  float f[EPT], s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) f[i] = tid + i * nt < C ? Elem<DT>::get(x[tid + i * nt]) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) s += f[i];
+  const float inv = __fdiv_rn(1.0f, (float)C), mu = row_sum(s, red[0]) * inv;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i)
+    if (tid + i * nt < C) {
+      f[i] -= mu;
+      s = __fmaf_rn(f[i], f[i], s);
+    }
+  const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(row_sum(s, red[1]), inv, a.eps)));
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    const int c = tid + i * nt;
+    if (c < C) {
+      float g, b;
+      load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g);
+      load_weights<WT, 1>(a.beta, c, false, 0.0f, &b);
+      y[c] = Elem<DT>::put(__fmaf_rn(f[i] * rs, g, b));
+    }
+  }
+  if (tid == 0) {
+    if (a.mean) a.mean[r] = mu;
+    if (a.rstd) a.rstd[r] = rs;
   }
 }
 
@@ -417,8 +462,8 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
       <<<NT == 32 ? warps : rows, NT == 32 ? 256 : NT, 0, stream>>>(a)
   const int threads = (int)((a.C / V + 31) / 32 * 32);
   const int64_t ctas = (int64_t)sm_count() * (threads <= 1024 ? 1024 / std::max(threads, 32) : 0);
-  if (vec && ctas > 0 && a.R >= ctas * 2 * kRingRows) {
-    const auto smem = [](int n) { return kFwdGroups * 2 * n * 16; };
+  if (DT != GS_F32 && vec && ctas > 0 && a.R >= ctas * kFwdRows) {
+    const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
     const auto kernel = layernorm_fwd_ring_kernel<DT, WT>;
     int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
     const cudaError_t e =
@@ -435,10 +480,13 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
     else if (nv <= 4096) GS_L(V, 1024, 4);
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   } else {
+    // a warp per row up to 128 columns, then CTAs of eight columns per thread
+    const auto width = [&](int each) { return (unsigned)((a.C + each * 32 - 1) / (each * 32) * 32); };
     if (a.C <= 128) GS_L(1, 32, 4);
-    else if (a.C <= 1024) GS_L(1, 256, 4);
-    else if (a.C <= 4096) GS_L(1, 512, 8);
-    else if (a.C <= 16384) GS_L(1, 1024, 16);
+    else if (a.C <= 8192)
+      layernorm_fwd_elem_kernel<DT, WT, 8><<<rows, width(8), 0, stream>>>(a);
+    else if (a.C <= 16384)
+      layernorm_fwd_elem_kernel<DT, WT, 16><<<rows, width(16), 0, stream>>>(a);
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   }
 #undef GS_L
@@ -652,8 +700,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
 }
 
 // Rows of any alignment, element by element: thread t owns columns t + i nt.
-// The next row's elements are loaded before this row's barrier.
-template <int DT, int WT, int EPT>
+// The next rows' elements are loaded before this row's barrier.
+template <int DT, int WT, int EPT, int AHEAD>
 __global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
   __shared__ float2 red[2][32];
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
@@ -661,7 +709,9 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormB
   const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy);
   typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx);
   float g[EPT], ag[EPT], ab[EPT];
-  typename Elem<DT>::type nx[EPT], nd[EPT];
+  // the rows ahead: AHEAD of them, by turns
+  typename Elem<DT>::type nx[AHEAD][EPT], nd[AHEAD][EPT];
+  float nmu[AHEAD], nrs[AHEAD];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = tid + i * nt;
@@ -670,48 +720,54 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormB
     if (c < C) load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g[i]);
   }
   const float inv = __fdiv_rn(1.0f, (float)C);
-  const auto fetch = [&](int64_t r) {
+  const auto fetch = [&](int64_t r, typename Elem<DT>::type* px, typename Elem<DT>::type* pd,
+                         float& mu, float& rs) {
+    if (r >= a.R) return;
+    const typename Elem<DT>::type* rx = x + r * a.ldx + tid;
+    const typename Elem<DT>::type* rd = dy + r * a.lddy + tid;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = tid + i * nt;
-      nx[i] = c < C ? x[r * a.ldx + c] : 0;
-      nd[i] = c < C ? dy[r * a.lddy + c] : 0;
-    }
+    for (int i = 0; i < EPT; ++i)
+      if (tid + i * nt < C) {
+        px[i] = rx[i * nt];
+        pd[i] = rd[i * nt];
+      }
+    mu = a.mean[r];
+    rs = a.rstd[r];
   };
-  float mu = 0.0f, rs = 0.0f;
-  int side = 0;
-  if (blockIdx.x < a.R) {
-    fetch(blockIdx.x);
-    mu = a.mean[blockIdx.x];
-    rs = a.rstd[blockIdx.x];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) nx[k][i] = nd[k][i] = 0;
+    fetch(blockIdx.x + (int64_t)k * gridDim.x, nx[k], nd[k], nmu[k], nrs[k]);
   }
-  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    float h[EPT], d[EPT];
-    float s1 = 0.0f, s2 = 0.0f;
+  int side = 0;
+  for (int64_t r0 = blockIdx.x; r0 < a.R; r0 += (int64_t)AHEAD * gridDim.x) {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      h[i] = tid + i * nt < C ? (Elem<DT>::get(nx[i]) - mu) * rs : 0.0f;
-      d[i] = Elem<DT>::get(nd[i]);
-      ab[i] += d[i];
-      ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
-      d[i] *= g[i];
-      s1 += d[i];
-      s2 = __fmaf_rn(d[i], h[i], s2);
-    }
-    const float this_rs = rs;
-    const int64_t next = r + gridDim.x;
-    if (next < a.R) {
-      fetch(next);
-      mu = a.mean[next];
-      rs = a.rstd[next];
-    }
-    const float2 s = row_sum2(s1, s2, red[side], warps);
-    side ^= 1;
-    const float c1 = s.x * inv, c2 = s.y * inv;
+    for (int k = 0; k < AHEAD; ++k) {
+      const int64_t r = r0 + (int64_t)k * gridDim.x;
+      if (r >= a.R) break;  // the same for the CTA
+      const float mu = nmu[k], rs = nrs[k];
+      float h[EPT], d[EPT];
+      float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const int c = tid + i * nt;
-      if (c < C) dx[r * a.lddx + c] = Elem<DT>::put(this_rs * __fmaf_rn(-h[i], c2, d[i] - c1));
+      for (int i = 0; i < EPT; ++i) {
+        h[i] = tid + i * nt < C ? (Elem<DT>::get(nx[k][i]) - mu) * rs : 0.0f;
+        d[i] = Elem<DT>::get(nd[k][i]);
+        ab[i] += d[i];
+        ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
+        d[i] *= g[i];
+        s1 += d[i];
+        s2 = __fmaf_rn(d[i], h[i], s2);
+      }
+      fetch(r + (int64_t)AHEAD * gridDim.x, nx[k], nd[k], nmu[k], nrs[k]);
+      const float2 s = row_sum2(s1, s2, red[side], warps);
+      side ^= 1;
+      const float c1 = s.x * inv, c2 = s.y * inv;
+      typename Elem<DT>::type* out = dx + r * a.lddx + tid;
+#pragma unroll
+      for (int i = 0; i < EPT; ++i)
+        if (tid + i * nt < C)
+          out[i * nt] = Elem<DT>::put(rs * __fmaf_rn(-h[i], c2, d[i] - c1));
     }
   }
   if (a.ws) {
@@ -838,9 +894,9 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
     const bool few = a.C <= 1024 * 4;
     const NormBwdPlan p = bwd_plan(a.R, a.C, few ? 4 : 8);
     if (few)
-      layernorm_bwd_elem_kernel<DT, WT, 4><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, 4, 2><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
     else
-      layernorm_bwd_elem_kernel<DT, WT, 8><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, 8, 1><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
     *partials = p.ctas;
   } else {
     const int64_t most = (int64_t)1 << 30;
