@@ -370,19 +370,27 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
 }
 
 // Rows of any alignment, element by element: thread t of a CTA just wide
-// enough holds columns t + i blockDim.x.
+// enough holds columns t + i blockDim.x, their weights for all of the CTA's
+// rows.
 template <int DT, int WT, int EPT>
 __global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs a) {
-  __shared__ float red[2][32];
-  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
-  const int64_t r = blockIdx.x;
-  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ldx;
-  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + r * a.ldy;
+  __shared__ float red[2][2][32];
+  const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, lane = tid & 31;
+  const int left = (int)a.C - tid;  // columns i with i nt < left are this thread's
+  const float inv = __fdiv_rn(1.0f, (float)a.C);
+  float g[EPT], b[EPT];
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) {
+    g[i] = b[i] = 0.0f;
+    if (i * nt < left) {
+      load_weights<WT, 1>(a.gamma, tid + i * nt, false, 1.0f, &g[i]);
+      load_weights<WT, 1>(a.beta, tid + i * nt, false, 0.0f, &b[i]);
+    }
+  }
   const auto row_sum = [&](float v, float* part) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     if (warps > 1) {
-      const int lane = tid & 31;
       if (lane == 0) part[tid >> 5] = v;
       __syncthreads();
       v = lane < warps ? part[lane] : 0.0f;
@@ -391,33 +399,36 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs
     }
     return v;
   };
-  float f[EPT], s = 0.0f;
+  int side = 0;
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    const typename Elem<DT>::type* x =
+        static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ldx + tid;
+    typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + r * a.ldy + tid;
+    typename Elem<DT>::type raw[EPT];
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) f[i] = tid + i * nt < C ? Elem<DT>::get(x[tid + i * nt]) : 0.0f;
+    for (int i = 0; i < EPT; ++i) raw[i] = i * nt < left ? x[i * nt] : 0;
+    float f[EPT], s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) s += f[i];
-  const float inv = __fdiv_rn(1.0f, (float)C), mu = row_sum(s, red[0]) * inv;
-  s = 0.0f;
+    for (int i = 0; i < EPT; ++i) {
+      f[i] = Elem<DT>::get(raw[i]);
+      s += f[i];
+    }
+    const float mu = row_sum(s, red[side][0]) * inv;
+    s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < EPT; ++i)
-    if (tid + i * nt < C) {
-      f[i] -= mu;
+    for (int i = 0; i < EPT; ++i) {
+      f[i] = i * nt < left ? f[i] - mu : 0.0f;
       s = __fmaf_rn(f[i], f[i], s);
     }
-  const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(row_sum(s, red[1]), inv, a.eps)));
+    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(__fmaf_rn(row_sum(s, red[side][1]), inv, a.eps)));
+    side ^= 1;  // free again: every thread passes two barriers after these reads
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    const int c = tid + i * nt;
-    if (c < C) {
-      float g, b;
-      load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g);
-      load_weights<WT, 1>(a.beta, c, false, 0.0f, &b);
-      y[c] = Elem<DT>::put(__fmaf_rn(f[i] * rs, g, b));
+    for (int i = 0; i < EPT; ++i)
+      if (i * nt < left) y[i * nt] = Elem<DT>::put(__fmaf_rn(f[i] * rs, g[i], b[i]));
+    if (tid == 0) {
+      if (a.mean) a.mean[r] = mu;
+      if (a.rstd) a.rstd[r] = rs;
     }
-  }
-  if (tid == 0) {
-    if (a.mean) a.mean[r] = mu;
-    if (a.rstd) a.rstd[r] = rs;
   }
 }
 
@@ -482,11 +493,14 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
   } else {
     // a warp per row up to 128 columns, then CTAs of eight columns per thread
     const auto width = [&](int each) { return (unsigned)((a.C + each * 32 - 1) / (each * 32) * 32); };
+    const auto some = [&](unsigned n) {  // CTAs, 8192 threads per SM: several rounds of them
+      return (unsigned)std::min<int64_t>(a.R, (int64_t)sm_count() * (8192 / n));
+    };
     if (a.C <= 128) GS_L(1, 32, 4);
     else if (a.C <= 8192)
-      layernorm_fwd_elem_kernel<DT, WT, 8><<<rows, width(8), 0, stream>>>(a);
+      layernorm_fwd_elem_kernel<DT, WT, 8><<<some(width(8)), width(8), 0, stream>>>(a);
     else if (a.C <= 16384)
-      layernorm_fwd_elem_kernel<DT, WT, 16><<<rows, width(16), 0, stream>>>(a);
+      layernorm_fwd_elem_kernel<DT, WT, 16><<<some(width(16)), width(16), 0, stream>>>(a);
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   }
 #undef GS_L
@@ -701,8 +715,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
 
 // Rows of any alignment, element by element: thread t owns columns t + i nt.
 // The next rows' elements are loaded before this row's barrier.
-template <int DT, int WT, int EPT, int AHEAD>
-__global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
+template <int DT, int WT, int EPT, int AHEAD, int NT, int CTAS>
+__global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
   __shared__ float2 red[2][32];
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
   const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x);
@@ -746,12 +760,12 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_elem_kernel(const NormB
     for (int k = 0; k < AHEAD; ++k) {
       const int64_t r = r0 + (int64_t)k * gridDim.x;
       if (r >= a.R) break;  // the same for the CTA
-      const float mu = nmu[k], rs = nrs[k];
+      const float rs = nrs[k], shift = -nmu[k] * rs;
       float h[EPT], d[EPT];
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        h[i] = tid + i * nt < C ? (Elem<DT>::get(nx[k][i]) - mu) * rs : 0.0f;
+      for (int i = 0; i < EPT; ++i) {  // (a column beyond the row has dy 0)
+        h[i] = __fmaf_rn(Elem<DT>::get(nx[k][i]), rs, shift);
         d[i] = Elem<DT>::get(nd[k][i]);
         ab[i] += d[i];
         ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
@@ -891,12 +905,19 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
     kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
     *partials = p.ctas;
   } else if (a.C <= 1024 * kElems) {
-    const bool few = a.C <= 1024 * 4;
-    const NormBwdPlan p = bwd_plan(a.R, a.C, few ? 4 : 8);
-    if (few)
-      layernorm_bwd_elem_kernel<DT, WT, 4, 2><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+    // eight columns per thread; between 2048 and 4096 four, two rows ahead (64
+    // registers hold no more)
+    const int64_t each = a.C <= 2048 || a.C > 4096 ? 8 : 4;
+    const NormBwdPlan p = bwd_plan(a.R, a.C, each);
+    if (a.C <= 2048)
+      layernorm_bwd_elem_kernel<DT, WT, 8, 1, 256, 3>
+          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+    else if (a.C <= 4096)
+      layernorm_bwd_elem_kernel<DT, WT, 4, 2, 1024, 1>
+          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
     else
-      layernorm_bwd_elem_kernel<DT, WT, 8, 1><<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, 8, 1, 1024, 1>
+          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
     *partials = p.ctas;
   } else {
     const int64_t most = (int64_t)1 << 30;
