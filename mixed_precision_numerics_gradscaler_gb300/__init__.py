@@ -119,8 +119,15 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle without the Stream object around it (3 us of a
+# call on a Grace core, more than the launch); None where torch has no CUDA.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -462,20 +469,21 @@ def fp8_gemm_block_scaled(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, 
            "fp8_gemm_block_scaled")
 
 
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+def _rows(t: torch.Tensor, name: str, shape=None) -> int:
     """The distance of two rows of a [R, C] tensor, in elements."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    st, sh = t.stride(), t.shape
+    if len(st) != 2 or (st[1] != 1 and sh[1] > 1):
         raise ValueError(f"{name} must be [rows, columns] with adjacent columns")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    if shape is not None and sh != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return st[0] if sh[0] > 1 else max(sh[1], 1)
 
 
-def _vector(t: torch.Tensor | None, name: str, n: int, *dtypes: torch.dtype) -> int | None:
+def _vector(t: torch.Tensor | None, name: str, n: int, dtype: torch.dtype) -> int | None:
     if t is None:
         return None
-    if t.numel() != n or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of {n} elements and one of {dtypes}")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, of {n} elements and {dtype}")
     return t.data_ptr()
 
 
@@ -484,15 +492,16 @@ def gs_layernorm_fwd(x: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Te
                      rstd: torch.Tensor | None = None, eps: float = 1e-5, stream=None) -> None:
     """x, y: [R, C] of one type (rows may be apart); gamma, beta: [C], float32
     or x's type, or None; mean, rstd: float32 [R] or None."""
-    ldx, ldy = _rows(x, "x"), _rows(y, "y", x)
-    R, C = x.shape
+    shape = x.shape
+    ldx, ldy = _rows(x, "x"), _rows(y, "y", shape)
+    R, C = shape
     if y.dtype != x.dtype:
         raise ValueError("y must have the type of x")
     w = gamma if gamma is not None else beta
     wt = torch.float32 if w is None else w.dtype
-    _check(_lib.gs_layernorm_fwd(_ptr(x), ldx, _DTYPES[x.dtype], R, C,
+    _check(_lib.gs_layernorm_fwd(x.data_ptr(), ldx, _DTYPES[x.dtype], R, C,
                                  _vector(gamma, "gamma", C, wt), _vector(beta, "beta", C, wt),
-                                 _DTYPES[wt], eps, _ptr(y), ldy,
+                                 _DTYPES[wt], eps, y.data_ptr(), ldy,
                                  _vector(mean, "mean", R, torch.float32),
                                  _vector(rstd, "rstd", R, torch.float32), _stream(stream)),
            "gs_layernorm_fwd")
@@ -508,8 +517,9 @@ def gs_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | No
                      ws: torch.Tensor | None = None, stream=None) -> None:
     """dy, x, dx: [R, C] of one type; dgamma, dbeta: [C] of one type (float32,
     bfloat16 or float16) or None; ws: gs_layernorm_ws_bytes(R, C) bytes."""
-    ldx, lddy, lddx = _rows(x, "x"), _rows(dy, "dy", x), _rows(dx, "dx", x)
-    R, C = x.shape
+    shape = x.shape
+    ldx, lddy, lddx = _rows(x, "x"), _rows(dy, "dy", shape), _rows(dx, "dx", shape)
+    R, C = shape
     if dy.dtype != x.dtype or dx.dtype != x.dtype:
         raise ValueError("dy and dx must have the type of x")
     wt = torch.float32 if gamma is None else gamma.dtype
@@ -557,7 +567,7 @@ def gs_token_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
                          loss_scale: torch.Tensor | None = None, stream=None) -> None:
     """dlogits: [R, V], any of the three types, or the logits themselves; lse
     and entropy as gs_token_logprob wrote them; loss_scale: float32 [1]."""
-    ld, ld_out = _rows(logits, "logits"), _rows(dlogits, "dlogits", logits)
+    ld, ld_out = _rows(logits, "logits"), _rows(dlogits, "dlogits", logits.shape)
     R, V = logits.shape
     f32 = torch.float32
     _check(_lib.gs_token_logprob_bwd(_ptr(logits), ld, _DTYPES[logits.dtype], R, V,

@@ -366,6 +366,22 @@ __device__ __forceinline__ uint4 masked16() {
   return make_uint4(w, w, w, w);
 }
 
+// The 32 largest of the warps' sorted lists, sorted, in warp 0.  `buf` holds
+// NT values; its reads before and after are the caller's to separate by
+// barriers.
+template <int NT>
+__device__ __forceinline__ unsigned long long join_warps(unsigned long long v,
+                                                         unsigned long long* buf, int warp,
+                                                         int lane) {
+#pragma unroll
+  for (int half = NT / 64; half > 0; half >>= 1) {
+    if (warp >= half && warp < 2 * half) buf[warp * 32 + lane] = v;
+    __syncthreads();
+    if (warp < half) v = merge_desc(v, buf[(warp + half) * 32 + lane], lane);
+  }
+  return v;
+}
+
 // The CTA's top_k pairs in order in warp 0 (other warps' result is unused).
 // `nan`: this thread read a NaN or +Inf; kept: the threads' peak blocks.
 template <int DT, int NT>
@@ -373,6 +389,7 @@ __device__ __forceinline__ unsigned long long alternatives(const Run<DT>& run, c
                                                            int64_t c0, const Peak& peak, bool nan,
                                                            int top_k, const uint4* kept,
                                                            unsigned long long* cand,
+                                                           unsigned long long* shared_bound,
                                                            int* n_cand) {
   constexpr int N = kVec<DT>, kWarps = NT / 32, U = kLossVecs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -415,16 +432,24 @@ __device__ __forceinline__ unsigned long long alternatives(const Run<DT>& run, c
         if (q > first) first = q;
       }
     }
-    bound = bound_of<NT>(first, top_k, cand, warp, lane);
-    mine = first != 0 && first >= bound;
+    // (The exact k-th: in rows in order the first ones are one warp's.)
+    const unsigned long long best_first = join_warps<NT>(sort_desc(first, lane), cand, warp, lane);
+    if (warp == 0 && lane == top_k - 1) *shared_bound = best_first;
     __syncthreads();
+    bound = *shared_bound;
+    mine = first != 0 && first >= bound;
   }
   const Candidates list{cand, n_cand};
-  const bool all = mine && other >= (uint32_t)(bound >> 32);
-  const float low = key_value((uint32_t)(bound >> 32));
+  // Whether another of this thread's blocks may hold one: its maximum is above
+  // the bound's logit, or equal to it and the next block (equal ones come after
+  // the first) begins before the bound's column.
+  const uint32_t bound_key = (uint32_t)(bound >> 32), bound_col = 0xFFFFFFFFu - (uint32_t)bound;
+  const uint32_t next_col = first_col + (uint32_t)(((peak.block + 1) * U * NT + tid) * N);
+  const bool all = mine && (nan || other > bound_key || (other == bound_key && next_col <= bound_col));
+  const float low = key_value(bound_key);
   if (mine && !all) {  // the block of the maximum
-    const int64_t v = tid + peak.block * U * NT;
-#pragma unroll
+    const int v = tid + peak.block * U * NT;
+#pragma unroll 1
     for (int u = 0; u < U; ++u)
       if (v + u * NT < run.nv)
         list.offer<DT>(kept[u * NT + tid], first_col + (uint32_t)((v + u * NT) * N), bound, low);
@@ -446,13 +471,19 @@ __device__ __forceinline__ unsigned long long alternatives(const Run<DT>& run, c
   __syncthreads();
   const int n = *n_cand;
   unsigned long long best = 0;
-  if (n <= kCandidates) {
-    if (warp == 0) {
-      best = sort_desc(lane < n ? cand[lane] : 0ull, lane);
-      for (int i = 32; i < n; i += 32)
-        best = merge_desc(best, sort_desc(i + lane < n ? cand[i + lane] : 0ull, lane), lane);
-    }
+  if (n <= 32) {
+    if (warp == 0) best = sort_desc(lane < n ? cand[lane] : 0ull, lane);
     return best;
+  }
+  if (n <= kCandidates) {  // every warp sorts its share, then pairs of warps join
+    const auto sorted = [&](int i) {
+      return sort_desc(i + lane < n ? cand[i + lane] : 0ull, lane);
+    };
+    best = sorted(warp * 32);
+    for (int i = (warp + kWarps) * 32; i < n; i += kWarps * 32)
+      best = merge_desc(best, sorted(i), lane);
+    __syncthreads();  // the reads of `cand` have ended
+    return join_warps<NT>(best, cand, warp, lane);
   }
   // A thread held many of the largest: insert them one by one instead.
   __syncthreads();
@@ -544,7 +575,7 @@ __global__ void __launch_bounds__(NT, CTAS) token_logprob_kernel(const LogprobAr
                           __shfl_xor_sync(0xFFFFFFFFu, st.t, o)});
     unsigned long long best = 0;
     if constexpr (TOP)
-      best = alternatives<DT, NT>(run, row, c0, peak, nan, a.top_k, kept, cand, &n_cand);
+      best = alternatives<DT, NT>(run, row, c0, peak, nan, a.top_k, kept, cand, &row_list[0], &n_cand);
 
     if constexpr (kWarps > 1) {
       if (lane == 0) part_stats[warp] = st;
