@@ -378,9 +378,13 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, lane = tid & 31;
   const int left = (int)a.C - tid;  // columns i with i nt < left are this thread's
   const float inv = __fdiv_rn(1.0f, (float)a.C);
+  constexpr uint32_t kSize = sizeof(typename Elem<DT>::type);
   float g[EPT], b[EPT];
+  uint32_t at[EPT];  // byte offsets in a row; beyond it the last column's, so that every
+                     // load is in bounds without a condition
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
+    at[i] = (uint32_t)min(tid + i * nt, (int)a.C - 1) * kSize;
     g[i] = b[i] = 0.0f;
     if (i * nt < left) {
       load_weights<WT, 1>(a.gamma, tid + i * nt, false, 1.0f, &g[i]);
@@ -401,17 +405,17 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs
   };
   int side = 0;
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    const typename Elem<DT>::type* x =
-        static_cast<const typename Elem<DT>::type*>(a.x) + r * a.ldx + tid;
-    typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + r * a.ldy + tid;
+    const char* x = static_cast<const char*>(a.x) + r * a.ldx * (int64_t)kSize;
+    char* y = static_cast<char*>(a.y) + r * a.ldy * (int64_t)kSize;
     typename Elem<DT>::type raw[EPT];
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) raw[i] = i * nt < left ? x[i * nt] : 0;
+    for (int i = 0; i < EPT; ++i)
+      raw[i] = *reinterpret_cast<const typename Elem<DT>::type*>(x + at[i]);
     float f[EPT], s = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
       f[i] = Elem<DT>::get(raw[i]);
-      s += f[i];
+      s += i * nt < left ? f[i] : 0.0f;
     }
     const float mu = row_sum(s, red[side][0]) * inv;
     s = 0.0f;
@@ -424,7 +428,9 @@ __global__ void __launch_bounds__(1024) layernorm_fwd_elem_kernel(const NormArgs
     side ^= 1;  // free again: every thread passes two barriers after these reads
 #pragma unroll
     for (int i = 0; i < EPT; ++i)
-      if (i * nt < left) y[i * nt] = Elem<DT>::put(__fmaf_rn(f[i] * rs, g[i], b[i]));
+      if (i * nt < left)
+        *reinterpret_cast<typename Elem<DT>::type*>(y + at[i]) =
+            Elem<DT>::put(__fmaf_rn(f[i] * rs, g[i], b[i]));
     if (tid == 0) {
       if (a.mean) a.mean[r] = mu;
       if (a.rstd) a.rstd[r] = rs;
@@ -719,16 +725,18 @@ template <int DT, int WT, int EPT, int AHEAD, int NT, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
   __shared__ float2 red[2][32];
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
-  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x);
-  const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy);
-  typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx);
+  constexpr uint32_t kSize = sizeof(typename Elem<DT>::type);
   float g[EPT], ag[EPT], ab[EPT];
+  // Byte offsets in a row; beyond it the last column's, so that every load is in
+  // bounds without a condition (its weight here is 0 and its sums are not kept).
+  uint32_t at[EPT];
   // the rows ahead: AHEAD of them, by turns
   typename Elem<DT>::type nx[AHEAD][EPT], nd[AHEAD][EPT];
   float nmu[AHEAD], nrs[AHEAD];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = tid + i * nt;
+    at[i] = (uint32_t)min(c, C - 1) * kSize;
     ag[i] = ab[i] = 0.0f;
     g[i] = 0.0f;
     if (c < C) load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g[i]);
@@ -737,23 +745,19 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
   const auto fetch = [&](int64_t r, typename Elem<DT>::type* px, typename Elem<DT>::type* pd,
                          float& mu, float& rs) {
     if (r >= a.R) return;
-    const typename Elem<DT>::type* rx = x + r * a.ldx + tid;
-    const typename Elem<DT>::type* rd = dy + r * a.lddy + tid;
+    const char* rx = static_cast<const char*>(a.x) + r * a.ldx * (int64_t)kSize;
+    const char* rd = static_cast<const char*>(a.dy) + r * a.lddy * (int64_t)kSize;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i)
-      if (tid + i * nt < C) {
-        px[i] = rx[i * nt];
-        pd[i] = rd[i * nt];
-      }
+    for (int i = 0; i < EPT; ++i) {
+      px[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rx + at[i]);
+      pd[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rd + at[i]);
+    }
     mu = a.mean[r];
     rs = a.rstd[r];
   };
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) nx[k][i] = nd[k][i] = 0;
+  for (int k = 0; k < AHEAD; ++k)
     fetch(blockIdx.x + (int64_t)k * gridDim.x, nx[k], nd[k], nmu[k], nrs[k]);
-  }
   int side = 0;
   for (int64_t r0 = blockIdx.x; r0 < a.R; r0 += (int64_t)AHEAD * gridDim.x) {
 #pragma unroll
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
       float h[EPT], d[EPT];
       float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {  // (a column beyond the row has dy 0)
+      for (int i = 0; i < EPT; ++i) {
         h[i] = __fmaf_rn(Elem<DT>::get(nx[k][i]), rs, shift);
         d[i] = Elem<DT>::get(nd[k][i]);
         ab[i] += d[i];
@@ -777,13 +781,15 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
       const float2 s = row_sum2(s1, s2, red[side], warps);
       side ^= 1;
       const float c1 = s.x * inv, c2 = s.y * inv;
-      typename Elem<DT>::type* out = dx + r * a.lddx + tid;
+      char* out = static_cast<char*>(a.dx) + r * a.lddx * (int64_t)kSize;
 #pragma unroll
       for (int i = 0; i < EPT; ++i)
         if (tid + i * nt < C)
-          out[i * nt] = Elem<DT>::put(rs * __fmaf_rn(-h[i], c2, d[i] - c1));
+          *reinterpret_cast<typename Elem<DT>::type*>(out + at[i]) =
+              Elem<DT>::put(rs * __fmaf_rn(-h[i], c2, d[i] - c1));
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;");
   if (a.ws) {
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
@@ -839,42 +845,53 @@ __global__ void __launch_bounds__(kDwThreads) layernorm_dw_long_kernel(const Nor
   a.ws[(P + blockIdx.y) * a.C + c] = sb;
 }
 
-// Adds the P partial sums of each column: 32 columns per CTA, every warp adds
-// each 32nd (of the CTA's 32 warps) and the CTA joins them in order.
-constexpr int kJoinWarps = 32;
+// Adds the P partial sums of each column: eight columns per CTA (a 32-byte
+// sector of each row of ws), four rows per warp at a time, so that a few
+// loads per thread, all in flight, cover every row; joined in a fixed order.
+constexpr int kJoinCols = 8;
 template <int OT>
-__global__ void __launch_bounds__(kJoinWarps * 32)
+__global__ void __launch_bounds__(1024)
     layernorm_join_kernel(const float* ws, int64_t P, int64_t C, void* dgamma, void* dbeta) {
-  __shared__ float part[kJoinWarps][33];
+  __shared__ float part[32][kJoinCols + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are written
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int step = warps * 4;  // rows of a step of the CTA
+  const int64_t c = (int64_t)blockIdx.x * kJoinCols + (lane & 7);
   void* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (!out) return;
   ws += blockIdx.y * P * C;
   float s = 0.0f;
   if (c < C)
-    for (int64_t i = warp; i < P; i += kJoinWarps) s += ws[i * C + c];
-  part[warp][lane] = s;
+    for (int64_t i = warp * 4 + (lane >> 3); i < P; i += 8 * step) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = i + k * step < P ? ws[(i + k * step) * C + c] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+  s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+  if (lane < kJoinCols) part[warp][lane] = s;
   __syncthreads();
-  // warp w joins column w
-  s = part[lane][warp];
+  if (warp >= kJoinCols) return;
+  s = lane < warps ? part[lane][warp] : 0.0f;  // warp w joins column w
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  const int64_t oc = (int64_t)blockIdx.x * 32 + warp;
+  const int64_t oc = (int64_t)blockIdx.x * kJoinCols + warp;
   if (lane == 0 && oc < C) store1<OT>(out, oc, s);
 }
 
-constexpr int kElems = 8;  // columns per thread of the element path
+constexpr int kElems = 8;  // most columns per thread of the element path
 struct NormBwdPlan {
   int threads;
   int64_t ctas;
 };
 // One CTA's threads and the CTAs of the grid, where a thread owns `each`
-// columns: 1024 threads per SM (64 registers each).
-static NormBwdPlan bwd_plan(int64_t R, int64_t C, int64_t each) {
+// columns: 1024 threads per SM at most (64 registers each).
+static NormBwdPlan bwd_plan(int64_t R, int64_t C, int64_t each, int64_t sm_threads = 1024) {
   const int64_t threads = ((C + each - 1) / each + 31) / 32 * 32;
-  const int64_t per_sm = std::min<int64_t>(32, 1024 / threads);
+  const int64_t per_sm = std::min<int64_t>(32, sm_threads / threads);
   return NormBwdPlan{(int)threads, std::min<int64_t>(R, sm_count() * per_sm)};
 }
 static int64_t long_partials(int64_t R) { return R < 128 ? R : 128; }
@@ -908,7 +925,7 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
     // eight columns per thread; between 2048 and 4096 four, two rows ahead (64
     // registers hold no more)
     const int64_t each = a.C <= 2048 || a.C > 4096 ? 8 : 4;
-    const NormBwdPlan p = bwd_plan(a.R, a.C, each);
+    const NormBwdPlan p = bwd_plan(a.R, a.C, each, a.C <= 2048 ? 768 : 1024);
     if (a.C <= 2048)
       layernorm_bwd_elem_kernel<DT, WT, 8, 1, 256, 3>
           <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
@@ -958,8 +975,8 @@ cudaError_t launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
   if (!dgamma && !dbeta) return cudaSuccess;
   // launched while the sums' kernel ends; it waits for them on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((C + 31) / 32), 2);
-  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.gridDim = dim3((unsigned)((C + kJoinCols - 1) / kJoinCols), 2);
+  cfg.blockDim = dim3(P <= 256 ? 256 : 1024);  // one step of eight loads per thread
   cfg.stream = stream;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
