@@ -63,25 +63,28 @@ __device__ __forceinline__ float decode_e4m3(uint8_t q) {
 struct AdamWStep {
   float coef, c1, c2;  // gradient factor; lr / (1 - b1^t); 1 / sqrt(1 - b2^t)
   uint32_t key;        // of the random bits, without the place's high word
+  bool skip;           // the step is not taken: nothing is written
 };
 
 // The step's factors, by the CTA's first thread for all of them (the
 // exponentials are a few hundred instructions).  1 - b^t = -expm1(t log b);
-// b = 0 gives 1.
+// b = 0 gives 1.  The last CTA to have read the step's number counts it.
 __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
   __shared__ AdamWStep shared;
   if (threadIdx.x == 0) {
     AdamWStep s;
-    s.coef = 1.0f;
-    if (a.max_norm > 0.0f) {
-      const float nrm = *a.grad_norm;
-      if (nrm > a.max_norm) s.coef = __fdiv_rn(a.max_norm, nrm);
-    }
     const int64_t t = *a.step + 1;
+    const float nrm = a.max_norm > 0.0f ? *a.grad_norm : 0.0f;
+    s.skip = *a.found_inf != 0;
+    s.coef = a.max_norm > 0.0f && nrm > a.max_norm ? __fdiv_rn(a.max_norm, nrm) : 1.0f;
     s.c1 = __fdiv_rn(a.lr, -expm1f((float)t * a.log_beta1));
     s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
     s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
     shared = s;
+    if (!s.skip && atomicAdd(a.arrived, 1u) == gridDim.x - 1) {
+      *a.arrived = 0;
+      *a.step = t;
+    }
   }
   __syncthreads();
   return shared;
@@ -125,18 +128,6 @@ __device__ __forceinline__ Adam1 adam1(const AdamWArgs& a, const AdamWStep& s, f
   o.w = __fsub_rn(__fmul_rn(w, keep),
                   quotient(__fmul_rn(o.m, s.c1), __fmaf_rn(o.r, s.c2, a.eps)));
   return o;
-}
-
-// The last CTA to arrive counts the step: every other one has read it.
-__device__ __forceinline__ void count_step(const AdamWArgs& a) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(a.arrived, 1u) == gridDim.x - 1) {
-      *a.arrived = 0;
-      *a.step += 1;
-    }
-  }
 }
 
 // Eight gradients, 16 bytes at a time.
@@ -187,10 +178,12 @@ __device__ __forceinline__ bool aligned_to(const void* p, uint32_t n) {
 template <int GT>
 __global__ void __launch_bounds__(kAdamThreads)
     adamw_f32_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
-  if (*a.found_inf) return;  // skipped step: leave every state untouched
+  AChunk ch{};
+  if (blockIdx.x < n_chunks) ch = chunks[blockIdx.x];  // on its way while the factors are formed
   const AdamWStep s = step_of(a);
+  if (s.skip) return;
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-    const AChunk ch = chunks[c];
+    if (c != blockIdx.x) ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
     float* m = static_cast<float*>(ch.m);
     float* v = static_cast<float*>(ch.v);
@@ -227,7 +220,6 @@ __global__ void __launch_bounds__(kAdamThreads)
       if (ch.w_bf16) ch.w_bf16[i] = Elem<GS_BF16>::put(o.w);
     }
   }
-  count_step(a);
 }
 
 // Two elements' new moments and weights: adam1, both at once (f32x2
@@ -362,12 +354,14 @@ __device__ __forceinline__ uint32_t pack4(const uint32_t* q) {
 template <int GT>
 __global__ void __launch_bounds__(kAdamThreads, 4)
     adamw_e4m3_kernel(const AChunk* __restrict__ chunks, int64_t n_chunks, const AdamWArgs a) {
-  if (*a.found_inf) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kWarps = kAdamThreads / 32, U = kAdamBlocks;
+  AChunk ch{};
+  if (blockIdx.x < n_chunks) ch = chunks[blockIdx.x];  // on its way while the factors are formed
   const AdamWStep s = step_of(a);
+  if (s.skip) return;
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-    const AChunk ch = chunks[c];
+    if (c != blockIdx.x) ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
     uint8_t* mq = static_cast<uint8_t*>(ch.m);
     uint8_t* vq = static_cast<uint8_t*>(ch.v);
@@ -469,7 +463,6 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       }
     }
   }
-  count_step(a);
 }
 
 cudaError_t launch_master_update_adamw(const AChunk* d_chunks, int64_t n_chunks, int grad_dtype,

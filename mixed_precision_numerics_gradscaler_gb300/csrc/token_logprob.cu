@@ -79,16 +79,13 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // ---- running softmax statistics -------------------------------------------
-// s: sum 2^d, t: sum 2^d d with d = (x - m) log2 e, m a logit near the maximum
-// of what was taken: it follows the maximum once that is more than kLag above
-// it (a thread's maximum grows slowly, and in a warp some thread's does at
-// almost every step; 2^d stays below 2^6).  A NaN or +Inf logit makes s NaN.
+// m: the maximum (NaN left out); s: sum 2^d, t: sum 2^d d with
+// d = (x - m) log2 e.  A NaN or +Inf logit makes s NaN.
 struct Stats {
   float m, s, t;
 };
-constexpr float kLag = 4.0f;
 
-// Brings (s, t) from reference m to the larger M.  m = -Inf (nothing yet,
+// Brings (s, t) from maximum m to the larger M.  m = -Inf (nothing yet,
 // s = 0) must not turn into 0 * Inf: the shift is kept finite.
 __device__ __forceinline__ void rescale(float m, float M, float& s, float& t) {
   const float D = fmaxf((m - M) * kLog2e, -1e30f);
@@ -145,7 +142,7 @@ __device__ __forceinline__ void unpack16(const uint4& v, float* x) {
 // all the same, so that a masked logit adds 0 and not 0 * Inf to t.
 template <int N>
 __device__ __forceinline__ void take(Stats& a, const float* x, float lm) {
-  if (lm > a.m + kLag) {
+  if (lm > a.m) {
     rescale(a.m, lm, a.s, a.t);
     a.m = lm;
   }
@@ -662,15 +659,20 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   // Threads of a CTA: short rows leave most of a wide CTA's time to its
-  // joins (16000 rows of 8000 bf16, lse alone: 76 us with 64 threads, 101 with
-  // 256); long ones want few joins (4096 x 128256 with 8 alternatives: 188 us
-  // with 256, 250 with 128).
+  // joins (16000 rows of 8000 bf16, lse alone: 75 us with 64 threads, 101 with
+  // 256); long ones want few joins (4096 x 128256 bf16 with 8 alternatives:
+  // 194 us with 256 threads, 210 with 128), but where the rows alone do not
+  // fill the device, smaller CTAs spread the joins (512 rows: 42 and 37 us, 100
+  // rows: 25 and 19 us; a few rows are again faster with 256, 13 and 15 us).
+  const bool few = R >= sm_count() / 2 && R < want;
 #define GS_N(DT, NT, CTAS)                                                     \
   (cfg.blockDim = dim3(NT),                                                    \
    top_k ? cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, NT, CTAS, true>, a) \
          : cudaLaunchKernelEx(&cfg, token_logprob_kernel<DT, NT, CTAS, false>, a))
-#define GS_F(DT)                                                               \
-  return part > 12288 ? GS_N(DT, 256, 5) : part > 1536 ? GS_N(DT, 64, 16) : GS_N(DT, 32, 32)
+#define GS_F(DT)                                                              \
+  return part <= 1536 ? GS_N(DT, 32, 32)                                      \
+         : part <= 12288 ? GS_N(DT, 64, 16)                                   \
+         : few ? GS_N(DT, 128, 10) : GS_N(DT, 256, 5)
   if (dtype == GS_F32) GS_F(GS_F32);
   if (dtype == GS_F16) GS_F(GS_F16);
   GS_F(GS_BF16);
@@ -684,7 +686,7 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
 // element.  A CTA takes one run of a row and issues its loads before anything
 // that waits for the row's scalars.
 
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 128;
 
 // Columns of a thread's granule: 32 bytes of the wider type.
 template <int DT, int OT>
@@ -775,7 +777,7 @@ struct Granule {
 };
 
 template <int DT, int OT, bool ENT>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kBwdThreads, DT == GS_F32 ? 12 : 10)
     token_logprob_bwd_kernel(const LogprobBwdArgs a) {
   __shared__ float red[kBwdThreads / 32];
   constexpr int G = kGranule<DT, OT>, U = kBwdGranules;
@@ -827,13 +829,23 @@ __global__ void __launch_bounds__(kBwdThreads)
       ls = logf(block_sum<kBwdThreads>(s, red));
     }
     const float base = none ? 0.0f : l;
-    // gradient of one logit; d stays above -30000, where p is 0 all the same,
-    // so that a masked logit gives 0 and not 0 * Inf
-    const auto grad = [&](float x) {
-      float d = (x - base) - ls;
-      if constexpr (ENT) asm("max.NaN.f32 %0, %0, %1;" : "+f"(d) : "f"(-30000.0f));
-      const float p = ex2(d * kLog2e);
-      return ENT ? p * __fmaf_rn(-ge, d + eh, -g) : p * -g;
+    // gradient of two logits, without the target's own term; d stays above
+    // -30000, where p is 0 all the same, so that a masked logit gives 0 and not
+    // 0 * Inf
+    const uint64_t nbase = pk_f32x2(-base, -base), nls = pk_f32x2(-ls, -ls);
+    const uint64_t ng = pk_f32x2(-g, -g), nge = pk_f32x2(-ge, -ge), eh2 = pk_f32x2(eh, eh);
+    const auto grad2 = [&](float& x0, float& x1) {
+      uint64_t d = add_f32x2(add_f32x2(pk_f32x2(x0, x1), nbase), nls);
+      if constexpr (ENT) {
+        upk_f32x2(d, x0, x1);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-30000.0f));
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-30000.0f));
+        d = pk_f32x2(x0, x1);
+      }
+      float e0, e1;
+      upk_f32x2(mul_f32x2(d, pk_f32x2(kLog2e, kLog2e)), e0, e1);
+      const uint64_t p = pk_f32x2(ex2(e0), ex2(e1));
+      upk_f32x2(mul_f32x2(p, ENT ? fma_f32x2(nge, add_f32x2(d, eh2), ng) : ng), x0, x1);
     };
     for (int k = run;; ++k) {
 #pragma unroll
@@ -843,7 +855,7 @@ __global__ void __launch_bounds__(kBwdThreads)
         float x[G];
         w[u].unpack(x);
 #pragma unroll
-        for (int j = 0; j < G; ++j) x[j] = grad(x[j]);
+        for (int j = 0; j < G; j += 2) grad2(x[j], x[j + 1]);
         const uint64_t hot = (uint64_t)(at - (head + v * G));
         if (hot < G) {
 #pragma unroll
@@ -861,7 +873,9 @@ __global__ void __launch_bounds__(kBwdThreads)
       const int64_t odd = a.V - nv * G;
       for (int64_t i = threadIdx.x; i < odd; i += kBwdThreads) {
         const int64_t c = i < head ? i : nv * G + i;
-        store1<OT>(out, c, grad(load1<DT>(in, c)) + (c == at ? g : 0.0f));
+        float x = load1<DT>(in, c), unused = 0.0f;
+        grad2(x, unused);
+        store1<OT>(out, c, x + (c == at ? g : 0.0f));
       }
     }
     if (gridDim.y < a.R) __syncthreads();  // `red` is free for the next row
