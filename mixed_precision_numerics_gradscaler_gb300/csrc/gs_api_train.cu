@@ -249,7 +249,8 @@ int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
       if (numels[i] > 0 && numels[i] <= (INT64_MAX >> 4) && total <= (INT64_MAX >> 1))
         total += numels[i];
     const int64_t chunk = total / kChunkElems < (int64_t)sm_count() * 4 ? kChunkElems / 4
-                                                                       : kChunkElems;
+                           : total / kChunkElems < (int64_t)sm_count() * 64 ? kChunkElems
+                                                                              : 4 * kChunkElems;
     for (int32_t i = 0; i < n_tensors; ++i) {
       const int64_t n = numels[i];
       if (n < 0 || n > (INT64_MAX >> 4) || place > (INT64_MAX >> 1) - n) return GS_ERR_SHAPE;
