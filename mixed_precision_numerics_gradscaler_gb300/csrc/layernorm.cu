@@ -720,8 +720,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
 }
 
 // Rows of any alignment, element by element: thread t owns columns t + i nt.
-// The next rows' elements are loaded before this row's barrier.
-template <int DT, int WT, int EPT, int AHEAD, int NT, int CTAS>
+// The next row's elements are loaded before this row's barrier.
+template <int DT, int WT, int EPT, int NT, int CTAS>
 __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const NormBwdArgs a) {
   __shared__ float2 red[2][32];
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, C = (int)a.C;
@@ -730,9 +730,8 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
   // Byte offsets in a row; beyond it the last column's, so that every load is in
   // bounds without a condition (its weight here is 0 and its sums are not kept).
   uint32_t at[EPT];
-  // the rows ahead: AHEAD of them, by turns
-  typename Elem<DT>::type nx[AHEAD][EPT], nd[AHEAD][EPT];
-  float nmu[AHEAD], nrs[AHEAD];
+  typename Elem<DT>::type nx[EPT], nd[EPT];  // the next row's
+  float nmu = 0.0f, nrs = 0.0f;
 #pragma unroll
   for (int i = 0; i < EPT; ++i) {
     const int c = tid + i * nt;
@@ -742,52 +741,44 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
     if (c < C) load_weights<WT, 1>(a.gamma, c, false, 1.0f, &g[i]);
   }
   const float inv = __fdiv_rn(1.0f, (float)C);
-  const auto fetch = [&](int64_t r, typename Elem<DT>::type* px, typename Elem<DT>::type* pd,
-                         float& mu, float& rs) {
+  const auto fetch = [&](int64_t r) {
     if (r >= a.R) return;
     const char* rx = static_cast<const char*>(a.x) + r * a.ldx * (int64_t)kSize;
     const char* rd = static_cast<const char*>(a.dy) + r * a.lddy * (int64_t)kSize;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      px[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rx + at[i]);
-      pd[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rd + at[i]);
+      nx[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rx + at[i]);
+      nd[i] = *reinterpret_cast<const typename Elem<DT>::type*>(rd + at[i]);
     }
-    mu = a.mean[r];
-    rs = a.rstd[r];
+    nmu = a.mean[r];
+    nrs = a.rstd[r];
   };
-#pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-    fetch(blockIdx.x + (int64_t)k * gridDim.x, nx[k], nd[k], nmu[k], nrs[k]);
+  fetch(blockIdx.x);
   int side = 0;
-  for (int64_t r0 = blockIdx.x; r0 < a.R; r0 += (int64_t)AHEAD * gridDim.x) {
+  for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
+    const float rs = nrs, shift = -nmu * rs;
+    float h[EPT], d[EPT];
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      const int64_t r = r0 + (int64_t)k * gridDim.x;
-      if (r >= a.R) break;  // the same for the CTA
-      const float rs = nrs[k], shift = -nmu[k] * rs;
-      float h[EPT], d[EPT];
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        h[i] = __fmaf_rn(Elem<DT>::get(nx[k][i]), rs, shift);
-        d[i] = Elem<DT>::get(nd[k][i]);
-        ab[i] += d[i];
-        ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
-        d[i] *= g[i];
-        s1 += d[i];
-        s2 = __fmaf_rn(d[i], h[i], s2);
-      }
-      fetch(r + (int64_t)AHEAD * gridDim.x, nx[k], nd[k], nmu[k], nrs[k]);
-      const float2 s = row_sum2(s1, s2, red[side], warps);
-      side ^= 1;
-      const float c1 = s.x * inv, c2 = s.y * inv;
-      char* out = static_cast<char*>(a.dx) + r * a.lddx * (int64_t)kSize;
-#pragma unroll
-      for (int i = 0; i < EPT; ++i)
-        if (tid + i * nt < C)
-          *reinterpret_cast<typename Elem<DT>::type*>(out + at[i]) =
-              Elem<DT>::put(rs * __fmaf_rn(-h[i], c2, d[i] - c1));
+    for (int i = 0; i < EPT; ++i) {
+      h[i] = __fmaf_rn(Elem<DT>::get(nx[i]), rs, shift);
+      d[i] = Elem<DT>::get(nd[i]);
+      ab[i] += d[i];
+      ag[i] = __fmaf_rn(d[i], h[i], ag[i]);
+      d[i] *= g[i];
+      s1 += d[i];
+      s2 = __fmaf_rn(d[i], h[i], s2);
     }
+    fetch(r + gridDim.x);
+    const float2 s = row_sum2(s1, s2, red[side], warps);
+    side ^= 1;  // free again: every thread passes the next barrier after these reads
+    const float c1 = s.x * inv, c2 = s.y * inv;
+    char* out = static_cast<char*>(a.dx) + r * a.lddx * (int64_t)kSize;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i)
+      if (tid + i * nt < C)
+        *reinterpret_cast<typename Elem<DT>::type*>(out + at[i]) =
+            Elem<DT>::put(rs * __fmaf_rn(-h[i], c2, d[i] - c1));
   }
   asm volatile("griddepcontrol.launch_dependents;");
   if (a.ws) {
@@ -882,7 +873,7 @@ __global__ void __launch_bounds__(1024)
   if (lane == 0 && oc < C) store1<OT>(out, oc, s);
 }
 
-constexpr int kElems = 8;  // most columns per thread of the element path
+constexpr int kElems = 8;  // columns per thread of the element path
 struct NormBwdPlan {
   int threads;
   int64_t ctas;
@@ -922,19 +913,19 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
     kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
     *partials = p.ctas;
   } else if (a.C <= 1024 * kElems) {
-    // eight columns per thread; between 2048 and 4096 four, two rows ahead (64
-    // registers hold no more)
-    const int64_t each = a.C <= 2048 || a.C > 4096 ? 8 : 4;
-    const NormBwdPlan p = bwd_plan(a.R, a.C, each, a.C <= 2048 ? 768 : 1024);
+    // As many registers as the width leaves: 16384 x 4001 fp16 takes 117 us with
+    // 512 threads of 128 registers, 189 us with 1024 of 64 that own four
+    // columns each.
+    const NormBwdPlan p = bwd_plan(a.R, a.C, kElems, a.C <= 2048 ? 768 : 1024);
+    const unsigned ctas = (unsigned)p.ctas;
     if (a.C <= 2048)
-      layernorm_bwd_elem_kernel<DT, WT, 8, 1, 256, 3>
-          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, kElems, 256, 3><<<ctas, p.threads, 0, stream>>>(a);
     else if (a.C <= 4096)
-      layernorm_bwd_elem_kernel<DT, WT, 4, 2, 1024, 1>
-          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, kElems, 512, 1><<<ctas, p.threads, 0, stream>>>(a);
+    else if (a.C <= 6144)
+      layernorm_bwd_elem_kernel<DT, WT, kElems, 768, 1><<<ctas, p.threads, 0, stream>>>(a);
     else
-      layernorm_bwd_elem_kernel<DT, WT, 8, 1, 1024, 1>
-          <<<(unsigned)p.ctas, p.threads, 0, stream>>>(a);
+      layernorm_bwd_elem_kernel<DT, WT, kElems, 1024, 1><<<ctas, p.threads, 0, stream>>>(a);
     *partials = p.ctas;
   } else {
     const int64_t most = (int64_t)1 << 30;

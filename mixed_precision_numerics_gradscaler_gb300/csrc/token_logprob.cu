@@ -441,7 +441,7 @@ __device__ __forceinline__ unsigned long long alternatives(const Run<DT>& run, c
   // the bound's logit, or equal to it and the next block (equal ones come after
   // the first) begins before the bound's column.
   const uint32_t bound_key = (uint32_t)(bound >> 32), bound_col = 0xFFFFFFFFu - (uint32_t)bound;
-  const uint32_t next_col = first_col + (uint32_t)(((peak.block + 1) * U * NT + tid) * N);
+  const uint32_t next_col = first_col + (uint32_t)((peak.block + 1) * U * NT + tid) * N;
   const bool all = mine && (nan || other > bound_key || (other == bound_key && next_col <= bound_col));
   const float low = key_value(bound_key);
   if (mine && !all) {  // the block of the maximum

@@ -128,6 +128,37 @@ def test_forward_nonfinite_rows_stay_apart(gs):
             assert torch.equal(y[r], y2[r])
 
 
+@pytest.mark.parametrize("R,C", [(6000, 8192), (6003, 520), (20003, 200), (5000, 1001)])
+def test_nonfinite_rows_among_many(gs, R, C):
+    """Rows with NaN or Inf change no other row, forward or backward, whichever
+    rows share a barrier with them."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(C)
+    x, dy = (torch.randn(R, C, device=DEV, generator=gen).bfloat16() for _ in range(2))
+    bad = torch.arange(0, R, 7, device=DEV)
+    xb, dyb = x.clone(), dy.clone()
+    xb[bad, bad % C], dyb[bad[::2], 0], xb[bad[::3], C - 1] = float("nan"), float("inf"), float("-inf")
+    ys = []
+    mean, rstd = x.float().mean(1), x.float().var(1).rsqrt()
+    for a, d in ((x, dy), (xb, dyb)):
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+        gs.gs_layernorm_fwd(a, None, None, y)
+        ws = torch.empty(gs.gs_layernorm_ws_bytes(R, C), dtype=torch.uint8, device=DEV)
+        gs.gs_layernorm_bwd(d, a, None, mean, rstd, dx, dg, db, ws)
+        ys.append((y, dx))
+    keep = torch.ones(R, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    assert torch.equal(ys[0][0][keep], ys[1][0][keep]) and torch.equal(ys[0][1][keep], ys[1][1][keep])
+    assert torch.isnan(ys[1][0][bad]).any(1).all()
+    # where the infinity stands in the NaN's place the gradient holds infinities only
+    xh = (xb[bad].double() - mean[bad, None]) * rstd[bad, None]
+    d = dyb[bad].double()
+    ref = rstd[bad, None] * (d - d.mean(1, keepdim=True) - xh * (d * xh).mean(1, keepdim=True))
+    assert torch.equal(torch.isnan(ys[1][1][bad]).any(1), torch.isnan(ref).any(1))
+    assert not torch.isfinite(ys[1][1][bad]).all(1).any()
+
+
 def bwd_case(gs, R, C, dtype, wt, pad=0, offset=0, dw=torch.float32, affine=True, sums=(True, True)):
     gen = torch.Generator(device=DEV)
     gen.manual_seed(R * 7919 + C)
