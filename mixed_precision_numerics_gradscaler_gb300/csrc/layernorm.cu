@@ -8,6 +8,10 @@
 //   dx = rstd (d - sum d / C - xhat (sum d xhat) / C)
 //   dgamma = sum over rows of dy xhat,  dbeta = sum over rows of dy
 //
+// xhat is formed from the difference, never as x rstd - mean rstd: where a
+// row is nearly constant and eps small, the rounding of mean rstd would stand
+// in xhat's place.
+//
 // Both passes are HBM-bound: forward 2 elements moved per element, backward 3.
 //
 // Forward: a row is read once into registers (at most 32 values per thread),
@@ -296,32 +300,31 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   int slot = 0, side = 0;
   for (; rows > 0; rows -= stride, to += stride * a.ldy) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    uint4 raw[Q];
-    float s[Q];
+    const uint4* mine = ring + slot * Q * nt + tid;
+    // this thread's sums, and its squared deviations from its own means
+    float s[Q], dev[Q];
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
-      raw[i] = live && rows > i ? ring[(slot * Q + i) * nt + tid] : make_uint4(0, 0, 0, 0);
-      uint64_t f[P];
-      unpack_pairs<DT>(raw[i], f);
-#pragma unroll
-      for (int j = 1; j < P; ++j) f[0] = add_f32x2(f[0], f[j]);
-      s[i] = sum_of(f[0]);
-    }
-    copy_group(slot);
-    slot = slot + 1 < D ? slot + 1 : 0;
-    // this warp's means, and the squared deviations from them
-    const float wm = warp_sum4(s, lane) * inv_warp;
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      const uint64_t m2 = both(-__shfl_sync(0xFFFFFFFFu, wm, 8 * i));
       uint64_t f[P], t = 0;
-      unpack_pairs<DT>(raw[i], f);
+      unpack_pairs<DT>(live && rows > i ? mine[i * nt] : make_uint4(0, 0, 0, 0), f);
+      uint64_t sum = f[0];
+#pragma unroll
+      for (int j = 1; j < P; ++j) sum = add_f32x2(sum, f[j]);
+      s[i] = sum_of(sum);
+      const uint64_t m2 = both(s[i] * (-1.0f / W));
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         f[j] = add_f32x2(f[j], m2);
         t = fma_f32x2(f[j], f[j], t);
       }
-      s[i] = live ? sum_of(t) : 0.0f;
+      dev[i] = sum_of(t);
+    }
+    // this warp's means, and the squared deviations from them
+    const float wm = warp_sum4(s, lane) * inv_warp;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const float d = __fmaf_rn(s[i], 1.0f / W, -__shfl_sync(0xFFFFFFFFu, wm, 8 * i));
+      s[i] = live ? __fmaf_rn(W * d, d, dev[i]) : 0.0f;
     }
     const float wq = warp_sum4(s, lane);
     float mu, var;  // of row `row8` of the group, in this lane
@@ -355,17 +358,20 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
       if (a.mean) a.mean[a.R - rows + row8] = mu;
       if (a.rstd) a.rstd[a.R - rows + row8] = rs;
     }
-    const float shift = -mu * rs;
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
       const uint64_t scale2 = both(__shfl_sync(0xFFFFFFFFu, rs, 8 * i));
-      const uint64_t shift2 = both(__shfl_sync(0xFFFFFFFFu, shift, 8 * i));
+      const uint64_t m2 = both(-__shfl_sync(0xFFFFFFFFu, mu, 8 * i));
+      if (!(live && rows > i)) continue;
       uint64_t f[P];
-      unpack_pairs<DT>(raw[i], f);
+      unpack_pairs<DT>(mine[i * nt], f);
 #pragma unroll
-      for (int j = 0; j < P; ++j) f[j] = fma_f32x2(fma_f32x2(f[j], scale2, shift2), g[j], b[j]);
-      if (live && rows > i) st_stream(reinterpret_cast<uint4*>(to + i * a.ldy), pack_pairs<DT>(f));
+      for (int j = 0; j < P; ++j)
+        f[j] = fma_f32x2(mul_f32x2(add_f32x2(f[j], m2), scale2), g[j], b[j]);
+      st_stream(reinterpret_cast<uint4*>(to + i * a.ldy), pack_pairs<DT>(f));
     }
+    copy_group(slot);
+    slot = slot + 1 < D ? slot + 1 : 0;
   }
 }
 
@@ -479,15 +485,19 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
       <<<NT == 32 ? warps : rows, NT == 32 ? 256 : NT, 0, stream>>>(a)
   const int threads = (int)((a.C / V + 31) / 32 * 32);
   const int64_t ctas = (int64_t)sm_count() * (threads <= 1024 ? 1024 / std::max(threads, 32) : 0);
-  if (DT != GS_F32 && vec && ctas > 0 && a.R >= ctas * kFwdRows) {
-    const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
-    const auto kernel = layernorm_fwd_ring_kernel<DT, WT>;
-    int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
-    const cudaError_t e =
-        kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
-    if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, threads, smem(threads), stream>>>(a);
-  } else if (vec) {
+  if constexpr (DT != GS_F32) {
+    if (vec && ctas > 0 && a.R >= ctas * kFwdRows) {
+      const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
+      const auto kernel = layernorm_fwd_ring_kernel<DT, WT>;
+      int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
+      const cudaError_t e =
+          kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
+      if (e != cudaSuccess) return e;
+      kernel<<<(unsigned)ctas, threads, smem(threads), stream>>>(a);
+      return cudaGetLastError();
+    }
+  }
+  if (vec) {
     const int64_t nv = a.C / V;
     if (nv <= 32) GS_L(V, 32, 1);
     else if (nv <= 128) GS_L(V, 32, 4);
@@ -663,10 +673,10 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
       uint64_t h[P], d[P], s1 = 0, s2 = 0;
       unpack_pairs<DT>(mine[2 * q * nt], h);
       unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
-      const uint64_t scale = both(rs[q]), shift = both(-mu[q] * rs[q]);
+      const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        h[j] = fma_f32x2(h[j], scale, shift);
+        h[j] = mul_f32x2(add_f32x2(h[j], m2), scale);
         ab[j] = add_f32x2(ab[j], d[j]);
         ag[j] = fma_f32x2(d[j], h[j], ag[j]);
         d[j] = mul_f32x2(d[j], g[j]);
@@ -695,11 +705,11 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
       uint64_t h[P], d[P];
       unpack_pairs<DT>(mine[2 * q * nt], h);
       unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
-      const uint64_t scale = both(rs[q]), shift = both(-mu[q] * rs[q]);
-      const uint64_t n1 = both(-c1), n2 = both(-c2);
+      const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
+      const uint64_t n1 = both(-c1), n2 = both(-c2 * rs[q]);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
-        h[j] = fma_f32x2(h[j], scale, shift);
+        h[j] = add_f32x2(h[j], m2);
         d[j] = mul_f32x2(fma_f32x2(h[j], n2, fma_f32x2(d[j], g[j], n1)), scale);
       }
       st_stream(reinterpret_cast<uint4*>(to_dx + (q ? a.lddx : 0)), pack_pairs<DT>(d));
@@ -756,12 +766,12 @@ __global__ void __launch_bounds__(NT, CTAS) layernorm_bwd_elem_kernel(const Norm
   fetch(blockIdx.x);
   int side = 0;
   for (int64_t r = blockIdx.x; r < a.R; r += gridDim.x) {
-    const float rs = nrs, shift = -nmu * rs;
+    const float rs = nrs, mu = nmu;
     float h[EPT], d[EPT];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-      h[i] = __fmaf_rn(Elem<DT>::get(nx[i]), rs, shift);
+      h[i] = (Elem<DT>::get(nx[i]) - mu) * rs;
       d[i] = Elem<DT>::get(nd[i]);
       ab[i] += d[i];
       ag[i] = __fmaf_rn(d[i], h[i], ag[i]);

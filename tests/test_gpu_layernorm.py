@@ -159,6 +159,35 @@ def test_nonfinite_rows_among_many(gs, R, C):
     assert not torch.isfinite(ys[1][1][bad]).all(1).any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("R,C", [(5, 1024), (700, 8192), (5000, 512), (64, 16384), (300, 1023), (300, 4097)])
+def test_constant_rows_small_eps(gs, R, C, dtype):
+    """Rows of one value with a tiny eps: x - mean is 0 however large 1 / sqrt(eps)
+    is.  Sums of C equal small integers are exact in fp32; for a C that is no
+    power of two the mean's own rounding counts, so there the backward alone."""
+    x = (torch.arange(R, device=DEV) % 13 - 6).to(dtype)[:, None].expand(R, C).contiguous()
+    ones = torch.ones(C, device=DEV)
+    if C & (C - 1) == 0:
+        y, rstd = torch.empty_like(x), torch.empty(R, device=DEV)
+        gs.gs_layernorm_fwd(x, ones, 0.25 * ones, y, rstd=rstd, eps=1.1e-12)
+        assert (y == 0.25).all() and (rstd > 0.9e6).all()
+    mean, rstd = x[:, 0].float().contiguous(), torch.full((R,), 987654.3125, device=DEV)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(R)
+    dy, dx = torch.randn(R, C, device=DEV, generator=gen).to(dtype), torch.empty_like(x)
+    dg, db = torch.ones(C, device=DEV), torch.empty(C, device=DEV)
+    ws = torch.empty(gs.gs_layernorm_ws_bytes(R, C), dtype=torch.uint8, device=DEV)
+    gs.gs_layernorm_bwd(dy, x, ones, mean, rstd, dx, dg, db, ws)
+    assert (dg == 0).all()
+    d = dy.double()
+    ref = 987654.3125 * (d - d.mean(1, keepdim=True))
+    if dtype != torch.float16:  # (1e6 is beyond it)
+        # dx: the mean of dy (sum in fp32 over 2^5 terms a thread and a tree of 2^10)
+        # and three roundings, each 2^-24 of what it rounds; then the store's
+        tol = 1e6 * 64 * 2**-24 * d.abs().amax() + (2**-8 if dtype == torch.bfloat16 else 2**-22) * ref.abs()
+        assert ((dx.double() - ref).abs() <= tol).all()
+
+
 def bwd_case(gs, R, C, dtype, wt, pad=0, offset=0, dw=torch.float32, affine=True, sums=(True, True)):
     gen = torch.Generator(device=DEV)
     gen.manual_seed(R * 7919 + C)
