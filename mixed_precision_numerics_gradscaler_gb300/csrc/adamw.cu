@@ -66,6 +66,14 @@ struct AdamWStep {
   bool skip;           // the step is not taken: nothing is written
 };
 
+// One more CTA has read the step's number: how many had before.  Acquire and
+// release, so that the last one's write comes after every CTA's read.
+__device__ __forceinline__ uint32_t arrive(uint32_t* arrived) {
+  uint32_t before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(arrived) : "memory");
+  return before;
+}
+
 // The step's factors, by the CTA's first thread for all of them (the
 // exponentials are a few hundred instructions).  1 - b^t = -expm1(t log b);
 // b = 0 gives 1.  The last CTA to have read the step's number counts it.
@@ -81,7 +89,7 @@ __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
     s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
     s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
     shared = s;
-    if (!s.skip && atomicAdd(a.arrived, 1u) == gridDim.x - 1) {
+    if (!s.skip && arrive(a.arrived) == gridDim.x - 1) {
       *a.arrived = 0;
       *a.step = t;
     }
@@ -369,7 +377,22 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
                      aligned_to(vq, 4) && aligned_to(ch.w_bf16, 8);
     // blocks of the vector path, whole ones in pairs
     const int whole = vec ? (int)(ch.n / kMomentBlock) / U * U : 0;
+    // The warp's next blocks are brought to the L2 cache while these are worked
+    // on (567 M parameters: 1792 us without, 1590 with; two steps ahead the same,
+    // four 1690): lanes 0-3 ask for one array each, where it allows the copy.
+    const char* from = static_cast<const char*>(lane == 0   ? static_cast<const void*>(ch.w)
+                                                : lane == 1 ? ch.g
+                                                : lane == 2 ? ch.m
+                                                            : ch.v);
+    const uint32_t block_bytes = kMomentBlock * (lane == 0 ? 4 : lane == 1 ? (GT == GS_F32 ? 4 : 2) : 1);
+    const bool asks = lane < 4 && aligned_to(from, 16);
     for (int b0 = warp * U; b0 < whole; b0 += kWarps * U) {
+      const int b1 = b0 + kWarps * U;
+      if (asks && b1 < whole)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         from + (int64_t)b1 * block_bytes),
+                     "r"(U * block_bytes)
+                     : "memory");
       RawBlock<GT> now[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
