@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   extern __shared__ uint4 ring[];  // [D][Q][blockDim.x]
   // per row of the group: the warps' means, and their squared deviations
   __shared__ float4 part_mean[2][Q][8], part_dev[2][Q][8];
+  __shared__ float4 columns[8];  // of the row, each warp's
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
   const int c = tid * W, row8 = lane >> 3;  // the group's row that this lane joins
   const bool live = c < a.C;
@@ -266,16 +267,12 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
 #pragma unroll
     for (int j = 0; j < P; ++j) b[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
   }
-  // columns of warp i
-  const auto columns = [&](int i) {
-    const int n = (int)a.C - i * 32 * W;
-    return (float)(n < 0 ? 0 : n < 32 * W ? n : 32 * W);
-  };
+  if (tid < 32) reinterpret_cast<float*>(columns)[tid] = (float)max(0, min((int)a.C - tid * 32 * W, 32 * W));
   const float inv = __fdiv_rn(1.0f, (float)a.C);
-  const float inv_warp = __fdiv_rn(1.0f, fmaxf(columns(warp), 1.0f));
   for (int i = tid; i < 2 * Q * 8; i += nt)  // of warps that do not exist
     (&part_mean[0][0][0])[i] = (&part_dev[0][0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   __syncthreads();
+  const float inv_warp = __fdiv_rn(1.0f, fmaxf(reinterpret_cast<float*>(columns)[warp], 1.0f));
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
   const int64_t stride = (int64_t)gridDim.x * Q, first = (int64_t)blockIdx.x * Q;
@@ -337,15 +334,14 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
       const float4 m = part_mean[side][row8][lane & 7], q = part_dev[side][row8][lane & 7];
       side ^= 1;  // free again: every thread passes the next barrier after these reads
       // four warps' sums, each with its columns (fewer in the last one)
-      const int w0 = (lane & 7) * 4;
-      const float n0 = columns(w0), n1 = columns(w0 + 1), n2 = columns(w0 + 2), n3 = columns(w0 + 3);
-      float t = __fmaf_rn(n0, m.x, n1 * m.y) + __fmaf_rn(n2, m.z, n3 * m.w);
+      const float4 n = columns[lane & 7];
+      float t = __fmaf_rn(n.x, m.x, n.y * m.y) + __fmaf_rn(n.z, m.z, n.w * m.w);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       mu = t * inv;
       const float d0 = m.x - mu, d1 = m.y - mu, d2 = m.z - mu, d3 = m.w - mu;
-      t = (__fmaf_rn(n0 * d0, d0, q.x) + __fmaf_rn(n1 * d1, d1, q.y)) +
-          (__fmaf_rn(n2 * d2, d2, q.z) + __fmaf_rn(n3 * d3, d3, q.w));
+      t = (__fmaf_rn(n.x * d0, d0, q.x) + __fmaf_rn(n.y * d1, d1, q.y)) +
+          (__fmaf_rn(n.z * d2, d2, q.z) + __fmaf_rn(n.w * d3, d3, q.w));
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       var = t * inv;
