@@ -14,25 +14,30 @@
 //
 // Both passes are HBM-bound: forward 2 elements moved per element, backward 3.
 //
-// Forward: a row is read once into registers (at most 32 values per thread),
-// the variance formed about the mean from there (two block sums; a one-pass
-// variance would cancel for rows far from zero), and written.  A warp takes a
-// short row by itself, a CTA a long one; several rows per SM overlap.  Longer
-// rows than a CTA's registers hold are read three times, out of L2 after the
-// first.
+// Many rows of 16 bits, forward, and rows of any type, backward, go through a
+// ring of asynchronous copies in shared memory (below): each thread owns the
+// same 16 bytes of every row, so that its weights and its share of dgamma and
+// dbeta stay in registers.  16384 x 8192 bf16 takes 86 us forward (6.2 TB/s) and
+// 146 us backward (5.5 TB/s); with odd rows (8001) 111 and 175 us.  What is left
+// to the copy rate is issue: 65 to 70 % of the issue slots are taken.
 //
-// Backward: one pass over dy and x.  A CTA keeps its share of dgamma and
-// dbeta in registers while it walks the rows; every thread owns the same
-// columns of every row and copies its part of the next rows into shared
-// memory itself (cp.async), so that no thread waits for another's copy and
-// the memory stays busy across the one barrier of a row (its two sums).  At
-// the end each CTA writes one row of partial sums, which a second kernel adds
-// in a fixed order: no atomics, the result depends on the sizes and the
-// device alone.
+// Few rows, and fp32 forward: a row is read once into registers (at most 32
+// values per thread), the variance formed about the mean from there (two block
+// sums; a one-pass variance would cancel for rows far from zero), and written.  A
+// warp takes a short row by itself, a CTA a long one.
+//
+// Rows that neither can take, element by element: a thread owns columns t + i nt.
+// Longer rows than a CTA's registers hold are read again, out of L2 after the
+// first time.
+//
+// dgamma and dbeta: each CTA writes one row of partial sums at its end, which a
+// second kernel adds in a fixed order: no atomics, the result depends on the
+// sizes and the device alone.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_elem.cuh"
 #include "gs_internal.h"
@@ -134,7 +139,8 @@ struct NormArgs {
   int64_t ldy;
   float* mean;
   float* rstd;
-  bool w_vec;  // gamma and beta are 16-byte aligned (or absent)
+  bool w_vec;   // gamma and beta are 16-byte aligned (or absent)
+  int classes;  // of rows by alignment
 };
 
 // Sum over the NT threads that share a row: a warp's, or the CTA's; `red`
@@ -224,7 +230,8 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 // that no thread waits for another's copy and the memory stays busy across
 // the barriers.  Two rows (backward) or four (forward) share a barrier: the
 // sums' latency, some 800 cycles of shuffles and barrier, would take half the
-// time of a row otherwise.
+// time of a row otherwise.  A row is read from the ring again after the barrier:
+// held in registers it costs spills (forward 110 us, so 89).
 // 1024 threads per SM with 64 registers each, one CTA of them for the widest
 // rows, up to 32 for the narrowest.
 
@@ -239,10 +246,121 @@ __device__ __forceinline__ float warp_sum4(const float* s, int lane) {
   for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
+// Rows that do not begin or end on 16 bytes (EDGE; W elements are 16 bytes): in a
+// tensor that begins on 16 bytes, rows W apart stand alike to the boundaries.
+// Such rows are a class: each begins e elements behind a boundary, and in the
+// other tensors too if their pitches agree modulo W.  A CTA takes rows of one
+// class and a thread the W columns between two boundaries, so that all copies and
+// stores are of 16 bytes but a row's first and last, whose threads have the
+// columns [lo, hi) of their vector only.  A first vector's other bytes belong to
+// the row before (or the gap), are read and left out; a last vector's are not
+// read.  Only the warps of those two threads run the code that masks.
+template <int W, bool EDGE>
+struct RowClass {
+  int C, K, k, e;          // columns; classes, this CTA's, and its e
+  int64_t R, block, blocks;  // rows of the class; this CTA among the class's
+  int c, lo, hi;
+  bool live, partial;
+  __device__ __forceinline__ RowClass(int classes, int64_t rows, int64_t columns, int64_t ld)
+      : C((int)columns), K(EDGE ? classes : 1) {
+    k = EDGE ? (int)(blockIdx.x % (uint32_t)K) : 0;
+    e = EDGE ? (int)(k * ld % W) : 0;
+    R = EDGE ? (rows - k + K - 1) / K : rows;
+    block = EDGE ? blockIdx.x / (uint32_t)K : blockIdx.x;
+    blocks = EDGE ? gridDim.x / (uint32_t)K : gridDim.x;
+    c = (int)threadIdx.x * W - e;
+    live = c < C;
+    lo = EDGE ? max(-c, 0) : 0;
+    hi = EDGE ? min(C - c, W) : W;
+    partial = EDGE && live && hi - lo < W;
+  }
+  __device__ __forceinline__ int64_t row(int64_t i) const { return EDGE ? k + K * i : i; }
+  // columns of warp w
+  __device__ __forceinline__ int columns_of(int w) const {
+    const int from = w * 32 * W - e;
+    return max(0, min(C, from + 32 * W) - max(0, from));
+  }
+  __device__ __forceinline__ bool has(int j) const { return j >= lo && j < hi; }
+  template <int WT>
+  __device__ __forceinline__ void weights(const void* p, bool vec, float missing, uint64_t* w) const {
+    float f[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) f[j] = 0.0f;
+    if (EDGE) {
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+        if (live && has(j)) load_weights<WT, 1>(p, c + j, false, missing, &f[j]);
+    } else if (live) {
+      load_weights<WT, W>(p, c, vec, missing, f);
+    }
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) w[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
+  }
+  template <int DT>
+  __device__ __forceinline__ void copy(uint32_t to, const typename Elem<DT>::type* from) const {
+    if constexpr (EDGE) {
+      const int bytes = hi * (int)sizeof(*from);  // the rest of the 16 is zeroed
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                   : "memory");
+    } else {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+    }
+  }
+  // The columns of the warp's partial vectors, which are in their slots of the
+  // ring, to their places in an output row: a lane each, so that it is one store
+  // instruction and not W.
+  template <int DT>
+  __device__ __forceinline__ void store_partial(typename Elem<DT>::type* to, const uint4* slot) const {
+    const uint32_t edges = __ballot_sync(0xFFFFFFFFu, partial);
+    const int lane = threadIdx.x & 31, first = __ffs(edges) - 1, last = 31 - __clz(edges);
+    const int from = lane < W ? first : last, col = c + (from - lane) * W + lane % W;
+    if ((lane < W || (lane < 2 * W && first != last)) && col >= 0 && col < C)
+      to[col - c] = reinterpret_cast<const typename Elem<DT>::type*>(slot + (from - lane))[lane % W];
+  }
+};
+// The bits of a vector that are the thread's own, as in memory and as fp32
+// pairs: of a row's first thread, its last, and any other.
+template <int DT>
+struct EdgeMasks {
+  static constexpr int W = kVecElems<DT>;
+  uint4 raw[3];
+  uint64_t pair[3][W / 2];
+  __device__ __forceinline__ static int kind(bool partial, int c) { return !partial ? 2 : c > 0; }
+  // By threads of one kind alike.
+  __device__ __forceinline__ void make(int kind, int lo, int hi) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const uint32_t keep = kind == 2 || (j >= lo && j < hi) ? 0xFFFFFFFFu : 0;
+      w[j * 4 / W] |= W == 4 ? keep : keep & (j & 1 ? 0xFFFF0000u : 0x0000FFFFu);
+      reinterpret_cast<uint32_t*>(pair[kind])[j] = keep;
+    }
+    raw[kind] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+__device__ __forceinline__ uint4 and4(const uint4& a, const uint4& b) {
+  return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w);
+}
+// Classes of rows `ld` elements apart.
+static int row_classes(int64_t ld, int W) { return ld % W == 0 ? 1 : W; }
+
+// CTAs of a ring kernel's grid, 1024 threads per SM, whole numbers of every
+// class; none if a row is too wide.
+struct RingPlan {
+  int threads;
+  int64_t ctas;
+};
+static RingPlan ring_plan(int64_t C, int W, int classes, bool edge) {
+  const int64_t vectors = std::max<int64_t>((C + (edge ? W - 1 : 0) + W - 1) / W, 1);
+  const int64_t threads = (vectors + 31) / 32 * 32;
+  if (threads > 1024) return RingPlan{0, 0};
+  return RingPlan{(int)threads, (int64_t)sm_count() * (1024 / threads) / classes * classes};
+}
+
 constexpr int kFwdRows = 4, kFwdGroups = 3;  // forward: rows that share a barrier, groups in the ring
 constexpr int kBwdGroups = 3;                // backward: pairs of rows in the ring
 
-template <int DT, int WT>
+template <int DT, int WT, bool EDGE>
 __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormArgs a) {
   constexpr int W = kVecElems<DT>, P = W / 2, D = kFwdGroups, Q = kFwdRows;
   static_assert(Q == 4, "the joins below are of four rows");
@@ -250,24 +368,24 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   // per row of the group: the warps' means, and their squared deviations
   __shared__ float4 part_mean[2][Q][8], part_dev[2][Q][8];
   __shared__ float4 columns[8];  // of the row, each warp's
+  __shared__ EdgeMasks<DT> masks;
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const int c = tid * W, row8 = lane >> 3;  // the group's row that this lane joins
-  const bool live = c < a.C;
-  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
-  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + c;
+  const RowClass<W, EDGE> own(a.classes, a.R, a.C, a.ldx);
+  const int c = own.c, row8 = lane >> 3;  // row8: the group's row that this lane joins
+  const bool live = own.live;
+  const int64_t ldx = own.K * a.ldx, ldy = own.K * a.ldy;
+  const typename Elem<DT>::type* x =
+      static_cast<const typename Elem<DT>::type*>(a.x) + own.k * a.ldx + c;
+  typename Elem<DT>::type* y = static_cast<typename Elem<DT>::type*>(a.y) + own.k * a.ldy + c;
   uint64_t g[P], b[P];
-#pragma unroll
-  for (int j = 0; j < P; ++j) g[j] = b[j] = 0;
-  if (live) {
-    float f[W];
-    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, f);
-#pragma unroll
-    for (int j = 0; j < P; ++j) g[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
-    load_weights<WT, W>(a.beta, c, a.w_vec, 0.0f, f);
-#pragma unroll
-    for (int j = 0; j < P; ++j) b[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
-  }
-  if (tid < 32) reinterpret_cast<float*>(columns)[tid] = (float)max(0, min((int)a.C - tid * 32 * W, 32 * W));
+  own.template weights<WT>(a.gamma, a.w_vec, 1.0f, g);
+  own.template weights<WT>(a.beta, a.w_vec, 0.0f, b);
+  const int kind = EdgeMasks<DT>::kind(own.partial, c);
+  if (EDGE && live) masks.make(kind, own.lo, own.hi);
+  const bool edge_warp = EDGE && __any_sync(0xFFFFFFFFu, own.partial);
+  const float n_own = EDGE ? (float)max(own.hi - own.lo, 1) : (float)W;
+  const float inv_own = EDGE ? __frcp_rn(n_own) : 1.0f / W;
+  if (tid < 32) reinterpret_cast<float*>(columns)[tid] = (float)own.columns_of(tid);
   const float inv = __fdiv_rn(1.0f, (float)a.C);
   for (int i = tid; i < 2 * Q * 8; i += nt)  // of warps that do not exist
     (&part_mean[0][0][0])[i] = (&part_dev[0][0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -275,53 +393,57 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   const float inv_warp = __fdiv_rn(1.0f, fmaxf(reinterpret_cast<float*>(columns)[warp], 1.0f));
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
-  const int64_t stride = (int64_t)gridDim.x * Q, first = (int64_t)blockIdx.x * Q;
+  const int64_t stride = own.blocks * Q, first = own.block * Q;
   // the rows left from the group to copy next, and from the group in hand
-  int64_t ahead = a.R - first, rows = a.R - first;
-  const typename Elem<DT>::type* from = x + first * a.ldx;
-  typename Elem<DT>::type* to = y + first * a.ldy;
+  int64_t ahead = own.R - first, rows = own.R - first;
+  const typename Elem<DT>::type* from = x + first * ldx;
+  typename Elem<DT>::type* to = y + first * ldy;
   const auto copy_group = [&](int slot) {
     const uint32_t at = slot0 + slot * Q * nt * 16;
 #pragma unroll
     for (int i = 0; i < Q; ++i)
-      if (live && ahead > i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + i * nt * 16),
-                     "l"(from + i * a.ldx)
-                     : "memory");
+      if (live && ahead > i) own.template copy<DT>(at + i * nt * 16, from + i * ldx);
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead -= stride;
-    from += stride * a.ldx;
+    from += stride * ldx;
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) copy_group(i);
   int slot = 0, side = 0;
-  for (; rows > 0; rows -= stride, to += stride * a.ldy) {
+  for (; rows > 0; rows -= stride, to += stride * ldy) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-    const uint4* mine = ring + slot * Q * nt + tid;
+    uint4* mine = ring + slot * Q * nt + tid;
     // this thread's sums, and its squared deviations from its own means
     float s[Q], dev[Q];
+    const auto sums = [&](auto edge) {
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      uint64_t f[P], t = 0;
-      unpack_pairs<DT>(live && rows > i ? mine[i * nt] : make_uint4(0, 0, 0, 0), f);
-      uint64_t sum = f[0];
+      for (int i = 0; i < Q; ++i) {
+        uint4 raw = live && rows > i ? mine[i * nt] : make_uint4(0, 0, 0, 0);
+        if constexpr (edge.value) raw = and4(raw, masks.raw[kind]);
+        uint64_t f[P], t = 0;
+        unpack_pairs<DT>(raw, f);
+        uint64_t sum = f[0];
 #pragma unroll
-      for (int j = 1; j < P; ++j) sum = add_f32x2(sum, f[j]);
-      s[i] = sum_of(sum);
-      const uint64_t m2 = both(s[i] * (-1.0f / W));
+        for (int j = 1; j < P; ++j) sum = add_f32x2(sum, f[j]);
+        s[i] = sum_of(sum);
+        const uint64_t m2 = both(-s[i] * (edge.value ? inv_own : 1.0f / W));
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        f[j] = add_f32x2(f[j], m2);
-        t = fma_f32x2(f[j], f[j], t);
+        for (int j = 0; j < P; ++j) {
+          f[j] = add_f32x2(f[j], m2);
+          if constexpr (edge.value) f[j] &= masks.pair[kind][j];
+          t = fma_f32x2(f[j], f[j], t);
+        }
+        dev[i] = sum_of(t);
       }
-      dev[i] = sum_of(t);
-    }
+    };
+    if (EDGE && edge_warp) sums(std::integral_constant<bool, EDGE>());
+    else sums(std::false_type());
     // this warp's means, and the squared deviations from them
     const float wm = warp_sum4(s, lane) * inv_warp;
 #pragma unroll
     for (int i = 0; i < Q; ++i) {
-      const float d = __fmaf_rn(s[i], 1.0f / W, -__shfl_sync(0xFFFFFFFFu, wm, 8 * i));
-      s[i] = live ? __fmaf_rn(W * d, d, dev[i]) : 0.0f;
+      const float d = __fmaf_rn(s[i], inv_own, -__shfl_sync(0xFFFFFFFFu, wm, 8 * i));
+      s[i] = live ? __fmaf_rn(n_own * d, d, dev[i]) : 0.0f;
     }
     const float wq = warp_sum4(s, lane);
     float mu, var;  // of row `row8` of the group, in this lane
@@ -351,21 +473,34 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
     }
     const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
     if (warp == 0 && (lane & 7) == 0 && rows > row8) {
-      if (a.mean) a.mean[a.R - rows + row8] = mu;
-      if (a.rstd) a.rstd[a.R - rows + row8] = rs;
+      const int64_t at = own.row(own.R - rows + row8);
+      if (a.mean) a.mean[at] = mu;
+      if (a.rstd) a.rstd[at] = rs;
     }
+    const auto finish = [&](auto edge) {
 #pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      const uint64_t scale2 = both(__shfl_sync(0xFFFFFFFFu, rs, 8 * i));
-      const uint64_t m2 = both(-__shfl_sync(0xFFFFFFFFu, mu, 8 * i));
-      if (!(live && rows > i)) continue;
-      uint64_t f[P];
-      unpack_pairs<DT>(mine[i * nt], f);
+      for (int i = 0; i < Q; ++i) {
+        const uint64_t scale2 = both(__shfl_sync(0xFFFFFFFFu, rs, 8 * i));
+        const uint64_t m2 = both(-__shfl_sync(0xFFFFFFFFu, mu, 8 * i));
+        if (!(live && rows > i)) continue;
+        uint64_t f[P];
+        unpack_pairs<DT>(mine[i * nt], f);
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-        f[j] = fma_f32x2(mul_f32x2(add_f32x2(f[j], m2), scale2), g[j], b[j]);
-      st_stream(reinterpret_cast<uint4*>(to + i * a.ldy), pack_pairs<DT>(f));
-    }
+        for (int j = 0; j < P; ++j)
+          f[j] = fma_f32x2(mul_f32x2(add_f32x2(f[j], m2), scale2), g[j], b[j]);
+        if (edge.value && own.partial) mine[i * nt] = pack_pairs<DT>(f);
+        else st_stream(reinterpret_cast<uint4*>(to + i * ldy), pack_pairs<DT>(f));
+      }
+      if constexpr (edge.value) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+          if (rows > i) own.template store_partial<DT>(to + i * ldy, mine + i * nt);
+        __syncwarp();  // before the slots' next copies
+      }
+    };
+    if (EDGE && edge_warp) finish(std::integral_constant<bool, EDGE>());
+    else finish(std::false_type());
     copy_group(slot);
     slot = slot + 1 < D ? slot + 1 : 0;
   }
@@ -479,17 +614,24 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
 #define GS_L(W, NT, VPT)                                                                      \
   layernorm_fwd_kernel<DT, WT, W, NT, VPT>                                                    \
       <<<NT == 32 ? warps : rows, NT == 32 ? 256 : NT, 0, stream>>>(a)
-  const int threads = (int)((a.C / V + 31) / 32 * 32);
-  const int64_t ctas = (int64_t)sm_count() * (threads <= 1024 ? 1024 / std::max(threads, 32) : 0);
+  // The ring where a CTA gets a group of rows at least (8192 columns of
+  // bf16 on alignment: 608 rows 9.6 us, 8.7 from registers; 1216 rows 11 and 15;
+  // 16384 rows 87 and 132), and the rows of no alignment are not narrow
+  // (16384 x 4097 fp16 82 us, 109 element by element; 16384 x 1001: 21 and 26; 100000
+  // x 501: 69 and 67).  fp32 has enough bytes in flight without (16384 x 4096: 81
+  // us from registers, 98 through the ring).
   if constexpr (DT != GS_F32) {
-    if (vec && ctas > 0 && a.R >= ctas * kFwdRows) {
+    const bool edge = !vec && aligned16(a.x) && aligned16(a.y) && (a.ldx - a.ldy) % V == 0;
+    const RingPlan p = ring_plan(a.C, V, edge ? a.classes : 1, edge);
+    if ((vec || (edge && a.C > 512)) && p.ctas > 0 && a.R >= p.ctas * kFwdRows) {
       const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
-      const auto kernel = layernorm_fwd_ring_kernel<DT, WT>;
+      const auto kernel =
+          edge ? layernorm_fwd_ring_kernel<DT, WT, true> : layernorm_fwd_ring_kernel<DT, WT, false>;
       int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
       const cudaError_t e =
           kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
       if (e != cudaSuccess) return e;
-      kernel<<<(unsigned)ctas, threads, smem(threads), stream>>>(a);
+      kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
       return cudaGetLastError();
     }
   }
@@ -541,7 +683,7 @@ cudaError_t launch_layernorm_fwd(const void* x, int64_t ldx, int dtype, int64_t 
                      std::min(most, R - r0), C, gamma, beta, eps,
                      static_cast<char*>(y) + r0 * ldy * esz, ldy,
                      mean ? mean + r0 : nullptr, rstd ? rstd + r0 : nullptr,
-                     aligned16(gamma) && aligned16(beta)};
+                     aligned16(gamma) && aligned16(beta), row_classes(ldx, dtype == GS_F32 ? 4 : 8)};
     cudaError_t e = cudaSuccess;
 #define GS_F(DT, WT) e = fwd_launch<DT, WT>(a, stream);
     GS_NORM_TYPES(dtype, w_dtype, GS_F)
@@ -565,6 +707,7 @@ struct NormBwdArgs {
   int64_t lddx;
   float* ws;  // [2, gridDim.x, C] partial sums, or nullptr
   bool w_vec;
+  int classes;  // of rows by alignment
 };
 
 // The two sums of a row over the CTA, the same in every thread; `red` holds
@@ -591,97 +734,104 @@ __device__ __forceinline__ float2 row_sum2(float s1, float s2, float2* red, int 
   return make_float2(s1, s2);
 }
 
-// Rows 16 bytes at a time, two per barrier.  The rows are read from the ring
-// again after it (registers hold the weights and both sums' accumulators).
-template <int DT, int WT>
+// Rows 16 bytes at a time, two per barrier; registers hold the weights and both
+// sums' accumulators.
+template <int DT, int WT, bool EDGE>
 __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormBwdArgs a) {
   constexpr int W = kVecElems<DT>, D = kBwdGroups;
   extern __shared__ uint4 ring[];  // [D][2][x, dy][blockDim.x]
   __shared__ float4 part4[2][32];  // per value of the pair's four: eight warps' sums a float4
   float* const part = reinterpret_cast<float*>(part4);  // [2][4][32]
   __shared__ float4 stats[D][32];  // a pair's means and rstd, one copy per warp
+  __shared__ EdgeMasks<DT> masks;
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const int c = tid * W;
-  const bool live = c < a.C;
-  const typename Elem<DT>::type* x = static_cast<const typename Elem<DT>::type*>(a.x) + c;
-  const typename Elem<DT>::type* dy = static_cast<const typename Elem<DT>::type*>(a.dy) + c;
-  typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx) + c;
+  const RowClass<W, EDGE> own(a.classes, a.R, a.C, a.ldx);
+  const int c = own.c;
+  const bool live = own.live;
+  const int64_t ldx = own.K * a.ldx, lddy = own.K * a.lddy, lddx = own.K * a.lddx;
+  const typename Elem<DT>::type* x =
+      static_cast<const typename Elem<DT>::type*>(a.x) + own.k * a.ldx + c;
+  const typename Elem<DT>::type* dy =
+      static_cast<const typename Elem<DT>::type*>(a.dy) + own.k * a.lddy + c;
+  typename Elem<DT>::type* dx = static_cast<typename Elem<DT>::type*>(a.dx) + own.k * a.lddx + c;
   constexpr int P = W / 2;  // pairs of columns
   uint64_t g[P], ag[P], ab[P];
 #pragma unroll
-  for (int j = 0; j < P; ++j) g[j] = ag[j] = ab[j] = 0;
-  if (live) {
-    float f[W];
-    load_weights<WT, W>(a.gamma, c, a.w_vec, 1.0f, f);
-#pragma unroll
-    for (int j = 0; j < P; ++j) g[j] = pk_f32x2(f[2 * j], f[2 * j + 1]);
-  }
+  for (int j = 0; j < P; ++j) ag[j] = ab[j] = 0;
+  own.template weights<WT>(a.gamma, a.w_vec, 1.0f, g);
+  const int kind = EdgeMasks<DT>::kind(own.partial, c);
+  if (EDGE && live) masks.make(kind, own.lo, own.hi);
+  const bool edge_warp = EDGE && __any_sync(0xFFFFFFFFu, own.partial);
   const float inv = __fdiv_rn(1.0f, (float)a.C);
   for (int i = tid; i < 256; i += nt) part[i] = 0.0f;  // of warps that do not exist
   __syncthreads();
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
   const uint32_t stat0 = (uint32_t)__cvta_generic_to_shared(&stats[0][warp]);
-  const int64_t stride = (int64_t)gridDim.x * 2, first = (int64_t)blockIdx.x * 2;
+  const int64_t stride = own.blocks * 2, first = own.block * 2;
   // the rows left from the pair to copy next, and from the pair in hand
-  int64_t ahead = a.R - first, rows = a.R - first;
-  const typename Elem<DT>::type* from_x = x + first * a.ldx;
-  const typename Elem<DT>::type* from_dy = dy + first * a.lddy;
-  typename Elem<DT>::type* to_dx = dx + first * a.lddx;
+  int64_t ahead = own.R - first, rows = own.R - first;
+  const typename Elem<DT>::type* from_x = x + first * ldx;
+  const typename Elem<DT>::type* from_dy = dy + first * lddy;
+  typename Elem<DT>::type* to_dx = dx + first * lddx;
   const auto copy_pair = [&](int slot) {
     const uint32_t at = slot0 + slot * 4 * nt * 16;
     if (live && ahead > 0) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from_x) : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 16), "l"(from_dy)
-                   : "memory");
+      own.template copy<DT>(at, from_x);
+      own.template copy<DT>(at + nt * 16, from_dy);
     }
     if (live && ahead > 1) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 32),
-                   "l"(from_x + a.ldx)
-                   : "memory");
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + nt * 48),
-                   "l"(from_dy + a.lddy)
-                   : "memory");
+      own.template copy<DT>(at + nt * 32, from_x + ldx);
+      own.template copy<DT>(at + nt * 48, from_dy + lddy);
     }
     // the rows' statistics, for the warp: lanes 0, 1 the means, 2, 3 rstd
     if (lane < 4 && ahead > (lane & 1))
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(stat0 + slot * 512 + lane * 4),
-                   "l"((lane < 2 ? a.mean : a.rstd) + (a.R - ahead) + (lane & 1))
+                   "l"((lane < 2 ? a.mean : a.rstd) + own.row(own.R - ahead + (lane & 1)))
                    : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead -= stride;
-    from_x += stride * a.ldx;
-    from_dy += stride * a.lddy;
+    from_x += stride * ldx;
+    from_dy += stride * lddy;
   };
 #pragma unroll
   for (int i = 0; i < D; ++i) copy_pair(i);
   int slot = 0, side = 0;
-  for (; rows > 0; rows -= stride, to_dx += stride * a.lddx) {
+  for (; rows > 0; rows -= stride, to_dx += stride * lddx) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     __syncwarp();  // the statistics are other lanes' copies
     const float4 st = stats[slot][warp];
     const float mu[2] = {st.x, st.y}, rs[2] = {st.z, st.w};
-    const uint4* mine = ring + slot * 4 * nt + tid;
+    uint4* mine = ring + slot * 4 * nt + tid;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const auto sums = [&](auto edge) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      if (!(live && rows > q)) continue;
-      uint64_t h[P], d[P], s1 = 0, s2 = 0;
-      unpack_pairs<DT>(mine[2 * q * nt], h);
-      unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
-      const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
+      for (int q = 0; q < 2; ++q) {
+        if (!(live && rows > q)) continue;
+        uint4 rx = mine[2 * q * nt], rd = mine[(2 * q + 1) * nt];
+        if constexpr (edge.value) {
+          rx = and4(rx, masks.raw[kind]);
+          rd = and4(rd, masks.raw[kind]);
+        }
+        uint64_t h[P], d[P], s1 = 0, s2 = 0;
+        unpack_pairs<DT>(rx, h);
+        unpack_pairs<DT>(rd, d);
+        const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        h[j] = mul_f32x2(add_f32x2(h[j], m2), scale);
-        ab[j] = add_f32x2(ab[j], d[j]);
-        ag[j] = fma_f32x2(d[j], h[j], ag[j]);
-        d[j] = mul_f32x2(d[j], g[j]);
-        s1 = add_f32x2(s1, d[j]);
-        s2 = fma_f32x2(d[j], h[j], s2);
+        for (int j = 0; j < P; ++j) {
+          h[j] = mul_f32x2(add_f32x2(h[j], m2), scale);
+          ab[j] = add_f32x2(ab[j], d[j]);
+          ag[j] = fma_f32x2(d[j], h[j], ag[j]);
+          d[j] = mul_f32x2(d[j], g[j]);
+          s1 = add_f32x2(s1, d[j]);
+          s2 = fma_f32x2(d[j], h[j], s2);
+        }
+        s[2 * q] = sum_of(s1);
+        s[2 * q + 1] = sum_of(s2);
       }
-      s[2 * q] = sum_of(s1);
-      s[2 * q + 1] = sum_of(s2);
-    }
+    };
+    if (EDGE && edge_warp) sums(std::integral_constant<bool, EDGE>());
+    else sums(std::false_type());
     float t = warp_sum4(s, lane);
     if (warps > 1) {
       if ((lane & 7) == 0) part[side * 128 + (lane >> 3) * 32 + warp] = t;
@@ -693,30 +843,61 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
     t *= inv;
+    const auto finish = [&](auto edge) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float c1 = __shfl_sync(0xFFFFFFFFu, t, 16 * q);
-      const float c2 = __shfl_sync(0xFFFFFFFFu, t, 16 * q + 8);
-      if (!(live && rows > q)) continue;
-      uint64_t h[P], d[P];
-      unpack_pairs<DT>(mine[2 * q * nt], h);
-      unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
-      const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
-      const uint64_t n1 = both(-c1), n2 = both(-c2 * rs[q]);
+      for (int q = 0; q < 2; ++q) {
+        const float c1 = __shfl_sync(0xFFFFFFFFu, t, 16 * q);
+        const float c2 = __shfl_sync(0xFFFFFFFFu, t, 16 * q + 8);
+        if (!(live && rows > q)) continue;
+        uint64_t h[P], d[P];
+        unpack_pairs<DT>(mine[2 * q * nt], h);
+        unpack_pairs<DT>(mine[(2 * q + 1) * nt], d);
+        const uint64_t scale = both(rs[q]), m2 = both(-mu[q]);
+        const uint64_t n1 = both(-c1), n2 = both(-c2 * rs[q]);
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        h[j] = add_f32x2(h[j], m2);
-        d[j] = mul_f32x2(fma_f32x2(h[j], n2, fma_f32x2(d[j], g[j], n1)), scale);
+        for (int j = 0; j < P; ++j) {
+          h[j] = add_f32x2(h[j], m2);
+          d[j] = mul_f32x2(fma_f32x2(h[j], n2, fma_f32x2(d[j], g[j], n1)), scale);
+        }
+        if (edge.value && own.partial) mine[2 * q * nt] = pack_pairs<DT>(d);
+        else st_stream(reinterpret_cast<uint4*>(to_dx + (q ? lddx : 0)), pack_pairs<DT>(d));
       }
-      st_stream(reinterpret_cast<uint4*>(to_dx + (q ? a.lddx : 0)), pack_pairs<DT>(d));
-    }
+      if constexpr (edge.value) {
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (rows > q) own.template store_partial<DT>(to_dx + (q ? lddx : 0), mine + 2 * q * nt);
+        __syncwarp();  // before the slots' next copies
+      }
+    };
+    if (EDGE && edge_warp) finish(std::integral_constant<bool, EDGE>());
+    else finish(std::false_type());
     copy_pair(slot);
     slot = slot + 1 < D ? slot + 1 : 0;
   }
   asm volatile("griddepcontrol.launch_dependents;");  // the join may take this SM next
-  if (a.ws && live) {
-    float* pg = a.ws + (int64_t)blockIdx.x * a.C + c;
-    float* pb = pg + (int64_t)gridDim.x * a.C;
+  if (!a.ws) return;
+  float* pg = a.ws + (int64_t)blockIdx.x * a.C;
+  float* pb = pg + (int64_t)gridDim.x * a.C;
+  if constexpr (EDGE) {  // through the ring, all of its copies done and read
+    float* sum = reinterpret_cast<float*>(ring);
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    for (int side = 0; side < 2; ++side) {
+      __syncthreads();
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          float v[2];
+          upk_f32x2(side ? ab[j / 2] : ag[j / 2], v[0], v[1]);
+          if (own.has(j)) sum[c + j] = v[j & 1];
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < a.C; i += nt) (side ? pb : pg)[i] = sum[i];
+    }
+  } else if (live) {
+    pg += c;
+    pb += c;
 #pragma unroll
     for (int j = 0; j < P; j += 2) {  // C is a multiple of 4: the rows of ws are aligned
       *reinterpret_cast<ulonglong2*>(pg + 2 * j) = make_ulonglong2(ag[j], ag[j + 1]);
@@ -908,16 +1089,26 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
   constexpr int V = kVecElems<DT>;
   const bool vec = aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) && a.C % V == 0 &&
                    a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0;
-  if (vec && a.C <= 1024 * V) {
-    const NormBwdPlan p = bwd_plan(a.R, a.C, V);
-    const auto smem = [](int threads) { return kBwdGroups * 4 * threads * 16; };
-    const auto kernel = layernorm_bwd_ring_kernel<DT, WT>;
+  // Through the ring with rows of no alignment where a CTA gets a dozen of them
+  // and more than 1024 columns (bf16, through the ring and element by element:
+  // 16384 x 8001 175 and 391 us, 8000 x 2001 36 and 37, 4000 x 2001 27 and 23, 65536
+  // x 1023 125 and 117; fp32, whose elements are twice as wide: 16384 x 2001 78 and
+  // 80).
+  const bool edge = DT != GS_F32 && !vec && aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) &&
+                    (a.ldx - a.lddy) % V == 0 && (a.ldx - a.lddx) % V == 0;
+  const RingPlan ring = ring_plan(a.C, V, edge ? a.classes : 1, edge);
+  if (ring.ctas > 0 && (vec || (edge && a.C > 1024 && a.R >= 12 * ring.ctas))) {
+    const int64_t ctas = std::min(a.R, ring.ctas);
+    const int smem = kBwdGroups * 4 * ring.threads * 16;
+    void (*kernel)(NormBwdArgs) = layernorm_bwd_ring_kernel<DT, WT, false>;
+    if constexpr (DT != GS_F32)
+      if (edge) kernel = layernorm_bwd_ring_kernel<DT, WT, true>;
     int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
-    const cudaError_t e =
-        kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
+    const cudaError_t e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024,
+                                               kBwdGroups * 4 * 1024 * 16, &per_sm);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
-    *partials = p.ctas;
+    kernel<<<(unsigned)ctas, ring.threads, smem, stream>>>(a);
+    *partials = ctas;
   } else if (a.C <= 1024 * kElems) {
     // As many registers as the width leaves: 16384 x 4001 fp16 takes 117 us with
     // 512 threads of 128 registers, 189 us with 1024 of 64 that own four
@@ -962,7 +1153,7 @@ cudaError_t launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
   int64_t P = 0;
   if (R > 0) {
     const NormBwdArgs a{dy,   lddy, x,  ldx,  R,  C, gamma, mean, rstd, dx,
-                        lddx, ws,   aligned16(gamma)};
+                        lddx, ws,   aligned16(gamma), row_classes(ldx, dtype == GS_F32 ? 4 : 8)};
     cudaError_t e = cudaSuccess;
 #define GS_F(DT, WT) e = bwd_launch<DT, WT>(a, &P, stream);
     GS_NORM_TYPES(dtype, w_dtype, GS_F)

@@ -188,6 +188,66 @@ def test_constant_rows_small_eps(gs, R, C, dtype):
         assert ((dx.double() - ref).abs() <= tol).all()
 
 
+# many rows whose pitch is no multiple of 16 bytes, or is one and their width not
+MANY = [(700, 8177, 0), (640, 8001, 3), (2001, 4097, 1), (3100, 2049, 7), (5003, 1025, 0),
+        (2500, 2001, 23), (700, 8001, 7), (12001, 515, 0)]
+
+
+@pytest.mark.parametrize("dtype,wt", [("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("R,C,pad", MANY)
+def test_many_odd_rows_forward(gs, R, C, pad, dtype, wt):
+    fwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad)
+    fwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, offset=8, shift=30.0)
+    fwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, affine=False)
+
+
+@pytest.mark.parametrize("dtype,wt", [("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("R,C,pad", [(1900, 8177, 0), (1830, 6001, 1), (3700, 4001, 3), (5500, 3001, 7),
+                                     (7400, 2001, 23), (11003, 1025, 0)])
+def test_many_odd_rows_backward(gs, R, C, pad, dtype, wt):
+    bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad)
+    bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, offset=8, dw=torch.float16, sums=(True, False))
+    bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, affine=False, sums=(False, False))
+
+
+@pytest.mark.parametrize("pads", [(1, 1, 1), (1, 9, 17), (7, 2, 0)])
+def test_odd_rows_neighbours(gs, pads):
+    """What stands between odd rows, and in the rows beside them, is none of a row's
+    business: NaN there changes nothing; pitches that agree modulo 8 or do not."""
+    R, C = 2000, 8001
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+
+    def view(pad, like=None):
+        buf = torch.full((R, C + pad), float("nan"), dtype=torch.bfloat16, device=DEV)
+        v = buf[:, :C]
+        v.copy_(torch.randn(R, C, device=DEV, generator=gen) if like is None else like)
+        return v
+
+    x, dy = view(pads[0]), view(pads[1])
+    bad = torch.arange(3, R, 5, device=DEV)
+    keep = torch.ones(R, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    gamma = torch.rand(C, device=DEV, generator=gen) + 0.5
+    want = None
+    for spoilt in (False, True):
+        if spoilt:  # whole rows, their first and last columns beside the others' ends
+            x[bad], dy[bad] = float("nan"), float("inf")
+        y, dx = view(pads[2], 0.0 * x), view(pads[2], 0.0 * x)
+        mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+        gs.gs_layernorm_fwd(x, gamma, None, y, mean, rstd)
+        if not spoilt:
+            stats = mean.clone(), rstd.clone()
+        ws = torch.empty(gs.gs_layernorm_ws_bytes(R, C), dtype=torch.uint8, device=DEV)
+        gs.gs_layernorm_bwd(dy, x, gamma, *stats, dx, torch.empty(C, device=DEV),
+                            torch.empty(C, device=DEV), ws)
+        got = y[keep], dx[keep], mean[keep], rstd[keep]
+        assert all(torch.isfinite(t).all() for t in got)
+        assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.isnan(y._base[:, C:]).all() and torch.isnan(dx._base[:, C:]).all()
+        want = got
+
+
 def bwd_case(gs, R, C, dtype, wt, pad=0, offset=0, dw=torch.float32, affine=True, sums=(True, True)):
     gen = torch.Generator(device=DEV)
     gen.manual_seed(R * 7919 + C)
