@@ -159,6 +159,36 @@ cudaError_t kernel_blocks_per_sm(const void* kernel, int threads, int smem_bytes
   return cudaSuccess;
 }
 
+cudaError_t kernel_clusters(const void* kernel, int threads, int smem_bytes, int size,
+                            int* clusters) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, unsigned long long, int, int, int>, int> cache;
+  unsigned long long ctx = 0;
+  cudaError_t e = context_id(&ctx);
+  if (e != cudaSuccess) return e;
+  const auto key = std::make_tuple(kernel, ctx, threads, smem_bytes, size);
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(key);
+  if (it == cache.end()) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem_bytes;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)size;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    it = cache.emplace(key, n).first;
+  }
+  *clusters = it->second;
+  return cudaSuccess;
+}
+
 void record_cuda_error(cudaError_t e) { t_last_cuda_error = (int)e; }
 
 // The status word's address in the current context.

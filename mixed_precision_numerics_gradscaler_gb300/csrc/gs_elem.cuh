@@ -60,4 +60,32 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
+// ---- thread-block clusters ---------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile(
+      "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+          : "memory");
+}
+// Shared memory of another CTA of the cluster, at the address of p in ours.
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(d)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void store_remote_f32(float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote(p, rank)), "f"(v) : "memory");
+}
+
 }  // namespace gs

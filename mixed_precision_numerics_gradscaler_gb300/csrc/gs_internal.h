@@ -19,6 +19,10 @@ int sm_count();
 // context after cudaDeviceReset needs them again).  Thread-safe; cached
 // under the context's ID.
 cudaError_t kernel_blocks_per_sm(const void* kernel, int threads, int smem_bytes, int* blocks);
+// Resident clusters of `size` blocks of it on the device, after a call of
+// kernel_blocks_per_sm; cached likewise.
+cudaError_t kernel_clusters(const void* kernel, int threads, int smem_bytes, int size,
+                            int* clusters);
 int current_device();
 
 // ID of the CUDA context current on this thread (0 and true when none is

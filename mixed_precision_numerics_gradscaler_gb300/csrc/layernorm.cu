@@ -255,20 +255,23 @@ __device__ __forceinline__ float warp_sum4(const float* s, int lane) {
 // columns [lo, hi) of their vector only.  A first vector's other bytes belong to
 // the row before (or the gap), are read and left out; a last vector's are not
 // read.  Only the warps of those two threads run the code that masks.
-template <int W, bool EDGE>
+// Rows wider than a CTA's threads (WIDE) are a cluster's, rank 0 with the first of
+// them.
+template <int W, bool EDGE, bool WIDE>
 struct RowClass {
   int C, K, k, e;          // columns; classes, this CTA's, and its e
-  int64_t R, block, blocks;  // rows of the class; this CTA among the class's
+  int64_t R, block, blocks;  // rows of the class; this CTA (or cluster) among the class's
   int c, lo, hi;
   bool live, partial;
   __device__ __forceinline__ RowClass(int classes, int64_t rows, int64_t columns, int64_t ld)
       : C((int)columns), K(EDGE ? classes : 1) {
-    k = EDGE ? (int)(blockIdx.x % (uint32_t)K) : 0;
+    const uint32_t size = WIDE ? cluster_size() : 1, id = blockIdx.x / size;
+    k = EDGE ? (int)(id % (uint32_t)K) : 0;
     e = EDGE ? (int)(k * ld % W) : 0;
     R = EDGE ? (rows - k + K - 1) / K : rows;
-    block = EDGE ? blockIdx.x / (uint32_t)K : blockIdx.x;
-    blocks = EDGE ? gridDim.x / (uint32_t)K : gridDim.x;
-    c = (int)threadIdx.x * W - e;
+    block = EDGE ? id / (uint32_t)K : id;
+    blocks = gridDim.x / size / (uint32_t)K;
+    c = (int)(threadIdx.x + (WIDE ? cluster_rank() * blockDim.x : 0)) * W - e;
     live = c < C;
     lo = EDGE ? max(-c, 0) : 0;
     hi = EDGE ? min(C - c, W) : W;
@@ -345,16 +348,20 @@ __device__ __forceinline__ uint4 and4(const uint4& a, const uint4& b) {
 static int row_classes(int64_t ld, int W) { return ld % W == 0 ? 1 : W; }
 
 // CTAs of a ring kernel's grid, 1024 threads per SM, whole numbers of every
-// class; none if a row is too wide.
+// class; `size` CTAs per row.  None if a row is too wide.
+constexpr int kRingCluster = 8;  // most CTAs of a row
 struct RingPlan {
-  int threads;
+  int threads, size;
   int64_t ctas;
 };
-static RingPlan ring_plan(int64_t C, int W, int classes, bool edge) {
+static RingPlan ring_plan(int64_t C, int W, int classes, bool edge, int most) {
   const int64_t vectors = std::max<int64_t>((C + (edge ? W - 1 : 0) + W - 1) / W, 1);
-  const int64_t threads = (vectors + 31) / 32 * 32;
-  if (threads > 1024) return RingPlan{0, 0};
-  return RingPlan{(int)threads, (int64_t)sm_count() * (1024 / threads) / classes * classes};
+  int size = 1;
+  while (size < most && vectors > 1024 * size) size *= 2;
+  const int64_t threads = ((vectors + size - 1) / size + 31) / 32 * 32;
+  if (threads > 1024) return RingPlan{0, 0, 0};
+  const int64_t ctas = (int64_t)sm_count() * (1024 / threads) / (classes * size) * (classes * size);
+  return RingPlan{(int)threads, size, ctas};
 }
 
 constexpr int kFwdRows = 4, kFwdGroups = 3;  // forward: rows that share a barrier, groups in the ring
@@ -370,7 +377,7 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   __shared__ float4 columns[8];  // of the row, each warp's
   __shared__ EdgeMasks<DT> masks;
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const RowClass<W, EDGE> own(a.classes, a.R, a.C, a.ldx);
+  const RowClass<W, EDGE, false> own(a.classes, a.R, a.C, a.ldx);
   const int c = own.c, row8 = lane >> 3;  // row8: the group's row that this lane joins
   const bool live = own.live;
   const int64_t ldx = own.K * a.ldx, ldy = own.K * a.ldy;
@@ -622,7 +629,7 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
   // us from registers, 98 through the ring).
   if constexpr (DT != GS_F32) {
     const bool edge = !vec && aligned16(a.x) && aligned16(a.y) && (a.ldx - a.ldy) % V == 0;
-    const RingPlan p = ring_plan(a.C, V, edge ? a.classes : 1, edge);
+    const RingPlan p = ring_plan(a.C, V, edge ? a.classes : 1, edge, 1);
     if ((vec || (edge && a.C > 512)) && p.ctas > 0 && a.R >= p.ctas * kFwdRows) {
       const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
       const auto kernel =
@@ -736,16 +743,19 @@ __device__ __forceinline__ float2 row_sum2(float s1, float s2, float2* red, int 
 
 // Rows 16 bytes at a time, two per barrier; registers hold the weights and both
 // sums' accumulators.
-template <int DT, int WT, bool EDGE>
+template <int DT, int WT, bool EDGE, bool WIDE>
 __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormBwdArgs a) {
-  constexpr int W = kVecElems<DT>, D = kBwdGroups;
+  constexpr int W = kVecElems<DT>, D = kBwdGroups, S = WIDE ? kRingCluster : 1;
   extern __shared__ uint4 ring[];  // [D][2][x, dy][blockDim.x]
-  __shared__ float4 part4[2][32];  // per value of the pair's four: eight warps' sums a float4
-  float* const part = reinterpret_cast<float*>(part4);  // [2][4][32]
+  // Of each CTA of the row, per value of the pair's four: the warps' sums, four a
+  // float4; every CTA of the cluster has them all.
+  __shared__ float4 part4[2][S][32];
+  float* const part = reinterpret_cast<float*>(part4);  // [2][S][4][32]
+  const uint32_t ranks = WIDE ? cluster_size() : 1, rank = WIDE ? cluster_rank() : 0;
   __shared__ float4 stats[D][32];  // a pair's means and rstd, one copy per warp
   __shared__ EdgeMasks<DT> masks;
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const RowClass<W, EDGE> own(a.classes, a.R, a.C, a.ldx);
+  const RowClass<W, EDGE, WIDE> own(a.classes, a.R, a.C, a.ldx);
   const int c = own.c;
   const bool live = own.live;
   const int64_t ldx = own.K * a.ldx, lddy = own.K * a.lddy, lddx = own.K * a.lddx;
@@ -763,8 +773,9 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
   if (EDGE && live) masks.make(kind, own.lo, own.hi);
   const bool edge_warp = EDGE && __any_sync(0xFFFFFFFFu, own.partial);
   const float inv = __fdiv_rn(1.0f, (float)a.C);
-  for (int i = tid; i < 256; i += nt) part[i] = 0.0f;  // of warps that do not exist
+  for (int i = tid; i < 256 * S; i += nt) part[i] = 0.0f;  // of warps that do not exist
   __syncthreads();
+  if constexpr (WIDE) cluster_barrier();  // before another CTA's sums arrive
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
   const uint32_t stat0 = (uint32_t)__cvta_generic_to_shared(&stats[0][warp]);
@@ -833,12 +844,28 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
     if (EDGE && edge_warp) sums(std::integral_constant<bool, EDGE>());
     else sums(std::false_type());
     float t = warp_sum4(s, lane);
-    if (warps > 1) {
-      if ((lane & 7) == 0) part[side * 128 + (lane >> 3) * 32 + warp] = t;
-      __syncthreads();
-      const float4 p = part4[side][lane];  // value lane / 8, four warps of it
+    if (WIDE || warps > 1) {
+      if ((lane & 7) == 0) {
+        float* const at = part + ((side * S + rank) * 4 + (lane >> 3)) * 32 + warp;
+        if constexpr (WIDE) {
+          for (uint32_t q = 0; q < ranks; ++q) store_remote_f32(at, q, t);
+        } else {
+          *at = t;
+        }
+      }
+      if constexpr (WIDE) {
+        __syncwarp();
+        cluster_barrier();
+      } else {
+        __syncthreads();
+      }
+      t = 0.0f;
+#pragma unroll
+      for (int q = 0; q < S; ++q) {
+        const float4 p = part4[side][q][lane];  // value lane / 8, four warps of it
+        t += (p.x + p.y) + (p.z + p.w);
+      }
       side ^= 1;  // free again: every thread passes the next barrier after these reads
-      t = (p.x + p.y) + (p.z + p.w);
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     }
@@ -877,8 +904,8 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
   }
   asm volatile("griddepcontrol.launch_dependents;");  // the join may take this SM next
   if (!a.ws) return;
-  float* pg = a.ws + (int64_t)blockIdx.x * a.C;
-  float* pb = pg + (int64_t)gridDim.x * a.C;
+  float* pg = a.ws + (int64_t)(blockIdx.x / ranks) * a.C;
+  float* pb = pg + (int64_t)(gridDim.x / ranks) * a.C;
   if constexpr (EDGE) {  // through the ring, all of its copies done and read
     float* sum = reinterpret_cast<float*>(ring);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -889,11 +916,13 @@ __global__ void __launch_bounds__(1024, 1) layernorm_bwd_ring_kernel(const NormB
         for (int j = 0; j < W; ++j) {
           float v[2];
           upk_f32x2(side ? ab[j / 2] : ag[j / 2], v[0], v[1]);
-          if (own.has(j)) sum[c + j] = v[j & 1];
+          if (own.has(j)) sum[tid * W + j] = v[j & 1];
         }
       }
       __syncthreads();
-      for (int i = tid; i < a.C; i += nt) (side ? pb : pg)[i] = sum[i];
+      const int from = c - tid * W;  // the first thread's
+      for (int i = tid; i < nt * W; i += nt)
+        if (from + i >= 0 && from + i < a.C) (side ? pb : pg)[from + i] = sum[i];
     }
   } else if (live) {
     pg += c;
@@ -1081,6 +1110,7 @@ int64_t layernorm_partials(int64_t R, int64_t C) {
   int64_t most = long_partials(R);
   for (int64_t each : {8, 4})
     if (C <= 1024 * each) most = std::max(most, bwd_plan(R, C, each).ctas);
+    else if (C <= 1024 * each * kRingCluster) most = std::max(most, std::min<int64_t>(R, sm_count()));
   return most;
 }
 
@@ -1096,18 +1126,41 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
   // 80).
   const bool edge = DT != GS_F32 && !vec && aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) &&
                     (a.ldx - a.lddy) % V == 0 && (a.ldx - a.lddx) % V == 0;
-  const RingPlan ring = ring_plan(a.C, V, edge ? a.classes : 1, edge);
-  if (ring.ctas > 0 && (vec || (edge && a.C > 1024 && a.R >= 12 * ring.ctas))) {
-    const int64_t ctas = std::min(a.R, ring.ctas);
-    const int smem = kBwdGroups * 4 * ring.threads * 16;
-    void (*kernel)(NormBwdArgs) = layernorm_bwd_ring_kernel<DT, WT, false>;
+  const RingPlan ring = ring_plan(a.C, V, edge ? a.classes : 1, edge, kRingCluster);
+  if (ring.ctas > 0 && (vec || (edge && a.C > 1024 && a.R >= 12 * ring.ctas / ring.size))) {
+    const int size = ring.size, smem = kBwdGroups * 4 * ring.threads * 16;
+    void (*kernel)(NormBwdArgs) = size > 1 ? layernorm_bwd_ring_kernel<DT, WT, false, true>
+                                           : layernorm_bwd_ring_kernel<DT, WT, false, false>;
     if constexpr (DT != GS_F32)
-      if (edge) kernel = layernorm_bwd_ring_kernel<DT, WT, true>;
+      if (edge)
+        kernel = size > 1 ? layernorm_bwd_ring_kernel<DT, WT, true, true>
+                          : layernorm_bwd_ring_kernel<DT, WT, true, false>;
     int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
-    const cudaError_t e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024,
-                                               kBwdGroups * 4 * 1024 * 16, &per_sm);
+    cudaError_t e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024,
+                                         kBwdGroups * 4 * 1024 * 16, &per_sm);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, ring.threads, smem, stream>>>(a);
+    int64_t ctas = ring.ctas / size;  // clusters, of which only resident ones share the rows evenly
+    if (size > 1) {
+      int clusters = 0;
+      e = kernel_clusters(reinterpret_cast<const void*>(kernel), ring.threads, smem, size, &clusters);
+      if (e != cudaSuccess) return e;
+      const int k = edge ? a.classes : 1;
+      if (clusters < ctas) ctas = std::max(clusters / k, 1) * k;
+    }
+    ctas = std::min(a.R, ctas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * size));
+    cfg.blockDim = dim3((unsigned)ring.threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)size;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = size > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) return e;
     *partials = ctas;
   } else if (a.C <= 1024 * kElems) {
     // As many registers as the width leaves: 16384 x 4001 fp16 takes 117 us with

@@ -203,11 +203,21 @@ def test_many_odd_rows_forward(gs, R, C, pad, dtype, wt):
 
 @pytest.mark.parametrize("dtype,wt", [("bf16", "f32"), ("f16", "f16")])
 @pytest.mark.parametrize("R,C,pad", [(1900, 8177, 0), (1830, 6001, 1), (3700, 4001, 3), (5500, 3001, 7),
-                                     (7400, 2001, 23), (11003, 1025, 0)])
+                                     (7400, 2001, 23), (11003, 1025, 0), (1000, 16383, 0), (930, 9001, 1),
+                                     (470, 20001, 2), (200, 40001, 0)])
 def test_many_odd_rows_backward(gs, R, C, pad, dtype, wt):
     bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad)
     bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, offset=8, dw=torch.float16, sums=(True, False))
     bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, affine=False, sums=(False, False))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("R,C", [(1, 8200), (3, 65536), (37, 65528), (161, 12000), (600, 16384), (90, 32768), (77, 4100)])
+def test_wide_rows_backward(gs, R, C, dtype):
+    """Rows that several CTAs share."""
+    bwd_case(gs, R, C, TYPES[dtype], torch.float32)
+    bwd_case(gs, R, C, TYPES[dtype], torch.float32, pad=8, offset=8, sums=(False, True))
+    bwd_case(gs, R, C, TYPES[dtype], TYPES[dtype], affine=False, dw=TYPES[dtype])
 
 
 @pytest.mark.parametrize("pads", [(1, 1, 1), (1, 9, 17), (7, 2, 0)])
