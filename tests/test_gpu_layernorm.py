@@ -211,6 +211,14 @@ def test_many_odd_rows_backward(gs, R, C, pad, dtype, wt):
     bwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, affine=False, sums=(False, False))
 
 
+@pytest.mark.parametrize("dtype,wt", [("bf16", "f32"), ("f16", "f16")])
+@pytest.mark.parametrize("R,C,pad", [(400, 16384, 0), (310, 8200, 8), (170, 32768, 0), (80, 65536, 0),
+                                     (400, 12001, 1), (200, 16383, 0), (100, 40001, 2)])
+def test_wide_rows_forward(gs, R, C, pad, dtype, wt):
+    fwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad)
+    fwd_case(gs, R, C, TYPES[dtype], TYPES[wt], pad=pad, offset=8, shift=30.0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("R,C", [(1, 8200), (3, 65536), (37, 65528), (161, 12000), (600, 16384), (90, 32768), (77, 4100)])
 def test_wide_rows_backward(gs, R, C, dtype):
