@@ -71,17 +71,9 @@ struct AdamWStep {
   bool skip;           // the step is not taken: nothing is written
 };
 
-// One more CTA has read the step's number: how many had before.  Acquire and
-// release, so that the last one's write comes after every CTA's read.
-__device__ __forceinline__ uint32_t arrive(uint32_t* arrived) {
-  uint32_t before;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(arrived) : "memory");
-  return before;
-}
-
 // The step's factors, by the CTA's first thread for all of them (the
 // exponentials are a few hundred instructions).  1 - b^t = -expm1(t log b);
-// b = 0 gives 1.  The last CTA to have read the step's number counts it.
+// b = 0 gives 1.
 __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
   __shared__ AdamWStep shared;
   if (threadIdx.x == 0) {
@@ -94,13 +86,29 @@ __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
     s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
     s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
     shared = s;
-    if (!s.skip && arrive(a.arrived) == gridDim.x - 1) {
-      *a.arrived = 0;
-      *a.step = t;
-    }
   }
   __syncthreads();
   return shared;
+}
+
+// The last CTA to have read the step's number counts it.  Each arrives, its read
+// released, after the barrier behind the read, and asks which it was only at its
+// end, so that no chunk waits for the answer (a microsecond of a short list's 8).
+__device__ __forceinline__ uint32_t arrive(const AdamWArgs& a) {
+  uint32_t before = 0;
+  if (threadIdx.x == 0)
+    asm volatile("atom.release.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(a.arrived)
+                 : "memory");
+  return before;
+}
+__device__ __forceinline__ void count_step(const AdamWArgs& a, uint32_t before) {
+  if (threadIdx.x == 0 && before == gridDim.x - 1) {
+    __threadfence();  // every CTA's read comes before the write
+    *a.arrived = 0;
+    *a.step += 1;
+  }
 }
 
 // n / d, off by 2 ulp at most, for a normal d (here at least eps + the root of
@@ -195,6 +203,7 @@ __global__ void __launch_bounds__(kAdamThreads)
   if (blockIdx.x < n_chunks) ch = chunks[blockIdx.x];  // on its way while the factors are formed
   const AdamWStep s = step_of(a);
   if (s.skip) return;
+  const uint32_t before = arrive(a);
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     if (c != blockIdx.x) ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
@@ -233,6 +242,7 @@ __global__ void __launch_bounds__(kAdamThreads)
       if (ch.w_bf16) ch.w_bf16[i] = Elem<GS_BF16>::put(o.w);
     }
   }
+  count_step(a, before);
 }
 
 // Two elements' new moments and weights: adam1, both at once (f32x2
@@ -373,6 +383,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
   if (blockIdx.x < n_chunks) ch = chunks[blockIdx.x];  // on its way while the factors are formed
   const AdamWStep s = step_of(a);
   if (s.skip) return;
+  const uint32_t before = arrive(a);
   for (int64_t c = blockIdx.x; c < n_chunks; c += gridDim.x) {
     if (c != blockIdx.x) ch = chunks[c];
     const float keep = __fsub_rn(1.0f, __fmul_rn(a.lr, __fmul_rn(a.weight_decay, ch.decay)));
@@ -491,6 +502,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       }
     }
   }
+  count_step(a, before);
 }
 
 cudaError_t launch_master_update_adamw(const AChunk* d_chunks, int64_t n_chunks, int grad_dtype,
