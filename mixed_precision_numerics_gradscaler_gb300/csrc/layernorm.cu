@@ -711,6 +711,11 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
     }
   }
   if (vec) {
+    // A row's threads: a warp while it holds the row in four vectors a lane (fp32,
+    // 262144 x 128: 57 us with one vector each, 71 with a warp of four; 65536 x 512: 44,
+    // 99 with 256 threads), then CTAs with as many vectors a thread as keep several of
+    // them on an SM (16384 x 4096: 81 us with 256 threads, 95 with 512; 8192 x 8192: 85
+    // with 512, 106 with 1024).
     const int64_t nv = a.C / V;
     if (nv <= 32) GS_L(V, 32, 1);
     else if (nv <= 128) GS_L(V, 32, 4);
@@ -720,16 +725,16 @@ static cudaError_t fwd_launch(const NormArgs& a, cudaStream_t stream) {
     else if (nv <= 4096) GS_L(V, 1024, 4);
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   } else {
-    // a warp per row up to 128 columns, then CTAs of eight columns per thread
-    const auto width = [&](int each) { return (unsigned)((a.C + each * 32 - 1) / (each * 32) * 32); };
-    const auto some = [&](unsigned n) {  // CTAs, 8192 threads per SM: several rounds of them
-      return (unsigned)std::min<int64_t>(a.R, (int64_t)sm_count() * (8192 / n));
-    };
+    // A warp per row up to 128 columns (262144 x 100 bf16 64 us, 66 by the next), then
+    // CTAs of eight columns per thread, 8192 threads per SM: several rounds of them.
+    // (Sixteen columns per thread for twice the width: 4000 x 15000 117 us, 124 by the
+    // last, but 4000 x 10000 93 and 90.)
+    constexpr int kEach = 8;
+    const unsigned nt = (unsigned)((a.C + kEach * 32 - 1) / (kEach * 32) * 32);
     if (a.C <= 128) GS_L(1, 32, 4);
-    else if (a.C <= 8192)
-      layernorm_fwd_elem_kernel<DT, WT, 8><<<some(width(8)), width(8), 0, stream>>>(a);
-    else if (a.C <= 16384)
-      layernorm_fwd_elem_kernel<DT, WT, 16><<<some(width(16)), width(16), 0, stream>>>(a);
+    else if (a.C <= 1024 * kEach)
+      layernorm_fwd_elem_kernel<DT, WT, kEach>
+          <<<(unsigned)std::min<int64_t>(a.R, (int64_t)sm_count() * (8192 / nt)), nt, 0, stream>>>(a);
     else layernorm_fwd_long_kernel<DT, WT><<<rows, kLongThreads, 0, stream>>>(a);
   }
 #undef GS_L
