@@ -423,8 +423,9 @@ int fp8_gemm_block_scaled(const uint8_t* qa, const float* sa, const uint8_t* qb,
  * scaled gradients start.  16-bit or fp32 tensors in and out, every sum and
  * statistic in fp32.
  * Rows may lie further apart than their length: ld* is the distance of two
- * rows in elements (>= the row's length); the elements between are neither
- * read nor written.
+ * rows in elements (>= the row's length).  The elements between are not
+ * written and change nothing; a load of 16 bytes that begins in one of them
+ * and ends in a row may span a few.
  * --------------------------------------------------------------------- */
 
 /* Layer norm of each row of x [R, C]:
