@@ -66,7 +66,8 @@ __device__ __forceinline__ float decode_e4m3(uint8_t q) {
 }
 
 struct AdamWStep {
-  float coef, c1, c2;  // gradient factor; lr / (1 - b1^t); 1 / sqrt(1 - b2^t)
+  // gradient factor; lr / (1 - b1^t) and 1 / sqrt(1 - b2^t), both times eps_shift
+  float coef, c1, c2;
   uint32_t key;        // of the random bits, without the place's high word
   bool skip;           // the step is not taken: nothing is written
 };
@@ -82,8 +83,8 @@ __device__ __forceinline__ AdamWStep step_of(const AdamWArgs& a) {
     const float nrm = a.max_norm > 0.0f ? *a.grad_norm : 0.0f;
     s.skip = *a.found_inf != 0;
     s.coef = a.max_norm > 0.0f && nrm > a.max_norm ? __fdiv_rn(a.max_norm, nrm) : 1.0f;
-    s.c1 = __fdiv_rn(a.lr, -expm1f((float)t * a.log_beta1));
-    s.c2 = __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
+    s.c1 = a.eps_shift * __fdiv_rn(a.lr, -expm1f((float)t * a.log_beta1));
+    s.c2 = a.eps_shift * __fdiv_rn(1.0f, __fsqrt_rn(-expm1f((float)t * a.log_beta2)));
     s.key = a.seed + 0x9E3779B9u * (uint32_t)t;
     shared = s;
   }
@@ -111,8 +112,10 @@ __device__ __forceinline__ void count_step(const AdamWArgs& a, uint32_t before) 
   }
 }
 
-// n / d, off by 2 ulp at most, for a normal d (here at least eps + the root of
-// the smallest fp32 number, or 0: a quotient of NaN or Inf).
+// n / d, off by 2 ulp at most, where d and 1 / d are normal numbers (or d is 0:
+// NaN or Inf).  Here d = r c2 + eps: a root is 0 or at least 2^-75, and r c2 at
+// most 2^76 (both times eps_shift); eps by itself is brought into range by the
+// factor eps_shift of numerator and divisor.
 __device__ __forceinline__ float quotient(float n, float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));

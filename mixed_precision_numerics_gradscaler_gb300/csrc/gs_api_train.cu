@@ -358,7 +358,10 @@ int gs_master_update_adamw(const gs_adamw_list* list, float lr, float beta1, flo
   a.lr = lr;
   a.beta1 = beta1;
   a.beta2 = beta2;
-  a.eps = eps;
+  // An eps with no normal reciprocal is brought to one that has: 2^23 times the
+  // smallest subnormal is 2^-126, a quarter of the largest number below 2^126.
+  a.eps_shift = eps > 0.0f && eps < 0x1p-126f ? 0x1p23f : eps > 0x1p126f ? 0.25f : 1.0f;
+  a.eps = eps * a.eps_shift;
   a.weight_decay = weight_decay;
   a.max_norm = max_norm;
   a.one_beta1 = (float)(1.0 - (double)beta1);

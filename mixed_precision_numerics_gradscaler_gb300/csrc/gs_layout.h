@@ -121,7 +121,9 @@ __host__ __device__ inline int64_t achunk_head(const float* w, const uint16_t* w
 }
 
 struct AdamWArgs {
-  float lr, beta1, beta2, eps, weight_decay, max_norm;
+  float lr, beta1, beta2, weight_decay, max_norm;
+  float eps;                    // times eps_shift
+  float eps_shift;              // power of two, 1 for an eps in [2^-126, 2^126]
   float one_beta1, one_beta2;   // fp32(1 - beta), from double
   float log_beta1, log_beta2;   // fp32(log beta), from double (-Inf for 0)
   const float* grad_norm;

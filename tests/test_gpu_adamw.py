@@ -364,3 +364,25 @@ def test_refusals(gs):
             gs.gs_master_update_adamw(al, step, found, **{"lr": 1e-3, **bad})
     torch.cuda.synchronize()
     assert int(step) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("off", [0, 1])
+def test_eps_whose_reciprocal_is_no_normal_number(gs, e4m3, off):
+    """eps below 2^-126, where the divisor is eps alone (v = 0, with m = 0 and
+    with m small enough for v to underflow), and above 2^126."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(21)
+    for eps in (1e-45, 1e-41, 1.1e-38, 1.2e-38):
+        p = Params(gs, [1000, 8192], e4m3, off=off, zero=True)
+        for g in p.g:
+            g.copy_(torch.randn(g.numel(), device=DEV, generator=gen) * 1e-25)
+            g[::3] = 0
+        for _ in range(2):
+            run_and_check(gs, p, dict(HP, eps=f32(eps)))
+    for eps in (1e38, 3.4e38):
+        p = Params(gs, [1000, 8192], e4m3, off=off, zero=True)
+        for g in p.g:
+            g.copy_((torch.rand(g.numel(), device=DEV, generator=gen) - 0.5) * 4e18)
+        run_and_check(gs, p, dict(HP, lr=f32(1e20), eps=f32(eps), weight_decay=0.0))
+        assert (p.w[0].abs() > 0.01).any()
