@@ -368,9 +368,12 @@ def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torc
                            grad_norm: torch.Tensor | None = None, seed: int = 0,
                            stream=None) -> None:
     """step: int64 [1], the number of updates made so far (advanced on the
-    device unless found_inf is set)."""
+    device unless found_inf is set), this list's own; found_inf: int32 [1];
+    grad_norm: float32 [1]."""
     _check(_lib.gs_master_update_adamw(alist.handle, lr, beta1, beta2, eps, weight_decay, max_norm,
-                                       _ptr(grad_norm), _ptr(found_inf), _ptr(step), seed,
+                                       _scalar(grad_norm, "grad_norm", torch.float32),
+                                       _scalar(found_inf, "found_inf", torch.int32),
+                                       _scalar(step, "step", torch.int64), seed,
                                        _stream(stream)), "gs_master_update_adamw")
 
 
@@ -484,6 +487,14 @@ def _vector(t: torch.Tensor | None, name: str, n: int, dtype: torch.dtype) -> in
         return None
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of {n} elements and {dtype}")
+    return t.data_ptr()
+
+
+def _scalar(t: torch.Tensor | None, name: str, dtype: torch.dtype) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != 1:
+        raise ValueError(f"{name} must be of one element and {dtype}")
     return t.data_ptr()
 
 

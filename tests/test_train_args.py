@@ -68,3 +68,25 @@ def test_adamw_arguments(gs):
     for bad in (dict(lr=-1.0), dict(lr=nan), dict(b1=1.0), dict(b1=nan), dict(b2=-0.5), dict(eps=-1.0),
                 dict(wd=inf), dict(mx=nan), dict(s=ctypes.c_void_p(0x1004)), dict(f=ctypes.c_void_p(0x1002))):
         assert step(**bad) == gs.GS_ERR_ARG, bad
+
+
+class NoList:
+    handle = None       # the library refuses it: no call gets as far as the device
+
+
+def test_adamw_scalars_have_the_type_the_kernel_reads(gs):
+    """The step's number is read and written as 8 bytes: a tensor of another
+    type or length is refused before the library sees its address."""
+    import torch
+    one = lambda dtype, n=1: torch.zeros(n, dtype=dtype)  # noqa: E731
+    good = dict(step=one(torch.int64), found_inf=one(torch.int32), grad_norm=one(torch.float32))
+    with pytest.raises(gs.GsError):
+        gs.gs_master_update_adamw(NoList, lr=1e-3, stream=0, **good)
+    with pytest.raises(gs.GsError):
+        gs.gs_master_update_adamw(NoList, lr=1e-3, stream=0, **{**good, "grad_norm": None, "step": one(torch.int64)[0]})
+    for bad in (dict(step=one(torch.int32)), dict(step=one(torch.float32)), dict(step=one(torch.int64, 2)),
+                dict(step=one(torch.int64, 0)), dict(found_inf=one(torch.bool)), dict(found_inf=one(torch.int64)),
+                dict(found_inf=one(torch.int32, 3)), dict(grad_norm=one(torch.float64)),
+                dict(grad_norm=one(torch.float16)), dict(grad_norm=one(torch.float32, 2))):
+        with pytest.raises(ValueError):
+            gs.gs_master_update_adamw(NoList, lr=1e-3, stream=0, **{**good, **bad})
