@@ -536,8 +536,9 @@ def gs_layernorm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | No
     wt = torch.float32 if gamma is None else gamma.dtype
     d = dgamma if dgamma is not None else dbeta
     dt = torch.float32 if d is None else d.dtype
-    if ws is not None and ws.numel() * ws.element_size() < gs_layernorm_ws_bytes(R, C):
-        raise ValueError("ws is smaller than gs_layernorm_ws_bytes(R, C)")
+    if ws is not None and (not ws.is_contiguous() or
+                           ws.numel() * ws.element_size() < gs_layernorm_ws_bytes(R, C)):
+        raise ValueError("ws must be contiguous, of gs_layernorm_ws_bytes(R, C) bytes at least")
     _check(_lib.gs_layernorm_bwd(_ptr(dy), lddy, _ptr(x), ldx, _DTYPES[x.dtype], R, C,
                                  _vector(gamma, "gamma", C, wt), _DTYPES[wt],
                                  _vector(mean, "mean", R, torch.float32),

@@ -90,3 +90,19 @@ def test_adamw_scalars_have_the_type_the_kernel_reads(gs):
                 dict(grad_norm=one(torch.float16)), dict(grad_norm=one(torch.float32, 2))):
         with pytest.raises(ValueError):
             gs.gs_master_update_adamw(NoList, lr=1e-3, stream=0, **{**good, **bad})
+
+
+def test_layernorm_workspace_is_one_piece(gs):
+    """The workspace is written from its first byte on: a view with gaps, whose
+    elements would count as enough, is refused, and so is a short one."""
+    import torch
+    x, mean, rstd, dg = torch.zeros(4, 64), torch.zeros(4), torch.ones(4), torch.zeros(64)
+    n = gs.gs_layernorm_ws_bytes(4, 64)
+    assert n >= 4 * 2 * 64 * 4
+    bwd = lambda ws: gs.gs_layernorm_bwd(x, x, None, mean, rstd, torch.zeros_like(x), dg, None, ws, stream=0)  # noqa: E731
+    with pytest.raises(ValueError):
+        bwd(torch.zeros(2 * n, dtype=torch.uint8)[::2])
+    with pytest.raises(ValueError):
+        bwd(torch.zeros(n - 1, dtype=torch.uint8))
+    with pytest.raises(gs.GsError):                  # host memory
+        bwd(torch.zeros(n, dtype=torch.uint8))
