@@ -342,3 +342,33 @@ def test_refusals(gs):
     # no rows: nothing to do
     gs.gs_token_logprob(x[:0], t[:0], lp[:0])
     gs.gs_token_logprob_bwd(x[:0], t[:0], lp[:0], g[:0], d[:0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [700, 32003, 128256, 200001, 1000003, 16000001])
+def test_backward_sum_of_many_equal_terms(gs, V, dtype):
+    """|lse| > 256 and equal logits: p = 1 / V.  The row's sum is formed anew to
+    be closer than lse's own rounding; equal terms added one after another
+    in fp32 would all round alike (1e-5 off at V = 128256, 1e-3 at 16 M).
+    Tolerance, in 2^-24: the two products with log2 e and the difference from
+    log s round d = ln V three times, two exponentials by 8 in all, blocks of
+    terms and the threads' join by 16, independently of V."""
+    tol = (3 * math.log(V) + 24) * E
+    rows = 3 if V < 1 << 20 else 1
+    for value, pad in ((300.0, 0), (-300.0, 1), (1000.0, 5)):
+        x, _ = view(rows, V, pad, TYPES[dtype], 0)
+        x.fill_(value)
+        t = torch.full((rows,), -1, device=DEV)
+        t[0] = V // 2
+        lse = torch.full((rows,), value + math.log(V), dtype=torch.float64, device=DEV).float()
+        g = torch.ones(rows, device=DEV)
+        outs = [torch.empty(rows, V, device=DEV)]
+        gs.gs_token_logprob_bwd(x, t, lse, g, outs[0], loss_scale=torch.full((1,), -float(V), device=DEV))
+        if dtype == "f32":
+            gs.gs_token_logprob_bwd(x, t, lse, g, x, loss_scale=torch.full((1,), -float(V), device=DEV))
+            outs.append(x)
+        for d in outs:
+            d = d.double()
+            d[0, V // 2] += V
+            assert ((d[0] - 1).abs() <= tol + V * E * (torch.arange(V, device=DEV) == V // 2)).all()
+            assert (d[1:] == 0).all()          # no target, no gradient
