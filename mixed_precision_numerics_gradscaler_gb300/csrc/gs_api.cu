@@ -143,8 +143,10 @@ cudaError_t kernel_blocks_per_sm(const void* kernel, int threads, int smem_bytes
   if (ce != cudaSuccess) return ce;
   const auto key = std::make_tuple(kernel, ctx, threads, smem_bytes);
   std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(key);
-  if (it == cache.end()) {
+  const auto it = cache.find(key);
+  if (it != cache.end()) {
+    *blocks = it->second;
+  } else {
     if (smem_bytes > 48 * 1024) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            smem_bytes);
@@ -153,9 +155,12 @@ cudaError_t kernel_blocks_per_sm(const void* kernel, int threads, int smem_bytes
     int occ = 0;
     cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kernel, threads, smem_bytes);
     if (e != cudaSuccess) return e;
-    it = cache.emplace(key, occ).first;
+    *blocks = occ;
+    try {
+      cache.emplace(key, occ);
+    } catch (...) {  // no memory to remember it: nothing may throw across the C ABI
+    }
   }
-  *blocks = it->second;
   return cudaSuccess;
 }
 
@@ -168,8 +173,10 @@ cudaError_t kernel_clusters(const void* kernel, int threads, int smem_bytes, int
   if (e != cudaSuccess) return e;
   const auto key = std::make_tuple(kernel, ctx, threads, smem_bytes, size);
   std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(key);
-  if (it == cache.end()) {
+  const auto it = cache.find(key);
+  if (it != cache.end()) {
+    *clusters = it->second;
+  } else {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)size);
     cfg.blockDim = dim3((unsigned)threads);
@@ -183,9 +190,12 @@ cudaError_t kernel_clusters(const void* kernel, int threads, int smem_bytes, int
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
-    it = cache.emplace(key, n).first;
+    *clusters = n;
+    try {
+      cache.emplace(key, n);
+    } catch (...) {  // as above
+    }
   }
-  *clusters = it->second;
   return cudaSuccess;
 }
 
