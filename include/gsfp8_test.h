@@ -14,6 +14,8 @@
 #ifndef GSFP8_TEST_H
 #define GSFP8_TEST_H
 
+#include <stdint.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -24,6 +26,11 @@ extern "C" {
  * GS_ERR_TIMEOUT.  on == 0 restores normal operation.  Process-wide; set it
  * only while no other thread launches that kernel.  Returns GS_OK. */
 int gs_test_set_stall(int on);
+
+/* r[i] = sqrt(v[i]) (device, n even, not overlapping) by the code that forms
+ * the roots of the AdamW step with 8-bit moments, whose outputs show a root
+ * only through eight-bit codes and block scales. */
+int gs_test_adamw_root(const float* v, float* r, int64_t n, void* stream);
 
 #ifdef __cplusplus
 }

@@ -79,6 +79,7 @@ def _load_lib() -> ctypes.CDLL:
         "gs_noalloc_limits": (ci, [ctypes.POINTER(i32), ctypes.POINTER(i64), ctypes.POINTER(i64)]),
         "fp8_gemm_block_scaled": (ci, [vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp, vp]),
         "gs_test_set_stall": (ci, [ci]),
+        "gs_test_adamw_root": (ci, [vp, vp, i64, vp]),
         "gs_layernorm_fwd": (ci, [vp, i64, ci, i64, i64, vp, vp, ci, f32, vp, i64, vp, vp, vp]),
         "gs_layernorm_ws_bytes": (ctypes.c_size_t, [i64, i64]),
         "gs_layernorm_bwd": (ci, [vp, i64, vp, i64, ci, i64, i64, vp, ci, vp, vp, vp, i64, vp, vp,
@@ -597,6 +598,14 @@ def gs_test_set_stall(on: bool) -> None:
     """Test hook: the block-scaled FP8 GEMM issues no TMA loads while on, so
     its bounded waits run out and it reports GS_ERR_TIMEOUT."""
     _check(_lib.gs_test_set_stall(1 if on else 0), "gs_test_set_stall")
+
+
+def gs_test_adamw_root(v: torch.Tensor, r: torch.Tensor, stream=None) -> None:
+    """Test hook: r = sqrt(v) as the 8-bit AdamW step forms it; float32, of one
+    even length."""
+    n = v.numel()
+    _check(_lib.gs_test_adamw_root(_vector(v, "v", n, torch.float32), _vector(r, "r", n, torch.float32),
+                                   n, _stream(stream)), "gs_test_adamw_root")
 
 
 def gs_device_status(stream=None) -> int:

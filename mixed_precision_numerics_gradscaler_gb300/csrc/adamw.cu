@@ -126,8 +126,8 @@ __device__ __forceinline__ float quotient(float n, float d) {
 // h = y / 2 with y near 1 / sqrt(v), then s + h (v - s^2), the residual exact by
 // a fused multiply-add (Markstein, "IA-64 and Elementary Functions", 2000,
 // chapter 9: one such step from an estimate within an ulp rounds correctly
-// but where y is too coarse; all significands of both binades were compared
-// with the IEEE root on the device, and a test does so again).
+// but where y is too coarse; a test compares it with the IEEE root at every
+// significand of two binades, at the middle and at both ends of the range).
 __device__ __forceinline__ uint64_t sqrt_f32x2(uint64_t v) {
   float v0, v1, y0, y1;
   upk_f32x2(v, v0, v1);
@@ -136,6 +136,17 @@ __device__ __forceinline__ uint64_t sqrt_f32x2(uint64_t v) {
   const uint64_t y = pk_f32x2(y0, y1), s = mul_f32x2(v, y);
   const uint64_t e = fma_f32x2(s ^ 0x8000000080000000ull, s, v);
   return fma_f32x2(e, mul_f32x2(y, pk_f32x2(0.5f, 0.5f)), s);
+}
+// The roots of any two, rounded to nearest.
+__device__ __forceinline__ void roots2(uint64_t v, float* r) {
+  float v0, v1;
+  upk_f32x2(v, v0, v1);
+  if (fminf(v0, v1) >= 0x1p-96f && fmaxf(v0, v1) <= 0x1p96f) {
+    upk_f32x2(sqrt_f32x2(v), r[0], r[1]);
+  } else {
+    r[0] = __fsqrt_rn(v0);
+    r[1] = __fsqrt_rn(v1);
+  }
 }
 
 // One element's new moments and weight.
@@ -273,14 +284,7 @@ __device__ __forceinline__ Adam2 adam2(const AdamWArgs& a, const AdamWStep& s, f
                 product_f32x2(a, mul_f32x2(g, pk1(a.one_beta2)), g));
   Adam2 o;
   upk_f32x2(m, o.m[0], o.m[1]);
-  float v0, v1;
-  upk_f32x2(v, v0, v1);
-  if (fminf(v0, v1) >= 0x1p-96f && fmaxf(v0, v1) <= 0x1p96f) {
-    upk_f32x2(sqrt_f32x2(v), o.r[0], o.r[1]);
-  } else {
-    o.r[0] = __fsqrt_rn(v0);
-    o.r[1] = __fsqrt_rn(v1);
-  }
+  roots2(v, o.r);
   const uint64_t num = mul_f32x2(m, pk1(s.c1));
   const uint64_t den = fma_f32x2(pk_f32x2(o.r[0], o.r[1]), pk1(s.c2), pk1(a.eps));
   float n0, n1, d0, d1;
@@ -526,6 +530,19 @@ cudaError_t launch_master_update_adamw(const AChunk* d_chunks, int64_t n_chunks,
     GS_F(adamw_e4m3_kernel)
   }
 #undef GS_F
+  return cudaGetLastError();
+}
+
+// The step's roots by themselves, for a test (n even).
+__global__ void __launch_bounds__(kAdamThreads)
+    adamw_root_kernel(const float* __restrict__ v, float* __restrict__ r, int64_t n) {
+  const int64_t step = (int64_t)gridDim.x * kAdamThreads * 2;
+  for (int64_t i = ((int64_t)blockIdx.x * kAdamThreads + threadIdx.x) * 2; i < n; i += step)
+    roots2(pk_f32x2(v[i], v[i + 1]), r + i);
+}
+cudaError_t launch_adamw_root(const float* v, float* r, int64_t n, cudaStream_t stream) {
+  const int64_t ctas = (n / 2 + kAdamThreads - 1) / kAdamThreads, most = (int64_t)sm_count() * 8;
+  adamw_root_kernel<<<(unsigned)(ctas < most ? ctas : most), kAdamThreads, 0, stream>>>(v, r, n);
   return cudaGetLastError();
 }
 

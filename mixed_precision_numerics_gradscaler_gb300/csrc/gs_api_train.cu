@@ -13,6 +13,7 @@
 #include "gs_args.h"
 #include "gs_internal.h"
 #include "gsfp8.h"
+#include "gsfp8_test.h"
 
 struct gs_adamw_list {
   int device;
@@ -377,6 +378,17 @@ int gs_master_update_adamw(const gs_adamw_list* list, float lr, float beta1, flo
   const cudaError_t e = launch_master_update_adamw(list->d_chunks, list->n_chunks,
                                                    list->grad_dtype, list->moments, a,
                                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+int gs_test_adamw_root(const float* v, float* r, int64_t n, void* stream) {
+  if (n < 0 || n % 2 || !mul_ok(n, 4)) return GS_ERR_SHAPE;
+  if (n == 0) return GS_OK;
+  if (!v || !r) return GS_ERR_NULL;
+  if (!aligned(v, 4) || !aligned(r, 4) || !device_reachable(v) || !device_reachable(r) ||
+      overlaps(v, (size_t)n * 4, r, (size_t)n * 4))
+    return GS_ERR_ARG;
+  const cudaError_t e = launch_adamw_root(v, r, n, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GS_OK : cuda_fail(e);
 }
 

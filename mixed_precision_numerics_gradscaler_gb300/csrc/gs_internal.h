@@ -120,6 +120,7 @@ cudaError_t launch_token_logprob_bwd(const void* logits, int64_t ld, int dtype, 
                                      cudaStream_t stream);
 cudaError_t launch_master_update_adamw(const AChunk* d_chunks, int64_t n_chunks, int grad_dtype,
                                        int moments, const AdamWArgs& args, cudaStream_t stream);
+cudaError_t launch_adamw_root(const float* v, float* r, int64_t n, cudaStream_t stream);
 cudaError_t launch_set_state(float* scale, int32_t* tracker, float h_scale, int32_t h_tracker,
                              cudaStream_t stream);
 

@@ -386,3 +386,53 @@ def test_eps_whose_reciprocal_is_no_normal_number(gs, e4m3, off):
             g.copy_((torch.rand(g.numel(), device=DEV, generator=gen) - 0.5) * 4e18)
         run_and_check(gs, p, dict(HP, lr=f32(1e20), eps=f32(eps), weight_decay=0.0))
         assert (p.w[0].abs() > 0.01).any()
+
+
+def root_bits(gs, bits):
+    """The bits of the 8-bit step's roots of the numbers with these bits."""
+    v = torch.from_numpy(bits.view(np.int32)).to(DEV).view(torch.float32)
+    r = torch.full_like(v, 7.0)
+    gs.gs_test_adamw_root(v, r)
+    return r.cpu().numpy().view(np.uint32)
+
+
+@pytest.mark.parametrize("exponent", [0, -96, 94])
+def test_root_of_every_significand_of_two_binades(gs, exponent):
+    """[2^e, 2^(e + 2)) whole, in the middle and at both ends of the range
+    that has the step's own root: the bits of the IEEE root (numpy's)."""
+    first = (127 + exponent) << 23
+    bits = np.arange(first, first + (1 << 24), dtype=np.uint32)
+    want = np.sqrt(bits.view(np.float32)).view(np.uint32)
+    assert np.array_equal(root_bits(gs, bits), want)
+    # paired otherwise: each number's root is its own lane's
+    order = np.random.default_rng(exponent + 100).permutation(bits.size)[:1 << 22]
+    assert np.array_equal(root_bits(gs, bits[order]), want[order])
+
+
+def test_roots_over_the_whole_type(gs):
+    """Random pairs over every exponent, both kinds of number in a pair
+    included, and zeros, subnormals and infinities: the IEEE root's bits; NaN
+    for NaN."""
+    rng = np.random.default_rng(11)
+    bits = rng.integers(0, 0x7F800001, 1 << 22, dtype=np.uint32)
+    ends = np.array([0, 1, 2, 0x007FFFFF, 0x00800000, 0x7F7FFFFF, 0x7F800000,
+                     (127 - 96) << 23, ((127 - 96) << 23) - 1, (127 + 96) << 23, ((127 + 96) << 23) + 1], np.uint32)
+    bits = np.concatenate([bits, np.repeat(ends, ends.size), np.tile(ends, ends.size), ends, ends])
+    bits = np.concatenate([bits, np.stack([np.repeat(ends, ends.size), np.tile(ends, ends.size)], 1).ravel()])
+    want = np.sqrt(bits.view(np.float32)).view(np.uint32)
+    assert np.array_equal(root_bits(gs, bits), want)
+    nan = np.array([0x7FC00000, 0x3F800000, 0x3F800000, 0x7FC00000, 0x7FC00000, 0], np.uint32)
+    got = root_bits(gs, nan).view(np.float32)
+    assert np.array_equal(np.isnan(got), np.isnan(nan.view(np.float32))) and got[1] == got[2] == 1 and got[5] == 0
+
+
+def test_root_refusals(gs):
+    v = torch.ones(64, device=DEV)
+    with pytest.raises(gs.GsError):
+        gs.gs_test_adamw_root(v[:63], torch.empty(63, device=DEV))
+    with pytest.raises(gs.GsError):
+        gs.gs_test_adamw_root(v, v)
+    with pytest.raises(ValueError):
+        gs.gs_test_adamw_root(v, torch.empty(62, device=DEV))
+    with pytest.raises(gs.GsError):
+        gs.gs_test_adamw_root(v.cpu(), torch.empty(64, device=DEV))
