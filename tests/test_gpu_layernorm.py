@@ -445,3 +445,103 @@ def test_refusals(gs):
         gs.gs_layernorm_bwd(x, x, None, s, s, y, dg, None, ws[4:])  # not 16-byte aligned
     with pytest.raises(gs.GsError):
         gs.gs_layernorm_bwd(x, x, None, s, s, y, s[:1].expand(64).clone()[:64], y[0], ws)
+
+
+# One size at least for every way through the rows: a warp's, a CTA's, the copy
+# rings of one and of several CTAs, on and off alignment, element by element,
+# rows read again.  (dtype, R, C, pad, offset)
+WAYS = [("bf16", 61, 256, 0, 0), ("f32", 61, 512, 0, 0), ("f16", 61, 2048, 0, 0), ("f32", 61, 4096, 0, 0),
+        ("bf16", 61, 16384, 0, 0), ("f32", 61, 16384, 0, 0), ("bf16", 61, 40000, 0, 0), ("f32", 61, 20000, 0, 0),
+        ("bf16", 5003, 4096, 0, 0), ("f16", 20003, 200, 0, 0), ("f32", 3001, 4096, 0, 0), ("bf16", 1300, 8192, 8, 8),
+        ("f16", 5001, 4097, 0, 0), ("bf16", 12001, 1025, 0, 0), ("bf16", 2001, 8001, 3, 8),
+        ("bf16", 403, 16384, 0, 0), ("f16", 170, 32768, 0, 0), ("bf16", 83, 65536, 0, 0), ("f32", 100, 16384, 0, 0),
+        ("f16", 1003, 12001, 1, 0), ("bf16", 470, 20001, 2, 0), ("bf16", 200, 40001, 0, 0),
+        ("bf16", 2003, 100, 1, 1), ("f32", 61, 1001, 0, 1), ("f16", 61, 3001, 0, 1), ("bf16", 61, 5001, 0, 1),
+        ("f32", 61, 8001, 0, 1), ("f16", 61, 20001, 0, 1), ("bf16", 152, 8192, 0, 0), ("bf16", 153, 8192, 0, 0),
+        ("bf16", 303, 8192, 0, 0), ("bf16", 305, 8192, 0, 0), ("f16", 9001, 264, 0, 0)]
+
+
+def telling_columns(C):
+    """The first and last ones, those about multiples of 256, and some others
+    (all of a short row), in no order."""
+    rng = np.random.default_rng(C)
+    if C <= 2048:
+        return rng.permutation(C)
+    near = (np.arange(0, C + 1, 256)[:, None] + np.arange(-1, 2)).ravel()
+    some = np.concatenate([np.arange(40), np.arange(C - 40, C), near, rng.integers(0, C, 300)])
+    return rng.permutation(np.unique(some[(some >= 0) & (some < C)]))
+
+
+def one_per_row(R, C, columns, first):
+    return torch.from_numpy(columns[(np.arange(R) + first) % columns.size]).to(DEV)
+
+
+@pytest.mark.parametrize("dtype,R,C,pad,offset", WAYS)
+def test_forward_every_column_counts_once(gs, dtype, R, C, pad, offset):
+    """Rows of zeros but one 1: mean 1 / C, variance (1 - 1 / C) / C.  A column
+    left out or read twice makes them 0 or twice that, whatever C is; the
+    statistics are allowed 2^-16 of themselves, y two roundings of the type."""
+    dt = TYPES[dtype]
+    x, _ = rows(R, C, pad, dt, torch.Generator(device=DEV), 0.0, 0.0, offset)
+    y, _ = rows(R, C, pad, dt, torch.Generator(device=DEV), 0.0, 7.0, offset)
+    mean, rstd = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+    columns, at = telling_columns(C), torch.arange(R, device=DEV)
+    wm, wr = 1 / C, C / (1 - 1 / C) ** 0.5 * C ** -0.5
+    for first in range(0, columns.size, R):
+        c = one_per_row(R, C, columns, first)
+        x[at, c] = 1
+        gs.gs_layernorm_fwd(x, None, None, y, mean, rstd, 0.0)
+        x[at, c] = 0
+        assert ((mean.double() / wm - 1).abs() <= 2.0 ** -16).all()
+        assert ((rstd.double() / wr - 1).abs() <= 2.0 ** -16).all()
+        tol = 2.0 ** -15 + 2 * HALF_ULP[dt]
+        peak = y[at, c].double()
+        assert ((peak / ((1 - wm) * wr) - 1).abs() <= tol).all()
+        y[at, c] = y[at, (c + 1) % C]
+        assert ((y.double() / (-wm * wr) - 1).abs().amax() <= tol)
+
+
+@pytest.mark.parametrize("dtype,R,C,pad,offset", WAYS)
+def test_backward_every_column_counts_once(gs, dtype, R, C, pad, offset):
+    """xhat = 1 and dy of zeros but one 1 per row: dx = 1[column] - 2 / C, where a
+    column left out or read twice makes 2 / C zero or twice that; dgamma and
+    dbeta count the rows of each column, exactly."""
+    dt = TYPES[dtype]
+    x, _ = rows(R, C, pad, dt, torch.Generator(device=DEV), 0.0, 1.0, offset)
+    dy, _ = rows(R, C, pad, dt, torch.Generator(device=DEV), 0.0, 0.0, offset)
+    dx, _ = rows(R, C, pad, dt, torch.Generator(device=DEV), 0.0, 7.0, offset)
+    mean, rstd = torch.zeros(R, device=DEV), torch.ones(R, device=DEV)
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    ws = torch.empty(gs.gs_layernorm_ws_bytes(R, C), dtype=torch.uint8, device=DEV)
+    columns, at = telling_columns(C), torch.arange(R, device=DEV)
+    for first in range(0, columns.size, R):
+        c = one_per_row(R, C, columns, first)
+        dy[at, c] = 1
+        gs.gs_layernorm_bwd(dy, x, None, mean, rstd, dx, dg, db, ws)
+        dy[at, c] = 0
+        count = torch.bincount(c, minlength=C).float()
+        assert torch.equal(dg, count) and torch.equal(db, count)
+        tol = 2.0 ** -16 + HALF_ULP[dt]
+        assert ((dx[at, c].double() - (1 - 2 / C)).abs() <= tol).all()
+        dx[at, c] = dx[at, (c + 1) % C]
+        assert ((dx.double() * C / -2 - 1).abs().amax() <= tol)
+
+
+@pytest.mark.parametrize("dtype,R,C,pad,offset", WAYS + [("bf16", 70001, 33, 0, 0), ("f16", 20011, 96, 0, 0),
+                                                          ("bf16", 5500, 3001, 7, 0), ("f16", 11003, 1025, 0, 0)])
+def test_backward_sums_over_rows_are_exact_for_whole_numbers(gs, dtype, R, C, pad, offset):
+    """xhat and dy small whole numbers: every partial sum of dgamma and dbeta is one
+    below 2^24, so that any order of addition gives the sums exactly, and a row
+    dropped or counted twice shows."""
+    r, c = torch.arange(R, device=DEV)[:, None], torch.arange(C, device=DEV)[None, :]
+    xi, di = (r * 5 + c * 11) % 9 - 4, 1 + (r * 7 + c * 3 + r // 5) % 3
+    x, _ = rows(R, C, pad, TYPES[dtype], torch.Generator(device=DEV), 0.0, 0.0, offset)
+    dy, _ = rows(R, C, pad, TYPES[dtype], torch.Generator(device=DEV), 0.0, 0.0, offset)
+    x.copy_(xi)
+    dy.copy_(di)
+    dg, db = torch.empty(C, device=DEV), torch.empty(C, device=DEV)
+    ws = torch.full((gs.gs_layernorm_ws_bytes(R, C),), 0xFF, dtype=torch.uint8, device=DEV)
+    gs.gs_layernorm_bwd(dy, x, None, torch.zeros(R, device=DEV), torch.ones(R, device=DEV), torch.empty_like(x), dg,
+                        db, ws)
+    assert torch.equal(db.long(), di.sum(0))
+    assert torch.equal(dg.long(), (di * xi).sum(0))
