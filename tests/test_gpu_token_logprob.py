@@ -372,3 +372,73 @@ def test_backward_sum_of_many_equal_terms(gs, V, dtype):
             d[0, V // 2] += V
             assert ((d[0] - 1).abs() <= tol + V * E * (torch.arange(V, device=DEV) == V // 2)).all()
             assert (d[1:] == 0).all()          # no target, no gradient
+
+
+# rows and columns that take every number of CTAs per row and of threads per CTA
+ONE_BY_ONE = [(400, 100), (300, 1536), (300, 1537), (64, 4097), (2, 8192), (40, 12289), (900, 12288), (5, 32003),
+              (150, 32003), (1, 128256), (16, 128256), (40, 128256), (100, 128256), (420, 128256), (900, 50001),
+              (3, 200001), (800, 32003)]
+
+
+def telling_columns(V):
+    """The first and last ones, those about the edges of vectors, blocks and parts,
+    and some others (all of a short row)."""
+    gen = torch.Generator()
+    gen.manual_seed(V)
+    if V <= 1537:
+        return torch.randperm(V, generator=gen)
+    edges = torch.cat([torch.arange(0, V + 1, 2048)] +
+                      [torch.arange(0, p + 1) * ((-(-V // p) + 7) // 8 * 8) for p in (2, 4, 8)])
+    near = (edges[:, None] + torch.tensor([-9, -8, -1, 0, 1, 7, 8])).flatten()
+    some = torch.cat([torch.arange(40), torch.arange(V - 40, V), near, torch.randint(0, V, (200,), generator=gen)])
+    some = some[(some >= 0) & (some < V)].unique()
+    return some[torch.randperm(some.numel(), generator=gen)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R,V", ONE_BY_ONE)
+def test_every_logit_counts_once(gs, R, V, dtype):
+    """Rows of -Inf but two equal logits: lse - x = entropy = ln 2, each log
+    probability -ln 2, each p one half.  A logit left out or read twice makes
+    that 0 or ln 3, whatever V is.  With x = 0, and with x = 300, where the
+    gradient forms the sum itself; tolerance: a few roundings of 300."""
+    columns = telling_columns(V)
+    ln2 = math.log(2.0)
+    at = torch.arange(R, device=DEV)
+    x, _ = view(R, V, 1, TYPES[dtype], 0)
+    x.fill_(-INF)
+    d, _ = view(R, V, 1, torch.float32, 0)
+    f = lambda: torch.empty(R, device=DEV)  # noqa: E731
+    lp, lse, h, tlp = f(), f(), f(), torch.empty(R, 3, device=DEV)
+    ids = torch.empty(R, 3, dtype=torch.int32, device=DEV)
+    for k, first in enumerate(range(0, columns.numel(), R)):
+        value, tol = ((0.0, 4 * E), (300.0, 2048 * E))[k % 2]
+        c = columns[(torch.arange(R) + first) % columns.numel()].to(DEV)
+        o = (c + V // 2) % V
+        x[at, c] = x[at, o] = value
+        gs.gs_token_logprob(x, c, lp, lse, h, ids, tlp)
+        gs.gs_token_logprob_bwd(x, c, lse, torch.ones(R, device=DEV), d)
+        x[at, c] = x[at, o] = -INF
+        for got, want in ((lse - value, ln2), (h, ln2), (lp, -ln2), (tlp[:, :2], -ln2)):
+            assert ((got.double() - want).abs() <= tol).all()
+        assert torch.equal(ids[:, :2].long(), torch.stack([torch.minimum(c, o), torch.maximum(c, o)], 1))
+        assert (tlp[:, 2] == -INF).all()
+        assert ((d[at, c].double() - 0.5).abs() <= tol).all() and ((d[at, o].double() + 0.5).abs() <= tol).all()
+        d[at, c] = d[at, o] = 0
+        assert (d == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", VOCABS)
+def test_equal_logits_are_all_counted(gs, V, dtype):
+    """Equal logits: every term is 1 and the sum V exactly, so that lse - x is ln V
+    within its own rounding: 2^-22 of it, less than one logit's share."""
+    for R in (1, 5, 40, 150):
+        x, _ = view(R, V, 3, TYPES[dtype], 1)
+        x.fill_(0.0)
+        lse, h = torch.empty(R, device=DEV), torch.empty(R, device=DEV)
+        gs.gs_token_logprob(x, None, None, lse, h)
+        want = math.log(V)
+        assert V == 1 or want * 2.0 ** -22 < 0.75 / V
+        for got in (lse, h):
+            assert ((got.double() - want).abs() <= want * 2.0 ** -22).all()
