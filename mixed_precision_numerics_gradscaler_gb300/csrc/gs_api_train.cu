@@ -252,10 +252,10 @@ int gs_adamw_list_create(float* const* master, uint16_t* const* master_bf16,
     // the half and the whole: 1 M parameters 7.5, 8.0 and 10.1 us, 4 M 18.6, 16.6 and
     // 18.3; the whole and fourfold: 350 M 1048 and 1005).
     const int64_t wave = (int64_t)sm_count() * 4;
-    const int64_t chunk = total <= wave * (kChunkElems / 4)  ? kChunkElems / 4
+    const int64_t chunk = total <= wave * kAChunkLeast       ? kAChunkLeast
                           : total <= wave * kChunkElems      ? kChunkElems / 2
                           : total < wave * 16 * kChunkElems ? kChunkElems
-                                                            : 4 * kChunkElems;
+                                                            : kAChunkMost;
     for (int32_t i = 0; i < n_tensors; ++i) {
       const int64_t n = numels[i];
       if (n < 0 || n > (INT64_MAX >> 4) || place > (INT64_MAX >> 1) - n) return GS_ERR_SHAPE;

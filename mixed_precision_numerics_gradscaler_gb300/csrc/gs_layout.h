@@ -86,9 +86,10 @@ __host__ __device__ inline int64_t mchunk_head(const float* w, const uint16_t* w
 }
 
 // One contiguous run of a parameter tensor for the AdamW step: at most
-// kChunkElems elements; with 8-bit moments beginning at a multiple of
-// kChunkElems elements of the tensor (so that a block of 128 that shares a
-// moment's scale lies in one chunk).
+// kAChunkMost elements, so that an index in it is an int; with 8-bit moments
+// beginning at a multiple of kAChunkLeast elements of the tensor, a multiple of two
+// blocks of 128 that share a moment's scale.
+constexpr int64_t kAChunkLeast = kChunkElems / 4, kAChunkMost = 4 * kChunkElems;
 struct AChunk {
   float* w;            // fp32 master weights (updated in place)
   uint16_t* w_bf16;    // bf16 copy, or nullptr
@@ -103,6 +104,8 @@ struct AChunk {
   float decay;         // the tensor's factor of the weight decay
 };
 constexpr int kMomentBlock = 128;
+static_assert(kAChunkMost <= INT32_MAX / 4 && kAChunkLeast % (2 * kMomentBlock) == 0,
+              "the kernels index a chunk by int and take its blocks in pairs");
 
 // Elements of a tensor with fp32 moments before the first one at which w, m
 // and v are 32-byte aligned and the gradients (gsz bytes each) and the bf16
