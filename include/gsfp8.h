@@ -235,13 +235,17 @@ int gs_adamw_list_destroy(gs_adamw_list* list);
  * a / 448, and x * (448 / a) is rounded to E4M3 up or down at random in
  * proportion to the distance (so that the mean of many steps keeps what
  * rounding to nearest would always drop: beta2 near 1 moves v by less than
- * half a step of the format); a positive r is never stored as zero.  The
+ * half a step of the format); a positive r is never stored as zero.  The mean
+ * kept is the root's: its square, the next step's v, is larger by the
+ * rounding's variance, which adds up to 2 % (beta2 0.95) to 5 % (0.999) of v.  The
  * random bits are a function of (seed, t, the element's place in the list):
  * the same inputs give the same bits.  Non-finite gradients are for the
  * check before this step to find; here they give non-finite states.
  * beta1, beta2 in [0, 1); lr, weight_decay, eps finite and >= 0.  grad_norm
  * may be NULL when max_norm <= 0.  Calls on one list must be ordered on one
- * stream. */
+ * stream.  *step counts the calls of one list: a model whose parameters are in
+ * several lists (gradients or moments of two types) keeps a counter for each,
+ * since one that they shared would advance once per list. */
 int gs_master_update_adamw(const gs_adamw_list* list, float lr, float beta1, float beta2,
                            float eps, float weight_decay, float max_norm,
                            const float* grad_norm, const int32_t* found_inf, int64_t* step,
@@ -489,7 +493,9 @@ int gs_token_logprob(const void* logits, int64_t ld, int dtype, int64_t R, int64
  * a value beyond the type's range becomes Inf, which the loss scaler's check
  * then finds.  lse and entropy: as gs_token_logprob wrote them (where |lse| >
  * 256, so that its own rounding would show in p, the row's sum is formed
- * anew: a row whose every logit is the type's lowest value has p = 1 / V);
+ * anew: a row whose every logit is the type's lowest value has p = 1 / V; at a
+ * price, as each part of such a row reads all of it: 8192 rows of 128256 bf16
+ * take 8.6 times the time of others, in place 1.9 times);
  * dlogprob, dentropy: fp32 [R]; entropy and dentropy may both be NULL; loss_scale:
  * device fp32 scalar S, or NULL for 1.  A negative target contributes no
  * logprob term, one >= V makes its row NaN; a row with lse -Inf has gradient
