@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "gs_layout.h"
+#include "gs_layout_train.h"
 
 namespace gs {
 

@@ -52,6 +52,13 @@ def test_recorded_traffic_is_dropped_when_the_kernel_sources_change(tmp_path, mo
     assert bench.measured_traffic("no_such_kernel") is None
 
 
+def test_committed_traffic_is_of_the_present_sources():
+    """Every kernel's recorded DRAM traffic was counted from the sources as they
+    are: the benchmark's line keeps the figure."""
+    for key in bench.KERNEL_SOURCES:
+        assert bench.measured_traffic(key), key
+
+
 def test_oracle_parallel_runs_exactly_the_requested_steps():
     class Counter:
         def __init__(self):
