@@ -123,12 +123,15 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 # The current stream's handle without the Stream object around it (3 us of a
 # call on a Grace core, more than the launch); None where torch has no CUDA.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_cuda_is_up = torch.cuda.is_initialized
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def _stream(stream) -> int:
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch._C._cuda_getDevice())
+        if _raw_stream is not None and _cuda_is_up():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -371,10 +374,13 @@ def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torc
     """step: int64 [1], the number of updates made so far (advanced on the
     device unless found_inf is set), this list's own; found_inf: int32 [1];
     grad_norm: float32 [1]."""
+    # (in line, and without what _vector looks at besides: small lists are bound by this call)
+    if (step is not None and (step.dtype is not _I64 or step.numel() != 1) or
+            found_inf is not None and (found_inf.dtype is not _I32 or found_inf.numel() != 1) or
+            grad_norm is not None and (grad_norm.dtype is not _F32 or grad_norm.numel() != 1)):
+        raise ValueError("step must be int64, found_inf int32 and grad_norm float32, of one element each")
     _check(_lib.gs_master_update_adamw(alist.handle, lr, beta1, beta2, eps, weight_decay, max_norm,
-                                       _scalar(grad_norm, "grad_norm", torch.float32),
-                                       _scalar(found_inf, "found_inf", torch.int32),
-                                       _scalar(step, "step", torch.int64), seed,
+                                       _ptr(grad_norm), _ptr(found_inf), _ptr(step), seed,
                                        _stream(stream)), "gs_master_update_adamw")
 
 
@@ -488,14 +494,6 @@ def _vector(t: torch.Tensor | None, name: str, n: int, dtype: torch.dtype) -> in
         return None
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of {n} elements and {dtype}")
-    return t.data_ptr()
-
-
-def _scalar(t: torch.Tensor | None, name: str, dtype: torch.dtype) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.numel() != 1:
-        raise ValueError(f"{name} must be of one element and {dtype}")
     return t.data_ptr()
 
 
