@@ -374,14 +374,19 @@ def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torc
     """step: int64 [1], the number of updates made so far (advanced on the
     device unless found_inf is set), this list's own; found_inf: int32 [1];
     grad_norm: float32 [1]."""
-    # (in line, and without what _vector looks at besides: small lists are bound by this call)
-    if (step is not None and (step.dtype is not _I64 or step.numel() != 1) or
-            found_inf is not None and (found_inf.dtype is not _I32 or found_inf.numel() != 1) or
-            grad_norm is not None and (grad_norm.dtype is not _F32 or grad_norm.numel() != 1)):
+    # (_vector, _ptr and _check in line: small lists are bound by this call, and the
+    # checks alone are 0.5 us of it)
+    if (step is not None and (step.dtype is not _I64 or step.nbytes != 8) or
+            found_inf is not None and (found_inf.dtype is not _I32 or found_inf.nbytes != 4) or
+            grad_norm is not None and (grad_norm.dtype is not _F32 or grad_norm.nbytes != 4)):
         raise ValueError("step must be int64, found_inf int32 and grad_norm float32, of one element each")
-    _check(_lib.gs_master_update_adamw(alist.handle, lr, beta1, beta2, eps, weight_decay, max_norm,
-                                       _ptr(grad_norm), _ptr(found_inf), _ptr(step), seed,
-                                       _stream(stream)), "gs_master_update_adamw")
+    status = _lib.gs_master_update_adamw(
+        alist.handle, lr, beta1, beta2, eps, weight_decay, max_norm,
+        None if grad_norm is None else grad_norm.data_ptr(),
+        None if found_inf is None else found_inf.data_ptr(),
+        None if step is None else step.data_ptr(), seed, _stream(stream))
+    if status != GS_OK:
+        raise GsError(status, "gs_master_update_adamw")
 
 
 def gs_unscale_check_update_hysteresis(tlist: TensorList, scale: torch.Tensor,
