@@ -495,7 +495,7 @@ int gs_token_logprob(const void* logits, int64_t ld, int dtype, int64_t R, int64
  * 256, so that its own rounding would show in p, the row's sum is formed
  * anew: a row whose every logit is the type's lowest value has p = 1 / V; at a
  * price, as each part of such a row reads all of it: 8192 rows of 128256 bf16
- * take 8.6 times the time of others, in place 1.9 times);
+ * take 9 times the time of others, in place 1.9 times);
  * dlogprob, dentropy: fp32 [R]; entropy and dentropy may both be NULL; loss_scale:
  * device fp32 scalar S, or NULL for 1.  A negative target contributes no
  * logprob term, one >= V makes its row NaN; a row with lse -Inf has gradient
