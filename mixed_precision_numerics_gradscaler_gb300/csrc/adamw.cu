@@ -26,7 +26,7 @@
 // fp32 moments: HBM-bound, 567 M parameters with fp32 gradients and a bf16 copy in
 // 2485 us, 6.85 TB/s of their 30 bytes each.  8-bit moments: some 80 instructions
 // per element beside 18 bytes, both near their limits: 1595 us, 6.45 TB/s.  Short
-// lists (1 M parameters: 5.8 and 7.5 us from a graph) are the launch and one pass's latency.
+// lists (1 M parameters: 5.9 and 7.6 us from a graph) are the launch and one pass's latency.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -237,9 +237,10 @@ __global__ void __launch_bounds__(NT < 256 ? 256 : NT)
 // The grid is planned for 1024 threads per SM with 64 registers each: one CTA per
 // SM for rows of more than 512 threads, 32 for the narrowest, of which the shared
 // memory of an SM (ring, sums and what the system keeps: some 9.5 KB each) holds 24
-// at a time.  (One CTA of 513 to 1023 threads leaves a part of them unused:
+// at a time.  One CTA of 513 to 1023 threads leaves a part of the SM unused:
 // 16384 x 5120, 6144 and 7168 bf16 take 62, 70 and 79 us forward, 102, 117 and 134 us
-// backward, 1.12 to 1.24 and 1.27 to 1.36 times the bytes at the copy rate.)
+// backward, beside 52 and 86 us at 4096 and 89 and 148 us at 8192 columns (timed
+// one by one, caches flushed).
 
 // Sums of four values over the warp: lane 8 q and its seven neighbours return
 // the sum of s[q].
