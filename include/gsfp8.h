@@ -507,6 +507,121 @@ int gs_token_logprob_bwd(const void* logits, int64_t ld, int dtype, int64_t R, i
                          void* dlogits, int64_t ld_out, int out_dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit tensors: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), two to a byte (the even element in the low four bits),
+ * with one scale per 32 (GS_MXFP4, E8M0) or 16 (GS_NVFP4, E4M3) consecutive
+ * elements of a row, NVFP4 with an fp32 scale of the whole tensor besides.
+ *   MXFP4: e = floor(log2(amax)) - 2, clamped to [-127, 127], -127 for a block
+ *          of zeros; scale byte e + 127; q = e2m1(x * 2^-e).  (OCP
+ *          Microscaling, as fp8_quant_mx.)
+ *   NVFP4: t = max(amax of the tensor, 1e-12) / 2688;  s = e4m3(amax / (6 t));
+ *          q = e2m1(x * (1 / (s t))), 0 where s is 0; every step in fp32.
+ * Roundings to nearest even, saturating; a zero keeps its sign.  A block with
+ * Inf or NaN gets a scale of NaN (255; 0x7F) and codes 0; Inf or NaN anywhere
+ * makes a tensor scale formed here NaN, and with it every block's.
+ *
+ * Scales lie in tiles of 128 rows x 4 scales (512 bytes), as the tensor cores'
+ * block-scaled products read them: the byte of row r and scale k (k = column /
+ * block) of an R x C matrix is at
+ *   ((r / 128) * K4 + k / 4) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4 + k % 4,
+ * K4 = ceil(C / (4 * block)).  Bytes past the edges are written as zeros and
+ * have to be zeros where a product reads them.
+ * --------------------------------------------------------------------- */
+typedef enum gs_fp4 { GS_MXFP4 = 0, GS_NVFP4 = 1 } gs_fp4;
+
+/* Bytes of the scales of an R x C matrix (0 for sizes it refuses). */
+size_t fp4_scale_bytes(int64_t R, int64_t C, int fmt);
+
+/* Quantises x [R, C] (in_dtype, row distance ldx in elements), C % 32 == 0:
+ *   q [R, C / 2], scales (fp4_scale_bytes(R, C))       -- as x lies, and/or
+ *   qt [C, R / 2], scales_t (fp4_scale_bytes(C, R))    -- its transpose, blocks
+ *       along x's columns (R % 32 == 0): the operands of the two products of a
+ *       backward pass, whose sums run over the other dimension.
+ * Either pair may be NULL, not both.
+ *   tensor_scale -- device fp32 scalar, GS_NVFP4 only (else NULL).  With ws
+ *       (device, gs_ws_bytes() bytes, 4-byte aligned) it is formed from x in a
+ *       pass of its own and written; with ws NULL it is read (a scale of the
+ *       steps before, say): one outside [2^-100, 2^120] makes every block's
+ *       scale NaN, elements beyond 6 * 448 times it saturate.
+ * q, scales, qt, scales_t 16-byte aligned.  Calls sharing a ws must be ordered
+ * on one stream.  R == 0 or C == 0 writes the tensor scale alone. */
+int fp4_quant(const void* x, int64_t ldx, int in_dtype, int64_t R, int64_t C, int fmt, uint8_t* q,
+              uint8_t* scales, uint8_t* qt, uint8_t* scales_t, float* tensor_scale, void* ws,
+              void* stream);
+
+/* y = decode(q) * scale [* tensor_scale] in fp32, rounded to out_dtype (any of
+ * the three) to nearest even; y [R, C] with row distance ldy. */
+int fp4_dequant(const uint8_t* q, const uint8_t* scales, const float* tensor_scale, int64_t R,
+                int64_t C, int fmt, int out_dtype, void* y, int64_t ldy, void* stream);
+
+/* D = A B^T with A [M, K] and B [N, K] (a weight stored [out, in]) 4-bit
+ * tensors of one format, times the product of their tensor scales ta and tb
+ * (device fp32 scalars, GS_NVFP4 only, else NULL):
+ *   D[m][n] = ta tb sum over k of decode(qa[m][k]) sa[m][k / block]
+ *                                 decode(qb[n][k]) sb[n][k / block].
+ * The backward products of Y = X W^T are the same call on transposed operands:
+ * dX = dY (W^T)^T and dW = dY^T (X^T)^T, from the qt of fp4_quant.
+ *   d: [M, N] with row distance ldd, out_dtype GS_F32 or GS_BF16 (rounded to
+ *      nearest even from the fp32 sum); what lies between rows is not written.
+ * Products and scales are exact in the tensor cores, sums in fp32 in an order
+ * that depends on the sizes and the device alone: |error| <= 2^-24 (K / 16 +
+ * 8) sum of |terms| before the output's rounding.
+ * K % 32 == 0, M, N, K < 2^31 and fewer than 2^30 tiles of 128 x 128 (else
+ * GS_ERR_SHAPE); any M and N; K == 0 writes zeros.  Codes and scales 16-byte
+ * aligned.  A wait that runs out records GS_ERR_TIMEOUT (gs_device_status) and
+ * leaves d unspecified. */
+int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta, const uint8_t* qb,
+                          const uint8_t* sb, const float* tb, int64_t M, int64_t N, int64_t K,
+                          int fmt, int out_dtype, void* d, int64_t ldd, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The clipped policy loss over packed sequences, and its gradient with respect
+ * to the tokens' log probabilities (which gs_token_logprob forms and
+ * gs_token_logprob_bwd takes on to the logits, with the loss scale).
+ * For a token with log probability x, x' under the policy that sampled it, x''
+ * under a reference, and advantage A:
+ *   rho = exp(x - x'),
+ *   obj = rho A, but (1 + clip_high) A where A > 0 and rho > 1 + clip_high,
+ *         (1 - clip_low) A where A < 0 and rho < 1 - clip_low, and
+ *         dual_clip A where A < 0 and rho > dual_clip (dual_clip 0: none),
+ *   kl  = exp(x'' - x) - 1 - (x'' - x),
+ *   l   = -obj + kl_coef kl,      loss = sum over tokens of w l.
+ * reduction: w = 1 / (tokens that count) for GS_LOSS_TOKEN_MEAN; 1 / (S' n_s)
+ * for GS_LOSS_SEQUENCE_MEAN (n_s tokens that count in the token's sequence, S'
+ * sequences that have any); 1 for GS_LOSS_SUM.
+ *   logprob, old_logprob, ref_logprob: fp32 [T]; ref_logprob may be NULL with
+ *       kl_coef 0;
+ *   advantages: fp32, n_advantages = T (one per token) or S (one per sequence;
+ *       where T == S, one per token);
+ *   targets: int64 [T] as gs_token_logprob takes them: a token with a negative
+ *       one does not count, whatever the other arrays hold there; NULL: all do;
+ *   seq_offsets: int64 [S + 1], not decreasing: sequence s is the tokens
+ *       [seq_offsets[s], seq_offsets[s + 1]); empty ones are fine.  Tokens before the
+ *       first and after the last are in none: they do not count and their
+ *       dlogprob is left as it was.  NULL: one sequence of all T (S = 1);
+ *   dloss: device fp32 scalar that the gradient is multiplied by, or NULL (1);
+ *   loss: device fp32 scalar, written; stats: fp32 [4] or NULL, over the tokens
+ *       that count: their number, and the means of rho, of "obj is held" (0 or
+ *       1) and of kl;
+ *   dlogprob: fp32 [T] or NULL: dloss w dl/dx, 0 for tokens that do not count.
+ *   ws: device workspace of gs_policy_loss_ws_bytes(T, S) bytes, 16-byte
+ *       aligned, any contents; calls sharing one must be ordered on one stream.
+ * clip_low, clip_high >= 0 (1 or more, Inf: never held there); dual_clip 0 or
+ * >= 1.  No token that counts: loss, statistics and gradient 0.  T, S <= 2^40,
+ * S >= 1.  The same inputs give the same bits. */
+typedef enum gs_loss_reduction {
+  GS_LOSS_TOKEN_MEAN = 0,
+  GS_LOSS_SEQUENCE_MEAN = 1,
+  GS_LOSS_SUM = 2
+} gs_loss_reduction;
+size_t gs_policy_loss_ws_bytes(int64_t T, int64_t S);
+int gs_policy_loss(const float* logprob, const float* old_logprob, const float* ref_logprob,
+                   const float* advantages, int64_t n_advantages, const int64_t* targets, int64_t T,
+                   const int64_t* seq_offsets, int64_t S, float clip_low, float clip_high,
+                   float dual_clip, float kl_coef, int reduction, const float* dloss, float* loss,
+                   float* stats, float* dlogprob, void* ws, void* stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics.
  * --------------------------------------------------------------------- */
 

@@ -25,7 +25,8 @@ __all__ = [
     "gs_unscale_check_update_norm", "ParamList", "gs_param_list_create", "gs_master_update_sgd",
     "AdamWList", "gs_adamw_list_create", "gs_master_update_adamw", "gs_layernorm_fwd",
     "gs_layernorm_bwd", "gs_layernorm_ws_bytes", "gs_token_logprob", "gs_token_logprob_bwd",
-    "GS_MAX_TOP", "GS_MOMENTS_F32", "GS_MOMENTS_E4M3",
+    "GS_MAX_TOP", "GS_MOMENTS_F32", "GS_MOMENTS_E4M3", "GS_MXFP4", "GS_NVFP4", "fp4_scale_bytes",
+    "fp4_quant", "fp4_dequant", "fp4_gemm_block_scaled", "gs_policy_loss", "gs_policy_loss_ws_bytes",
 ]
 
 GS_OK, GS_ERR_NULL, GS_ERR_SHAPE, GS_ERR_DTYPE, GS_ERR_ARG, GS_ERR_CUDA, GS_ERR_TIMEOUT = range(7)
@@ -33,8 +34,12 @@ GS_F16, GS_BF16, GS_F32 = 0, 1, 2
 GS_E4M3, GS_E5M2 = 0, 1
 GS_MOMENTS_F32, GS_MOMENTS_E4M3 = 0, 1
 GS_MAX_TOP = 32
+GS_MXFP4, GS_NVFP4 = 0, 1
+GS_LOSS_TOKEN_MEAN, GS_LOSS_SEQUENCE_MEAN, GS_LOSS_SUM = 0, 1, 2
 
 _DTYPES = {torch.float16: GS_F16, torch.bfloat16: GS_BF16, torch.float32: GS_F32}
+_FMTS4 = {"mxfp4": GS_MXFP4, "nvfp4": GS_NVFP4, GS_MXFP4: GS_MXFP4, GS_NVFP4: GS_NVFP4}
+_REDUCTIONS = {"token": GS_LOSS_TOKEN_MEAN, "sequence": GS_LOSS_SEQUENCE_MEAN, "sum": GS_LOSS_SUM}
 _FMTS = {"e4m3": GS_E4M3, "e5m2": GS_E5M2, GS_E4M3: GS_E4M3, GS_E5M2: GS_E5M2}
 
 
@@ -87,6 +92,13 @@ def _load_lib() -> ctypes.CDLL:
         "gs_token_logprob": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp]),
         "gs_token_logprob_bwd": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci,
                                       vp]),
+        "fp4_scale_bytes": (ctypes.c_size_t, [i64, i64, ci]),
+        "fp4_quant": (ci, [vp, i64, ci, i64, i64, ci, vp, vp, vp, vp, vp, vp, vp]),
+        "fp4_dequant": (ci, [vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]),
+        "fp4_gemm_block_scaled": (ci, [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, vp, i64, vp]),
+        "gs_policy_loss_ws_bytes": (ctypes.c_size_t, [i64, i64]),
+        "gs_policy_loss": (ci, [vp, vp, vp, vp, i64, vp, i64, vp, i64, f32, f32, f32, f32, ci, vp, vp,
+                                vp, vp, vp, vp]),
         "gs_adamw_list_create": (ci, [vp, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp, i32,
                                       ctypes.POINTER(vp)]),
         "gs_adamw_list_destroy": (ci, [vp]),
@@ -595,6 +607,103 @@ def gs_token_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
                                      _vector(loss_scale, "loss_scale", 1, f32), _ptr(dlogits),
                                      ld_out, _DTYPES[dlogits.dtype], _stream(stream)),
            "gs_token_logprob_bwd")
+
+
+def fp4_scale_bytes(rows: int, cols: int, fmt) -> int:
+    """Bytes of the scales of a [rows, cols] 4-bit tensor (tiles of 512 bytes)."""
+    return int(_lib.fp4_scale_bytes(rows, cols, _FMTS4[fmt]))
+
+
+def _codes4(q: torch.Tensor, scales: torch.Tensor, name: str, R: int, C: int, fmt: int) -> None:
+    """Checks that q holds the codes and scales the scales of [R, C] values."""
+    if q.dtype is not torch.uint8 or tuple(q.shape) != (R, C // 2) or not q.is_contiguous():
+        raise ValueError(f"{name} must be contiguous uint8 [{R}, {C // 2}]")
+    if scales.dtype is not torch.uint8 or not scales.is_contiguous() or \
+            scales.numel() != _lib.fp4_scale_bytes(R, C, fmt):
+        raise ValueError(f"the scales of {name} must be contiguous uint8, of "
+                         f"{_lib.fp4_scale_bytes(R, C, fmt)} bytes")
+
+
+def fp4_quant(x: torch.Tensor, fmt, q: torch.Tensor | None, scales: torch.Tensor | None,
+              tensor_scale: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+              qt: torch.Tensor | None = None, scales_t: torch.Tensor | None = None, stream=None) -> None:
+    """x: [R, C] bf16 / f16 / f32 (rows may be apart); q: uint8 [R, C/2], scales:
+    uint8, fp4_scale_bytes(R, C) of them; qt: uint8 [C, R/2] and scales_t
+    (fp4_scale_bytes(C, R)) for the transpose; either pair may be None.
+    tensor_scale ("nvfp4"): float32 [1], formed from x and written where ws
+    (gs_ws_bytes() bytes) is given, else read."""
+    ldx, f = _rows(x, "x"), _FMTS4[fmt]
+    R, C = x.shape
+    if (q is None) != (scales is None) or (qt is None) != (scales_t is None):
+        raise ValueError("codes and scales go together")
+    if q is not None:
+        _codes4(q, scales, "q", R, C, f)
+    if qt is not None:
+        _codes4(qt, scales_t, "qt", C, R, f)
+    if ws is not None and (not ws.is_contiguous() or ws.nbytes < gs_ws_bytes()):
+        raise ValueError("ws must be contiguous, of gs_ws_bytes() bytes at least")
+    _check(_lib.fp4_quant(_ptr(x), ldx, _DTYPES[x.dtype], R, C, f, _ptr(q), _ptr(scales), _ptr(qt),
+                          _ptr(scales_t), _vector(tensor_scale, "tensor_scale", 1, _F32), _ptr(ws),
+                          _stream(stream)), "fp4_quant")
+
+
+def fp4_dequant(q: torch.Tensor, scales: torch.Tensor, fmt, y: torch.Tensor,
+                tensor_scale: torch.Tensor | None = None, stream=None) -> None:
+    """y: [R, C], any of the three types (rows may be apart), from q [R, C/2]."""
+    ldy, f = _rows(y, "y"), _FMTS4[fmt]
+    R, C = y.shape
+    _codes4(q, scales, "q", R, C, f)
+    _check(_lib.fp4_dequant(_ptr(q), _ptr(scales), _vector(tensor_scale, "tensor_scale", 1, _F32), R, C,
+                            f, _DTYPES[y.dtype], _ptr(y), ldy, _stream(stream)), "fp4_dequant")
+
+
+def fp4_gemm_block_scaled(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor, fmt,
+                          d: torch.Tensor, ta: torch.Tensor | None = None,
+                          tb: torch.Tensor | None = None, stream=None) -> None:
+    """d[M, N] = ta tb (qa[M, K/2] with scales sa) @ (qb[N, K/2] with sb)^T;
+    d float32 or bfloat16, rows may be apart; ta, tb: float32 [1] ("nvfp4")."""
+    ldd, f = _rows(d, "d"), _FMTS4[fmt]
+    M, N = d.shape
+    K = 2 * qa.shape[-1]
+    _codes4(qa, sa, "qa", M, K, f)
+    _codes4(qb, sb, "qb", N, K, f)
+    _check(_lib.fp4_gemm_block_scaled(qa.data_ptr(), sa.data_ptr(), _vector(ta, "ta", 1, _F32),
+                                      qb.data_ptr(), sb.data_ptr(), _vector(tb, "tb", 1, _F32), M, N, K,
+                                      f, _DTYPES[d.dtype], d.data_ptr(), ldd, _stream(stream)),
+           "fp4_gemm_block_scaled")
+
+
+def gs_policy_loss_ws_bytes(tokens: int, seqs: int = 1) -> int:
+    return int(_lib.gs_policy_loss_ws_bytes(tokens, seqs))
+
+
+def gs_policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages: torch.Tensor,
+                   loss: torch.Tensor, ws: torch.Tensor, dlogprob: torch.Tensor | None = None,
+                   stats: torch.Tensor | None = None, ref_logprob: torch.Tensor | None = None,
+                   targets: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
+                   dloss: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                   dual_clip: float = 0.0, kl_coef: float = 0.0, reduction: str = "token",
+                   stream=None) -> None:
+    """logprob, old_logprob, ref_logprob, dlogprob: float32 [T]; advantages:
+    float32 [T] or [S]; targets: int64 [T] (negative: the token does not
+    count); seq_offsets: int64 [S + 1]; loss, dloss: float32 [1]; stats:
+    float32 [4] (tokens, mean ratio, held fraction, mean divergence); ws:
+    gs_policy_loss_ws_bytes(T, S) bytes; reduction: "token", "sequence" or
+    "sum"."""
+    T = logprob.numel()
+    S = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    n = advantages.numel()
+    if not ws.is_contiguous() or ws.nbytes < _lib.gs_policy_loss_ws_bytes(T, S):
+        raise ValueError("ws must be contiguous, of gs_policy_loss_ws_bytes(T, S) bytes at least")
+    status = _lib.gs_policy_loss(
+        _vector(logprob, "logprob", T, _F32), _vector(old_logprob, "old_logprob", T, _F32),
+        _vector(ref_logprob, "ref_logprob", T, _F32), _vector(advantages, "advantages", n, _F32), n,
+        _vector(targets, "targets", T, _I64), T, _vector(seq_offsets, "seq_offsets", S + 1, _I64), S,
+        clip_low, clip_high, dual_clip, kl_coef, _REDUCTIONS[reduction], _vector(dloss, "dloss", 1, _F32),
+        _vector(loss, "loss", 1, _F32), _vector(stats, "stats", 4, _F32),
+        _vector(dlogprob, "dlogprob", T, _F32), ws.data_ptr(), _stream(stream))
+    if status != GS_OK:
+        raise GsError(status, "gs_policy_loss")
 
 
 def gs_test_set_stall(on: bool) -> None:

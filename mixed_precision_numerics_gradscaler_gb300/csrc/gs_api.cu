@@ -202,7 +202,7 @@ cudaError_t kernel_clusters(const void* kernel, int threads, int smem_bytes, int
 void record_cuda_error(cudaError_t e) { t_last_cuda_error = (int)e; }
 
 // The status word's address in the current context.
-static cudaError_t device_status_ptr(int32_t** out) {
+cudaError_t device_status_ptr(int32_t** out) {
   void* p = nullptr;
   const cudaError_t e = symbol_address((const void*)&g_gs_device_status, &p);
   *out = static_cast<int32_t*>(p);

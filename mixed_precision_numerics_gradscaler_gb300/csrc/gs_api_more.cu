@@ -1,0 +1,208 @@
+// gs_api_more.cu -- the C entry points of the 4-bit tensors and of the policy
+// loss (include/gsfp8.h).  Argument validation on the host; nothing is launched
+// unless every check passes.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "gs_args.h"
+#include "gs_fp4.h"
+#include "gs_internal.h"
+#include "gs_policy.h"
+#include "gsfp8.h"
+
+namespace gs {
+
+static int cuda_fail(cudaError_t e) {
+  record_cuda_error(e);
+  return GS_ERR_CUDA;
+}
+
+static bool valid_fmt4(int f) { return f == GS_MXFP4 || f == GS_NVFP4; }
+
+// Reachable or absent.
+static bool reach(const void* p) { return !p || device_reachable(p); }
+
+// The bytes [p, p + n) as a range; empty for a null p.
+static Span span(const void* p, int64_t n) {
+  return Span{(uintptr_t)p, (uintptr_t)p + (p ? (uintptr_t)n : 0)};
+}
+
+// R rows of C elements of `esz` bytes, ld apart: every address computable.
+static bool rows_ok(int64_t R, int64_t C, int64_t ld, size_t esz) {
+  return ld >= C && mul_ok(R, ld) && mul_ok(R * ld, (int64_t)esz);
+}
+static int64_t rows_bytes(int64_t R, int64_t C, int64_t ld, size_t esz) {
+  return R == 0 || C == 0 ? 0 : ((R - 1) * ld + C) * (int64_t)esz;
+}
+
+// log(v) for v = 1 + x as two fp32 numbers (from fp64: 2^-48 of it).
+static Border border(double log_v) {
+  Border b;
+  b.hi = (float)log_v;
+  b.lo = std::isfinite(log_v) ? (float)(log_v - (double)b.hi) : 0.0f;
+  return b;
+}
+
+}  // namespace gs
+
+using namespace gs;
+
+extern "C" {
+
+size_t fp4_scale_bytes(int64_t R, int64_t C, int fmt) {
+  if (!valid_fmt4(fmt) || R < 0 || C < 0) return 0;
+  const int64_t a = fp4_scale_tiles(R, 128), b = fp4_scale_tiles(C, fmt == GS_NVFP4 ? 64 : 128);
+  if (!mul_ok(a, b) || !mul_ok(a * b, 512)) return 0;
+  return (size_t)(a * b) * 512;
+}
+
+int fp4_quant(const void* x, int64_t ldx, int in_dtype, int64_t R, int64_t C, int fmt, uint8_t* q,
+              uint8_t* scales, uint8_t* qt, uint8_t* scales_t, float* tensor_scale, void* ws,
+              void* stream) {
+  if (!valid_dtype(in_dtype) || !valid_fmt4(fmt)) return GS_ERR_DTYPE;
+  const size_t esz = dtype_size(in_dtype);
+  if (R < 0 || C < 0 || !rows_ok(R, C, ldx, esz) || C % 32 || (qt && R % 32)) return GS_ERR_SHAPE;
+  const bool nv = fmt == GS_NVFP4, empty = R == 0 || C == 0;
+  if (!empty && !x) return GS_ERR_NULL;
+  if ((!q && !qt) || !q != !scales || !qt != !scales_t || nv != (tensor_scale != nullptr))
+    return GS_ERR_NULL;
+  if (!nv && ws) return GS_ERR_ARG;
+  if (!aligned(x, esz) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(qt, 16) ||
+      !aligned(scales_t, 16) || !aligned(tensor_scale, 4) || !aligned(ws, 4))
+    return GS_ERR_ARG;
+  if (!(empty || reach(x)) || !(empty || (reach(q) && reach(scales) && reach(qt) && reach(scales_t))) ||
+      !reach(tensor_scale) || !reach(ws))
+    return GS_ERR_ARG;
+  const int64_t codes = R * C / 2;
+  const Span in[] = {span(x, rows_bytes(R, C, ldx, esz)), span(ws ? nullptr : tensor_scale, 4)};
+  Span out[] = {span(q, codes),
+                span(scales, (int64_t)fp4_scale_bytes(R, C, fmt)),
+                span(qt, codes),
+                span(scales_t, (int64_t)fp4_scale_bytes(C, R, fmt)),
+                span(ws ? tensor_scale : nullptr, 4),
+                span(ws, (int64_t)gs_ws_bytes())};
+  if (spans_conflict(out, 6, in, 2)) return GS_ERR_ARG;
+  const cudaError_t e =
+      launch_quant4(x, ldx, in_dtype, R, C, fmt, q, scales, qt, scales_t, tensor_scale,
+                    static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+int fp4_dequant(const uint8_t* q, const uint8_t* scales, const float* tensor_scale, int64_t R,
+                int64_t C, int fmt, int out_dtype, void* y, int64_t ldy, void* stream) {
+  if (!valid_dtype(out_dtype) || !valid_fmt4(fmt)) return GS_ERR_DTYPE;
+  const size_t esz = dtype_size(out_dtype);
+  if (R < 0 || C < 0 || !rows_ok(R, C, ldy, esz) || C % 32) return GS_ERR_SHAPE;
+  if (R == 0 || C == 0) return GS_OK;
+  if (!q || !scales || !y || (fmt == GS_NVFP4) != (tensor_scale != nullptr)) return GS_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(scales, 16) || !aligned(tensor_scale, 4) || !aligned(y, esz))
+    return GS_ERR_ARG;
+  if (!reach(q) || !reach(scales) || !reach(tensor_scale) || !reach(y)) return GS_ERR_ARG;
+  const Span in[] = {span(q, R * C / 2), span(scales, (int64_t)fp4_scale_bytes(R, C, fmt)),
+                     span(tensor_scale, 4)};
+  Span out[] = {span(y, rows_bytes(R, C, ldy, esz))};
+  if (spans_conflict(out, 1, in, 3)) return GS_ERR_ARG;
+  const cudaError_t e = launch_dequant4(q, scales, tensor_scale, R, C, fmt, out_dtype, y, ldy,
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta, const uint8_t* qb,
+                          const uint8_t* sb, const float* tb, int64_t M, int64_t N, int64_t K,
+                          int fmt, int out_dtype, void* d, int64_t ldd, void* stream) {
+  if (!valid_fmt4(fmt) || !(out_dtype == GS_F32 || out_dtype == GS_BF16)) return GS_ERR_DTYPE;
+  const size_t esz = dtype_size(out_dtype);
+  if (M < 0 || N < 0 || K < 0 || K % 32 || M >= (1LL << 31) || N >= (1LL << 31) || K >= (1LL << 31) ||
+      ldd >= (1LL << 36) || !rows_ok(M, N, ldd, esz) || !mul_ok(M, K) || !mul_ok(N, K))
+    return GS_ERR_SHAPE;
+  if (fp4_scale_tiles(M, 128) * fp4_scale_tiles(N, 128) >= (1LL << 30)) return GS_ERR_SHAPE;
+  if (M == 0 || N == 0) return GS_OK;
+  const bool nv = fmt == GS_NVFP4;
+  if (!d || (K > 0 && (!qa || !sa || !qb || !sb))) return GS_ERR_NULL;
+  if (nv != (ta != nullptr) || nv != (tb != nullptr)) return GS_ERR_NULL;
+  if (!aligned(d, esz) || !aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
+      !aligned(ta, 4) || !aligned(tb, 4))
+    return GS_ERR_ARG;
+  if (!reach(d) || !reach(ta) || !reach(tb)) return GS_ERR_ARG;
+  if (K > 0 && (!reach(qa) || !reach(sa) || !reach(qb) || !reach(sb))) return GS_ERR_ARG;
+  const Span in[] = {span(qa, M * K / 2), span(sa, (int64_t)fp4_scale_bytes(M, K, fmt)),
+                     span(qb, N * K / 2), span(sb, (int64_t)fp4_scale_bytes(N, K, fmt)),
+                     span(ta, 4),         span(tb, 4)};
+  Span out[] = {span(d, rows_bytes(M, N, ldd, esz))};
+  if (spans_conflict(out, 1, in, 6)) return GS_ERR_ARG;
+  int32_t* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e == cudaSuccess)
+    e = launch_gemm_fp4(qa, sa, ta, qb, sb, tb, M, N, K, fmt, out_dtype, d, ldd, status,
+                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+size_t gs_policy_loss_ws_bytes(int64_t T, int64_t S) {
+  if (T < 0 || S < 0 || T > (int64_t)1 << 40 || S > (int64_t)1 << 40) return 0;
+  return sizeof(PolicyHead) + (size_t)S * 8 + kPolicyCtas * sizeof(PolicyPart);
+}
+
+int gs_policy_loss(const float* logprob, const float* old_logprob, const float* ref_logprob,
+                   const float* advantages, int64_t n_advantages, const int64_t* targets, int64_t T,
+                   const int64_t* seq_offsets, int64_t S, float clip_low, float clip_high,
+                   float dual_clip, float kl_coef, int reduction, const float* dloss, float* loss,
+                   float* stats, float* dlogprob, void* ws, void* stream) {
+  const size_t wsb = gs_policy_loss_ws_bytes(T, S);
+  if (!wsb || S < 1 || (!seq_offsets && S != 1)) return GS_ERR_SHAPE;
+  if (n_advantages != T && n_advantages != S) return GS_ERR_SHAPE;
+  if (reduction != GS_LOSS_TOKEN_MEAN && reduction != GS_LOSS_SEQUENCE_MEAN && reduction != GS_LOSS_SUM)
+    return GS_ERR_ARG;
+  if (!(clip_low >= 0.0f) || !(clip_high >= 0.0f) || !std::isfinite(kl_coef)) return GS_ERR_ARG;
+  if (!(dual_clip == 0.0f || dual_clip >= 1.0f)) return GS_ERR_ARG;
+  if (!loss || !ws || (T > 0 && (!logprob || !old_logprob || !advantages))) return GS_ERR_NULL;
+  if (T > 0 && kl_coef != 0.0f && !ref_logprob) return GS_ERR_NULL;
+  for (const void* p : {(const void*)logprob, (const void*)old_logprob, (const void*)ref_logprob,
+                        (const void*)advantages, (const void*)dloss, (const void*)loss,
+                        (const void*)stats, (const void*)dlogprob})
+    if (!aligned(p, 4)) return GS_ERR_ARG;
+  if (!aligned(targets, 8) || !aligned(seq_offsets, 8) || !aligned(ws, 16)) return GS_ERR_ARG;
+  if (T > 0 && (!reach(logprob) || !reach(old_logprob) || !reach(ref_logprob) || !reach(advantages) ||
+                !reach(targets) || !reach(dlogprob)))
+    return GS_ERR_ARG;
+  if (!reach(seq_offsets) || !reach(dloss) || !reach(loss) || !reach(stats) || !reach(ws))
+    return GS_ERR_ARG;
+  const Span in[] = {span(logprob, T * 4),           span(old_logprob, T * 4), span(ref_logprob, T * 4),
+                     span(advantages, n_advantages * 4), span(targets, T * 8),
+                     span(seq_offsets, (S + 1) * 8), span(dloss, 4)};
+  Span out[] = {span(loss, 4), span(stats, 16), span(dlogprob, T * 4), span(ws, (int64_t)wsb)};
+  if (spans_conflict(out, 4, in, 7)) return GS_ERR_ARG;
+  PolicyArgs a = {};
+  a.logprob = logprob;
+  a.old = old_logprob;
+  a.ref = ref_logprob;
+  a.adv = advantages;
+  a.targets = targets;
+  a.offsets = seq_offsets;
+  a.dloss = dloss;
+  a.loss = loss;
+  a.stats = stats;
+  a.grad = dlogprob;
+  a.T = T;
+  a.S = S;
+  a.reduction = reduction;
+  a.adv_per_seq = n_advantages != T;
+  const double low = 1.0 - (double)clip_low, high = 1.0 + (double)clip_high;
+  a.low = border(low > 0.0 ? std::log(low) : -HUGE_VAL);
+  a.high = border(std::log(high));
+  a.dual = border(dual_clip ? std::log((double)dual_clip) : HUGE_VAL);
+  a.factor_low = (float)low;
+  a.factor_high = (float)high;
+  a.factor_dual = dual_clip;
+  a.kl = kl_coef;
+  char* p = static_cast<char*>(ws);
+  a.head = reinterpret_cast<PolicyHead*>(p);
+  a.n = reinterpret_cast<unsigned long long*>(p + sizeof(PolicyHead));
+  a.part = reinterpret_cast<PolicyPart*>(p + sizeof(PolicyHead) + S * 8);
+  const cudaError_t e = launch_policy_loss(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+}  // extern "C"

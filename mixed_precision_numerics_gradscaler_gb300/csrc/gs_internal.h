@@ -40,6 +40,9 @@ bool current_context_id(unsigned long long* id);
 // no heap allocation).  Thread-safe.
 cudaError_t symbol_address(const void* symbol, void** out);
 
+// The device status word's address in the current context.
+cudaError_t device_status_ptr(int32_t** out);
+
 // Records e as the calling thread's last CUDA error (gs_last_cuda_error).
 void record_cuda_error(cudaError_t e);
 // True if the current device can dereference p as given: its own device
@@ -55,8 +58,9 @@ struct Span {
 // O((writes + reads) log writes).
 bool spans_conflict(Span* writes, size_t n_writes, const Span* reads, size_t n_reads);
 
-// Test hook (gs_test_set_stall): nonzero makes the block-scaled FP8 GEMM issue
-// no TMA loads, so that its bounded waits run out.
+// Test hook (gs_test_set_stall): nonzero makes the kernels fed by TMA on
+// barriers (the block-scaled GEMMs) issue no loads, so that their bounded waits
+// run out.
 int test_stall();
 
 // Launchers.  Each returns the launch's cudaError_t.
