@@ -25,8 +25,8 @@
  *     its host address); pointers the device cannot use as given are
  *     rejected with GS_ERR_ARG.  The caller owns all
  *     data buffers.  The library allocates only inside
- *     gs_tensor_list_create and gs_param_list_create; no compute call
- *     allocates.
+ *     gs_tensor_list_create, gs_param_list_create, gs_adamw_list_create and
+ *     gs_muon_list_create; no compute call allocates.
  *   - Layout: row-major and contiguous; element [r, c] of an R x C array is
  *     at offset r * C + c.  Outputs must not overlap inputs.  Any element-
  *     aligned address is accepted; 16-byte-aligned buffers take the
@@ -620,6 +620,51 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
                    const int64_t* seq_offsets, int64_t S, float clip_low, float clip_high,
                    float dual_clip, float kl_coef, int reduction, const float* dloss, float* loss,
                    float* stats, float* dlogprob, void* ws, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The update of weight matrices by their orthogonalised momentum (K. Jordan,
+ * "Muon: an optimizer for hidden layers in neural networks", 2024), on the
+ * fp32 masters and skipped on the device like the other updates.
+ * --------------------------------------------------------------------- */
+
+/* A list of matrices: master[i] fp32 [rows[i], cols[i]], its bf16 copy
+ * (master_bf16 or an entry of it may be NULL), gradients of grad_dtype (any of
+ * the three) and momentum[i] fp32, each contiguous, element-aligned, of the
+ * current device; nothing that is written may overlap anything else.  Fewer
+ * than 2^31 elements per matrix; empty ones are left out.  Allocates the list's
+ * workspace: 4 bytes per element (rows counted up to a multiple of 8 elements) and
+ * 4 per element of a square of the smaller side. */
+typedef struct gs_muon_list gs_muon_list;
+int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, const void* const* grads,
+                        int grad_dtype, float* const* momentum, const int64_t* rows,
+                        const int64_t* cols, int32_t n, gs_muon_list** out);
+/* Waits for the device and frees the list. */
+int gs_muon_list_destroy(gs_muon_list* list);
+
+typedef enum gs_muon_scale { GS_MUON_SCALE_RMS = 0, GS_MUON_SCALE_ASPECT = 1 } gs_muon_scale;
+
+/* One step of every matrix of the list, unless *found_inf is set (then nothing
+ * is written):
+ *   g = gradient * (max_norm / *grad_norm if 0 < max_norm < *grad_norm, else 1),
+ *   m = mu m + g,   u = g + mu m (nesterov) or m,   X = u / |u| (Frobenius; a
+ *       u of zeros stays zero),
+ *   ns_steps times, on the smaller side:  G = X X^T,
+ *       X = 3.4445 X + (-4.7750 G + 2.0315 G G) X,
+ *   w = w (1 - lr weight_decay) - lr scale X;   bf16 copy = w rounded to nearest
+ *       even;  scale = 0.2 sqrt(max(rows, cols)) (GS_MUON_SCALE_RMS: an update of
+ *       AdamW's size) or sqrt(max(1, rows / cols)) (GS_MUON_SCALE_ASPECT).
+ * X, G and the polynomial are held in fp16, scaled by powers of two to its range
+ * (11 bits where bf16 would keep 8), sums in fp32: X is within about 2^-11 of
+ * its norm.  Sums of squares are fp32 within groups of four: |u| below 2^-60 of an
+ * element counts as zero, above 2^60 gives NaN.  Non-finite gradients are for
+ * the check before this step to find.
+ * lr, weight_decay finite and >= 0, mu in [0, 1), ns_steps 1 to 20; grad_norm
+ * may be NULL when max_norm <= 0.  Calls on one list must be ordered on one
+ * stream.  A wait that runs out records GS_ERR_TIMEOUT (gs_device_status) and
+ * leaves the weights unspecified. */
+int gs_master_update_muon(const gs_muon_list* list, float lr, float mu, float weight_decay,
+                          int nesterov, int32_t ns_steps, int scale, float max_norm,
+                          const float* grad_norm, const int32_t* found_inf, void* stream);
 
 /* ------------------------------------------------------------------------
  * Diagnostics.

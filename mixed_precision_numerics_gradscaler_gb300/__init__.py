@@ -27,6 +27,7 @@ __all__ = [
     "gs_layernorm_bwd", "gs_layernorm_ws_bytes", "gs_token_logprob", "gs_token_logprob_bwd",
     "GS_MAX_TOP", "GS_MOMENTS_F32", "GS_MOMENTS_E4M3", "GS_MXFP4", "GS_NVFP4", "fp4_scale_bytes",
     "fp4_quant", "fp4_dequant", "fp4_gemm_block_scaled", "gs_policy_loss", "gs_policy_loss_ws_bytes",
+    "MuonList", "gs_muon_list_create", "gs_master_update_muon",
 ]
 
 GS_OK, GS_ERR_NULL, GS_ERR_SHAPE, GS_ERR_DTYPE, GS_ERR_ARG, GS_ERR_CUDA, GS_ERR_TIMEOUT = range(7)
@@ -39,6 +40,7 @@ GS_LOSS_TOKEN_MEAN, GS_LOSS_SEQUENCE_MEAN, GS_LOSS_SUM = 0, 1, 2
 
 _DTYPES = {torch.float16: GS_F16, torch.bfloat16: GS_BF16, torch.float32: GS_F32}
 _FMTS4 = {"mxfp4": GS_MXFP4, "nvfp4": GS_NVFP4, GS_MXFP4: GS_MXFP4, GS_NVFP4: GS_NVFP4}
+_MUON_SCALES = {"rms": 0, "aspect": 1}
 _REDUCTIONS = {"token": GS_LOSS_TOKEN_MEAN, "sequence": GS_LOSS_SEQUENCE_MEAN, "sum": GS_LOSS_SUM}
 _FMTS = {"e4m3": GS_E4M3, "e5m2": GS_E5M2, GS_E4M3: GS_E4M3, GS_E5M2: GS_E5M2}
 
@@ -92,6 +94,9 @@ def _load_lib() -> ctypes.CDLL:
         "gs_token_logprob": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, i32, vp, vp, vp]),
         "gs_token_logprob_bwd": (ci, [vp, i64, ci, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, ci,
                                       vp]),
+        "gs_muon_list_create": (ci, [vp, vp, vp, ci, vp, vp, vp, i32, ctypes.POINTER(vp)]),
+        "gs_muon_list_destroy": (ci, [vp]),
+        "gs_master_update_muon": (ci, [vp, f32, f32, f32, ci, i32, ci, f32, vp, vp, vp]),
         "fp4_scale_bytes": (ctypes.c_size_t, [i64, i64, ci]),
         "fp4_quant": (ci, [vp, i64, ci, i64, i64, ci, vp, vp, vp, vp, vp, vp, vp]),
         "fp4_dequant": (ci, [vp, vp, vp, i64, i64, ci, ci, vp, i64, vp]),
@@ -399,6 +404,70 @@ def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torc
         None if step is None else step.data_ptr(), seed, _stream(stream))
     if status != GS_OK:
         raise GsError(status, "gs_master_update_adamw")
+
+
+class MuonList:
+    """Owns a ``gs_muon_list`` handle: fp32 master matrices [rows, cols], their
+    gradients (all float32, bfloat16 or float16), fp32 momenta and optional bf16
+    copies, and the workspace of the step (4 to 8 bytes per element)."""
+
+    def __init__(self, master: list[torch.Tensor], grads: list[torch.Tensor],
+                 momentum: list[torch.Tensor], master_bf16: list[torch.Tensor] | None = None):
+        n = len(master)
+        for other in (grads, momentum, master_bf16):
+            if other is not None and len(other) != n:
+                raise ValueError("lists differ in length")
+        for i in range(n):
+            if master[i].dim() != 2:
+                raise ValueError(f"master {i} must be a matrix")
+            for t, name, dtype in ((master[i], "master", torch.float32), (grads[i], "grad", grads[0].dtype),
+                                   (momentum[i], "momentum", torch.float32),
+                                   (master_bf16 and master_bf16[i], "master_bf16", torch.bfloat16)):
+                if t is None:
+                    continue
+                _contig(t, name)
+                if t.dtype != dtype or t.shape != master[i].shape:
+                    raise ValueError(f"{name} {i} must be {dtype} of shape {tuple(master[i].shape)}")
+        self._keep = [list(t) for t in (master, grads, momentum, master_bf16 or [])]
+
+        def ptrs(ts):
+            return None if ts is None else (ctypes.c_void_p * max(n, 1))(*[_ptr(t) for t in ts])
+
+        rows = (ctypes.c_int64 * max(n, 1))(*[t.shape[0] for t in master])
+        cols = (ctypes.c_int64 * max(n, 1))(*[t.shape[1] for t in master])
+        h = ctypes.c_void_p()
+        _check(_lib.gs_muon_list_create(ptrs(master), ptrs(master_bf16), ptrs(grads),
+                                        _DTYPES[grads[0].dtype] if n else GS_F32, ptrs(momentum), rows,
+                                        cols, n, ctypes.byref(h)), "gs_muon_list_create")
+        self.handle = h
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            _lib.gs_muon_list_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def gs_muon_list_create(master, grads, momentum, master_bf16=None) -> MuonList:
+    return MuonList(master, grads, momentum, master_bf16)
+
+
+def gs_master_update_muon(mlist: MuonList, found_inf: torch.Tensor, lr: float, momentum: float = 0.95,
+                          weight_decay: float = 0.0, nesterov: bool = True, ns_steps: int = 5,
+                          scale: str = "rms", max_norm: float = 0.0,
+                          grad_norm: torch.Tensor | None = None, stream=None) -> None:
+    """found_inf: int32 [1]; grad_norm: float32 [1]; scale: "rms" or "aspect"."""
+    if (found_inf is not None and (found_inf.dtype is not _I32 or found_inf.nbytes != 4) or
+            grad_norm is not None and (grad_norm.dtype is not _F32 or grad_norm.nbytes != 4)):
+        raise ValueError("found_inf must be int32 and grad_norm float32, of one element each")
+    _check(_lib.gs_master_update_muon(mlist.handle, lr, momentum, weight_decay, int(nesterov), ns_steps,
+                                      _MUON_SCALES[scale], max_norm, _ptr(grad_norm), _ptr(found_inf),
+                                      _stream(stream)), "gs_master_update_muon")
 
 
 def gs_unscale_check_update_hysteresis(tlist: TensorList, scale: torch.Tensor,

@@ -1,16 +1,27 @@
-// gs_api_more.cu -- the C entry points of the 4-bit tensors and of the policy
-// loss (include/gsfp8.h).  Argument validation on the host; nothing is launched
+// gs_api_more.cu -- the C entry points of the 4-bit tensors, the policy loss and
+// the update by orthogonalised momentum (include/gsfp8.h).  Argument validation on the host; nothing is launched
 // unless every check passes.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
+#include <new>
+#include <vector>
 
 #include "gs_args.h"
 #include "gs_fp4.h"
 #include "gs_internal.h"
+#include "gs_muon.h"
 #include "gs_policy.h"
 #include "gsfp8.h"
+
+struct gs_muon_list {
+  int device;
+  int grad_dtype;
+  char* d_memory;   // tables, tensor maps, sums and the products' operands
+  gs::MuonTable table;
+};
 
 namespace gs {
 
@@ -202,6 +213,174 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
   a.n = reinterpret_cast<unsigned long long*>(p + sizeof(PolicyHead));
   a.part = reinterpret_cast<PolicyPart*>(p + sizeof(PolicyHead) + S * 8);
   const cudaError_t e = launch_policy_loss(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, const void* const* grads,
+                        int grad_dtype, float* const* momentum, const int64_t* rows,
+                        const int64_t* cols, int32_t n, gs_muon_list** out) {
+  if (!out) return GS_ERR_NULL;
+  *out = nullptr;
+  if (n < 0) return GS_ERR_SHAPE;
+  if (!valid_dtype(grad_dtype)) return GS_ERR_DTYPE;
+  if (n > 0 && (!master || !grads || !momentum || !rows || !cols)) return GS_ERR_NULL;
+  const size_t gsz = dtype_size(grad_dtype);
+  std::vector<MuonMat> mats;
+  std::vector<CUtensorMap> maps;
+  std::vector<int64_t> cost;
+  std::vector<Span> written, read;
+  MuonTable t = {};
+  size_t bytes = 0;
+  const auto take = [&](size_t b) {  // room in the list's memory, 256-byte aligned
+    const size_t at = bytes;
+    bytes += (b + 255) / 256 * 256;
+    return at;
+  };
+  size_t at_mats, at_maps, at_partials, at_arrived, at_factor;
+  std::vector<size_t> at_x;
+  try {
+    for (int32_t i = 0; i < n; ++i) {
+      const int64_t R = rows[i], C = cols[i];
+      if (R < 0 || C < 0 || !mul_ok(R, C) || R * C >= (1LL << 31) || R >= (1LL << 31) || C >= (1LL << 31))
+        return GS_ERR_SHAPE;
+      if (R == 0 || C == 0) continue;
+      uint16_t* wb = master_bf16 ? master_bf16[i] : nullptr;
+      if (!master[i] || !grads[i] || !momentum[i]) return GS_ERR_NULL;
+      if (!aligned(master[i], 4) || !aligned(wb, 2) || !aligned(grads[i], gsz) || !aligned(momentum[i], 4))
+        return GS_ERR_ARG;
+      if (!reach(master[i]) || !reach(wb) || !reach(grads[i]) || !reach(momentum[i])) return GS_ERR_ARG;
+      written.push_back(span(master[i], R * C * 4));
+      written.push_back(span(wb, R * C * 2));
+      written.push_back(span(momentum[i], R * C * 4));
+      read.push_back(span(grads[i], R * C * (int64_t)gsz));
+      MuonMat m = {};
+      m.w = master[i];
+      m.wb = wb;
+      m.g = grads[i];
+      m.m = momentum[i];
+      m.rows = (int)R;
+      m.cols = (int)C;
+      m.s = (int)std::min(R, C);
+      m.ldx = (int)((C + 7) / 8 * 8);
+      m.lds = (m.s + 7) / 8 * 8;
+      m.tall = R > C;
+      // x begins with elements of 1 / sqrt(R C) and ends with 1 / sqrt(l) in the
+      // mean and 1.21 at most; gram begins with a diagonal of 1 / s and ends near 1
+      m.sx = std::ldexp(1.0f, (int)std::min<long>(14, std::lround(std::log2(std::sqrt((double)R * C)))));
+      m.sa = std::ldexp(1.0f, (int)std::min<long>(14, std::lround(std::log2((double)m.s))));
+      mats.push_back(m);
+    }
+    if (spans_conflict(written.data(), written.size(), read.data(), read.size())) return GS_ERR_ARG;
+    // the longest sums first, so that a launch's last tiles are short ones
+    std::stable_sort(mats.begin(), mats.end(), [](const MuonMat& x, const MuonMat& y) {
+      return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
+    });
+    int64_t sym = 0, app = 0;
+    for (MuonMat& m : mats) {
+      m.first_chunk = t.chunks;
+      m.first_sym = (int)sym;
+      m.first_app = (int)app;
+      t.chunks += fp4_scale_tiles((int64_t)m.rows * m.cols, kMuonChunk);
+      const int64_t ts = fp4_scale_tiles(m.s, kMuonTile);
+      sym += ts * (ts + 1) / 2;
+      app += fp4_scale_tiles(m.rows, kMuonTile) * fp4_scale_tiles(m.cols, kMuonTile);
+      if (sym >= (1LL << 30) || app >= (1LL << 30)) return GS_ERR_SHAPE;
+    }
+    t.n = (int)mats.size();
+    t.sym_tiles = (int)sym;
+    t.app_tiles = (int)app;
+    at_mats = take(mats.size() * sizeof(MuonMat));
+    at_maps = take(mats.size() * 4 * sizeof(CUtensorMap));
+    at_partials = take((size_t)t.chunks * sizeof(double));
+    at_arrived = take(mats.size() * sizeof(unsigned));
+    at_factor = take(mats.size() * sizeof(float));
+    for (const MuonMat& m : mats) {
+      const size_t x = (size_t)m.rows * m.ldx * 2, g = (size_t)m.s * m.lds * 2;
+      for (const size_t b : {x, x, g, g}) at_x.push_back(take(b));
+    }
+    maps.resize(mats.size() * 4);
+  } catch (...) {
+    return GS_ERR_ARG;
+  }
+  gs_muon_list* l = new (std::nothrow) gs_muon_list{current_device(), grad_dtype, nullptr, t};
+  if (!l) return GS_ERR_ARG;
+  if (mats.empty()) {
+    *out = l;
+    return GS_OK;
+  }
+  char* d = nullptr;
+  cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&d), bytes);
+  if (e == cudaSuccess) {
+    for (size_t i = 0; i < mats.size() && e == cudaSuccess; ++i) {
+      MuonMat& m = mats[i];
+      uint16_t* p[4];
+      for (int j = 0; j < 4; ++j) p[j] = reinterpret_cast<uint16_t*>(d + at_x[4 * i + j]);
+      m.x[0] = p[0];
+      m.x[1] = p[1];
+      m.gram = p[2];
+      m.poly = p[3];
+      for (int j = 0; j < 4; ++j)
+        if (!muon_encode(&maps[4 * i + j], p[j], j < 2 ? m.rows : m.s, j < 2 ? m.cols : m.s,
+                         j < 2 ? m.ldx : m.lds))
+          e = cudaErrorNotSupported;
+    }
+    MuonTable& lt = l->table;
+    lt.mats = reinterpret_cast<const MuonMat*>(d + at_mats);
+    lt.maps = reinterpret_cast<const CUtensorMap*>(d + at_maps);
+    lt.partials = reinterpret_cast<double*>(d + at_partials);
+    lt.arrived = reinterpret_cast<unsigned*>(d + at_arrived);
+    lt.factor = reinterpret_cast<float*>(d + at_factor);
+    // operands' padding is read by 16-byte loads: numbers from the start
+    if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, bytes, cudaStreamLegacy);
+    if (e == cudaSuccess)
+      e = cudaMemcpyAsync(d + at_mats, mats.data(), mats.size() * sizeof(MuonMat), cudaMemcpyHostToDevice,
+                          cudaStreamLegacy);
+    if (e == cudaSuccess)
+      e = cudaMemcpyAsync(d + at_maps, maps.data(), maps.size() * sizeof(CUtensorMap),
+                          cudaMemcpyHostToDevice, cudaStreamLegacy);
+    // on the device before the call returns: the step may follow on any stream
+    if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+  }
+  if (e != cudaSuccess) {
+    if (d) cudaFree(d);
+    delete l;
+    return cuda_fail(e);
+  }
+  l->d_memory = d;
+  *out = l;
+  return GS_OK;
+}
+
+int gs_muon_list_destroy(gs_muon_list* list) {
+  if (!list) return GS_OK;
+  const int prev = current_device();
+  cudaSetDevice(list->device);
+  const cudaError_t e = cudaDeviceSynchronize();
+  if (list->d_memory) cudaFree(list->d_memory);
+  cudaSetDevice(prev);
+  delete list;
+  return e == cudaSuccess ? GS_OK : cuda_fail(e);
+}
+
+int gs_master_update_muon(const gs_muon_list* list, float lr, float mu, float weight_decay,
+                          int nesterov, int32_t ns_steps, int scale, float max_norm,
+                          const float* grad_norm, const int32_t* found_inf, void* stream) {
+  if (!list || !found_inf || (max_norm > 0.0f && !grad_norm)) return GS_ERR_NULL;
+  for (const float x : {lr, weight_decay})
+    if (!std::isfinite(x) || x < 0.0f) return GS_ERR_ARG;
+  if (!(mu >= 0.0f && mu < 1.0f) || std::isnan(max_norm) || ns_steps < 1 || ns_steps > 20)
+    return GS_ERR_ARG;
+  if (scale != GS_MUON_SCALE_RMS && scale != GS_MUON_SCALE_ASPECT) return GS_ERR_ARG;
+  if (!aligned(found_inf, 4) || !aligned(grad_norm, 4)) return GS_ERR_ARG;
+  if (list->device != current_device()) return GS_ERR_ARG;
+  if (!reach(found_inf) || (max_norm > 0.0f && !reach(grad_norm))) return GS_ERR_ARG;
+  int32_t* status = nullptr;
+  cudaError_t e = device_status_ptr(&status);
+  if (e != cudaSuccess) return cuda_fail(e);
+  const MuonArgs a = {lr,       mu,    weight_decay,     max_norm,  nesterov ? 1 : 0, ns_steps,
+                      scale,    list->grad_dtype, grad_norm, found_inf, status,
+                      test_stall()};
+  e = launch_master_update_muon(list->table, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GS_OK : cuda_fail(e);
 }
 

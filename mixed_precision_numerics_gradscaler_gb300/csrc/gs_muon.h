@@ -1,0 +1,56 @@
+// gs_muon.h -- the tables of a list of matrices updated by their orthogonalised
+// momentum, and the launcher of the update.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace gs {
+
+constexpr int kMuonTile = 256;               // rows and columns of a product's tile
+constexpr int64_t kMuonChunk = 8192;         // elements of an element-wise step's CTA
+
+// One matrix [rows, cols]; s = min, l = max of the two.  The products' operands
+// are fp16 times a power of two each: x by sx, gram and poly by sa and sa / 4.
+struct MuonMat {
+  float* w;
+  uint16_t* wb;              // bf16 copy, or null
+  const void* g;
+  float* m;
+  uint16_t* x[2];            // [rows, ldx], in turns
+  uint16_t *gram, *poly;     // [s, lds]
+  int rows, cols, s, ldx, lds;
+  int tall;                  // rows > cols
+  float sx, sa;
+  int64_t first_chunk;       // of the list's chunks of elements
+  int first_sym, first_app;  // of the list's tiles of either kind of product
+};
+
+struct MuonTable {
+  const MuonMat* mats;
+  const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly
+  double* partials;          // one per chunk
+  unsigned int* arrived;     // per matrix, 0 between calls
+  float* factor;             // per matrix: sx / |u|
+  int n;
+  int64_t chunks;
+  int sym_tiles, app_tiles;
+  int wide_any, tall_any;
+};
+
+struct MuonArgs {
+  float lr, mu, weight_decay, max_norm;
+  int nesterov, steps, scale_mode, grad_dtype;
+  const float* grad_norm;
+  const int32_t* found_inf;
+  int32_t* status;
+  int stall;
+};
+
+// A tensor map of an fp16 matrix [rows, cols] with row distance ld, boxes of
+// 64 x 64 in the 128-byte swizzle.
+bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld);
+cudaError_t launch_master_update_muon(const MuonTable& t, const MuonArgs& a, cudaStream_t st);
+
+}  // namespace gs

@@ -1,0 +1,552 @@
+// muon.cu -- the update of weight matrices by their orthogonalised momentum
+// (K. Jordan, "Muon: an optimizer for hidden layers in neural networks", 2024):
+//   m = mu m + g,  u = g + mu m (nesterov) or m,  X = u / |u|_F,
+//   steps times:  G = X X^T,  P = b G + c G G,  X = a X + P X
+//                 (for more rows than columns: G = X^T X, X = a X + X P),
+//   w = w (1 - lr weight_decay) - lr scale X,
+// (a, b, c) = (3.4445, -4.7750, 2.0315), a quintic in the singular values that
+// takes (0, 1] to near 1.
+//
+// The products take s^2 (l + s) operations each way of G and P with their
+// symmetric halves left out, 2 s^2 l for X: all on the tensor cores.  Operands
+// are fp16, not bf16: every value is bounded (singular values of X stay below
+// 1.21, of G below 1.46, of P below 2.82), so that a power of two per matrix
+// keeps them in fp16's normal range with three more bits than bf16 has, at the
+// same rate.  Sums are fp32 in tensor memory, the polynomial's fp32 sums round
+// to fp16 once per product, and the last product's sums go into w unrounded.
+//
+// One launch per product takes every matrix of the list: persistent pairs of
+// CTAs walk the list's tiles of 256 x 256 (largest sums first).  A pair shares an
+// MMA of 256 x 256 x 16, each CTA loading half of either operand (TMA, 64 x 64
+// boxes, six stages of 64 of the sum); operands lie with the sum along their
+// rows or across them, which the MMA's descriptors tell.  Two accumulators of
+// 256 columns: eight warps store one while the other is formed.  Tiles above
+// the diagonal of G and P are stored transposed from the ones below.
+// Every wait is bounded and reports GS_ERR_TIMEOUT.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "gs_internal.h"
+#include "gs_muon.h"
+#include "gs_tcgen05.cuh"
+
+namespace gs {
+
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+constexpr int kMThreads = 384;               // warps 0-3: loads, MMA, two idle; 4-11 store
+constexpr int kMEThreads = 256;              // of the element-wise steps
+constexpr int kMBox = 64 * 128;              // bytes of a 64 x 64 box
+constexpr int kMStage = 4 * kMBox;           // a CTA's 128 x 64 of either operand
+constexpr int kMStages = 6;
+constexpr int kMSmem = kMStages * kMStage + 1024 + 256;
+
+// The matrix that holds item t: the last one whose first is not above t.
+template <typename T>
+__device__ __forceinline__ int mat_of(const MuonMat* __restrict__ mats, int n, T t, T MuonMat::*first) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (mats[mid].*first <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float clip_of(const MuonArgs& a) {
+  if (!(a.max_norm > 0.0f)) return 1.0f;
+  const float n = *a.grad_norm;
+  return n > a.max_norm ? __fdiv_rn(a.max_norm, n) : 1.0f;
+}
+
+// Four elements from p + i; whole and aligned, or up to n.
+template <int DT>
+__device__ __forceinline__ void get4(const void* p, int64_t i, int64_t n, bool vec, float (&v)[4]) {
+  using T = typename Elem<DT>::type;
+  if (vec && i + 4 <= n) {
+    if constexpr (DT == GS_F32) {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const T*>(p) + i);
+      v[0] = Elem<DT>::get((T)(w.x & 0xFFFFu)), v[1] = Elem<DT>::get((T)(w.x >> 16));
+      v[2] = Elem<DT>::get((T)(w.y & 0xFFFFu)), v[3] = Elem<DT>::get((T)(w.y >> 16));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = i + j < n ? load1<DT>(p, i + j) : 0.0f;
+  }
+}
+
+// m = mu m + clip g, and the sum of squares of u; a matrix's last chunk to
+// finish forms its factor sx / |u|, from the chunks' sums in their order.
+template <int DT>
+__global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, MuonArgs a) {
+  if (*a.found_inf) return;
+  __shared__ double red[kMEThreads / 32];
+  __shared__ bool last;
+  const float clip = clip_of(a);
+  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
+    const MuonMat& mat = t.mats[id];
+    const int64_t n = (int64_t)mat.rows * mat.cols, base = (c - mat.first_chunk) * kMuonChunk;
+    const int64_t end = min(n, base + kMuonChunk);
+    const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
+      const int64_t i = base + ((int64_t)j * kMEThreads + threadIdx.x) * 4;
+      if (i >= end) continue;
+      float g[4], m[4];
+      get4<DT>(mat.g, i, end, vec_g, g);
+      get4<GS_F32>(mat.m, i, end, vec_m, m);
+      float sq = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = __fmul_rn(g[e], clip);
+        m[e] = __fmaf_rn(a.mu, m[e], g[e]);
+        const float u = a.nesterov ? __fmaf_rn(a.mu, m[e], g[e]) : m[e];
+        sq = __fmaf_rn(u, u, sq);
+      }
+      sum += (double)sq;
+      if (vec_m && i + 4 <= end) {
+        *reinterpret_cast<float4*>(mat.m + i) = make_float4(m[0], m[1], m[2], m[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < end) mat.m[i + e] = m[e];
+      }
+    }
+    // the block's sum, and the matrix's once its last chunk is in
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xFFFFFFFFu, sum, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    const int64_t chunks = (n + kMuonChunk - 1) / kMuonChunk;
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kMEThreads / 32; ++w) sum += red[w];
+      t.partials[c] = sum;
+      __threadfence();
+      last = atomicAdd(&t.arrived[id], 1u) == (unsigned)chunks - 1;
+      __threadfence();
+    }
+    __syncthreads();
+    if (last) {
+      double all = 0.0;
+      for (int64_t k = threadIdx.x; k < chunks; k += kMEThreads)
+        all += __ldcg(&t.partials[mat.first_chunk + k]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all += __shfl_down_sync(0xFFFFFFFFu, all, o);
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = all;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        for (int w = 1; w < kMEThreads / 32; ++w) all += red[w];
+        // a momentum of zeros stays one; one whose squares have no sum shows as NaN
+        t.factor[id] = all == 0.0 ? 0.0f
+                       : all < (double)INFINITY ? (float)((double)mat.sx / sqrt(all))
+                                                : __uint_as_float(0x7FFFFFFFu);
+        t.arrived[id] = 0;
+      }
+      __syncthreads();
+    }
+    __syncthreads();
+  }
+}
+
+// x[0] = fp16(u sx / |u|).
+template <int DT>
+__global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, MuonArgs a) {
+  if (*a.found_inf) return;
+  const float clip = clip_of(a);
+  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
+    const MuonMat& mat = t.mats[id];
+    const int64_t n = (int64_t)mat.rows * mat.cols, base = (c - mat.first_chunk) * kMuonChunk;
+    const int64_t end = min(n, base + kMuonChunk);
+    const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
+    const bool rows4 = mat.cols % 4 == 0;  // four elements lie in one row
+    const float f = t.factor[id];
+#pragma unroll
+    for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
+      const int64_t i = base + ((int64_t)j * kMEThreads + threadIdx.x) * 4;
+      if (i >= end) continue;
+      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m[4];
+      get4<GS_F32>(mat.m, i, end, vec_m, m);
+      if (a.nesterov) get4<DT>(mat.g, i, end, vec_g, g);
+      uint16_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float u = a.nesterov ? __fmaf_rn(a.mu, m[e], __fmul_rn(g[e], clip)) : m[e];
+        h[e] = Elem<GS_F16>::put(__fmul_rn(u, f));
+      }
+      unsigned row = (unsigned)i / (unsigned)mat.cols, col = (unsigned)i - row * (unsigned)mat.cols;
+      if (rows4) {  // i + 4 <= end: the matrix is a multiple of 4
+        *reinterpret_cast<uint2*>(mat.x[0] + (int64_t)row * mat.ldx + col) =
+            make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (i + e < end) mat.x[0][(int64_t)row * mat.ldx + col] = h[e];
+          if (++col == (unsigned)mat.cols) col = 0, ++row;
+        }
+      }
+    }
+  }
+}
+
+// ---- products -----------------------------------------------------------------
+enum { kGram, kPoly, kApply, kLast };
+
+// Instruction descriptor: fp16 operands, fp32 sums, 256 x 256; t: the operand's
+// sum dimension runs across its rows.
+__device__ __forceinline__ uint32_t idesc16(bool ta, bool tb) {
+  return (1u << 4) | (ta ? 1u << 15 : 0u) | (tb ? 1u << 16 : 0u) | ((uint32_t)(kMuonTile >> 3) << 17) |
+         ((uint32_t)(kMuonTile >> 4) << 24);
+}
+__device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Step kk (16 of the sum) of a stage's 128 x 64 operand.  Sum along the rows: two
+// boxes of 64 rows, 32 bytes a step.  Across: boxes of 64 (of 128) x 64 of the
+// sum, a step is 16 rows of 128 bytes, the boxes 8192 bytes apart.
+__device__ __forceinline__ uint64_t desc16(uint32_t base, int kk, bool across) {
+  if (!across) return tc_desc_k(base + 32 * kk);
+  return (uint64_t)(((base + 2048 * kk) >> 4) & 0x3FFFu) | ((uint64_t)(kMBox >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Where tile t of a product lies, and what its operands are.
+struct Product {
+  int id;                // matrix
+  int m0, n0;            // first row and column of the result
+  int M, N, K;
+  bool ta, tb;           // operand with its sum across the rows
+  int map_a, map_b;      // of the matrix's four maps
+  bool mirror;           // a tile below the diagonal
+};
+template <int KIND>
+__device__ __forceinline__ Product product(const MuonTable& t, int tile, int turn) {
+  Product p;
+  constexpr bool kSym = KIND == kGram || KIND == kPoly;
+  p.id = mat_of(t.mats, t.n, tile, kSym ? &MuonMat::first_sym : &MuonMat::first_app);
+  const MuonMat& mat = t.mats[p.id];
+  const int at = tile - (kSym ? mat.first_sym : mat.first_app);
+  int mt, nt;
+  if constexpr (kSym) {  // row mt of a triangle holds tiles mt (mt + 1) / 2 ...
+    mt = (int)((sqrtf(8.0f * (float)at + 1.0f) - 1.0f) * 0.5f);
+    while ((mt + 1) * (mt + 2) / 2 <= at) ++mt;
+    while (mt * (mt + 1) / 2 > at) --mt;
+    nt = at - mt * (mt + 1) / 2;
+    p.M = p.N = mat.s;
+    p.mirror = mt != nt;
+  } else {
+    const int tm = (mat.rows + kMuonTile - 1) / kMuonTile, tn = (mat.cols + kMuonTile - 1) / kMuonTile;
+    tc_tile(at, 8, tm, tn, mt, nt);
+    p.M = mat.rows;
+    p.N = mat.cols;
+    p.mirror = false;
+  }
+  p.m0 = mt * kMuonTile;
+  p.n0 = nt * kMuonTile;
+  if constexpr (KIND == kGram) {
+    p.K = mat.tall ? mat.rows : mat.cols;
+    p.ta = p.tb = mat.tall;
+    p.map_a = p.map_b = turn;
+  } else if constexpr (KIND == kPoly) {
+    p.K = mat.s;
+    p.ta = p.tb = false;
+    p.map_a = p.map_b = 2;
+  } else {
+    p.K = mat.s;
+    p.ta = false;
+    p.tb = !mat.tall;
+    p.map_a = mat.tall ? turn : 3;
+    p.map_b = mat.tall ? 3 : turn;
+  }
+  return p;
+}
+
+// Before a CTA's first use of a tensor map in global memory.
+__device__ __forceinline__ void map_fence(const CUtensorMap* m) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.sys [%0], 128;" ::"l"(m) : "memory");
+}
+
+// turn: which of x[0], x[1] the step reads.
+template <int KIND>
+__global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
+    muon_product_kernel(MuonTable t, MuonArgs a, int turn) {
+  if (*a.found_inf) return;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
+  uint8_t* stages = smem_raw + pad;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + kMStages * kMStage);
+  uint64_t* empty = full + kMStages;
+  uint64_t* tfull = empty + kMStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
+  const int tiles = KIND == kGram || KIND == kPoly ? t.sym_tiles : t.app_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMStages; ++s) {
+      tc_bar_init(&full[s], 1);
+      tc_bar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc_bar_init(&tfull[b], 1);
+      tc_bar_init(&tempty[b], 16);
+    }
+    tc_bar_init(drain, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tc_alloc<2>(tmem_slot, 512);
+  tc_before();
+  __syncthreads();
+  cluster_barrier();
+  tc_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {  // loads
+    uint32_t it = 0;
+    int seen = -1;
+    bool go = !a.stall;
+    for (int tile = first; go && tile < tiles; tile += step) {
+      const Product p = product<KIND>(t, tile, turn);
+      const CUtensorMap* ma = t.maps + 4 * p.id + p.map_a;
+      const CUtensorMap* mb = t.maps + 4 * p.id + p.map_b;
+      if (p.id != seen) {
+        map_fence(ma);
+        if (mb != ma) map_fence(mb);
+        seen = p.id;
+      }
+      const int m0 = p.m0 + 128 * (int)rank, n0 = p.n0 + 128 * (int)rank;
+      for (int k = 0; k < p.K; k += 64, ++it) {
+        const uint32_t s = it % kMStages, ph = (it / kMStages) & 1u;
+        if (!tc_wait(&empty[s], ph ^ 1u, abort_flag, a.status)) {
+          go = false;
+          break;
+        }
+        uint8_t* st = stages + s * kMStage;
+        const uint32_t bar = tc_leader<2>(&full[s]);
+        if (rank == 0) tc_expect(&full[s], 2 * kMStage);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          tc_load2<2>(ma, bar, st + h * kMBox, p.ta ? m0 + 64 * h : k, p.ta ? k : m0 + 64 * h);
+          tc_load2<2>(mb, bar, st + (2 + h) * kMBox, p.tb ? n0 + 64 * h : k, p.tb ? k : n0 + 64 * h);
+        }
+      }
+    }
+    const uint32_t tail = it < kMStages ? it : kMStages;
+    for (uint32_t j = it - tail; j != it; ++j) tc_drain(&empty[j % kMStages], (j / kMStages) & 1u);
+  } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA
+    uint32_t it = 0, n = 0;
+    bool go = true;
+    for (int tile = first; go && tile < tiles; tile += step, ++n) {
+      const Product p = product<KIND>(t, tile, turn);
+      const uint32_t b = n & 1u, tph = (n >> 1) & 1u;
+      if (!tc_wait(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
+      tc_after();
+      const uint32_t idesc = idesc16(p.ta, p.tb);
+      for (int k = 0; k < p.K; k += 64, ++it) {
+        const uint32_t s = it % kMStages, ph = (it / kMStages) & 1u;
+        if (!tc_wait(&full[s], ph, abort_flag, a.status)) {
+          go = false;
+          break;
+        }
+        tc_after();
+        const uint32_t a0 = tc_smem(stages + s * kMStage), b0 = a0 + 2 * kMBox;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma16(tmem + b * 256, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc, k > 0 || kk > 0 ? 1u : 0u);
+        tc_commit<2>(&empty[s]);
+      }
+      if (go) tc_commit<2>(&tfull[b]);
+    }
+    tc_commit<2>(drain);
+    tc_drain(drain, 0);
+  } else if (warp >= 4) {  // store
+    const int q = warp & 3, h = (warp - 4) >> 2;
+    uint32_t n = 0;
+    for (int tile = first; tile < tiles; tile += step, ++n) {
+      const Product p = product<KIND>(t, tile, turn);
+      const MuonMat& mat = t.mats[p.id];
+      const uint32_t b = n & 1u, tph = (n >> 1) & 1u;
+      const bool got = tc_wait(&tfull[b], tph, abort_flag, a.status);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      tc_after();
+      const int row = p.m0 + 128 * (int)rank + 32 * q + lane;
+      // result = alpha acc + beta old, old read where the result goes in shape
+      float alpha, beta = 0.0f;
+      const uint16_t* old = nullptr;
+      uint16_t* out = nullptr;
+      int ld = mat.lds;
+      if constexpr (KIND == kGram) {
+        alpha = __fdiv_rn(mat.sa, __fmul_rn(mat.sx, mat.sx));
+        out = mat.gram;
+      } else if constexpr (KIND == kPoly) {
+        alpha = __fdiv_rn(0.25f * kNsC, mat.sa);  // gram gram is by sa^2, poly by sa / 4
+        beta = 0.25f * kNsB;
+        old = mat.gram;
+        out = mat.poly;
+      } else {
+        alpha = __fdiv_rn(4.0f, mat.sa);
+        beta = kNsA;
+        old = mat.x[turn];
+        out = mat.x[turn ^ 1];
+        ld = mat.ldx;
+      }
+      float decay = 1.0f, to_w = 0.0f;
+      if constexpr (KIND == kLast) {
+        const float big = (float)max(mat.rows, mat.cols);
+        const float scale = a.scale_mode == GS_MUON_SCALE_RMS
+                                ? 0.2f * sqrtf(big)
+                                : sqrtf(fmaxf(1.0f, __fdiv_rn((float)mat.rows, (float)mat.cols)));
+        decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
+        to_w = __fdiv_rn(__fmul_rn(a.lr, scale), mat.sx);
+      }
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 32) {
+        const int col = p.n0 + 128 * h + c;
+        uint32_t v[32];
+        tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * 256 + 128 * h + c, v);
+        tc_wait_ld<32>(v);
+        if (c == 96) {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) tc_arrive_at(&tempty[b], 0);
+        }
+        if (col >= p.N) continue;
+        if (row < p.M) {
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __fmul_rn(__uint_as_float(v[j]), alpha);
+          const int64_t at = (int64_t)row * ld + col;  // 16-byte aligned: ld % 8 == 0
+          if constexpr (KIND != kGram) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (col + j < p.N) {  // to the row's end, whose padding may be read
+                const uint4 w = *reinterpret_cast<const uint4*>(old + at + j);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[j + 2 * e] = __fmaf_rn(beta, lo_f16(ww[e]), o[j + 2 * e]);
+                  o[j + 2 * e + 1] = __fmaf_rn(beta, hi_f16(ww[e]), o[j + 2 * e + 1]);
+                }
+              }
+            }
+          }
+          if constexpr (KIND == kLast) {
+            const int64_t wat = (int64_t)row * mat.cols + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (col + j < p.N) {
+                const float w = __fmaf_rn(-to_w, o[j], __fmul_rn(mat.w[wat + j], decay));
+                mat.w[wat + j] = w;
+                if (mat.wb) mat.wb[wat + j] = Elem<GS_BF16>::put(w);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (col + j < p.N) {  // the padding's values are read by nothing
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = (uint32_t)Elem<GS_F16>::put(o[j + 2 * e]) |
+                         (uint32_t)Elem<GS_F16>::put(o[j + 2 * e + 1]) << 16;
+                *reinterpret_cast<uint4*>(out + at + j) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+            if (p.mirror) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col + j < p.N) out[(int64_t)(col + j) * ld + row] = Elem<GS_F16>::put(o[j]);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  cluster_barrier();
+  tc_after();
+  if (warp == 1) tc_dealloc<2>(tmem, 512);
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult qr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) ==
+            cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld) {
+  if (!encode_fn()) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND>
+static cudaError_t product_t(const MuonTable& t, const MuonArgs& a, int turn, cudaStream_t st) {
+  auto k = muon_product_kernel<KIND>;
+  int occ = 0;  // also raises the shared-memory limit in this context
+  const cudaError_t e = kernel_blocks_per_sm((const void*)k, kMThreads, kMSmem, &occ);
+  if (e != cudaSuccess) return e;
+  if (occ < 1) return cudaErrorInvalidConfiguration;
+  const int tiles = KIND == kGram || KIND == kPoly ? t.sym_tiles : t.app_tiles;
+  const int pairs = std::min(tiles, sm_count() / 2);
+  k<<<2 * pairs, kMThreads, kMSmem, st>>>(t, a, turn);
+  return cudaGetLastError();
+}
+
+template <int DT>
+static cudaError_t muon_dt(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)std::min<int64_t>(t.chunks, (int64_t)sm_count() * 32);
+  muon_momentum_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
+  muon_scale_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
+  cudaError_t e = cudaGetLastError();
+  for (int s = 0; e == cudaSuccess && s < a.steps; ++s) {
+    e = product_t<kGram>(t, a, s & 1, st);
+    if (e == cudaSuccess) e = product_t<kPoly>(t, a, s & 1, st);
+    if (e == cudaSuccess)
+      e = s + 1 < a.steps ? product_t<kApply>(t, a, s & 1, st) : product_t<kLast>(t, a, s & 1, st);
+  }
+  return e;
+}
+
+cudaError_t launch_master_update_muon(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
+  if (t.n == 0) return cudaSuccess;
+  if (a.grad_dtype == GS_F32) return muon_dt<GS_F32>(t, a, st);
+  if (a.grad_dtype == GS_F16) return muon_dt<GS_F16>(t, a, st);
+  return muon_dt<GS_BF16>(t, a, st);
+}
+
+}  // namespace gs
