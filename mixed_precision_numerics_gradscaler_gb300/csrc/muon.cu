@@ -1,8 +1,8 @@
 // muon.cu -- the update of weight matrices by their orthogonalised momentum
 // (K. Jordan, "Muon: an optimizer for hidden layers in neural networks", 2024):
 //   m = mu m + g,  u = g + mu m (nesterov) or m,  X = u / |u|_F,
-//   steps times:  G = X X^T,  P = b G + c G G,  X = a X + P X
-//                 (for more rows than columns: G = X^T X, X = a X + X P),
+//   steps times:  G = X X^T,  P = (a - 1) I + b G + c G G,  X = X + P X
+//                 (for more rows than columns: G = X^T X, X = X + X P),
 //   w = w (1 - lr weight_decay) - lr scale X,
 // (a, b, c) = (3.4445, -4.7750, 2.0315), a quintic in the singular values that
 // takes (0, 1] to near 1.
@@ -10,10 +10,13 @@
 // The products take s^2 (l + s) operations each way of G and P with their
 // symmetric halves left out, 2 s^2 l for X: all on the tensor cores.  Operands
 // are fp16, not bf16: every value is bounded (singular values of X stay below
-// 1.21, of G below 1.46, of P below 2.82), so that a power of two per matrix
+// 1.21, of G below 1.46, of P below 2.45), so that a power of two per matrix
 // keeps them in fp16's normal range with three more bits than bf16 has, at the
-// same rate.  Sums are fp32 in tensor memory, the polynomial's fp32 sums round
-// to fp16 once per product, and the last product's sums go into w unrounded.
+// same rate.  Sums are fp32 in tensor memory and round to fp16 once per product;
+// the last product's go into w unrounded.  One X is left out of P: where singular
+// values are near 1, P is then the small difference between X and the result,
+// and its rounding counts for as much (five steps end 1.1e-3 of |X| from the exact
+// polynomial, 1.5e-3 with X = a X + (b G + c G G) X; with bf16 1e-2).
 //
 // One launch per product takes every matrix of the list: persistent pairs of
 // CTAs walk the list's tiles of 256 x 256 (largest sums first).  A pair shares an
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         out = mat.poly;
       } else {
         alpha = __fdiv_rn(4.0f, mat.sa);
-        beta = kNsA;
+        beta = 1.0f;
         old = mat.x[turn];
         out = mat.x[turn ^ 1];
         ld = mat.ldx;
@@ -449,6 +452,12 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
                 }
               }
             }
+          }
+          if constexpr (KIND == kPoly) {
+            const float one = __fmul_rn(0.25f * (kNsA - 1.0f), mat.sa);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j == row) o[j] = __fadd_rn(o[j], one);
           }
           if constexpr (KIND == kLast) {
             const int64_t wat = (int64_t)row * mat.cols + col;
