@@ -10,10 +10,10 @@
 // Persistent clusters of CG CTAs (a pair shares one MMA of 256 rows: each CTA
 // loads half of either operand, which halves what shared memory has to take and
 // give per operation) walk tiles of 128 CG x BN of D.  Roles of a CTA:
-//   warp 0 (one lane)  TMA loads, 256 elements of K a stage: codes in the
+//   warp 0             TMA loads, 256 elements of K a stage: codes in the
 //                      128-byte swizzle, scale tiles as they lie;
-//   warp 1 (one lane of the leading CTA)  copies a stage's scales to tensor
-//                      memory and issues its four MMAs, in order in one pipe;
+//   warp 1 (of the leading CTA)  copies a stage's scales to tensor memory and
+//                      issues its four MMAs, in order in one pipe;
 //   warps 4-11         read the sum from tensor memory into registers, hand the
 //                      accumulator back at once and store while the next tile's
 //                      MMAs run.  A sum of 256 columns and the scales leave no
@@ -154,77 +154,87 @@ __global__ void __launch_bounds__(kQThreads, 1)
   tc_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {  // loads
-    uint32_t it = 0;
+  if (warp == 0) {  // loads
+    uint32_t s = 0, ph = 0, used = 0;
     bool go = !a.stall;
     for (int t = first; go && t < n_tiles; t += step) {
       int mt, nt;
       tc_tile(t, a.group, tiles_m, tiles_n, mt, nt);
       const int row_a = (mt * CG + (int)rank) * 128, row_b = nt * BN + (int)rank * S::kBRows;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % S::kStages, ph = (it / S::kStages) & 1u;
-        if (!tc_wait(&empty[s], ph ^ 1u, abort_flag, a.status)) {
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!tc_wait_warp(&empty[s], ph ^ 1u, abort_flag, a.status)) {
           go = false;
           break;
         }
         uint8_t* st = stages + s * S::kStage;
-        const uint32_t bar = tc_leader<CG>(&full[s]);
-        if (rank == 0) tc_expect(&full[s], CG * S::kBytes);
-        tc_load2<CG>(&map_a, bar, st, kb * kQRow, row_a);
-        tc_load2<CG>(&map_b, bar, st + S::kA, kb * kQRow, row_b);
-        tc_load3<CG>(&map_sa, bar, st + S::kA + S::kB, 0, kb * S::kTiles, row_a / 128);
-        tc_load3<CG>(&map_sb, bar, st + S::kA + S::kB + S::kSA, 0, kb * S::kTiles, nt * BN / 128);
+        if (tc_elect()) {
+          const uint32_t bar = tc_leader<CG>(&full[s]);
+          if (rank == 0) tc_expect(&full[s], CG * S::kBytes);
+          tc_load2<CG>(&map_a, bar, st, kb * kQRow, row_a);
+          tc_load2<CG>(&map_b, bar, st + S::kA, kb * kQRow, row_b);
+          tc_load3<CG>(&map_sa, bar, st + S::kA + S::kB, 0, kb * S::kTiles, row_a / 128);
+          tc_load3<CG>(&map_sb, bar, st + S::kA + S::kB + S::kSA, 0, kb * S::kTiles, nt * BN / 128);
+        }
+        __syncwarp();
+        used |= 1u << s;
+        if (++s == S::kStages) s = 0, ph ^= 1u;
       }
     }
     // the MMAs that read the last stages, and with them the loads, are done
-    const uint32_t tail = it < S::kStages ? it : S::kStages;
-    for (uint32_t j = it - tail; j != it; ++j)
-      tc_drain(&empty[j % S::kStages], (j / S::kStages) & 1u);
-  } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA
-    uint32_t it = 0, n = 0;
+    for (int j = 0; j < S::kStages; ++j) {
+      if (s == 0) s = S::kStages, ph ^= 1u;
+      --s;
+      if (used >> s & 1u) tc_drain(&empty[s], ph);
+    }
+  } else if (warp == 1 && rank == 0) {  // MMA
+    uint32_t s = 0, ph = 0, b = 0, tph = 0;
     bool go = true;
-    for (int t = first; go && t < n_tiles; t += step, ++n) {
+    for (int t = first; go && t < n_tiles; t += step) {
       int mt, nt;
       tc_tile(t, a.group, tiles_m, tiles_n, mt, nt);
-      const uint32_t b = n % S::kAccs, tph = (n / S::kAccs) & 1u;
-      if (!tc_wait(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
+      if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
       // where in its 128 rows' scales a narrow tile of B begins
       const uint32_t sb_at = BN < 128 ? (uint32_t)(nt * BN % 128) / 32 : 0;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % S::kStages, ph = (it / S::kStages) & 1u;
-        if (!tc_wait(&full[s], ph, abort_flag, a.status)) {
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
           break;
         }
         tc_after();
-        const uint32_t a0 = tc_smem(stages + s * S::kStage), b0 = a0 + S::kA;
+        const uint32_t a0 = tc_smem(stages) + s * S::kStage, b0 = a0 + S::kA;
         const uint32_t sa0 = b0 + S::kB, sb0 = sa0 + S::kSA;
-#pragma unroll
-        for (int j = 0; j < S::kTiles; ++j) {
-          cp_scales<CG>(tmem + S::kSfCol + 4 * j, tc_desc_scales(sa0 + 512 * j));
-#pragma unroll
-          for (int r = 0; r < S::kBTiles; ++r)
-            cp_scales<CG>(tmem + S::kSbCol + 4 * (j * S::kBTiles + r),
-                          tc_desc_scales(sb0 + 512 * (r * S::kTiles + j)));
-        }
         const int steps = (int)min((int64_t)4, (a.K - (int64_t)kb * kQK + 63) / 64);
+        if (tc_elect()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kk < steps) {
-            // NVFP4: a scale tile per 64 elements; MXFP4: one per 128, in halves
-            const int j = FMT == GS_NVFP4 ? kk : kk >> 1;
-            const uint32_t sf = FMT == GS_NVFP4 ? 0u : 2u * (kk & 1);
-            mma4<CG, FMT>(tmem + b * BN, tc_desc_k(a0 + 32 * kk), tc_desc_k(b0 + 32 * kk),
-                          idesc4<FMT>(128 * CG, BN, sf), tmem + S::kSfCol + 4 * j,
-                          tmem + S::kSbCol + 4 * j * S::kBTiles + sb_at, kb > 0 || kk > 0 ? 1u : 0u);
+          for (int j = 0; j < S::kTiles; ++j) {
+            cp_scales<CG>(tmem + S::kSfCol + 4 * j, tc_desc_scales(sa0 + 512 * j));
+#pragma unroll
+            for (int r = 0; r < S::kBTiles; ++r)
+              cp_scales<CG>(tmem + S::kSbCol + 4 * (j * S::kBTiles + r),
+                            tc_desc_scales(sb0 + 512 * (r * S::kTiles + j)));
           }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < steps) {
+              // NVFP4: a scale tile per 64 elements; MXFP4: one per 128, in halves
+              const int j = FMT == GS_NVFP4 ? kk : kk >> 1;
+              const uint32_t sf = FMT == GS_NVFP4 ? 0u : 2u * (kk & 1);
+              mma4<CG, FMT>(tmem + b * BN, tc_desc_k(a0 + 32 * kk), tc_desc_k(b0 + 32 * kk),
+                            idesc4<FMT>(128 * CG, BN, sf), tmem + S::kSfCol + 4 * j,
+                            tmem + S::kSbCol + 4 * j * S::kBTiles + sb_at, kb > 0 || kk > 0 ? 1u : 0u);
+            }
+          }
+          tc_commit<CG>(&empty[s]);
+          if (kb == nkb - 1) tc_commit<CG>(&tfull[b]);
         }
-        tc_commit<CG>(&empty[s]);
+        __syncwarp();
+        if (++s == S::kStages) s = 0, ph ^= 1u;
       }
-      if (go) tc_commit<CG>(&tfull[b]);
+      if (++b == S::kAccs) b = 0, tph ^= 1u;
     }
-    tc_commit<CG>(drain);
+    if (tc_elect()) tc_commit<CG>(drain);
+    __syncwarp();
     tc_drain(drain, 0);
   } else if (warp >= 4) {  // store
     const int q = warp & 3;            // the lanes of tensor memory this warp reads
