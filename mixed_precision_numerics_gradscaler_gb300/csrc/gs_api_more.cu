@@ -236,7 +236,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     bytes += (b + 255) / 256 * 256;
     return at;
   };
-  size_t at_mats, at_maps, at_partials, at_arrived, at_factor;
+  size_t at_mats, at_maps, at_partials, at_arrived, at_done, at_factor;
   std::vector<size_t> at_x;
   try {
     for (int32_t i = 0; i < n; ++i) {
@@ -282,9 +282,13 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
       m.first_app = (int)app;
       t.chunks += fp4_scale_tiles((int64_t)m.rows * m.cols, kMuonChunk);
       const int64_t ts = fp4_scale_tiles(m.s, kMuonTile);
-      sym += ts * (ts + 1) / 2;
-      app += fp4_scale_tiles(m.rows, kMuonTile) * fp4_scale_tiles(m.cols, kMuonTile);
-      if (sym >= (1LL << 30) || app >= (1LL << 30)) return GS_ERR_SHAPE;
+      const int64_t syms = ts * (ts + 1) / 2;
+      const int64_t apps = fp4_scale_tiles(m.rows, kMuonTile) * fp4_scale_tiles(m.cols, kMuonTile);
+      sym += syms;
+      app += apps;
+      if (2 * sym + app >= (1LL << 25)) return GS_ERR_SHAPE;  // of 20 steps: an int
+      m.syms = (int)syms;
+      m.apps = (int)apps;
     }
     t.n = (int)mats.size();
     t.sym_tiles = (int)sym;
@@ -293,6 +297,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     at_maps = take(mats.size() * 4 * sizeof(CUtensorMap));
     at_partials = take((size_t)t.chunks * sizeof(double));
     at_arrived = take(mats.size() * sizeof(unsigned));
+    at_done = take(mats.size() * sizeof(unsigned));
     at_factor = take(mats.size() * sizeof(float));
     for (const MuonMat& m : mats) {
       const size_t x = (size_t)m.rows * m.ldx * 2, g = (size_t)m.s * m.lds * 2;
@@ -329,6 +334,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     lt.maps = reinterpret_cast<const CUtensorMap*>(d + at_maps);
     lt.partials = reinterpret_cast<double*>(d + at_partials);
     lt.arrived = reinterpret_cast<unsigned*>(d + at_arrived);
+    lt.done = reinterpret_cast<unsigned*>(d + at_done);
     lt.factor = reinterpret_cast<float*>(d + at_factor);
     // operands' padding is read by 16-byte loads: numbers from the start
     if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, bytes, cudaStreamLegacy);

@@ -25,6 +25,7 @@ struct MuonMat {
   float sx, sa;
   int64_t first_chunk;       // of the list's chunks of elements
   int first_sym, first_app;  // of the list's tiles of either kind of product
+  int syms, apps;            // this matrix's tiles of either kind
 };
 
 struct MuonTable {
@@ -32,11 +33,11 @@ struct MuonTable {
   const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly
   double* partials;          // one per chunk
   unsigned int* arrived;     // per matrix, 0 between calls
+  unsigned int* done;        // per matrix: halves of tiles stored by the call's products
   float* factor;             // per matrix: sx / |u|
   int n;
   int64_t chunks;
   int sym_tiles, app_tiles;
-  int wide_any, tall_any;
 };
 
 struct MuonArgs {

@@ -18,13 +18,18 @@
 // and its rounding counts for as much (five steps end 1.1e-3 of |X| from the exact
 // polynomial, 1.5e-3 with X = a X + (b G + c G G) X; with bf16 1e-2).
 //
-// One launch per product takes every matrix of the list: persistent pairs of
-// CTAs walk the list's tiles of 256 x 256 (largest sums first).  A pair shares an
-// MMA of 256 x 256 x 16, each CTA loading half of either operand (TMA, 64 x 64
-// boxes, six stages of 64 of the sum); operands lie with the sum along their
-// rows or across them, which the MMA's descriptors tell.  Two accumulators of
-// 256 columns: eight warps store one while the other is formed.  Tiles above
-// the diagonal of G and P are stored transposed from the ones below.
+// One cooperative launch takes every product of every step and matrix of the
+// list: persistent pairs of CTAs walk the tiles of 256 x 256 (every G, every P,
+// every X of a step; longest sums first).  A tile waits until the matrix's tiles
+// of the products before are stored, told by a count per matrix, so that one
+// matrix's product fills the gap at the end of another's and nothing waits for
+// a launch.  Pairs take their tiles in the common order, so the first tile that
+// is not done never waits for one behind it.  A pair shares an MMA of
+// 256 x 256 x 16, each CTA loading half of either operand (TMA, 64 x 64 boxes, six
+// stages of 64 of the sum); operands lie with the sum along their rows or across
+// them, which the MMA's descriptors tell.  Two accumulators of 256 columns: eight
+// warps store one while the other is formed.  Tiles above the diagonal of G and
+// P are stored transposed from the ones below.
 // Every wait is bounded and reports GS_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -47,11 +52,12 @@ constexpr int kMEThreads = 256;              // of the element-wise steps
 constexpr int kMBox = 64 * 128;              // bytes of a 64 x 64 box
 constexpr int kMStage = 4 * kMBox;           // a CTA's 128 x 64 of either operand
 constexpr int kMStages = 6;
-constexpr int kMSmem = kMStages * kMStage + 1024 + 256;
+constexpr int kMSmem = kMStages * kMStage + 8 * 4096 + 1024 + 256;
+static_assert(kMSmem <= 232448, "dynamic shared memory above the per-CTA limit");
 
 // The matrix that holds item t: the last one whose first is not above t.
 template <typename T>
-__device__ __forceinline__ int mat_of(const MuonMat* __restrict__ mats, int n, T t, T MuonMat::*first) {
+__device__ __forceinline__ int mat_of(const MuonMat* mats, int n, T t, T MuonMat::*first) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -100,6 +106,7 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
     const int64_t n = (int64_t)mat.rows * mat.cols, base = (c - mat.first_chunk) * kMuonChunk;
     const int64_t end = min(n, base + kMuonChunk);
     const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
+    if (base == 0 && threadIdx.x == 0) t.done[id] = 0;  // for the products' launch
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
@@ -227,24 +234,38 @@ __device__ __forceinline__ uint64_t desc16(uint32_t base, int kk, bool across) {
          ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Where tile t of a product lies, and what its operands are.
+// One tile of a step's products: where it lies and what it takes.
 struct Product {
+  int kind, turn;        // turn: which of x[0], x[1] the step reads
   int id;                // matrix
   int m0, n0;            // first row and column of the result
   int M, N, K;
   bool ta, tb;           // operand with its sum across the rows
   int map_a, map_b;      // of the matrix's four maps
   bool mirror;           // a tile below the diagonal
+  unsigned need;         // halves of the matrix's tiles that have to be done before
 };
-template <int KIND>
-__device__ __forceinline__ Product product(const MuonTable& t, int tile, int turn) {
+// The step's tiles in their order: every matrix's G, every P, every X.
+__device__ __forceinline__ Product product(const MuonTable& t, int at, int steps) {
   Product p;
-  constexpr bool kSym = KIND == kGram || KIND == kPoly;
-  p.id = mat_of(t.mats, t.n, tile, kSym ? &MuonMat::first_sym : &MuonMat::first_app);
+  const int per = 2 * t.sym_tiles + t.app_tiles, step = at / per;
+  at -= step * per;
+  p.turn = step & 1;
+  const bool sym = at < 2 * t.sym_tiles;
+  if (sym) {
+    p.kind = at < t.sym_tiles ? kGram : kPoly;
+    if (p.kind == kPoly) at -= t.sym_tiles;
+  } else {
+    p.kind = step + 1 < steps ? kApply : kLast;
+    at -= 2 * t.sym_tiles;
+  }
+  p.id = mat_of(t.mats, t.n, at, sym ? &MuonMat::first_sym : &MuonMat::first_app);
   const MuonMat& mat = t.mats[p.id];
-  const int at = tile - (kSym ? mat.first_sym : mat.first_app);
+  at -= sym ? mat.first_sym : mat.first_app;
+  const int done = step * (2 * mat.syms + mat.apps);
+  p.need = 2u * (unsigned)(done + (p.kind == kGram ? 0 : p.kind == kPoly ? mat.syms : 2 * mat.syms));
   int mt, nt;
-  if constexpr (kSym) {  // row mt of a triangle holds tiles mt (mt + 1) / 2 ...
+  if (sym) {  // row mt of a triangle holds tiles mt (mt + 1) / 2 ...
     mt = (int)((sqrtf(8.0f * (float)at + 1.0f) - 1.0f) * 0.5f);
     while ((mt + 1) * (mt + 2) / 2 <= at) ++mt;
     while (mt * (mt + 1) / 2 > at) --mt;
@@ -260,11 +281,11 @@ __device__ __forceinline__ Product product(const MuonTable& t, int tile, int tur
   }
   p.m0 = mt * kMuonTile;
   p.n0 = nt * kMuonTile;
-  if constexpr (KIND == kGram) {
+  if (p.kind == kGram) {
     p.K = mat.tall ? mat.rows : mat.cols;
     p.ta = p.tb = mat.tall;
-    p.map_a = p.map_b = turn;
-  } else if constexpr (KIND == kPoly) {
+    p.map_a = p.map_b = p.turn;
+  } else if (p.kind == kPoly) {
     p.K = mat.s;
     p.ta = p.tb = false;
     p.map_a = p.map_b = 2;
@@ -272,8 +293,8 @@ __device__ __forceinline__ Product product(const MuonTable& t, int tile, int tur
     p.K = mat.s;
     p.ta = false;
     p.tb = !mat.tall;
-    p.map_a = mat.tall ? turn : 3;
-    p.map_b = mat.tall ? 3 : turn;
+    p.map_a = mat.tall ? p.turn : 3;
+    p.map_b = mat.tall ? 3 : p.turn;
   }
   return p;
 }
@@ -282,16 +303,43 @@ __device__ __forceinline__ Product product(const MuonTable& t, int tile, int tur
 __device__ __forceinline__ void map_fence(const CUtensorMap* m) {
   asm volatile("fence.proxy.tensormap::generic.acquire.sys [%0], 128;" ::"l"(m) : "memory");
 }
+__device__ __forceinline__ unsigned load_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+// Bounded wait for *p >= need; a whole warp goes on or gives up together.
+__device__ __forceinline__ bool wait_done(const unsigned* p, unsigned need, volatile int* abort_flag,
+                                          int32_t* status) {
+  bool ok = true;
+  if (load_acquire(p) < need) {
+    const uint64_t t0 = tc_now();
+    while (load_acquire(p) < need) {
+      if (*abort_flag) ok = false;
+      if (tc_now() - t0 > kTcWaitNs) {
+        *abort_flag = 1;
+        atomicExch(status, (int32_t)GS_ERR_TIMEOUT);
+        ok = false;
+      }
+      if (!ok) break;
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
 
-// turn: which of x[0], x[1] the step reads.
-template <int KIND>
+// 32 rows x 32 columns of fp32 in shared memory: 16-byte piece j of row r.
+__device__ __forceinline__ float* piece(float* buf, int r, int j) {
+  return buf + 32 * r + 4 * (j ^ (r & 7));
+}
+
 __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
-    muon_product_kernel(MuonTable t, MuonArgs a, int turn) {
+    muon_products_kernel(MuonTable t, MuonArgs a) {
   if (*a.found_inf) return;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + kMStages * kMStage);
+  float* out_stage = reinterpret_cast<float*>(stages + kMStages * kMStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + 8 * 1024);
   uint64_t* empty = full + kMStages;
   uint64_t* tfull = empty + kMStages;
   uint64_t* tempty = tfull + 2;
@@ -302,7 +350,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
-  const int tiles = KIND == kGram || KIND == kPoly ? t.sym_tiles : t.app_tiles;
+  const int tiles = a.steps * (2 * t.sym_tiles + t.app_tiles);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMStages; ++s) {
@@ -324,104 +372,123 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
   tc_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {  // loads
-    uint32_t it = 0;
+  if (warp == 0) {  // loads
+    uint32_t s = 0, ph = 0, used = 0;
     int seen = -1;
     bool go = !a.stall;
     for (int tile = first; go && tile < tiles; tile += step) {
-      const Product p = product<KIND>(t, tile, turn);
-      const CUtensorMap* ma = t.maps + 4 * p.id + p.map_a;
-      const CUtensorMap* mb = t.maps + 4 * p.id + p.map_b;
+      const Product p = product(t, tile, a.steps);
+      const CUtensorMap* maps = t.maps + 4 * p.id;
       if (p.id != seen) {
-        map_fence(ma);
-        if (mb != ma) map_fence(mb);
+        if (lane < 4) map_fence(maps + lane);
+        __syncwarp();
         seen = p.id;
       }
+      if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
+      // what other CTAs stored is read by TMA from here on
+      asm volatile("fence.proxy.async;" ::: "memory");
+      const CUtensorMap *ma = maps + p.map_a, *mb = maps + p.map_b;
       const int m0 = p.m0 + 128 * (int)rank, n0 = p.n0 + 128 * (int)rank;
-      for (int k = 0; k < p.K; k += 64, ++it) {
-        const uint32_t s = it % kMStages, ph = (it / kMStages) & 1u;
-        if (!tc_wait(&empty[s], ph ^ 1u, abort_flag, a.status)) {
+      for (int k = 0; k < p.K; k += 64) {
+        if (!tc_wait_warp(&empty[s], ph ^ 1u, abort_flag, a.status)) {
           go = false;
           break;
         }
         uint8_t* st = stages + s * kMStage;
-        const uint32_t bar = tc_leader<2>(&full[s]);
-        if (rank == 0) tc_expect(&full[s], 2 * kMStage);
+        if (tc_elect()) {
+          const uint32_t bar = tc_leader<2>(&full[s]);
+          if (rank == 0) tc_expect(&full[s], 2 * kMStage);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          tc_load2<2>(ma, bar, st + h * kMBox, p.ta ? m0 + 64 * h : k, p.ta ? k : m0 + 64 * h);
-          tc_load2<2>(mb, bar, st + (2 + h) * kMBox, p.tb ? n0 + 64 * h : k, p.tb ? k : n0 + 64 * h);
+          for (int h = 0; h < 2; ++h) {
+            tc_load2<2>(ma, bar, st + h * kMBox, p.ta ? m0 + 64 * h : k, p.ta ? k : m0 + 64 * h);
+            tc_load2<2>(mb, bar, st + (2 + h) * kMBox, p.tb ? n0 + 64 * h : k, p.tb ? k : n0 + 64 * h);
+          }
         }
+        __syncwarp();
+        used |= 1u << s;
+        if (++s == kMStages) s = 0, ph ^= 1u;
       }
     }
-    const uint32_t tail = it < kMStages ? it : kMStages;
-    for (uint32_t j = it - tail; j != it; ++j) tc_drain(&empty[j % kMStages], (j / kMStages) & 1u);
-  } else if (warp == 1 && lane == 0 && rank == 0) {  // MMA
-    uint32_t it = 0, n = 0;
+    // the MMAs that read the last stages, and with them the loads, are done
+    for (int j = 0; j < kMStages; ++j) {
+      if (s == 0) s = kMStages, ph ^= 1u;
+      --s;
+      if (used >> s & 1u) tc_drain(&empty[s], ph);
+    }
+  } else if (warp == 1 && rank == 0) {  // MMA
+    uint32_t s = 0, ph = 0, b = 0, tph = 0;
     bool go = true;
-    for (int tile = first; go && tile < tiles; tile += step, ++n) {
-      const Product p = product<KIND>(t, tile, turn);
-      const uint32_t b = n & 1u, tph = (n >> 1) & 1u;
-      if (!tc_wait(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
+    for (int tile = first; go && tile < tiles; tile += step) {
+      const Product p = product(t, tile, a.steps);
+      if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
       const uint32_t idesc = idesc16(p.ta, p.tb);
-      for (int k = 0; k < p.K; k += 64, ++it) {
-        const uint32_t s = it % kMStages, ph = (it / kMStages) & 1u;
-        if (!tc_wait(&full[s], ph, abort_flag, a.status)) {
+      for (int k = 0; k < p.K; k += 64) {
+        if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
           break;
         }
         tc_after();
-        const uint32_t a0 = tc_smem(stages + s * kMStage), b0 = a0 + 2 * kMBox;
+        const uint32_t a0 = tc_smem(stages) + s * kMStage, b0 = a0 + 2 * kMBox;
+        if (tc_elect()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma16(tmem + b * 256, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc, k > 0 || kk > 0 ? 1u : 0u);
-        tc_commit<2>(&empty[s]);
+          for (int kk = 0; kk < 4; ++kk)
+            mma16(tmem + b * 256, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc,
+                  k > 0 || kk > 0 ? 1u : 0u);
+          tc_commit<2>(&empty[s]);
+          if (k + 64 >= p.K) tc_commit<2>(&tfull[b]);
+        }
+        __syncwarp();
+        if (++s == kMStages) s = 0, ph ^= 1u;
       }
-      if (go) tc_commit<2>(&tfull[b]);
+      b ^= 1u;
+      if (b == 0) tph ^= 1u;
     }
-    tc_commit<2>(drain);
+    if (tc_elect()) tc_commit<2>(drain);
+    __syncwarp();
     tc_drain(drain, 0);
   } else if (warp >= 4) {  // store
     const int q = warp & 3, h = (warp - 4) >> 2;
-    uint32_t n = 0;
-    for (int tile = first; tile < tiles; tile += step, ++n) {
-      const Product p = product<KIND>(t, tile, turn);
+    float* const buf = out_stage + (warp - 4) * 1024;
+    uint32_t b = 0, tph = 0;
+    for (int tile = first; tile < tiles; tile += step) {
+      const Product p = product(t, tile, a.steps);
       const MuonMat& mat = t.mats[p.id];
-      const uint32_t b = n & 1u, tph = (n >> 1) & 1u;
-      const bool got = tc_wait(&tfull[b], tph, abort_flag, a.status);
-      if (!__all_sync(0xFFFFFFFFu, got)) break;
-      tc_after();
-      const int row = p.m0 + 128 * (int)rank + 32 * q + lane;
-      // result = alpha acc + beta old, old read where the result goes in shape
-      float alpha, beta = 0.0f;
+      // result = alpha acc + beta old, old in the result's shape
+      float alpha, beta = 0.0f, one = 0.0f, decay = 1.0f, to_w = 0.0f;
       const uint16_t* old = nullptr;
       uint16_t* out = nullptr;
       int ld = mat.lds;
-      if constexpr (KIND == kGram) {
+      if (p.kind == kGram) {
         alpha = __fdiv_rn(mat.sa, __fmul_rn(mat.sx, mat.sx));
         out = mat.gram;
-      } else if constexpr (KIND == kPoly) {
+      } else if (p.kind == kPoly) {
         alpha = __fdiv_rn(0.25f * kNsC, mat.sa);  // gram gram is by sa^2, poly by sa / 4
         beta = 0.25f * kNsB;
+        one = __fmul_rn(0.25f * (kNsA - 1.0f), mat.sa);
         old = mat.gram;
         out = mat.poly;
       } else {
         alpha = __fdiv_rn(4.0f, mat.sa);
         beta = 1.0f;
-        old = mat.x[turn];
-        out = mat.x[turn ^ 1];
+        old = mat.x[p.turn];
+        out = mat.x[p.turn ^ 1];
         ld = mat.ldx;
+        if (p.kind == kLast) {
+          const float big = (float)max(mat.rows, mat.cols);
+          const float scale = a.scale_mode == GS_MUON_SCALE_RMS
+                                  ? 0.2f * sqrtf(big)
+                                  : sqrtf(fmaxf(1.0f, __fdiv_rn((float)mat.rows, (float)mat.cols)));
+          decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
+          to_w = __fdiv_rn(__fmul_rn(a.lr, scale), mat.sx);
+        }
       }
-      float decay = 1.0f, to_w = 0.0f;
-      if constexpr (KIND == kLast) {
-        const float big = (float)max(mat.rows, mat.cols);
-        const float scale = a.scale_mode == GS_MUON_SCALE_RMS
-                                ? 0.2f * sqrtf(big)
-                                : sqrtf(fmaxf(1.0f, __fdiv_rn((float)mat.rows, (float)mat.cols)));
-        decay = __fsub_rn(1.0f, __fmul_rn(a.lr, a.weight_decay));
-        to_w = __fdiv_rn(__fmul_rn(a.lr, scale), mat.sx);
-      }
+      const bool vec_w = mat.cols % 4 == 0 && (uintptr_t)mat.w % 16 == 0 && (uintptr_t)mat.wb % 8 == 0;
+      const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
+      const bool got = tc_wait(&tfull[b], tph, abort_flag, a.status);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      tc_after();
+      load_acquire(t.done + p.id);  // at least p.need: old is as other CTAs stored it
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         const int col = p.n0 + 128 * h + c;
@@ -433,62 +500,99 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
           __syncwarp();
           if (lane == 0) tc_arrive_at(&tempty[b], 0);
         }
-        if (col >= p.N) continue;
-        if (row < p.M) {
-          float o[32];
+        if (col >= p.N || row0 >= p.M) continue;
+        if (p.kind == kGram && p.mirror && row < p.M) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __fmul_rn(__uint_as_float(v[j]), alpha);
-          const int64_t at = (int64_t)row * ld + col;  // 16-byte aligned: ld % 8 == 0
-          if constexpr (KIND != kGram) {
+          for (int j = 0; j < 32; ++j)
+            if (col + j < p.N)
+              out[(int64_t)(col + j) * ld + row] =
+                  Elem<GS_F16>::put(__fmul_rn(__uint_as_float(v[j]), alpha));
+        }
+        // through shared memory: eight lanes to a row's 32 columns
+        __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (col + j < p.N) {  // to the row's end, whose padding may be read
-                const uint4 w = *reinterpret_cast<const uint4*>(old + at + j);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < 8; ++j) {
+          float o[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  o[j + 2 * e] = __fmaf_rn(beta, lo_f16(ww[e]), o[j + 2 * e]);
-                  o[j + 2 * e + 1] = __fmaf_rn(beta, hi_f16(ww[e]), o[j + 2 * e + 1]);
-                }
-              }
+          for (int e = 0; e < 4; ++e) o[e] = __fmul_rn(__uint_as_float(v[4 * j + e]), alpha);
+          *reinterpret_cast<float4*>(piece(buf, lane, j)) = make_float4(o[0], o[1], o[2], o[3]);
+        }
+        __syncwarp();
+        const int c4 = col + 4 * (lane & 7);
+        uint2 w[8];
+        if (p.kind != kGram) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {  // the padding at a row's end may be read
+            const int r = row0 + 4 * i + (lane >> 3);
+            if (r < p.M && c4 < p.N) w[i] = __ldcg(reinterpret_cast<const uint2*>(old + (int64_t)r * ld + c4));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3), r = row0 + rr;
+          if (r >= p.M || c4 >= p.N) continue;
+          float* const at = piece(buf, rr, lane & 7);
+          float4 f = *reinterpret_cast<const float4*>(at);
+          float o[4] = {f.x, f.y, f.z, f.w};
+          if (p.kind != kGram) {
+            const float u[4] = {lo_f16(w[i].x), hi_f16(w[i].x), lo_f16(w[i].y), hi_f16(w[i].y)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[e] = __fmaf_rn(beta, u[e], o[e]);
+              if (p.kind == kPoly && c4 + e == r) o[e] = __fadd_rn(o[e], one);
             }
           }
-          if constexpr (KIND == kPoly) {
-            const float one = __fmul_rn(0.25f * (kNsA - 1.0f), mat.sa);
+          if (p.kind != kLast) {  // the padding's values are read by nothing
+            *reinterpret_cast<uint2*>(out + (int64_t)r * ld + c4) =
+                make_uint2((uint32_t)Elem<GS_F16>::put(o[0]) | (uint32_t)Elem<GS_F16>::put(o[1]) << 16,
+                           (uint32_t)Elem<GS_F16>::put(o[2]) | (uint32_t)Elem<GS_F16>::put(o[3]) << 16);
+            if (p.kind == kPoly && p.mirror)
+              *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
+          } else if (vec_w) {
+            float* const wp = mat.w + (int64_t)r * mat.cols + c4;
+            f = *reinterpret_cast<const float4*>(wp);
+            f.x = __fmaf_rn(-to_w, o[0], __fmul_rn(f.x, decay));
+            f.y = __fmaf_rn(-to_w, o[1], __fmul_rn(f.y, decay));
+            f.z = __fmaf_rn(-to_w, o[2], __fmul_rn(f.z, decay));
+            f.w = __fmaf_rn(-to_w, o[3], __fmul_rn(f.w, decay));
+            *reinterpret_cast<float4*>(wp) = f;
+            if (mat.wb)
+              *reinterpret_cast<uint2*>(mat.wb + (int64_t)r * mat.cols + c4) =
+                  make_uint2(cvt_f32x2_bf16x2(f.y, f.x), cvt_f32x2_bf16x2(f.w, f.z));
+          } else {
+            *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        if (p.kind == kPoly && p.mirror) {
+          __syncwarp();
+          if (row < p.M) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (col + j == row) o[j] = __fadd_rn(o[j], one);
+              if (col + j < p.N)
+                out[(int64_t)(col + j) * ld + row] = Elem<GS_F16>::put(piece(buf, lane, j >> 2)[j & 3]);
           }
-          if constexpr (KIND == kLast) {
-            const int64_t wat = (int64_t)row * mat.cols + col;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (col + j < p.N) {
-                const float w = __fmaf_rn(-to_w, o[j], __fmul_rn(mat.w[wat + j], decay));
-                mat.w[wat + j] = w;
-                if (mat.wb) mat.wb[wat + j] = Elem<GS_BF16>::put(w);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              if (col + j < p.N) {  // the padding's values are read by nothing
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[e] = (uint32_t)Elem<GS_F16>::put(o[j + 2 * e]) |
-                         (uint32_t)Elem<GS_F16>::put(o[j + 2 * e + 1]) << 16;
-                *reinterpret_cast<uint4*>(out + at + j) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-            if (p.mirror) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (col + j < p.N) out[(int64_t)(col + j) * ld + row] = Elem<GS_F16>::put(o[j]);
+        } else if (p.kind == kLast && !vec_w) {  // any address: a row's columns by lanes
+          __syncwarp();
+          const int rows = min(32, p.M - row0);
+          if (col + lane < p.N) {
+            for (int r = 0; r < rows; ++r) {
+              const int64_t at = (int64_t)(row0 + r) * mat.cols + col + lane;
+              const float f = __fmaf_rn(-to_w, piece(buf, r, lane >> 2)[lane & 3], __fmul_rn(mat.w[at], decay));
+              mat.w[at] = f;
+              if (mat.wb) mat.wb[at] = Elem<GS_BF16>::put(f);
             }
           }
         }
       }
+      // this CTA's half is stored: for loads of either kind by other CTAs
+      __threadfence();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (threadIdx.x == 128) {
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(t.done + p.id) : "memory");
+      }
+      b ^= 1u;
+      if (b == 0) tph ^= 1u;
     }
   }
   tc_before();
@@ -523,17 +627,25 @@ bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, i
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND>
-static cudaError_t product_t(const MuonTable& t, const MuonArgs& a, int turn, cudaStream_t st) {
-  auto k = muon_product_kernel<KIND>;
-  int occ = 0;  // also raises the shared-memory limit in this context
-  const cudaError_t e = kernel_blocks_per_sm((const void*)k, kMThreads, kMSmem, &occ);
+static cudaError_t launch_products(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
+  int occ = 0, pairs = 0;  // also raises the shared-memory limit in this context
+  cudaError_t e = kernel_blocks_per_sm((const void*)muon_products_kernel, kMThreads, kMSmem, &occ);
+  if (e == cudaSuccess)
+    e = kernel_clusters((const void*)muon_products_kernel, kMThreads, kMSmem, 2, &pairs);
   if (e != cudaSuccess) return e;
-  if (occ < 1) return cudaErrorInvalidConfiguration;
-  const int tiles = KIND == kGram || KIND == kPoly ? t.sym_tiles : t.app_tiles;
-  const int pairs = std::min(tiles, sm_count() / 2);
-  k<<<2 * pairs, kMThreads, kMSmem, st>>>(t, a, turn);
-  return cudaGetLastError();
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)std::min(std::max(t.sym_tiles, t.app_tiles), pairs));
+  cfg.blockDim = dim3(kMThreads);
+  cfg.dynamicSmemBytes = kMSmem;
+  cfg.stream = st;
+  // CTAs wait for one another's tiles: all of them have to be resident
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeCooperative;
+  at.val.cooperative = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, muon_products_kernel, t, a);
 }
 
 template <int DT>
@@ -541,14 +653,8 @@ static cudaError_t muon_dt(const MuonTable& t, const MuonArgs& a, cudaStream_t s
   const unsigned grid = (unsigned)std::min<int64_t>(t.chunks, (int64_t)sm_count() * 32);
   muon_momentum_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
   muon_scale_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
-  cudaError_t e = cudaGetLastError();
-  for (int s = 0; e == cudaSuccess && s < a.steps; ++s) {
-    e = product_t<kGram>(t, a, s & 1, st);
-    if (e == cudaSuccess) e = product_t<kPoly>(t, a, s & 1, st);
-    if (e == cudaSuccess)
-      e = s + 1 < a.steps ? product_t<kApply>(t, a, s & 1, st) : product_t<kLast>(t, a, s & 1, st);
-  }
-  return e;
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? launch_products(t, a, st) : e;
 }
 
 cudaError_t launch_master_update_muon(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
