@@ -153,7 +153,8 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
 
 size_t gs_policy_loss_ws_bytes(int64_t T, int64_t S) {
   if (T < 0 || S < 0 || T > (int64_t)1 << 40 || S > (int64_t)1 << 40) return 0;
-  return sizeof(PolicyHead) + (size_t)S * 8 + kPolicyCtas * sizeof(PolicyPart);
+  return sizeof(PolicyHead) + (size_t)S * 8 + kPolicyCtas * sizeof(PolicyPart) +
+         (size_t)policy_mask_words(T) * 4;
 }
 
 int gs_policy_loss(const float* logprob, const float* old_logprob, const float* ref_logprob,
@@ -212,6 +213,7 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
   a.head = reinterpret_cast<PolicyHead*>(p);
   a.n = reinterpret_cast<unsigned long long*>(p + sizeof(PolicyHead));
   a.part = reinterpret_cast<PolicyPart*>(p + sizeof(PolicyHead) + S * 8);
+  a.mask = reinterpret_cast<unsigned*>(a.part + kPolicyCtas);
   const cudaError_t e = launch_policy_loss(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? GS_OK : cuda_fail(e);
 }

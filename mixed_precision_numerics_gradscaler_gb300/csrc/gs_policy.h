@@ -22,6 +22,9 @@ struct PolicyHead {
 };
 static_assert(sizeof(PolicyHead) == 64, "the counts behind it are 8-byte aligned");
 
+// Words of a mask of T tokens, in runs of 256.
+inline int64_t policy_mask_words(int64_t T) { return (T + 255) / 256 * 8; }
+
 // A real number as the sum of two fp32 ones.
 struct Border {
   float hi, lo;
@@ -40,6 +43,7 @@ struct PolicyArgs {
   float factor_high, factor_low, factor_dual, kl;
   PolicyHead* head;
   unsigned long long* n;                   // tokens that count, by sequence
+  unsigned* mask;                          // a bit per token, where there are targets
   PolicyPart* part;
 };
 

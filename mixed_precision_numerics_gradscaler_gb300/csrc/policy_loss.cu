@@ -23,9 +23,10 @@
 // One pass reads 8 to 24 bytes per token and writes 4: HBM is the bound of a
 // long batch.  The gradient's weights need the counts first: a pass over the
 // targets alone (8 bytes per token) counts them with integer additions, whose
-// order changes nothing; the targets' second read comes from L2 where they fit
-// it.  Sums: four tokens' terms in fp32, everything beyond in fp64, joined in a
-// fixed order by the last CTA to finish.  Short batches are done by one CTA,
+// order changes nothing, and leaves a bit per token for the pass over the rest.
+// Sums: eight tokens' terms in fp32, a thread's sums with their rounding errors
+// carried along, everything beyond in fp64, joined in a fixed order by the last
+// CTA to finish.  Short batches are done by one CTA,
 // which counts and sums in one launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,19 +40,49 @@
 namespace gs {
 
 constexpr int kPThreads = 256;
-constexpr int kPRun = 4;                     // tokens per thread and step
+constexpr int kPRun = 8;                     // tokens per thread and step
 constexpr int kPTile = kPThreads * kPRun;    // tokens per CTA and step
 constexpr int kPSpan = 1024;                 // sequences of a step kept in shared memory
 
-// Tokens that one CTA of 1024 threads does alone (see launch_policy_loss).
-constexpr int64_t kPSmallTokens = 8192;
+// Tokens that one CTA does alone (see launch_policy_loss).
+constexpr int64_t kPSmallTokens = 4608;
 constexpr int64_t kPSmallSeqs = 2048;
-constexpr int kPSmallThreads = 1024;
+constexpr int kPSmallThreads = 512;
+
+// A sum in fp32 with its rounding errors carried along (the fp64 pipe would
+// take as long as everything else here).
+struct Pair {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v) {
+    const float s = __fadd_rn(hi, v), w = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, w)), __fsub_rn(v, w)));
+    hi = s;
+  }
+  // Takes in the sum of the lane o further on.
+  __device__ __forceinline__ void merge(int o) {
+    const float h = __shfl_down_sync(0xFFFFFFFFu, hi, o), l = __shfl_down_sync(0xFFFFFFFFu, lo, o);
+    add(h);
+    lo = __fadd_rn(lo, l);
+  }
+  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+};
 
 struct Sums {
   double loss, ratio, kl;
   unsigned long long held;
 };
+// Adds N (a power of two) lanes' sums; the result in lane 0.
+template <int N>
+__device__ __forceinline__ Sums warp_sums(Sums s) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1) {
+    s.loss += __shfl_down_sync(0xFFFFFFFFu, s.loss, o);
+    s.ratio += __shfl_down_sync(0xFFFFFFFFu, s.ratio, o);
+    s.kl += __shfl_down_sync(0xFFFFFFFFu, s.kl, o);
+    s.held += __shfl_down_sync(0xFFFFFFFFu, s.held, o);
+  }
+  return s;
+}
 
 // The first s in [lo, hi] with end[s] > t (hi where none is), end = offsets + 1.
 __device__ __forceinline__ int64_t seq_of(const int64_t* __restrict__ end, int64_t lo, int64_t hi,
@@ -99,24 +130,26 @@ struct Token {
   float value, slope, ratio, kl;  // l and dl/dx without the weight
   bool held;
 };
+template <bool REF>
 __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, float ref, float adv) {
   Token t;
   float d, e;
   two_diff(x, old, d, e);
   t.ratio = expf(d);
-  const bool up = adv > 0.0f && above(d, e, a.high);
-  const bool down = adv < 0.0f && below(d, e, a.low);
-  const bool far = adv < 0.0f && above(d, e, a.dual);
-  t.held = up || down || far;
-  const float factor = up ? a.factor_high : down ? a.factor_low : far ? a.factor_dual : t.ratio;
+  const bool gains = adv > 0.0f, loses = adv < 0.0f;
+  const Border top = gains ? a.high : a.dual;
+  const bool over = (gains || loses) && above(d, e, top);
+  const bool under = loses && below(d, e, a.low);
+  t.held = over || under;
+  const float factor = over ? (gains ? a.factor_high : a.factor_dual) : under ? a.factor_low : t.ratio;
   const float obj = adv == 0.0f ? 0.0f : __fmul_rn(factor, adv);
   t.slope = t.held ? 0.0f : -obj;
   t.kl = 0.0f;
   t.value = -obj;
-  if (a.ref) {
+  if constexpr (REF) {
     const float y = __fsub_rn(ref, x);
-    const float em1 = expm1f(y);
-    // y^2 (1/2 + y/6 + ... + y^7/9!): cut off at 2e-9 of it for |y| <= 1/2
+    // y^2 (1/2 + y/6 + ... + y^7/9!): cut off at 2e-9 of it for |y| <= 1/2;
+    // beyond, e^y - 1 keeps its digits but for two bits
     float p = 1.0f / 362880.0f;
     p = __fmaf_rn(p, y, 1.0f / 40320.0f);
     p = __fmaf_rn(p, y, 1.0f / 5040.0f);
@@ -125,33 +158,36 @@ __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, 
     p = __fmaf_rn(p, y, 1.0f / 24.0f);
     p = __fmaf_rn(p, y, 1.0f / 6.0f);
     p = __fmaf_rn(p, y, 0.5f);
-    t.kl = fabsf(y) <= 0.5f ? __fmul_rn(__fmul_rn(y, y), p) : __fsub_rn(em1, y);
+    p = __fmul_rn(__fmul_rn(y, y), p);
+    const bool near = fabsf(y) <= 0.5f;
+    const float far_em1 = __fsub_rn(expf(y), 1.0f);
+    const float em1 = near ? __fadd_rn(y, p) : far_em1;
+    t.kl = near ? p : __fsub_rn(far_em1, y);
     t.value = __fmaf_rn(a.kl, t.kl, t.value);
     t.slope = __fmaf_rn(-a.kl, em1, t.slope);
   }
   return t;
 }
 
-// Adds a block's sums; the result in thread 0.
+// Adds a block's sums, the threads' as fp32 pairs within a warp (512 threads'
+// additions in fp64 would take 2 us), the warps' in fp64; the result in thread 0.
 template <int NT>
-__device__ __forceinline__ Sums block_sums(Sums s) {
+__device__ __forceinline__ Sums block_sums(Pair loss, Pair ratio, Pair kl, unsigned long long held) {
   __shared__ Sums red[NT / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    s.loss += __shfl_down_sync(0xFFFFFFFFu, s.loss, o);
-    s.ratio += __shfl_down_sync(0xFFFFFFFFu, s.ratio, o);
-    s.kl += __shfl_down_sync(0xFFFFFFFFu, s.kl, o);
-    s.held += __shfl_down_sync(0xFFFFFFFFu, s.held, o);
+    loss.merge(o);
+    ratio.merge(o);
+    kl.merge(o);
+    held += __shfl_down_sync(0xFFFFFFFFu, held, o);
   }
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+  if ((threadIdx.x & 31) == 0)
+    red[threadIdx.x >> 5] = Sums{loss.value(), ratio.value(), kl.value(), held};
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < NT / 32; ++i) {
-      s.loss += red[i].loss;
-      s.ratio += red[i].ratio;
-      s.kl += red[i].kl;
-      s.held += red[i].held;
-    }
+  Sums s = {0.0, 0.0, 0.0, 0ull};
+  if (threadIdx.x < 32) {
+    if (threadIdx.x < NT / 32) s = red[threadIdx.x];
+    s = warp_sums<NT / 32>(s);
   }
   __syncthreads();
   return s;
@@ -180,11 +216,11 @@ __device__ __forceinline__ void token_range(const PolicyArgs& a, int64_t& lo, in
 }
 
 // ---- counts -------------------------------------------------------------------
-// Tokens that count, in all (head->tokens) and by sequence (n[s]); the last
-// CTA counts the sequences that have any.  Both are zero at the start.
+// Tokens that count: a bit each in mask (those in no sequence do not), their
+// number in all (head->tokens) and by sequence (n[s]); the last CTA counts the
+// sequences that have any.  head and n are zero at the start.
 __global__ void __launch_bounds__(kPThreads) policy_count_kernel(PolicyArgs a) {
-  __shared__ unsigned red[kPThreads / 32];
-  __shared__ int64_t range[2];
+  __shared__ unsigned long long red[kPThreads / 32];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t lo, hi;
@@ -192,31 +228,46 @@ __global__ void __launch_bounds__(kPThreads) policy_count_kernel(PolicyArgs a) {
   const bool by_seq = a.reduction == GS_LOSS_SEQUENCE_MEAN;
   unsigned long long total = 0;
   if (a.targets) {
-    const int64_t tiles = (a.T + kPTile - 1) / kPTile;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const int64_t base = tile * kPTile;
-      if (by_seq) {
-        __syncthreads();
-        if (warp < 2) {
-          const int64_t s = seq_of_warp(a.offsets + 1, a.S, warp ? min(base + kPTile, a.T) - 1 : base);
-          if (lane == 0) range[warp] = s;
+    // a warp takes 256 tokens at a time: eight words of the mask
+    constexpr int kTokens = 256;
+    const int64_t runs = (a.T + kTokens - 1) / kTokens;
+    const int64_t warps = (int64_t)gridDim.x * (kPThreads / 32);
+    for (int64_t run = (int64_t)blockIdx.x * (kPThreads / 32) + warp; run < runs; run += warps) {
+      const int64_t base = run * kTokens;
+      unsigned m[8], mine = 0, some = 0;
+      if (base >= lo && base + kTokens <= hi) {
+        int64_t v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __ldcs(a.targets + base + 32 * j + lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = v[j] >= 0;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t t = base + 32 * j + lane;
+          m[j] = t >= lo && t < hi ? (unsigned)(a.targets[t] >= 0) : 0u;
         }
-        __syncthreads();
       }
 #pragma unroll
-      for (int j = 0; j < kPRun; ++j) {
-        const int64_t t = base + j * kPThreads + threadIdx.x;
-        const bool in = t >= lo && t < hi && a.targets[t] >= 0;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, in);
-        if (lane == 0) total += __popc(m);
-        if (by_seq && m) {
-          if (range[0] == range[1]) {
-            if (lane == 0) atomicAdd(&a.n[range[0]], (unsigned long long)__popc(m));
-          } else {
-            const int64_t s = in ? seq_of(a.offsets + 1, range[0], range[1], t) : -1;
+      for (int j = 0; j < 8; ++j) {
+        m[j] = __ballot_sync(0xFFFFFFFFu, m[j]);
+        if (lane == j) mine = m[j];
+        some += __popc(m[j]);
+      }
+      if (lane < 8) a.mask[run * 8 + lane] = mine;
+      total += some;
+      if (by_seq && some) {
+        const int64_t s0 = seq_of_warp(a.offsets + 1, a.S, base);
+        const int64_t s1 = seq_of_warp(a.offsets + 1, a.S, min(base + kTokens, a.T) - 1);
+        if (s0 == s1) {
+          if (lane == 0) atomicAdd(&a.n[s0], (unsigned long long)some);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const bool in = m[j] >> lane & 1;
+            const int64_t s = in ? seq_of(a.offsets + 1, s0, s1, base + 32 * j + lane) : -1;
             const unsigned same = __match_any_sync(0xFFFFFFFFu, s);
-            if (in && lane == __ffs(same) - 1)
-              atomicAdd(&a.n[s], (unsigned long long)__popc(same));
+            if (in && lane == __ffs(same) - 1) atomicAdd(&a.n[s], (unsigned long long)__popc(same));
           }
         }
       }
@@ -229,12 +280,11 @@ __global__ void __launch_bounds__(kPThreads) policy_count_kernel(PolicyArgs a) {
     }
   }
   if (a.targets) {
-    if (lane == 0) red[warp] = (unsigned)total;  // below 2^32 tokens per CTA
+    if (lane == 0) red[warp] = total;
     __syncthreads();
     if (threadIdx.x == 0) {
-      unsigned long long sum = 0;
-      for (int i = 0; i < kPThreads / 32; ++i) sum += red[i];
-      if (sum) atomicAdd(&a.head->tokens, sum);
+      for (int i = 1; i < kPThreads / 32; ++i) total += red[i];
+      if (total) atomicAdd(&a.head->tokens, total);
     }
   } else if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.head->tokens = (unsigned long long)(hi - lo);
@@ -248,82 +298,81 @@ __global__ void __launch_bounds__(kPThreads) policy_count_kernel(PolicyArgs a) {
   }
   __syncthreads();
   if (!last) return;
-  unsigned any = 0;
+  unsigned long long any = 0;
   for (int64_t s = threadIdx.x; s < a.S; s += kPThreads) any += __ldcg(&a.n[s]) != 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) any += __shfl_down_sync(0xFFFFFFFFu, any, o);
   if (lane == 0) red[warp] = any;
   __syncthreads();
   if (threadIdx.x == 0) {
-    unsigned long long sum = 0;
-    for (int i = 0; i < kPThreads / 32; ++i) sum += red[i];
-    a.head->seqs = sum;
+    for (int i = 1; i < kPThreads / 32; ++i) any += red[i];
+    a.head->seqs = any;
   }
 }
 
 // ---- loss and gradient --------------------------------------------------------
-template <bool VEC>
-__global__ void __launch_bounds__(kPThreads) policy_loss_kernel(PolicyArgs a) {
+__device__ __forceinline__ void get8(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// VEC: 16-byte aligned arrays; REF: a reference policy; FIND: a token's sequence
+// is needed, for its advantage or its weight.
+template <bool VEC, bool REF, bool FIND>
+__global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a) {
   __shared__ int64_t range[2];
   __shared__ bool last;
   __shared__ int64_t ends[kPSpan];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t lo, hi;
   token_range(a, lo, hi);
-  const bool by_seq = a.reduction == GS_LOSS_SEQUENCE_MEAN;
-  const bool find = by_seq || a.adv_per_seq;
+  const bool by_seq = FIND && a.reduction == GS_LOSS_SEQUENCE_MEAN;
+  const bool adv_per_seq = FIND && a.adv_per_seq;
   const unsigned long long n = a.counted ? a.head->tokens : (unsigned long long)(hi - lo);
   const float up = a.dloss ? *a.dloss : 1.0f;
-  const double seqs = by_seq ? (double)a.head->seqs : 1.0;
+  const float seqs = by_seq ? (float)a.head->seqs : 1.0f;
   // the weight of the token mean is applied to the sum, and to each gradient
   const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN ? (n ? (float)(1.0 / (double)n) : 0.0f) : 1.0f;
-  Sums sums = {0.0, 0.0, 0.0, 0ull};
+  const float up_token = __fmul_rn(up, w_token);
+  Pair loss_sum = {0.0f, 0.0f}, ratio_sum = loss_sum, kl_sum = loss_sum;
+  unsigned long long held_sum = 0;
   const int64_t tiles = (a.T + kPTile - 1) / kPTile;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int64_t base = tile * kPTile, t0 = base + (int64_t)threadIdx.x * kPRun;
     float x[kPRun], old[kPRun], ref[kPRun], adv[kPRun];
-    bool live[kPRun], inside[kPRun];
     const bool whole = VEC && t0 + kPRun <= a.T;
-    if (whole) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(a.logprob + t0));
-      const float4 o = __ldcs(reinterpret_cast<const float4*>(a.old + t0));
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      old[0] = o.x, old[1] = o.y, old[2] = o.z, old[3] = o.w;
-      if (a.ref) {
-        const float4 r = __ldcs(reinterpret_cast<const float4*>(a.ref + t0));
-        ref[0] = r.x, ref[1] = r.y, ref[2] = r.z, ref[3] = r.w;
-      }
-      if (!a.adv_per_seq) {
-        const float4 v2 = __ldcs(reinterpret_cast<const float4*>(a.adv + t0));
-        adv[0] = v2.x, adv[1] = v2.y, adv[2] = v2.z, adv[3] = v2.w;
-      }
-      if (a.targets) {
-        const longlong2 p = __ldcs(reinterpret_cast<const longlong2*>(a.targets + t0));
-        const longlong2 q = __ldcs(reinterpret_cast<const longlong2*>(a.targets + t0 + 2));
-        live[0] = p.x >= 0, live[1] = p.y >= 0, live[2] = q.x >= 0, live[3] = q.y >= 0;
-      }
-    }
+    // bit j: token t0 + j lies in a sequence, and counts
+    unsigned inside = 0;
+    if (base >= lo && base + kPTile <= hi) {
+      inside = 0xFFu;
+    } else {
 #pragma unroll
-    for (int j = 0; j < kPRun; ++j) {
-      const int64_t t = t0 + j;
-      inside[j] = t >= lo && t < hi;
-      if (!whole) {
+      for (int j = 0; j < kPRun; ++j) inside |= (unsigned)(t0 + j >= lo && t0 + j < hi) << j;
+    }
+    unsigned live = inside;
+    if (a.targets && t0 < a.T) live &= reinterpret_cast<const uint8_t*>(a.mask)[t0 / kPRun];
+    if (whole) {
+      get8(a.logprob + t0, x);
+      get8(a.old + t0, old);
+      if constexpr (REF) get8(a.ref + t0, ref);
+      if (!adv_per_seq) get8(a.adv + t0, adv);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPRun; ++j) {
+        const int64_t t = t0 + j;
         const bool there = t < a.T;
         x[j] = there ? a.logprob[t] : 0.0f;
         old[j] = there ? a.old[t] : 0.0f;
-        ref[j] = there && a.ref ? a.ref[t] : 0.0f;
-        adv[j] = there && !a.adv_per_seq ? a.adv[t] : 0.0f;
-        live[j] = there && (!a.targets || a.targets[t] >= 0);
-      } else {
-        if (!a.ref) ref[j] = 0.0f;
-        if (!a.targets) live[j] = true;
+        ref[j] = REF && there ? a.ref[t] : 0.0f;
+        adv[j] = there && !adv_per_seq ? a.adv[t] : 0.0f;
       }
-      live[j] = live[j] && inside[j];
     }
-    float w[kPRun];
+    float w[FIND ? kPRun : 1];
+    if constexpr (FIND) {
 #pragma unroll
-    for (int j = 0; j < kPRun; ++j) w[j] = w_token;
-    if (find) {
+      for (int j = 0; j < kPRun; ++j) w[j] = 1.0f;
       __syncthreads();
       if (warp < 2) {
         const int64_t s = seq_of_warp(a.offsets + 1, a.S, warp ? min(base + kPTile, a.T) - 1 : base);
@@ -338,43 +387,42 @@ __global__ void __launch_bounds__(kPThreads) policy_loss_kernel(PolicyArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < kPRun; ++j) {
-        if (!live[j]) continue;
+        if (!(live >> j & 1)) continue;
         const int64_t s = span <= 0 ? first
                           : near    ? first + seq_of(ends, 0, span, t0 + j)
                                     : seq_of(a.offsets + 1, first, range[1], t0 + j);
-        if (a.adv_per_seq) adv[j] = a.adv[s];
-        if (by_seq) w[j] = (float)(1.0 / (seqs * (double)a.n[s]));
+        if (adv_per_seq) adv[j] = a.adv[s];
+        if (by_seq) w[j] = __fdiv_rn(1.0f, __fmul_rn(seqs, (float)a.n[s]));
       }
     }
     float loss = 0.0f, ratio = 0.0f, kl = 0.0f, grad[kPRun];
+    unsigned held = 0;
 #pragma unroll
     for (int j = 0; j < kPRun; ++j) {
-      grad[j] = 0.0f;
-      if (!live[j]) continue;
-      const Token tk = token(a, x[j], old[j], ref[j], adv[j]);
-      loss = __fadd_rn(loss, by_seq ? __fmul_rn(tk.value, w[j]) : tk.value);
-      ratio = __fadd_rn(ratio, tk.ratio);
-      kl = __fadd_rn(kl, tk.kl);
-      sums.held += tk.held;
-      grad[j] = __fmul_rn(__fmul_rn(up, w[j]), tk.slope);
+      const Token tk = token<REF>(a, x[j], old[j], ref[j], adv[j]);
+      const bool in = live >> j & 1;
+      loss = __fadd_rn(loss, in ? (FIND ? __fmul_rn(tk.value, w[j]) : tk.value) : 0.0f);
+      ratio = __fadd_rn(ratio, in ? tk.ratio : 0.0f);
+      kl = __fadd_rn(kl, in ? tk.kl : 0.0f);
+      held += in && tk.held;
+      grad[j] = in ? __fmul_rn(FIND ? __fmul_rn(up_token, w[j]) : up_token, tk.slope) : 0.0f;
     }
-    sums.loss += (double)loss;
-    sums.ratio += (double)ratio;
-    sums.kl += (double)kl;
+    held_sum += held;
+    loss_sum.add(loss);
+    ratio_sum.add(ratio);
+    kl_sum.add(kl);
     if (a.grad) {
-      bool all = whole;
-#pragma unroll
-      for (int j = 0; j < kPRun; ++j) all = all && inside[j];
-      if (all) {
+      if (whole && inside == 0xFFu) {
         __stcs(reinterpret_cast<float4*>(a.grad + t0), make_float4(grad[0], grad[1], grad[2], grad[3]));
+        __stcs(reinterpret_cast<float4*>(a.grad + t0) + 1, make_float4(grad[4], grad[5], grad[6], grad[7]));
       } else {
 #pragma unroll
         for (int j = 0; j < kPRun; ++j)
-          if (inside[j]) a.grad[t0 + j] = grad[j];
+          if (inside >> j & 1) a.grad[t0 + j] = grad[j];
       }
     }
   }
-  const Sums s = block_sums<kPThreads>(sums);
+  const Sums s = block_sums<kPThreads>(loss_sum, ratio_sum, kl_sum, held_sum);
   if (threadIdx.x == 0) {
     a.part[blockIdx.x] = PolicyPart{s.loss, s.ratio, s.kl, s.held};
     __threadfence();
@@ -383,87 +431,123 @@ __global__ void __launch_bounds__(kPThreads) policy_loss_kernel(PolicyArgs a) {
   }
   __syncthreads();
   if (!last) return;
+  if (warp > 0) return;
   Sums all = {0.0, 0.0, 0.0, 0ull};
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kPThreads) {
+  for (unsigned i = lane; i < gridDim.x; i += 32) {
     const volatile PolicyPart& p = a.part[i];
     all.loss += p.loss;
     all.ratio += p.ratio;
     all.kl += p.kl;
     all.held += p.held;
   }
-  all = block_sums<kPThreads>(all);
-  if (threadIdx.x == 0) finish(a, all, n);
+  all = warp_sums<32>(all);
+  if (lane == 0) finish(a, all, n);
 }
 
-// Everything by one CTA: counts in shared memory, then loss and gradient.
+// Everything by one CTA: offsets, counts and weights in shared memory, the
+// tokens' values loaded once, PER of them a thread.
+template <int PER, bool REF>
 __global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(PolicyArgs a) {
+  __shared__ int ends[kPSmallSeqs];
   __shared__ unsigned counts[kPSmallSeqs];
   __shared__ unsigned totals[2];  // tokens, sequences that have any
   const int tid = threadIdx.x;
   const bool by_seq = a.reduction == GS_LOSS_SEQUENCE_MEAN;
   const bool find = by_seq || a.adv_per_seq;
+  const int T = (int)a.T, S = (int)a.S;
+  float x[PER], old[PER], ref[PER], adv[PER];
+  bool in[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int t = j * kPSmallThreads + tid;
+    const bool there = t < T;
+    in[j] = there && (!a.targets || a.targets[t] >= 0);
+    x[j] = there ? a.logprob[t] : 0.0f;
+    old[j] = there ? a.old[t] : 0.0f;
+    ref[j] = REF && there ? a.ref[t] : 0.0f;
+    adv[j] = there && !a.adv_per_seq ? a.adv[t] : 0.0f;
+  }
+  const float up = a.dloss ? *a.dloss : 1.0f;
   int64_t lo, hi;
   token_range(a, lo, hi);
-  if (by_seq)
-    for (int64_t s = tid; s < a.S; s += kPSmallThreads) counts[s] = 0;
+  if (find)
+    for (int s = tid; s < S; s += kPSmallThreads) {
+      // (no two tokens of one sequence are told apart by what lies past T)
+      ends[s] = a.offsets ? (int)max((int64_t)0, min(a.T, a.offsets[s + 1])) : T;
+      counts[s] = 0;
+    }
   if (tid < 2) totals[tid] = 0;
   __syncthreads();
-  constexpr int kMost = (int)(kPSmallTokens / kPSmallThreads);
-  int seq[kMost];
-  float x[kMost], old[kMost], ref[kMost], adv[kMost];
-  unsigned live = 0;
+  int seq[PER];
+  unsigned mine = 0;
 #pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    const int64_t t = (int64_t)j * kPSmallThreads + tid;
-    const bool in = t >= lo && t < hi && (!a.targets || a.targets[t] >= 0);
-    x[j] = in ? a.logprob[t] : 0.0f;
-    old[j] = in ? a.old[t] : 0.0f;
-    ref[j] = in && a.ref ? a.ref[t] : 0.0f;
-    adv[j] = in && !a.adv_per_seq ? a.adv[t] : 0.0f;
-    seq[j] = in && find ? (int)seq_of(a.offsets + 1, 0, a.S - 1, t) : 0;
-    if (in && a.adv_per_seq) adv[j] = a.adv[seq[j]];
-    if (in) live |= 1u << j;
+  for (int j = 0; j < PER; ++j) {
+    const int t = j * kPSmallThreads + tid;
+    in[j] = in[j] && t >= lo && t < hi;
+    mine += in[j];
+    seq[j] = 0;
+    if (find) {
+      int l = 0, h = S - 1;
+      while (l < h) {
+        const int mid = (l + h) >> 1;
+        if (ends[mid] > t) h = mid;
+        else l = mid + 1;
+      }
+      seq[j] = l;
+    }
+    if (a.adv_per_seq && in[j]) adv[j] = a.adv[seq[j]];
     if (by_seq) {
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, in ? seq[j] : -1);
-      if (in && (tid & 31) == __ffs(same) - 1) atomicAdd(&counts[seq[j]], (unsigned)__popc(same));
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, in[j] ? seq[j] : -1);
+      if (in[j] && (tid & 31) == __ffs(same) - 1) atomicAdd(&counts[seq[j]], (unsigned)__popc(same));
     }
   }
-  const unsigned mine = __reduce_add_sync(0xFFFFFFFFu, (unsigned)__popc(live));
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
   if ((tid & 31) == 0 && mine) atomicAdd(&totals[0], mine);
   __syncthreads();
   if (by_seq) {
     unsigned any = 0;
-    for (int64_t s = tid; s < a.S; s += kPSmallThreads) any += counts[s] != 0;
+    for (int s = tid; s < S; s += kPSmallThreads) any += counts[s] != 0;
     any = __reduce_add_sync(0xFFFFFFFFu, any);
     if ((tid & 31) == 0 && any) atomicAdd(&totals[1], any);
     __syncthreads();
   }
   const unsigned n = totals[0];
-  const float up = a.dloss ? *a.dloss : 1.0f;
-  const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN ? (n ? (float)(1.0 / (double)n) : 0.0f) : 1.0f;
-  Sums sums = {0.0, 0.0, 0.0, 0ull};
+  // whole numbers below 2^24: their product's reciprocal rounds twice
+  const float seqs = (float)totals[1];
+  const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN ? (n ? __fdiv_rn(1.0f, (float)n) : 0.0f) : 1.0f;
+  float loss = 0.0f, ratio = 0.0f, kl = 0.0f;
+  unsigned held = 0;
 #pragma unroll
-  for (int j = 0; j < kMost; ++j) {
-    const int64_t t = (int64_t)j * kPSmallThreads + tid;
-    float grad = 0.0f;
-    if (live >> j & 1) {
-      const float w = by_seq ? (float)(1.0 / ((double)totals[1] * (double)counts[seq[j]])) : w_token;
-      const Token tk = token(a, x[j], old[j], ref[j], adv[j]);
-      sums.loss += (double)(by_seq ? __fmul_rn(tk.value, w) : tk.value);
-      sums.ratio += (double)tk.ratio;
-      sums.kl += (double)tk.kl;
-      sums.held += tk.held;
-      grad = __fmul_rn(__fmul_rn(up, w), tk.slope);
-    }
-    if (a.grad && t >= lo && t < hi) a.grad[t] = grad;
+  for (int j = 0; j < PER; ++j) {
+    const int t = j * kPSmallThreads + tid;
+    const float w = by_seq && in[j] ? __fdiv_rn(1.0f, __fmul_rn(seqs, (float)counts[seq[j]])) : w_token;
+    const Token tk = token<REF>(a, x[j], old[j], ref[j], adv[j]);
+    loss = __fadd_rn(loss, in[j] ? (by_seq ? __fmul_rn(tk.value, w) : tk.value) : 0.0f);
+    ratio = __fadd_rn(ratio, in[j] ? tk.ratio : 0.0f);
+    kl = __fadd_rn(kl, in[j] ? tk.kl : 0.0f);
+    held += in[j] && tk.held;
+    if (a.grad && t >= lo && t < hi)
+      a.grad[t] = in[j] ? __fmul_rn(__fmul_rn(up, w), tk.slope) : 0.0f;
   }
-  const Sums s = block_sums<kPSmallThreads>(sums);
+  const Sums s = block_sums<kPSmallThreads>(Pair{loss, 0.0f}, Pair{ratio, 0.0f}, Pair{kl, 0.0f}, held);
   if (tid == 0) finish(a, s, n);
+}
+
+template <int PER>
+static void launch_small(const PolicyArgs& a, cudaStream_t st) {
+  if (a.ref) policy_loss_small_kernel<PER, true><<<1, kPSmallThreads, 0, st>>>(a);
+  else policy_loss_small_kernel<PER, false><<<1, kPSmallThreads, 0, st>>>(a);
+}
+template <bool VEC, bool REF>
+static void launch_large(const PolicyArgs& a, unsigned grid, bool find, cudaStream_t st) {
+  if (find) policy_loss_kernel<VEC, REF, true><<<grid, kPThreads, 0, st>>>(a);
+  else policy_loss_kernel<VEC, REF, false><<<grid, kPThreads, 0, st>>>(a);
 }
 
 cudaError_t launch_policy_loss(PolicyArgs a, cudaStream_t st) {
   if (a.T <= kPSmallTokens && a.S <= kPSmallSeqs) {
-    policy_loss_small_kernel<<<1, kPSmallThreads, 0, st>>>(a);
+    if (a.T <= 2 * kPSmallThreads) launch_small<2>(a, st);
+    else launch_small<(int)(kPSmallTokens / kPSmallThreads)>(a, st);
     return cudaGetLastError();
   }
   const bool by_seq = a.reduction == GS_LOSS_SEQUENCE_MEAN;
@@ -472,21 +556,27 @@ cudaError_t launch_policy_loss(PolicyArgs a, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(a.head, 0, zero, st);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (a.T + kPTile - 1) / kPTile;
-  const int64_t most = std::min<int64_t>(kPolicyCtas, (int64_t)sm_count() * 8);
+  // one wave: four CTAs per SM (64 us for 8 M tokens; three 67, two 71)
+  const int64_t most = std::min<int64_t>(kPolicyCtas, (int64_t)sm_count() * 4);
   if (a.counted) {
-    const int64_t work = a.targets ? tiles : (a.S + kPThreads - 1) / kPThreads;
-    policy_count_kernel<<<(unsigned)std::max<int64_t>(1, std::min(work, most)), kPThreads, 0, st>>>(a);
+    const int64_t work = a.targets ? (a.T + 8 * kPThreads - 1) / (8 * kPThreads) : (a.S + kPThreads - 1) / kPThreads;
+    policy_count_kernel<<<(unsigned)std::max<int64_t>(1, std::min<int64_t>(work, (int64_t)sm_count() * 8)), kPThreads, 0, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min(tiles, most));
   bool vec = true;
   for (const void* p : {(const void*)a.logprob, (const void*)a.old, (const void*)a.ref,
-                        a.adv_per_seq ? nullptr : (const void*)a.adv, (const void*)a.targets,
-                        (const void*)a.grad})
+                        a.adv_per_seq ? nullptr : (const void*)a.adv, (const void*)a.grad})
     vec = vec && (uintptr_t)p % 16 == 0;
-  if (vec) policy_loss_kernel<true><<<grid, kPThreads, 0, st>>>(a);
-  else policy_loss_kernel<false><<<grid, kPThreads, 0, st>>>(a);
+  const bool find = by_seq || a.adv_per_seq;
+  if (vec) {
+    if (a.ref) launch_large<true, true>(a, grid, find, st);
+    else launch_large<true, false>(a, grid, find, st);
+  } else {
+    if (a.ref) launch_large<false, true>(a, grid, find, st);
+    else launch_large<false, false>(a, grid, find, st);
+  }
   return cudaGetLastError();
 }
 
