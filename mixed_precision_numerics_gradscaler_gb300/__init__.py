@@ -678,6 +678,9 @@ def gs_token_logprob_bwd(logits: torch.Tensor, targets: torch.Tensor, lse: torch
            "gs_token_logprob_bwd")
 
 
+_WS_BYTES = gs_ws_bytes()
+
+
 def fp4_scale_bytes(rows: int, cols: int, fmt) -> int:
     """Bytes of the scales of a [rows, cols] 4-bit tensor (tiles of 512 bytes)."""
     return int(_lib.fp4_scale_bytes(rows, cols, _FMTS4[fmt]))
@@ -685,12 +688,11 @@ def fp4_scale_bytes(rows: int, cols: int, fmt) -> int:
 
 def _codes4(q: torch.Tensor, scales: torch.Tensor, name: str, R: int, C: int, fmt: int) -> None:
     """Checks that q holds the codes and scales the scales of [R, C] values."""
-    if q.dtype is not torch.uint8 or tuple(q.shape) != (R, C // 2) or not q.is_contiguous():
+    if q.dtype is not torch.uint8 or q.shape != (R, C // 2) or not q.is_contiguous():
         raise ValueError(f"{name} must be contiguous uint8 [{R}, {C // 2}]")
-    if scales.dtype is not torch.uint8 or not scales.is_contiguous() or \
-            scales.numel() != _lib.fp4_scale_bytes(R, C, fmt):
-        raise ValueError(f"the scales of {name} must be contiguous uint8, of "
-                         f"{_lib.fp4_scale_bytes(R, C, fmt)} bytes")
+    n = -(-R // 128) * -(-C // (64 if fmt == GS_NVFP4 else 128)) * 512
+    if scales.dtype is not torch.uint8 or scales.numel() != n or not scales.is_contiguous():
+        raise ValueError(f"the scales of {name} must be contiguous uint8, of {n} bytes")
 
 
 def fp4_quant(x: torch.Tensor, fmt, q: torch.Tensor | None, scales: torch.Tensor | None,
@@ -709,7 +711,7 @@ def fp4_quant(x: torch.Tensor, fmt, q: torch.Tensor | None, scales: torch.Tensor
         _codes4(q, scales, "q", R, C, f)
     if qt is not None:
         _codes4(qt, scales_t, "qt", C, R, f)
-    if ws is not None and (not ws.is_contiguous() or ws.nbytes < gs_ws_bytes()):
+    if ws is not None and (not ws.is_contiguous() or ws.nbytes < _WS_BYTES):
         raise ValueError("ws must be contiguous, of gs_ws_bytes() bytes at least")
     _check(_lib.fp4_quant(_ptr(x), ldx, _DTYPES[x.dtype], R, C, f, _ptr(q), _ptr(scales), _ptr(qt),
                           _ptr(scales_t), _vector(tensor_scale, "tensor_scale", 1, _F32), _ptr(ws),
