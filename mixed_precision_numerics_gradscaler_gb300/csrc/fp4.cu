@@ -149,6 +149,23 @@ __device__ __forceinline__ float mag16(uint32_t m) {  // of a 16-bit pattern wit
   else return Half<DT>::lo(m);
 }
 
+// The larger magnitudes of m and w (for 16 bits of either half), NaN the largest
+// of all; signs in the result mean nothing.
+template <int DT>
+__device__ __forceinline__ uint32_t max_mag(uint32_t m, uint32_t w) {
+  uint32_t d;
+  if constexpr (DT == GS_F32) d = max(m, w & 0x7FFFFFFFu);
+  else if constexpr (DT == GS_BF16) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
+  else asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(m), "r"(w));
+  return d;
+}
+// What max_mag left, as the bit pattern of one fp32 magnitude.
+template <int DT>
+__device__ __forceinline__ uint32_t mag_of(uint32_t m) {
+  if constexpr (DT == GS_F32) return m;
+  else return __float_as_uint(mag16<DT>(max(m & 0x7FFFu, m >> 16 & 0x7FFFu)));
+}
+
 // 16 consecutive elements of a row in registers.
 template <int DT>
 struct Run16 {
@@ -183,18 +200,17 @@ struct Run16 {
       }
     }
   }
+  // Takes the elements into a running maximum of magnitudes (start: 0), in the
+  // elements' own type and, of 16 bits, by halves; see mag_of.
+  __device__ __forceinline__ void fold(uint32_t& m) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) m = max_mag<DT>(m, w[i]);
+  }
   // Bit pattern of the largest magnitude as fp32.
   __device__ __forceinline__ uint32_t amax() const {
     uint32_t m = 0;
-    if constexpr (DT == GS_F32) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
-      return m;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-      return __float_as_uint(mag16<DT>(max(m & 0xFFFFu, m >> 16)));
-    }
+    fold(m);
+    return mag_of<DT>(m);
   }
   __device__ __forceinline__ uint2 codes(float r, bool ok) const {
     uint32_t c[2];
@@ -220,11 +236,6 @@ template <int FMT>
 constexpr int kFScales = kFTile / kFBlk<FMT>;
 template <int FMT>
 constexpr int kFScaleBytes = kFTile * kFScales<FMT>;
-
-template <int FMT>
-__device__ __forceinline__ void put_scale(uint8_t* sc, int row, int k, uint32_t s) {
-  sc[(k >> 2) * 512 + scale_place(row, k)] = (uint8_t)s;
-}
 
 // Copies a tile's staged scale tiles to the matrix's; k_tiles: scale tiles per row tile.
 template <int FMT>
@@ -270,22 +281,13 @@ __device__ __forceinline__ float scale_of_amax(uint32_t m) {
              : __fdiv_rn(fmaxf(__uint_as_float(m), kAmaxFloor), Fp8Max<GS_E4M3>::value * kFMax);
 }
 
-// Thread tid's j-th run of 16 of tile (r0, c0): eight lanes to a row.
-template <int DT>
-__device__ __forceinline__ bool load_run(const Quant4Args& a, int64_t r0, int64_t c0, int j, Run16<DT>& v) {
-  const int64_t r = r0 + j * (kFThreads / 8) + threadIdx.x / 8, c = c0 + threadIdx.x % 8 * kFBlock;
-  const bool in = r < a.R && c < a.C;
-  v.zero();
-  if (in) v.load(a.x, r * a.ldx + c, a.align);
-  return in;
-}
-
 // ROW, COL: the directions wanted.  ONE: a single cluster forms the tensor scale
 // too.
 template <int DT, int FMT, bool ROW, bool COL, bool ONE>
 __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
   constexpr int kBlk = kFBlk<FMT>;
   constexpr int kRuns = kFTile * 8 / kFThreads;  // per thread and tile
+  static_assert(kFThreads == 256 && kRuns == 4, "a thread's runs are 32 rows apart");
   // Words per row of the tile kept for the transpose: odd, so that a column of
   // words and a row of them go to different banks.
   constexpr int kPitch = DT == GS_F32 ? kFTile + 1 : kFTile / 2 + 1;
@@ -311,8 +313,9 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
         for (int64_t at = blockIdx.x * kFThreads + tid; at < a.R * per_row; at += gridDim.x * kFThreads) {
           Run16<DT> v;
           v.load(a.x, at / per_row * a.ldx + at % per_row * kFBlock, a.align);
-          m = max(m, v.amax());
+          v.fold(m);
         }
+        m = mag_of<DT>(m);
         m = block_max(m, red);
         cluster_barrier();  // every CTA of the cluster has begun
         if (tid < (int)cluster_size())
@@ -339,13 +342,21 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
     const int64_t at = n_tiles - 1 - i;
     const int64_t tr = at / a.tiles_c, tc = at % a.tiles_c;
     const int64_t r0 = tr * kFTile, c0 = tc * kFTile;
+    // rows tid / 8 + 32 j: eight lanes to a row, a run of 16 each
+    const int blk = tid & 7, row0 = tid >> 3 & 31;
+    const int rows = c0 + blk * kFBlock < a.C ? (int)min((int64_t)kFTile, a.R - r0) : 0;
+    const int64_t first = (r0 + row0) * a.ldx + c0 + blk * kFBlock;
+    uint8_t* const to = ROW ? a.q + (r0 + row0) * (a.C / 2) + (c0 + blk * kFBlock) / 2 : nullptr;
     Run16<DT> v[kRuns];
-    bool in[kRuns];
-#pragma unroll
-    for (int j = 0; j < kRuns; ++j) in[j] = load_run<DT>(a, r0, c0, j, v[j]);
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
-      const int row = j * (kFThreads / 8) + tid / 8, blk = tid % 8;
+      v[j].zero();
+      if (row0 + 32 * j < rows) v[j].load(a.x, first + 32 * j * a.ldx, a.align);
+    }
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+      const int row = 32 * j + row0;
+      const bool in = row < rows;
       if constexpr (COL) {
 #pragma unroll
         for (int e = 0; e < Run16<DT>::kWords; ++e)
@@ -358,11 +369,10 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
         bool ok;
         const uint32_t s = block_scale4<FMT>(__uint_as_float(m), ts, r, ok);
         // past the edges: zeros in the padding of the scale tiles
+        const int k = FMT == GS_NVFP4 ? blk : blk >> 1;
         if (FMT == GS_NVFP4 || (blk & 1) == 0)
-          put_scale<FMT>(sc, row, FMT == GS_NVFP4 ? blk : blk >> 1, in[j] ? s : 0u);
-        if (in[j])
-          *reinterpret_cast<uint2*>(a.q + (r0 + row) * (a.C / 2) + (c0 + blk * kFBlock) / 2) =
-              v[j].codes(r, ok);
+          sc[(k >> 2) * 512 + (row0 << 4) + (j << 2) + (k & 3)] = (uint8_t)(in ? s : 0u);
+        if (in) *reinterpret_cast<uint2*>(to + 32 * j * (a.C / 2)) = v[j].codes(r, ok);
       }
     }
     if constexpr (COL) {
@@ -377,14 +387,11 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
 #pragma unroll
         for (int e = 0; e < kBlk; ++e) w[e] = tile[(k * kBlk + e) * kPitch + word];
         uint32_t m0 = 0, m1 = 0;
-        if constexpr (DT == GS_F32) {
 #pragma unroll
-          for (int e = 0; e < kBlk; ++e) m0 = max(m0, w[e] & 0x7FFFFFFFu);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kBlk; ++e) m0 = __vmaxu2(m0, w[e] & 0x7FFF7FFFu);
-          m1 = __float_as_uint(mag16<DT>(m0 >> 16));
-          m0 = __float_as_uint(mag16<DT>(m0 & 0xFFFFu));
+        for (int e = 0; e < kBlk; ++e) m0 = max_mag<DT>(m0, w[e]);
+        if constexpr (DT != GS_F32) {
+          m1 = __float_as_uint(mag16<DT>(m0 >> 16 & 0x7FFFu));
+          m0 = __float_as_uint(mag16<DT>(m0 & 0x7FFFu));
         }
 #pragma unroll
         for (int side = 0; side < (DT == GS_F32 ? 1 : 2); ++side) {
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
           float r;
           bool ok;
           const uint32_t s = block_scale4<FMT>(__uint_as_float(side ? m1 : m0), ts, r, ok);
-          put_scale<FMT>(sct, col, k, inside ? s : 0u);
+          sct[(k >> 2) * 512 + scale_place(col, k)] = (uint8_t)(inside ? s : 0u);
           uint32_t c[kBlk / 8];
 #pragma unroll
           for (int g = 0; g < kBlk / 8; ++g) {
@@ -461,9 +468,9 @@ __global__ void __launch_bounds__(kFThreads)
       next();
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) m = max(m, v[u].amax());
+    for (int u = 0; u < kAhead; ++u) v[u].fold(m);
   }
-  m = block_max(m, red);
+  m = block_max(mag_of<DT>(m), red);
   if (threadIdx.x == 0) partials[blockIdx.x] = m;
 }
 
