@@ -40,9 +40,11 @@ namespace gs {
 constexpr int kQThreads = 384;      // warps 0-3: loads, MMA, two idle; 4-11 store
 constexpr int kQRow = 128;          // bytes of a row of a stage: 256 elements
 constexpr int kQK = 256;
+constexpr int kQSlots = 3;          // a sum is split in four at most
 
 // One configuration's sizes.
-template <int CG, int BN, int FMT>
+// SLOTS: sums of other CTAs of a cluster that the leading one takes in.
+template <int CG, int BN, int FMT, int SLOTS>
 struct Q4 {
   static constexpr int kBRows = BN / CG;                   // of B that a CTA loads
   static constexpr int kTiles = FMT == GS_NVFP4 ? 4 : 2;   // scale tiles per stage and 128 rows
@@ -51,7 +53,9 @@ struct Q4 {
   static constexpr int kSA = kTiles * 512, kSB = kBTiles * kTiles * 512;
   static constexpr int kStage = ((kA + kB + kSA + kSB + 1023) / 1024) * 1024;
   static constexpr int kBytes = kA + kB + kSA + kSB;       // a CTA's loads per stage
-  static constexpr int kOut = 8 * 32 * 128;                // store staging, 8 warps
+  static constexpr int kSlot = 128 * BN * 4;
+  // store staging of 8 warps, or the other CTAs' sums
+  static constexpr int kOut = SLOTS ? SLOTS * kSlot : 8 * 32 * 128;
   static constexpr int kMost = (232448 - 1024 - 512 - kOut) / kStage;
   static constexpr int kStages = kMost > 6 ? 6 : kMost;
   static constexpr int kAccs = BN <= 128 ? 2 : 1;
@@ -70,6 +74,7 @@ struct Gemm4Args {
   int64_t ldd;
   int32_t* status;
   int group;              // tile rows of a raster group
+  int split;              // CTAs that share a tile's sum (TRANS)
   int stall;
 };
 
@@ -109,12 +114,15 @@ __device__ __forceinline__ void cp_scales(uint32_t tmem, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
+// Sums of a tile split along K (TRANS): cluster CTA r takes its part of the
+// stages, CTAs 1 .. split - 1 write their fp32 sums to the leading CTA's shared
+// memory, which adds them in their order.
 template <int CG, int BN, int FMT, int OUT, bool TRANS, bool TMA_STORE>
 __global__ void __launch_bounds__(kQThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
                     const __grid_constant__ CUtensorMap map_d, Gemm4Args a) {
-  using S = Q4<CG, BN, FMT>;
+  using S = Q4<CG, BN, FMT, TRANS ? kQSlots : 0>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // the same offset in both CTAs of a pair
@@ -124,15 +132,22 @@ __global__ void __launch_bounds__(kQThreads, 1)
   uint64_t* tfull = empty + S::kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* joined = drain + 1;    // the other CTAs' sums are in the leading CTA
+  uint64_t* taken = joined + 1;    // ... and this CTA's has been read there
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(taken + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-  const int nkb = (int)((a.K + kQK - 1) / kQK);
+  const uint32_t part = TRANS ? cluster_rank() : 0;
+  const int parts = TRANS ? a.split : CG;             // CTAs of a cluster
+  const int all_kb = (int)((a.K + kQK - 1) / kQK);
+  // this CTA's stages (split <= all_kb: none has no stage)
+  const int kb0 = TRANS ? (int)((int64_t)all_kb * part / a.split) : 0;
+  const int kb1 = TRANS ? (int)((int64_t)all_kb * (part + 1) / a.split) : all_kb;
   const int tiles_m = (int)((a.M + 128 * CG - 1) / (128 * CG)), tiles_n = (int)((a.N + BN - 1) / BN);
   const int n_tiles = tiles_m * tiles_n;
-  const int first = (int)blockIdx.x / CG, step = (int)gridDim.x / CG;
+  const int first = (int)blockIdx.x / parts, step = (int)gridDim.x / parts;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -144,13 +159,15 @@ __global__ void __launch_bounds__(kQThreads, 1)
       tc_bar_init(&tempty[b], 8 * CG);
     }
     tc_bar_init(drain, 1);
+    tc_bar_init(joined, TRANS ? 4 * (a.split > 1 ? a.split - 1 : 1) : 1);
+    tc_bar_init(taken, 4);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tc_alloc<CG>(tmem_slot, S::kAlloc);
   tc_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_barrier();  // the pair's barriers are there
+  if constexpr (CG == 2 || TRANS) cluster_barrier();  // the cluster's barriers are there
   tc_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -161,7 +178,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       int mt, nt;
       tc_tile(t, a.group, tiles_m, tiles_n, mt, nt);
       const int row_a = (mt * CG + (int)rank) * 128, row_b = nt * BN + (int)rank * S::kBRows;
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!tc_wait_warp(&empty[s], ph ^ 1u, abort_flag, a.status)) {
           go = false;
           break;
@@ -196,7 +213,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
       tc_after();
       // where in its 128 rows' scales a narrow tile of B begins
       const uint32_t sb_at = BN < 128 ? (uint32_t)(nt * BN % 128) / 32 : 0;
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
           break;
@@ -222,11 +239,11 @@ __global__ void __launch_bounds__(kQThreads, 1)
               const uint32_t sf = FMT == GS_NVFP4 ? 0u : 2u * (kk & 1);
               mma4<CG, FMT>(tmem + b * BN, tc_desc_k(a0 + 32 * kk), tc_desc_k(b0 + 32 * kk),
                             idesc4<FMT>(128 * CG, BN, sf), tmem + S::kSfCol + 4 * j,
-                            tmem + S::kSbCol + 4 * j * S::kBTiles + sb_at, kb > 0 || kk > 0 ? 1u : 0u);
+                            tmem + S::kSbCol + 4 * j * S::kBTiles + sb_at, kb > kb0 || kk > 0 ? 1u : 0u);
             }
           }
           tc_commit<CG>(&empty[s]);
-          if (kb == nkb - 1) tc_commit<CG>(&tfull[b]);
+          if (kb == kb1 - 1) tc_commit<CG>(&tfull[b]);
         }
         __syncwarp();
         if (++s == S::kStages) s = 0, ph ^= 1u;
@@ -261,10 +278,47 @@ __global__ void __launch_bounds__(kQThreads, 1)
       }
       tc_before();
       __syncwarp();
-      if (lane == 0) tc_arrive_at(&tempty[b], 0);
+      if (lane == 0) {
+        if constexpr (CG == 2) tc_arrive_at(&tempty[b], 0);
+        else tc_arrive(&tempty[b]);
+      }
       if (!mine) continue;
       const int64_t row = ((int64_t)mt * CG + rank) * 128 + 32 * q;  // this warp's first
       const int64_t col = (int64_t)nt * BN + h * kCols;
+      if constexpr (TRANS) {
+        // every CTA of the cluster comes to the same tiles with its part of the sum
+        if (a.split > 1) {
+          static_assert(BN == 32, "a slot is four warps' 32 columns");
+          float4* const slot = reinterpret_cast<float4*>(out_stage) + q * 256 + lane;
+          if (part > 0) {
+            // (n-th tile of this cluster: its sum before has been read)
+            if (!__all_sync(0xFFFFFFFFu, tc_wait_cluster(taken, (n & 1u) ^ 1u, abort_flag, a.status))) break;
+            const uint32_t to = remote(slot + (part - 1) * (S::kSlot / 16), 0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 512 * c), "r"(v[4 * c]),
+                           "r"(v[4 * c + 1]), "r"(v[4 * c + 2]), "r"(v[4 * c + 3])
+                           : "memory");
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tc_arrive_at(joined, 0);
+            continue;
+          }
+          if (!__all_sync(0xFFFFFFFFu, tc_wait_cluster(joined, n & 1u, abort_flag, a.status))) break;
+          for (int p = 1; p < a.split; ++p) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 f = slot[(p - 1) * (S::kSlot / 16) + 32 * c];
+              v[4 * c] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * c]), f.x));
+              v[4 * c + 1] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * c + 1]), f.y));
+              v[4 * c + 2] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * c + 2]), f.z));
+              v[4 * c + 3] = __float_as_uint(__fadd_rn(__uint_as_float(v[4 * c + 3]), f.w));
+            }
+          }
+          __syncwarp();
+          if (lane > 0 && lane < a.split) tc_arrive_at(taken, lane);
+        }
+      }
       if (row >= a.M || col >= a.N) continue;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) v[c] = __float_as_uint(__fmul_rn(__uint_as_float(v[c]), alpha));
@@ -328,7 +382,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
   }
   tc_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_barrier();  // nothing of the pair is under way
+  if constexpr (CG == 2 || TRANS) cluster_barrier();  // nothing of the cluster is under way
   tc_after();
   if (warp == 1) tc_dealloc<CG>(tmem, S::kAlloc);
 }
@@ -378,7 +432,7 @@ struct Operand {
 
 template <int CG, int BN, int FMT, int OUT, bool TRANS, bool TMA_STORE>
 static cudaError_t gemm4_run(const Operand& x, const Operand& y, Gemm4Args a, cudaStream_t st) {
-  using S = Q4<CG, BN, FMT>;
+  using S = Q4<CG, BN, FMT, TRANS ? kQSlots : 0>;
   auto k = gemm_fp4_kernel<CG, BN, FMT, OUT, TRANS, TMA_STORE>;
   int occ = 0;  // also raises the shared-memory limit in this context
   cudaError_t e = kernel_blocks_per_sm((const void*)k, kQThreads, S::kSmem, &occ);
@@ -402,29 +456,47 @@ static cudaError_t gemm4_run(const Operand& x, const Operand& y, Gemm4Args a, cu
       return cudaErrorInvalidValue;
   }
   const int64_t tiles = fp4_scale_tiles(a.M, 128 * CG) * fp4_scale_tiles(a.N, BN);
-  const int64_t clusters = std::min<int64_t>(tiles, sm_count() / CG);
+  const int per = TRANS ? a.split : CG;
+  const int64_t clusters = std::min<int64_t>(tiles, sm_count() / per);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * CG));
+  cfg.gridDim = dim3((unsigned)(clusters * per));
   cfg.blockDim = dim3(kQThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = CG;
+  at.val.clusterDim.x = (unsigned)per;
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
+  cfg.numAttrs = per > 1 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, k, ma, mb, msa, msb, md, a);
+}
+
+// Time of a shape's tiles on all SMs, in units of a stage of the large tile
+// (0.37 us): rounds of tiles times stages and the store.
+static double rounds(int64_t M, int64_t N, int64_t K, int tm, int tn, int ctas, double stage, double store) {
+  const int64_t tiles = fp4_scale_tiles(M, tm) * fp4_scale_tiles(N, tn), slots = sm_count() / ctas;
+  return (double)fp4_scale_tiles(tiles, slots) * ((double)fp4_scale_tiles(K, kQK) * stage + store);
 }
 
 template <int FMT, int OUT>
 static cudaError_t gemm4_pick(const Operand& x, const Operand& y, Gemm4Args a, bool tma, cudaStream_t st) {
   if (a.M <= 32) {  // few rows of A: they become a tile's columns
     std::swap(a.M, a.N);
+    // the split that leaves the fewest stages to the busiest SM
+    const int64_t tiles = fp4_scale_tiles(a.M, 128), kb = fp4_scale_tiles(a.K, kQK);
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 4 && s <= kb; s *= 2) {
+      const int64_t cost = fp4_scale_tiles(tiles, sm_count() / s) * (fp4_scale_tiles(kb, s) + 2);
+      if (cost < best) best = cost, a.split = s;
+    }
     return gemm4_run<1, 32, FMT, OUT, true, false>(y, x, a, st);
   }
-  if (tma) return gemm4_run<2, 256, FMT, OUT, false, true>(x, y, a, st);
-  return gemm4_run<2, 256, FMT, OUT, false, false>(x, y, a, st);
+  if (rounds(a.M, a.N, a.K, 128, 128, 1, 0.6, 3.0) < rounds(a.M, a.N, a.K, 256, 256, 2, 1.0, 5.0))
+    return tma ? gemm4_run<1, 128, FMT, OUT, false, true>(x, y, a, st)
+               : gemm4_run<1, 128, FMT, OUT, false, false>(x, y, a, st);
+  return tma ? gemm4_run<2, 256, FMT, OUT, false, true>(x, y, a, st)
+             : gemm4_run<2, 256, FMT, OUT, false, false>(x, y, a, st);
 }
 
 cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* ta, const uint8_t* qb,
@@ -437,7 +509,7 @@ cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* t
     return cudaMemset2DAsync(d, (size_t)ldd * esz, 0, (size_t)N * esz, (size_t)M, st);
   if (!encode_fn()) return cudaErrorNotSupported;
   const Operand x = {qa, sa, M}, y = {qb, sb, N};
-  const Gemm4Args a = {ta, tb, M, N, K, d, ldd, status, 16, test_stall()};
+  const Gemm4Args a = {ta, tb, M, N, K, d, ldd, status, 16, 1, test_stall()};
   const bool tma = (uintptr_t)d % 16 == 0 && ((size_t)ldd * esz) % 16 == 0;
   if (fmt == GS_NVFP4)
     return out_dtype == GS_F32 ? gemm4_pick<GS_NVFP4, GS_F32>(x, y, a, tma, st)

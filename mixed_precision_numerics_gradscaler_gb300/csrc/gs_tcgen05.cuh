@@ -60,6 +60,22 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
   }
   return true;
 }
+// The same where other CTAs of the cluster wrote what the barrier tells of.
+__device__ __forceinline__ bool tc_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(tc_smem(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool tc_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                int32_t* status) {
+  return tc_wait(bar, parity, abort_flag, status) && tc_try_wait_cluster(bar, parity);
+}
 // The same for a whole warp, which goes on or gives up together.
 __device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              int32_t* status) {
@@ -77,6 +93,9 @@ __device__ __forceinline__ void tc_bar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void tc_expect(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc_smem(bar)), "r"(bytes)
                : "memory");
+}
+__device__ __forceinline__ void tc_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc_smem(bar)) : "memory");
 }
 // Arrives at the barrier at bar's place in CTA `rank` of the cluster.
 __device__ __forceinline__ void tc_arrive_at(uint64_t* bar, uint32_t rank) {
