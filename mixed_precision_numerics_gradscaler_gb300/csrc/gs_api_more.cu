@@ -296,7 +296,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     t.sym_tiles = (int)sym;
     t.app_tiles = (int)app;
     at_mats = take(mats.size() * sizeof(MuonMat));
-    at_maps = take(mats.size() * 4 * sizeof(CUtensorMap));
+    at_maps = take(mats.size() * 8 * sizeof(CUtensorMap));
     at_partials = take((size_t)t.chunks * sizeof(double));
     at_arrived = take(mats.size() * sizeof(unsigned));
     at_done = take(mats.size() * sizeof(unsigned));
@@ -305,7 +305,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
       const size_t x = (size_t)m.rows * m.ldx * 2, g = (size_t)m.s * m.lds * 2;
       for (const size_t b : {x, x, g, g}) at_x.push_back(take(b));
     }
-    maps.resize(mats.size() * 4);
+    maps.resize(mats.size() * 8);
   } catch (...) {
     return GS_ERR_ARG;
   }
@@ -326,10 +326,12 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
       m.x[1] = p[1];
       m.gram = p[2];
       m.poly = p[3];
-      for (int j = 0; j < 4; ++j)
-        if (!muon_encode(&maps[4 * i + j], p[j], j < 2 ? m.rows : m.s, j < 2 ? m.cols : m.s,
-                         j < 2 ? m.ldx : m.lds))
+      for (int j = 0; j < 8; ++j) {
+        const int k = j % 4;
+        if (!muon_encode(&maps[8 * i + j], p[k], k < 2 ? m.rows : m.s, k < 2 ? m.cols : m.s,
+                         k < 2 ? m.ldx : m.lds, j < 4 ? 64 : 32))
           e = cudaErrorNotSupported;
+      }
     }
     MuonTable& lt = l->table;
     lt.mats = reinterpret_cast<const MuonMat*>(d + at_mats);
@@ -338,8 +340,8 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     lt.arrived = reinterpret_cast<unsigned*>(d + at_arrived);
     lt.done = reinterpret_cast<unsigned*>(d + at_done);
     lt.factor = reinterpret_cast<float*>(d + at_factor);
-    // operands' padding is read by 16-byte loads: numbers from the start
-    if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, bytes, cudaStreamLegacy);
+    // counts start at 0 (the products' operands are written before they are read)
+    if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, at_x[0], cudaStreamLegacy);
     if (e == cudaSuccess)
       e = cudaMemcpyAsync(d + at_mats, mats.data(), mats.size() * sizeof(MuonMat), cudaMemcpyHostToDevice,
                           cudaStreamLegacy);

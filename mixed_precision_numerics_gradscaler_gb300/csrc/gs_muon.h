@@ -30,10 +30,10 @@ struct MuonMat {
 
 struct MuonTable {
   const MuonMat* mats;
-  const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly
+  const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly by 64 x 64, then by 32 x 64
   double* partials;          // one per chunk
   unsigned int* arrived;     // per matrix, 0 between calls
-  unsigned int* done;        // per matrix: halves of tiles stored by the call's products
+  unsigned int* done;        // per matrix: warps' parts of tiles (16 each) stored by the call's products
   float* factor;             // per matrix: sx / |u|
   int n;
   int64_t chunks;
@@ -50,8 +50,8 @@ struct MuonArgs {
 };
 
 // A tensor map of an fp16 matrix [rows, cols] with row distance ld, boxes of
-// 64 x 64 in the 128-byte swizzle.
-bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld);
+// box_rows x 64 in the 128-byte swizzle.
+bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld, int box_rows);
 cudaError_t launch_master_update_muon(const MuonTable& t, const MuonArgs& a, cudaStream_t st);
 
 }  // namespace gs

@@ -51,8 +51,10 @@ constexpr int kMThreads = 384;               // warps 0-3: loads, MMA, two idle;
 constexpr int kMEThreads = 256;              // of the element-wise steps
 constexpr int kMBox = 64 * 128;              // bytes of a 64 x 64 box
 constexpr int kMStage = 4 * kMBox;           // a CTA's 128 x 64 of either operand
-constexpr int kMStages = 6;
-constexpr int kMSmem = kMStages * kMStage + 8 * 4096 + 1024 + 256;
+constexpr int kMStages = 5;
+constexpr int kMPiece = 32 * 128;            // bytes of a warp's 32 rows x 64 columns of fp16
+constexpr int kMKeys = 128;                  // matrices whose first tiles are kept in shared memory
+constexpr int kMSmem = kMStages * kMStage + 16 * kMPiece + 8 * kMKeys + 1024 + 512;
 static_assert(kMSmem <= 232448, "dynamic shared memory above the per-CTA limit");
 
 // The matrix that holds item t: the last one whose first is not above t.
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
     const int64_t end = min(n, base + kMuonChunk);
     const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
     if (base == 0 && threadIdx.x == 0) t.done[id] = 0;  // for the products' launch
-    double sum = 0.0;
+    float sum = 0.0f;  // of a thread's 32 squares, then of 32 threads: 2^-22 of it
 #pragma unroll
     for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
       const int64_t i = base + ((int64_t)j * kMEThreads + threadIdx.x) * 4;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
         const float u = a.nesterov ? __fmaf_rn(a.mu, m[e], g[e]) : m[e];
         sq = __fmaf_rn(u, u, sq);
       }
-      sum += (double)sq;
+      sum = __fadd_rn(sum, sq);
       if (vec_m && i + 4 <= end) {
         *reinterpret_cast<float4*>(mat.m + i) = make_float4(m[0], m[1], m[2], m[3]);
       } else {
@@ -134,13 +136,14 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
     }
     // the block's sum, and the matrix's once its last chunk is in
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xFFFFFFFFu, sum, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+    for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_down_sync(0xFFFFFFFFu, sum, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = (double)sum;
     __syncthreads();
     const int64_t chunks = (n + kMuonChunk - 1) / kMuonChunk;
     if (threadIdx.x == 0) {
-      for (int w = 1; w < kMEThreads / 32; ++w) sum += red[w];
-      t.partials[c] = sum;
+      double part = red[0];
+      for (int w = 1; w < kMEThreads / 32; ++w) part += red[w];
+      t.partials[c] = part;
       __threadfence();
       last = atomicAdd(&t.arrived[id], 1u) == (unsigned)chunks - 1;
       __threadfence();
@@ -243,10 +246,11 @@ struct Product {
   bool ta, tb;           // operand with its sum across the rows
   int map_a, map_b;      // of the matrix's four maps
   bool mirror;           // a tile below the diagonal
-  unsigned need;         // halves of the matrix's tiles that have to be done before
+  unsigned need;         // sixteenths of the matrix's tiles to be stored before
 };
 // The step's tiles in their order: every matrix's G, every P, every X.
-__device__ __forceinline__ Product product(const MuonTable& t, int at, int steps) {
+// keys: the matrices' first tiles of either kind, or null to read them from memory.
+__device__ __forceinline__ Product product(const MuonTable& t, const int* keys, int at, int steps) {
   Product p;
   const int per = 2 * t.sym_tiles + t.app_tiles, step = at / per;
   at -= step * per;
@@ -259,11 +263,22 @@ __device__ __forceinline__ Product product(const MuonTable& t, int at, int steps
     p.kind = step + 1 < steps ? kApply : kLast;
     at -= 2 * t.sym_tiles;
   }
-  p.id = mat_of(t.mats, t.n, at, sym ? &MuonMat::first_sym : &MuonMat::first_app);
+  if (keys) {
+    const int* k = keys + (sym ? 0 : kMKeys);
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (k[mid] <= at) lo = mid;
+      else hi = mid - 1;
+    }
+    p.id = lo;
+  } else {
+    p.id = mat_of(t.mats, t.n, at, sym ? &MuonMat::first_sym : &MuonMat::first_app);
+  }
   const MuonMat& mat = t.mats[p.id];
   at -= sym ? mat.first_sym : mat.first_app;
   const int done = step * (2 * mat.syms + mat.apps);
-  p.need = 2u * (unsigned)(done + (p.kind == kGram ? 0 : p.kind == kPoly ? mat.syms : 2 * mat.syms));
+  p.need = 16u * (unsigned)(done + (p.kind == kGram ? 0 : p.kind == kPoly ? mat.syms : 2 * mat.syms));
   int mt, nt;
   if (sym) {  // row mt of a triangle holds tiles mt (mt + 1) / 2 ...
     mt = (int)((sqrtf(8.0f * (float)at + 1.0f) - 1.0f) * 0.5f);
@@ -327,9 +342,58 @@ __device__ __forceinline__ bool wait_done(const unsigned* p, unsigned need, vola
   return __all_sync(0xFFFFFFFFu, ok);
 }
 
-// 32 rows x 32 columns of fp32 in shared memory: 16-byte piece j of row r.
-__device__ __forceinline__ float* piece(float* buf, int r, int j) {
-  return buf + 32 * r + 4 * (j ^ (r & 7));
+// Two fp32 values -> two fp16 (round to nearest even), hi in the high half.
+__device__ __forceinline__ uint32_t cvt_f32x2_f16x2(float hi, float lo) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// w = w decay - to_w o and its bf16 copy, of 32 rows (one per lane's o) and 32
+// columns from (row0, col): by way of buf (4096 bytes), so that neighbouring
+// lanes take neighbouring columns.
+__device__ __forceinline__ void update_weights(const MuonMat& mat, float* buf, const float* o, int row0,
+                                               int col, float decay, float to_w) {
+  if (col >= mat.cols) return;
+  const int lane = threadIdx.x & 31;
+  const auto piece = [&](int r, int j) { return buf + 32 * r + 4 * (j ^ (r & 7)); };
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<float4*>(piece(lane, j)) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+  __syncwarp();
+  const bool vec = mat.cols % 4 == 0 && (uintptr_t)mat.w % 16 == 0 && (uintptr_t)mat.wb % 8 == 0;
+  if (vec) {  // eight lanes to a row
+    const int c4 = col + 4 * (lane & 7), r0 = row0 + (lane >> 3);
+    float* wp = mat.w + (int64_t)r0 * mat.cols + c4;
+    float4 f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r0 + 4 * i < mat.rows && c4 < mat.cols)
+        f[i] = *reinterpret_cast<const float4*>(wp + (int64_t)4 * i * mat.cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (r0 + 4 * i < mat.rows && c4 < mat.cols) {
+        const float4 u = *reinterpret_cast<const float4*>(piece(4 * i + (lane >> 3), lane & 7));
+        f[i].x = __fmaf_rn(-to_w, u.x, __fmul_rn(f[i].x, decay));
+        f[i].y = __fmaf_rn(-to_w, u.y, __fmul_rn(f[i].y, decay));
+        f[i].z = __fmaf_rn(-to_w, u.z, __fmul_rn(f[i].z, decay));
+        f[i].w = __fmaf_rn(-to_w, u.w, __fmul_rn(f[i].w, decay));
+        *reinterpret_cast<float4*>(wp + (int64_t)4 * i * mat.cols) = f[i];
+        if (mat.wb)
+          *reinterpret_cast<uint2*>(mat.wb + (int64_t)(r0 + 4 * i) * mat.cols + c4) =
+              make_uint2(cvt_f32x2_bf16x2(f[i].y, f[i].x), cvt_f32x2_bf16x2(f[i].w, f[i].z));
+      }
+    }
+  } else if (col + lane < mat.cols) {  // any address: a row's columns by lanes
+    const int rows = min(32, mat.rows - row0);
+    for (int r = 0; r < rows; ++r) {
+      const int64_t at = (int64_t)(row0 + r) * mat.cols + col + lane;
+      const float f = __fmaf_rn(-to_w, piece(r, lane >> 2)[lane & 3], __fmul_rn(mat.w[at], decay));
+      mat.w[at] = f;
+      if (mat.wb) mat.wb[at] = Elem<GS_BF16>::put(f);
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
@@ -338,14 +402,17 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
-  float* out_stage = reinterpret_cast<float*>(stages + kMStages * kMStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + 8 * 1024);
+  uint8_t* pieces = stages + kMStages * kMStage;  // two per storing warp
+  int* key_space = reinterpret_cast<int*>(pieces + 16 * kMPiece);
+  uint64_t* full = reinterpret_cast<uint64_t*>(key_space + 2 * kMKeys);
   uint64_t* empty = full + kMStages;
   uint64_t* tfull = empty + kMStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* loaded = drain + 1;                   // a storing warp's pieces of old
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(loaded + 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int* keys = t.n <= kMKeys ? key_space : nullptr;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -362,10 +429,17 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
       tc_bar_init(&tempty[b], 16);
     }
     tc_bar_init(drain, 1);
+    for (int w = 0; w < 8; ++w) tc_bar_init(&loaded[w], 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tc_alloc<2>(tmem_slot, 512);
+  if (keys && threadIdx.x >= 64 && threadIdx.x - 64 < t.n) {
+    key_space[threadIdx.x - 64] = t.mats[threadIdx.x - 64].first_sym;
+    key_space[kMKeys + threadIdx.x - 64] = t.mats[threadIdx.x - 64].first_app;
+  }
+  // the tensor maps lie in global memory: once per CTA before their use
+  for (int i = threadIdx.x; i < 8 * t.n; i += kMThreads) map_fence(t.maps + i);
   tc_before();
   __syncthreads();
   cluster_barrier();
@@ -374,16 +448,10 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
 
   if (warp == 0) {  // loads
     uint32_t s = 0, ph = 0, used = 0;
-    int seen = -1;
     bool go = !a.stall;
     for (int tile = first; go && tile < tiles; tile += step) {
-      const Product p = product(t, tile, a.steps);
-      const CUtensorMap* maps = t.maps + 4 * p.id;
-      if (p.id != seen) {
-        if (lane < 4) map_fence(maps + lane);
-        __syncwarp();
-        seen = p.id;
-      }
+      const Product p = product(t, keys, tile, a.steps);
+      const CUtensorMap* maps = t.maps + 8 * p.id;
       if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
       // what other CTAs stored is read by TMA from here on
       asm volatile("fence.proxy.async;" ::: "memory");
@@ -419,7 +487,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t s = 0, ph = 0, b = 0, tph = 0;
     bool go = true;
     for (int tile = first; go && tile < tiles; tile += step) {
-      const Product p = product(t, tile, a.steps);
+      const Product p = product(t, keys, tile, a.steps);
       if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
       const uint32_t idesc = idesc16(p.ta, p.tb);
@@ -449,31 +517,29 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     tc_drain(drain, 0);
   } else if (warp >= 4) {  // store
     const int q = warp & 3, h = (warp - 4) >> 2;
-    float* const buf = out_stage + (warp - 4) * 1024;
-    uint32_t b = 0, tph = 0;
+    uint8_t* const mine = pieces + (warp - 4) * 2 * kMPiece;
+    uint64_t* const bar = &loaded[warp - 4];
+    uint32_t b = 0, tph = 0, lph = 0;
     for (int tile = first; tile < tiles; tile += step) {
-      const Product p = product(t, tile, a.steps);
+      const Product p = product(t, keys, tile, a.steps);
       const MuonMat& mat = t.mats[p.id];
       // result = alpha acc + beta old, old in the result's shape
       float alpha, beta = 0.0f, one = 0.0f, decay = 1.0f, to_w = 0.0f;
-      const uint16_t* old = nullptr;
-      uint16_t* out = nullptr;
-      int ld = mat.lds;
+      int map_old = 0, map_out = 0;
       if (p.kind == kGram) {
         alpha = __fdiv_rn(mat.sa, __fmul_rn(mat.sx, mat.sx));
-        out = mat.gram;
+        map_out = 2;
       } else if (p.kind == kPoly) {
         alpha = __fdiv_rn(0.25f * kNsC, mat.sa);  // gram gram is by sa^2, poly by sa / 4
         beta = 0.25f * kNsB;
         one = __fmul_rn(0.25f * (kNsA - 1.0f), mat.sa);
-        old = mat.gram;
-        out = mat.poly;
+        map_old = 2;
+        map_out = 3;
       } else {
         alpha = __fdiv_rn(4.0f, mat.sa);
         beta = 1.0f;
-        old = mat.x[p.turn];
-        out = mat.x[p.turn ^ 1];
-        ld = mat.ldx;
+        map_old = p.turn;
+        map_out = p.turn ^ 1;
         if (p.kind == kLast) {
           const float big = (float)max(mat.rows, mat.cols);
           const float scale = a.scale_mode == GS_MUON_SCALE_RMS
@@ -483,117 +549,115 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
           to_w = __fdiv_rn(__fmul_rn(a.lr, scale), mat.sx);
         }
       }
-      const bool vec_w = mat.cols % 4 == 0 && (uintptr_t)mat.w % 16 == 0 && (uintptr_t)mat.wb % 8 == 0;
-      const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane;
-      const bool got = tc_wait(&tfull[b], tph, abort_flag, a.status);
+      const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane, col0 = p.n0 + 128 * h;
+      const CUtensorMap* maps = t.maps + 8 * p.id + 4;  // boxes of 32 rows
+      const bool some = row0 < p.M && col0 < p.N;
+      if (p.kind != kGram && some) {
+        if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
+        // what other CTAs stored is read by TMA; this warp's own uses of its
+        // pieces are over
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (tc_elect()) {
+          tc_expect(bar, 2 * kMPiece);
+          tc_load2<1>(maps + map_old, tc_smem(bar), mine, col0, row0);
+          tc_load2<1>(maps + map_old, tc_smem(bar), mine + kMPiece, col0 + 64, row0);
+        }
+        __syncwarp();
+      }
+      bool got = tc_wait(&tfull[b], tph, abort_flag, a.status);
+      if (p.kind != kGram && some) {
+        // (also where the tile is given up: the loads have to land)
+        tc_drain(bar, lph);
+        lph ^= 1u;
+      }
       if (!__all_sync(0xFFFFFFFFu, got)) break;
       tc_after();
-      load_acquire(t.done + p.id);  // at least p.need: old is as other CTAs stored it
+      const bool mirror = p.mirror && row < p.M;
+      uint4 later[4] = {};
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        const int col = p.n0 + 128 * h + c;
-        uint32_t v[32];
-        tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * 256 + 128 * h + c, v);
+      for (int c = 0; c < 4; ++c) {
+        const int col = col0 + 32 * c;
+        uint8_t* const buf = mine + (c >> 1) * kMPiece;
+        float o[32];
+        uint32_t* const v = reinterpret_cast<uint32_t*>(o);
+        tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * 256 + 128 * h + 32 * c, v);
         tc_wait_ld<32>(v);
-        if (c == 96) {
+        if (c == 3) {
           tc_before();
           __syncwarp();
           if (lane == 0) tc_arrive_at(&tempty[b], 0);
         }
-        if (col >= p.N || row0 >= p.M) continue;
-        if (p.kind == kGram && p.mirror && row < p.M) {
+        // (the second half of a piece is stored with the first)
+        if (row0 >= p.M || col0 + 64 * (c >> 1) >= p.N) continue;
+        // 16 bytes j of row r lie at j ^ (r % 8)
+        const auto place = [&](int j) {
+          return reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4));
+        };
+        uint4 was[4];  // both halves are read before the piece is written
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (col + j < p.N)
-              out[(int64_t)(col + j) * ld + row] =
-                  Elem<GS_F16>::put(__fmul_rn(__uint_as_float(v[j]), alpha));
+        for (int j = 0; j < 4; ++j) was[j] = later[j];
+        if (p.kind != kGram && (c & 1) == 0) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) was[j] = *place(j), later[j] = *place(4 + j);
         }
-        // through shared memory: eight lanes to a row's 32 columns
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = __fmul_rn(__uint_as_float(v[4 * j + e]), alpha);
-          *reinterpret_cast<float4*>(piece(buf, lane, j)) = make_float4(o[0], o[1], o[2], o[3]);
-        }
-        __syncwarp();
-        const int c4 = col + 4 * (lane & 7);
-        uint2 w[8];
+        for (int j = 0; j < 32; ++j) o[j] = __fmul_rn(o[j], alpha);
         if (p.kind != kGram) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {  // the padding at a row's end may be read
-            const int r = row0 + 4 * i + (lane >> 3);
-            if (r < p.M && c4 < p.N) w[i] = __ldcg(reinterpret_cast<const uint2*>(old + (int64_t)r * ld + c4));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = 4 * i + (lane >> 3), r = row0 + rr;
-          if (r >= p.M || c4 >= p.N) continue;
-          float* const at = piece(buf, rr, lane & 7);
-          float4 f = *reinterpret_cast<const float4*>(at);
-          float o[4] = {f.x, f.y, f.z, f.w};
-          if (p.kind != kGram) {
-            const float u[4] = {lo_f16(w[i].x), hi_f16(w[i].x), lo_f16(w[i].y), hi_f16(w[i].y)};
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t ww[4] = {was[j].x, was[j].y, was[j].z, was[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              o[e] = __fmaf_rn(beta, u[e], o[e]);
-              if (p.kind == kPoly && c4 + e == r) o[e] = __fadd_rn(o[e], one);
+              o[8 * j + 2 * e] = __fmaf_rn(beta, lo_f16(ww[e]), o[8 * j + 2 * e]);
+              o[8 * j + 2 * e + 1] = __fmaf_rn(beta, hi_f16(ww[e]), o[8 * j + 2 * e + 1]);
             }
           }
-          if (p.kind != kLast) {  // the padding's values are read by nothing
-            *reinterpret_cast<uint2*>(out + (int64_t)r * ld + c4) =
-                make_uint2((uint32_t)Elem<GS_F16>::put(o[0]) | (uint32_t)Elem<GS_F16>::put(o[1]) << 16,
-                           (uint32_t)Elem<GS_F16>::put(o[2]) | (uint32_t)Elem<GS_F16>::put(o[3]) << 16);
-            if (p.kind == kPoly && p.mirror)
-              *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
-          } else if (vec_w) {
-            float* const wp = mat.w + (int64_t)r * mat.cols + c4;
-            f = *reinterpret_cast<const float4*>(wp);
-            f.x = __fmaf_rn(-to_w, o[0], __fmul_rn(f.x, decay));
-            f.y = __fmaf_rn(-to_w, o[1], __fmul_rn(f.y, decay));
-            f.z = __fmaf_rn(-to_w, o[2], __fmul_rn(f.z, decay));
-            f.w = __fmaf_rn(-to_w, o[3], __fmul_rn(f.w, decay));
-            *reinterpret_cast<float4*>(wp) = f;
-            if (mat.wb)
-              *reinterpret_cast<uint2*>(mat.wb + (int64_t)r * mat.cols + c4) =
-                  make_uint2(cvt_f32x2_bf16x2(f.y, f.x), cvt_f32x2_bf16x2(f.w, f.z));
-          } else {
-            *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        if (p.kind == kPoly && p.mirror) {
-          __syncwarp();
-          if (row < p.M) {
+          if (p.kind == kPoly && row0 < col + 32 && col < row0 + 32) {  // the diagonal is in it
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (col + j < p.N)
-                out[(int64_t)(col + j) * ld + row] = Elem<GS_F16>::put(piece(buf, lane, j >> 2)[j & 3]);
-          }
-        } else if (p.kind == kLast && !vec_w) {  // any address: a row's columns by lanes
-          __syncwarp();
-          const int rows = min(32, p.M - row0);
-          if (col + lane < p.N) {
-            for (int r = 0; r < rows; ++r) {
-              const int64_t at = (int64_t)(row0 + r) * mat.cols + col + lane;
-              const float f = __fmaf_rn(-to_w, piece(buf, r, lane >> 2)[lane & 3], __fmul_rn(mat.w[at], decay));
-              mat.w[at] = f;
-              if (mat.wb) mat.wb[at] = Elem<GS_BF16>::put(f);
-            }
+              if (col + j == row) o[j] = __fadd_rn(o[j], one);
           }
         }
+        if (p.kind != kLast) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = cvt_f32x2_f16x2(o[8 * j + 2 * e + 1], o[8 * j + 2 * e]);
+            *place(4 * (c & 1) + j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (c & 1) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (tc_elect()) {  // clipped at the matrix's edges
+              tc_store2(maps + map_out, buf, col - 32, row0);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            __syncwarp();
+          }
+          if (mirror) {
+            uint16_t* const out = (p.kind == kGram ? mat.gram : mat.poly) + row;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col + j < p.N) out[(int64_t)(col + j) * mat.lds] = Elem<GS_F16>::put(o[j]);
+          }
+        } else {
+          update_weights(mat, reinterpret_cast<float*>(buf), o, row0, col, decay, to_w);
+        }
       }
-      // this CTA's half is stored: for loads of either kind by other CTAs
+      // this warp's part is stored: for loads of either kind by other CTAs.  (Each
+      // warp counts for itself: one that gave up holds no other.)
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       __threadfence();
       asm volatile("fence.proxy.async;" ::: "memory");
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (threadIdx.x == 128) {
+      __syncwarp();
+      if (lane == 0)
         asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(t.done + p.id) : "memory");
-      }
       b ^= 1u;
       if (b == 0) tph ^= 1u;
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   tc_before();
   __syncthreads();
@@ -616,11 +680,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld) {
+bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
   if (!encode_fn()) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, 64}, one[2] = {1, 1};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, one[2] = {1, 1};
   return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, one,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
