@@ -564,8 +564,9 @@ int fp4_dequant(const uint8_t* q, const uint8_t* scales, const float* tensor_sca
  *   d: [M, N] with row distance ldd, out_dtype GS_F32 or GS_BF16 (rounded to
  *      nearest even from the fp32 sum); what lies between rows is not written.
  * Products and scales are exact in the tensor cores, sums in fp32 in an order
- * that depends on the sizes and the device alone: |error| <= 2^-24 (K / 16 +
- * 8) sum of |terms| before the output's rounding.
+ * that depends on the sizes and the device alone: |error| <= 2^-23 (K / 16 +
+ * 8) sum of |terms| before the output's rounding (an addition's error for each
+ * 16 products, however the tensor cores round it).
  * K % 32 == 0, M, N, K < 2^31 and fewer than 2^30 tiles of 128 x 128 (else
  * GS_ERR_SHAPE); any M and N; K == 0 writes zeros.  Codes and scales 16-byte
  * aligned.  A wait that runs out records GS_ERR_TIMEOUT (gs_device_status) and

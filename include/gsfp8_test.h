@@ -1,8 +1,9 @@
 /*
  * gsfp8_test.h -- test hooks of libgsfp8 (not part of the computation).
  *
- * The kernel fed by TMA -- fp8_gemm_block_scaled -- waits on shared-memory
- * barriers for its loads, for the tensor cores and for the promotion warps.
+ * The kernels fed by TMA -- fp8_gemm_block_scaled, fp4_gemm_block_scaled and the
+ * products of gs_master_update_muon -- wait on shared-memory barriers for their
+ * loads, for the tensor cores and for the warps that store.
  * Every such wait is bounded (about 2 s by %globaltimer); a kernel that gives
  * up records GS_ERR_TIMEOUT in the device status word (gs_device_status),
  * lets its own copies and MMAs in flight finish, frees its tensor memory and
@@ -20,11 +21,11 @@
 extern "C" {
 #endif
 
-/* on != 0: launches made from now on by this process of the kernel named
+/* on != 0: launches made from now on by this process of the kernels named
  * above issue no TMA loads, so their first bounded wait runs out: the launch
  * takes about 2 s, writes nothing valid to its outputs and records
  * GS_ERR_TIMEOUT.  on == 0 restores normal operation.  Process-wide; set it
- * only while no other thread launches that kernel.  Returns GS_OK. */
+ * only while no other thread launches those kernels.  Returns GS_OK. */
 int gs_test_set_stall(int on);
 
 /* r[i] = sqrt(v[i]) (device, n even, not overlapping) by the code that forms

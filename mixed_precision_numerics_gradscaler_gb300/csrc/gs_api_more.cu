@@ -77,9 +77,8 @@ int fp4_quant(const void* x, int64_t ldx, int in_dtype, int64_t R, int64_t C, in
   if (R < 0 || C < 0 || !rows_ok(R, C, ldx, esz) || C % 32 || (qt && R % 32)) return GS_ERR_SHAPE;
   const bool nv = fmt == GS_NVFP4, empty = R == 0 || C == 0;
   if (!empty && !x) return GS_ERR_NULL;
-  if ((!q && !qt) || !q != !scales || !qt != !scales_t || nv != (tensor_scale != nullptr))
-    return GS_ERR_NULL;
-  if (!nv && ws) return GS_ERR_ARG;
+  if ((!q && !qt) || !q != !scales || !qt != !scales_t || (nv && !tensor_scale)) return GS_ERR_NULL;
+  if (!nv && (tensor_scale || ws)) return GS_ERR_ARG;
   if (!aligned(x, esz) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(qt, 16) ||
       !aligned(scales_t, 16) || !aligned(tensor_scale, 4) || !aligned(ws, 4))
     return GS_ERR_ARG;
@@ -107,7 +106,8 @@ int fp4_dequant(const uint8_t* q, const uint8_t* scales, const float* tensor_sca
   const size_t esz = dtype_size(out_dtype);
   if (R < 0 || C < 0 || !rows_ok(R, C, ldy, esz) || C % 32) return GS_ERR_SHAPE;
   if (R == 0 || C == 0) return GS_OK;
-  if (!q || !scales || !y || (fmt == GS_NVFP4) != (tensor_scale != nullptr)) return GS_ERR_NULL;
+  if (!q || !scales || !y || (fmt == GS_NVFP4 && !tensor_scale)) return GS_ERR_NULL;
+  if (fmt != GS_NVFP4 && tensor_scale) return GS_ERR_ARG;
   if (!aligned(q, 16) || !aligned(scales, 16) || !aligned(tensor_scale, 4) || !aligned(y, esz))
     return GS_ERR_ARG;
   if (!reach(q) || !reach(scales) || !reach(tensor_scale) || !reach(y)) return GS_ERR_ARG;
@@ -132,7 +132,8 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
   if (M == 0 || N == 0) return GS_OK;
   const bool nv = fmt == GS_NVFP4;
   if (!d || (K > 0 && (!qa || !sa || !qb || !sb))) return GS_ERR_NULL;
-  if (nv != (ta != nullptr) || nv != (tb != nullptr)) return GS_ERR_NULL;
+  if (nv && (!ta || !tb)) return GS_ERR_NULL;
+  if (!nv && (ta || tb)) return GS_ERR_ARG;
   if (!aligned(d, esz) || !aligned(qa, 16) || !aligned(sa, 16) || !aligned(qb, 16) || !aligned(sb, 16) ||
       !aligned(ta, 4) || !aligned(tb, 4))
     return GS_ERR_ARG;

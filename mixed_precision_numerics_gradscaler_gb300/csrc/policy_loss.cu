@@ -275,7 +275,9 @@ __global__ void __launch_bounds__(kPThreads) policy_count_kernel(PolicyArgs a) {
   } else if (by_seq) {  // every token counts: lengths
     for (int64_t s = (int64_t)blockIdx.x * kPThreads + threadIdx.x; s < a.S;
          s += (int64_t)gridDim.x * kPThreads) {
-      const int64_t b = max(lo, min(hi, a.offsets[s])), e = max(lo, min(hi, a.offsets[s + 1]));
+      // (no offsets: one sequence, all of it)
+      const int64_t b = a.offsets ? max(lo, min(hi, a.offsets[s])) : lo;
+      const int64_t e = a.offsets ? max(lo, min(hi, a.offsets[s + 1])) : hi;
       a.n[s] = (unsigned long long)max((int64_t)0, e - b);
     }
   }
