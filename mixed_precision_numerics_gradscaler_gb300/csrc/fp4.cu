@@ -120,10 +120,11 @@ __device__ __forceinline__ uint32_t block_scale4(float amax, const Tensor4& ts, 
     r = __uint_as_float((uint32_t)(254 - c) << 23);
     return ok ? (uint32_t)c : 255u;
   } else {
-    // the quotient as IEEE division rounds it wherever it is not 0 in e4m3
+    // the quotient as IEEE division rounds it wherever it is not 0 in e4m3, or
+    // far beyond its range (where the residuals could overflow)
     ok = ts.ok && amax < __uint_as_float(0x7F800000u);
-    const uint32_t c =
-        ok ? cvt_f32x2_fp8x2<GS_E4M3>(0.0f, exact_quotient<2>(amax, ts.t6, ts.r6)) & 0x7Fu : kFp8NaN;
+    const float u = __fmul_rn(amax, ts.r6) < 1024.0f ? exact_quotient<2>(amax, ts.t6, ts.r6) : 1024.0f;
+    const uint32_t c = ok ? cvt_f32x2_fp8x2<GS_E4M3>(0.0f, u) & 0x7Fu : kFp8NaN;
     r = ts.table[c];
     return c;
   }

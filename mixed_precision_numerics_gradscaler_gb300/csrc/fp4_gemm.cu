@@ -510,7 +510,8 @@ cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* t
   if (!encode_fn()) return cudaErrorNotSupported;
   const Operand x = {qa, sa, M}, y = {qb, sb, N};
   const Gemm4Args a = {ta, tb, M, N, K, d, ldd, status, 16, 1, test_stall()};
-  const bool tma = (uintptr_t)d % 16 == 0 && ((size_t)ldd * esz) % 16 == 0;
+  // (a TMA store clips a row's end to 16 bytes: N must end there too)
+  const bool tma = (uintptr_t)d % 16 == 0 && ((size_t)ldd * esz) % 16 == 0 && ((size_t)N * esz) % 16 == 0;
   if (fmt == GS_NVFP4)
     return out_dtype == GS_F32 ? gemm4_pick<GS_NVFP4, GS_F32>(x, y, a, tma, st)
                                : gemm4_pick<GS_NVFP4, GS_BF16>(x, y, a, tma, st);

@@ -77,7 +77,8 @@ int fp4_quant(const void* x, int64_t ldx, int in_dtype, int64_t R, int64_t C, in
   if (R < 0 || C < 0 || !rows_ok(R, C, ldx, esz) || C % 32 || (qt && R % 32)) return GS_ERR_SHAPE;
   const bool nv = fmt == GS_NVFP4, empty = R == 0 || C == 0;
   if (!empty && !x) return GS_ERR_NULL;
-  if ((!q && !qt) || !q != !scales || !qt != !scales_t || (nv && !tensor_scale)) return GS_ERR_NULL;
+  if (nv && !tensor_scale) return GS_ERR_NULL;
+  if (!empty && ((!q && !qt) || !q != !scales || !qt != !scales_t)) return GS_ERR_NULL;
   if (!nv && (tensor_scale || ws)) return GS_ERR_ARG;
   if (!aligned(x, esz) || !aligned(q, 16) || !aligned(scales, 16) || !aligned(qt, 16) ||
       !aligned(scales_t, 16) || !aligned(tensor_scale, 4) || !aligned(ws, 4))
@@ -341,8 +342,9 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     lt.arrived = reinterpret_cast<unsigned*>(d + at_arrived);
     lt.done = reinterpret_cast<unsigned*>(d + at_done);
     lt.factor = reinterpret_cast<float*>(d + at_factor);
-    // counts start at 0 (the products' operands are written before they are read)
-    if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, at_x[0], cudaStreamLegacy);
+    // counts start at 0, and so do the paddings of operands' rows, which TMA takes
+    // in pieces of 16 bytes (it stores zeros there)
+    if (e == cudaSuccess) e = cudaMemsetAsync(d, 0, bytes, cudaStreamLegacy);
     if (e == cudaSuccess)
       e = cudaMemcpyAsync(d + at_mats, mats.data(), mats.size() * sizeof(MuonMat), cudaMemcpyHostToDevice,
                           cudaStreamLegacy);
