@@ -657,9 +657,9 @@ typedef enum gs_muon_scale { GS_MUON_SCALE_RMS = 0, GS_MUON_SCALE_ASPECT = 1 } g
  * X, G and the polynomial are held in fp16, scaled by powers of two to its range
  * (11 bits where bf16 would keep 8), sums in fp32: after five steps X is off the
  * exact polynomial by about 1.1e-3 of its norm (2^-11 per rounding, which the
- * polynomial's slope at small singular values carries on).  Sums of squares are fp32 within a warp's 1024 elements and fp64
- * beyond: elements of u below 2^-75 count as zero there, and a sum above fp32's
- * range makes the matrix NaN.  Non-finite gradients are for
+ * polynomial's slope at small singular values carries on).  Sums of squares are fp32 within a thread's elements and fp64
+ * beyond: elements of u below 2^-75 count as zero there, and a thread's sum above
+ * fp32's range makes the matrix NaN.  Non-finite gradients are for
  * the check before this step to find.
  * lr, weight_decay finite and >= 0, mu in [0, 1), ns_steps 1 to 20; grad_norm
  * may be NULL when max_norm <= 0.  Calls on one list must be ordered on one

@@ -649,14 +649,14 @@ __global__ void __launch_bounds__(kFThreads)
 template <int DT, int FMT>
 static cudaError_t dequant4_t(const uint8_t* q, const uint8_t* scales, const float* ts, int64_t R,
                               int64_t C, void* y, int64_t ldy, cudaStream_t st) {
-  const int64_t tiles_c = fp4_scale_tiles(C, kDCols);
+  const int64_t tiles_c = div_up(C, kDCols);
   const int align = run_align<DT>(y, R == 1 ? C : ldy);
-  const int64_t large = fp4_scale_tiles(R, kFTile) * tiles_c;
+  const int64_t large = div_up(R, kFTile) * tiles_c;
   if (large >= 4 * sm_count())
     dequant4_kernel<DT, FMT, kFTile>
         <<<(unsigned)large, kFThreads, 0, st>>>(q, scales, ts, R, C, y, ldy, align, tiles_c);
   else
-    dequant4_kernel<DT, FMT, 16><<<(unsigned)(fp4_scale_tiles(R, 16) * tiles_c), kFThreads, 0, st>>>(
+    dequant4_kernel<DT, FMT, 16><<<(unsigned)(div_up(R, 16) * tiles_c), kFThreads, 0, st>>>(
         q, scales, ts, R, C, y, ldy, align, tiles_c);
   return cudaGetLastError();
 }

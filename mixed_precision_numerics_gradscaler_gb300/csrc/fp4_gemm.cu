@@ -415,7 +415,7 @@ static bool encode_codes(CUtensorMap* m, const uint8_t* q, int64_t rows, int64_t
 // `row_tiles` row tiles; zeros past the edges.
 static bool encode_scales(CUtensorMap* m, const uint8_t* s, int64_t rows, int64_t K, int fmt,
                           uint32_t tiles, uint32_t row_tiles) {
-  const int64_t kt = fp4_scale_tiles(K, fmt == GS_NVFP4 ? 64 : 128), rt = fp4_scale_tiles(rows, 128);
+  const int64_t kt = div_up(K, fmt == GS_NVFP4 ? 64 : 128), rt = div_up(rows, 128);
   const cuuint64_t dims[3] = {128, (cuuint64_t)kt, (cuuint64_t)rt};
   const cuuint64_t strides[2] = {512, (cuuint64_t)kt * 512};
   const cuuint32_t box[3] = {128, tiles, row_tiles}, one[3] = {1, 1, 1};
@@ -455,7 +455,7 @@ static cudaError_t gemm4_run(const Operand& x, const Operand& y, Gemm4Args a, cu
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  const int64_t tiles = fp4_scale_tiles(a.M, 128 * CG) * fp4_scale_tiles(a.N, BN);
+  const int64_t tiles = div_up(a.M, 128 * CG) * div_up(a.N, BN);
   const int per = TRANS ? a.split : CG;
   const int64_t clusters = std::min<int64_t>(tiles, sm_count() / per);
   cudaLaunchConfig_t cfg = {};
@@ -475,8 +475,8 @@ static cudaError_t gemm4_run(const Operand& x, const Operand& y, Gemm4Args a, cu
 // Time of a shape's tiles on all SMs, in units of a stage of the large tile
 // (0.37 us): rounds of tiles times stages and the store.
 static double rounds(int64_t M, int64_t N, int64_t K, int tm, int tn, int ctas, double stage, double store) {
-  const int64_t tiles = fp4_scale_tiles(M, tm) * fp4_scale_tiles(N, tn), slots = sm_count() / ctas;
-  return (double)fp4_scale_tiles(tiles, slots) * ((double)fp4_scale_tiles(K, kQK) * stage + store);
+  const int64_t tiles = div_up(M, tm) * div_up(N, tn), slots = sm_count() / ctas;
+  return (double)div_up(tiles, slots) * ((double)div_up(K, kQK) * stage + store);
 }
 
 template <int FMT, int OUT>
@@ -484,10 +484,10 @@ static cudaError_t gemm4_pick(const Operand& x, const Operand& y, Gemm4Args a, b
   if (a.M <= 32) {  // few rows of A: they become a tile's columns
     std::swap(a.M, a.N);
     // the split that leaves the fewest stages to the busiest SM
-    const int64_t tiles = fp4_scale_tiles(a.M, 128), kb = fp4_scale_tiles(a.K, kQK);
+    const int64_t tiles = div_up(a.M, 128), kb = div_up(a.K, kQK);
     int64_t best = INT64_MAX;
     for (int s = 1; s <= 4 && s <= kb; s *= 2) {
-      const int64_t cost = fp4_scale_tiles(tiles, sm_count() / s) * (fp4_scale_tiles(kb, s) + 2);
+      const int64_t cost = div_up(tiles, sm_count() / s) * (div_up(kb, s) + 2);
       if (cost < best) best = cost, a.split = s;
     }
     return gemm4_run<1, 32, FMT, OUT, true, false>(y, x, a, st);

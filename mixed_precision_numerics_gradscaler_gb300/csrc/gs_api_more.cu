@@ -64,7 +64,7 @@ extern "C" {
 
 size_t fp4_scale_bytes(int64_t R, int64_t C, int fmt) {
   if (!valid_fmt4(fmt) || R < 0 || C < 0) return 0;
-  const int64_t a = fp4_scale_tiles(R, 128), b = fp4_scale_tiles(C, fmt == GS_NVFP4 ? 64 : 128);
+  const int64_t a = div_up(R, 128), b = div_up(C, fmt == GS_NVFP4 ? 64 : 128);
   if (!mul_ok(a, b) || !mul_ok(a * b, 512)) return 0;
   return (size_t)(a * b) * 512;
 }
@@ -129,7 +129,7 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
   if (M < 0 || N < 0 || K < 0 || K % 32 || M >= (1LL << 31) || N >= (1LL << 31) || K >= (1LL << 31) ||
       ldd >= (1LL << 36) || !rows_ok(M, N, ldd, esz) || !mul_ok(M, K) || !mul_ok(N, K))
     return GS_ERR_SHAPE;
-  if (fp4_scale_tiles(M, 128) * fp4_scale_tiles(N, 128) >= (1LL << 30)) return GS_ERR_SHAPE;
+  if (div_up(M, 128) * div_up(N, 128) >= (1LL << 30)) return GS_ERR_SHAPE;
   if (M == 0 || N == 0) return GS_OK;
   const bool nv = fmt == GS_NVFP4;
   if (!d || (K > 0 && (!qa || !sa || !qb || !sb))) return GS_ERR_NULL;
@@ -284,10 +284,10 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
       m.first_chunk = t.chunks;
       m.first_sym = (int)sym;
       m.first_app = (int)app;
-      t.chunks += fp4_scale_tiles((int64_t)m.rows * m.cols, kMuonChunk);
-      const int64_t ts = fp4_scale_tiles(m.s, kMuonTile);
+      t.chunks += div_up((int64_t)m.rows * m.cols, kMuonChunk);
+      const int64_t ts = div_up(m.s, kMuonTile);
       const int64_t syms = ts * (ts + 1) / 2;
-      const int64_t apps = fp4_scale_tiles(m.rows, kMuonTile) * fp4_scale_tiles(m.cols, kMuonTile);
+      const int64_t apps = div_up(m.rows, kMuonTile) * div_up(m.cols, kMuonTile);
       sym += syms;
       app += apps;
       if (2 * sym + app >= (1LL << 25)) return GS_ERR_SHAPE;  // of 20 steps: an int

@@ -22,7 +22,4 @@ cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* t
                             int fmt, int out_dtype, void* d, int64_t ldd, int32_t* status,
                             cudaStream_t st);
 
-// Bytes of the scales of an R x C matrix.
-inline int64_t fp4_scale_tiles(int64_t n, int64_t per) { return n / per + (n % per != 0); }
-
 }  // namespace gs

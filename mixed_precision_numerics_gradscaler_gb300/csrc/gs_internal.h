@@ -10,6 +10,9 @@
 
 namespace gs {
 
+// n / per, counted up; n >= 0.
+inline int64_t div_up(int64_t n, int64_t per) { return n / per + (n % per != 0); }
+
 // Cached device properties of the current device.
 int sm_count();
 

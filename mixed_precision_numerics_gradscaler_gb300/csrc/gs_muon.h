@@ -9,7 +9,7 @@
 namespace gs {
 
 constexpr int kMuonTile = 256;               // rows and columns of a product's tile
-constexpr int64_t kMuonChunk = 8192;         // elements of an element-wise step's CTA
+constexpr int64_t kMuonChunk = 4096;         // elements of an element-wise step's CTA
 
 // One matrix [rows, cols]; s = min, l = max of the two.  The products' operands
 // are fp16 times a power of two each: x by sx, gram and poly by sa and sa / 4.

@@ -49,6 +49,7 @@ namespace gs {
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr int kMThreads = 384;               // warps 0-3: loads, MMA, two idle; 4-11 store
 constexpr int kMEThreads = 256;              // of the element-wise steps
+constexpr int kMRuns = (int)(kMuonChunk / (4 * kMEThreads));  // of four elements, per thread
 constexpr int kMBox = 64 * 128;              // bytes of a 64 x 64 box
 constexpr int kMStage = 4 * kMBox;           // a CTA's 128 x 64 of either operand
 constexpr int kMStages = 5;
@@ -94,14 +95,18 @@ __device__ __forceinline__ void get4(const void* p, int64_t i, int64_t n, bool v
   }
 }
 
-// m = mu m + clip g, and the sum of squares of u; a matrix's last chunk to
-// finish forms its factor sx / |u|, from the chunks' sums in their order.
+// m = mu m + clip g, and the sum of squares of u.  CTAs take chunks by turns (runs
+// of chunks, a few hundred KB apart at any time, took 1.7 times as long); what one
+// has of a matrix is one part of its sum, and the last part to arrive forms the
+// factor sx / |u| from all of them in their order.
 template <int DT>
 __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, MuonArgs a) {
   if (*a.found_inf) return;
   __shared__ double red[kMEThreads / 32];
   __shared__ bool last;
   const float clip = clip_of(a);
+  float sum = 0.0f;
+  int64_t begun = -1;  // this CTA's first chunk of the matrix
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
     const MuonMat& mat = t.mats[id];
@@ -109,49 +114,62 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
     const int64_t end = min(n, base + kMuonChunk);
     const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
     if (base == 0 && threadIdx.x == 0) t.done[id] = 0;  // for the products' launch
-    float sum = 0.0f;  // of a thread's 32 squares, then of 32 threads: 2^-22 of it
+    // everything is loaded before anything is stored: the loads do not wait for
+    // one another
+    float g[kMRuns][4], m[kMRuns][4];
 #pragma unroll
-    for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
-      const int64_t i = base + ((int64_t)j * kMEThreads + threadIdx.x) * 4;
+    for (int j = 0; j < kMRuns; ++j) {
+      const int64_t i = base + (j * kMEThreads + threadIdx.x) * 4;
+      if (i < end) {
+        get4<DT>(mat.g, i, end, vec_g, g[j]);
+        get4<GS_F32>(mat.m, i, end, vec_m, m[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kMRuns; ++j) {
+      const int64_t i = base + (j * kMEThreads + threadIdx.x) * 4;
       if (i >= end) continue;
-      float g[4], m[4];
-      get4<DT>(mat.g, i, end, vec_g, g);
-      get4<GS_F32>(mat.m, i, end, vec_m, m);
       float sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        g[e] = __fmul_rn(g[e], clip);
-        m[e] = __fmaf_rn(a.mu, m[e], g[e]);
-        const float u = a.nesterov ? __fmaf_rn(a.mu, m[e], g[e]) : m[e];
+        const float gc = __fmul_rn(g[j][e], clip);
+        m[j][e] = __fmaf_rn(a.mu, m[j][e], gc);
+        const float u = a.nesterov ? __fmaf_rn(a.mu, m[j][e], gc) : m[j][e];
         sq = __fmaf_rn(u, u, sq);
       }
       sum = __fadd_rn(sum, sq);
       if (vec_m && i + 4 <= end) {
-        *reinterpret_cast<float4*>(mat.m + i) = make_float4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<float4*>(mat.m + i) = make_float4(m[j][0], m[j][1], m[j][2], m[j][3]);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (i + e < end) mat.m[i + e] = m[e];
+          if (i + e < end) mat.m[i + e] = m[j][e];
       }
     }
-    // the block's sum, and the matrix's once its last chunk is in
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_down_sync(0xFFFFFFFFu, sum, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = (double)sum;
-    __syncthreads();
     const int64_t chunks = (n + kMuonChunk - 1) / kMuonChunk;
+    if (begun < 0) begun = c;
+    if (c + gridDim.x < mat.first_chunk + chunks) continue;
+    // this CTA's part of the matrix's sum.  A thread's is a few hundred squares in
+    // fp32, all positive: 2^-24 of it each; fp64 from there
+    double part = (double)sum;
+    sum = 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_down_sync(0xFFFFFFFFu, part, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = part;
+    __syncthreads();
+    const int64_t parts = min(chunks, (int64_t)gridDim.x);  // their places: the first chunks
     if (threadIdx.x == 0) {
-      double part = red[0];
+      part = red[0];
       for (int w = 1; w < kMEThreads / 32; ++w) part += red[w];
-      t.partials[c] = part;
+      t.partials[begun] = part;
       __threadfence();
-      last = atomicAdd(&t.arrived[id], 1u) == (unsigned)chunks - 1;
+      last = atomicAdd(&t.arrived[id], 1u) == (unsigned)parts - 1;
       __threadfence();
     }
     __syncthreads();
     if (last) {
       double all = 0.0;
-      for (int64_t k = threadIdx.x; k < chunks; k += kMEThreads)
+      for (int64_t k = threadIdx.x; k < parts; k += kMEThreads)
         all += __ldcg(&t.partials[mat.first_chunk + k]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) all += __shfl_down_sync(0xFFFFFFFFu, all, o);
@@ -165,9 +183,9 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
                                                 : __uint_as_float(0x7FFFFFFFu);
         t.arrived[id] = 0;
       }
-      __syncthreads();
     }
     __syncthreads();
+    begun = -1;
   }
 }
 
@@ -184,17 +202,23 @@ __global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, Muo
     const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
     const bool rows4 = mat.cols % 4 == 0;  // four elements lie in one row
     const float f = t.factor[id];
+    float g[kMRuns][4], m[kMRuns][4];
 #pragma unroll
-    for (int j = 0; j < (int)(kMuonChunk / (4 * kMEThreads)); ++j) {
-      const int64_t i = base + ((int64_t)j * kMEThreads + threadIdx.x) * 4;
+    for (int j = 0; j < kMRuns; ++j) {
+      const int64_t i = base + (j * kMEThreads + threadIdx.x) * 4;
+      if (i < end) {
+        get4<GS_F32>(mat.m, i, end, vec_m, m[j]);
+        if (a.nesterov) get4<DT>(mat.g, i, end, vec_g, g[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kMRuns; ++j) {
+      const int64_t i = base + (j * kMEThreads + threadIdx.x) * 4;
       if (i >= end) continue;
-      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m[4];
-      get4<GS_F32>(mat.m, i, end, vec_m, m);
-      if (a.nesterov) get4<DT>(mat.g, i, end, vec_g, g);
       uint16_t h[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float u = a.nesterov ? __fmaf_rn(a.mu, m[e], __fmul_rn(g[e], clip)) : m[e];
+        const float u = a.nesterov ? __fmaf_rn(a.mu, m[j][e], __fmul_rn(g[j][e], clip)) : m[j][e];
         h[e] = Elem<GS_F16>::put(__fmul_rn(u, f));
       }
       unsigned row = (unsigned)i / (unsigned)mat.cols, col = (unsigned)i - row * (unsigned)mat.cols;
@@ -714,8 +738,9 @@ static cudaError_t launch_products(const MuonTable& t, const MuonArgs& a, cudaSt
 
 template <int DT>
 static cudaError_t muon_dt(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
+  const unsigned wave = (unsigned)std::min<int64_t>(t.chunks, (int64_t)sm_count() * 4);
+  muon_momentum_kernel<DT><<<wave, kMEThreads, 0, st>>>(t, a);
   const unsigned grid = (unsigned)std::min<int64_t>(t.chunks, (int64_t)sm_count() * 32);
-  muon_momentum_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
   muon_scale_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? launch_products(t, a, st) : e;

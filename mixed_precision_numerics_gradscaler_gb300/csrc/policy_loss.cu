@@ -45,9 +45,9 @@ constexpr int kPTile = kPThreads * kPRun;    // tokens per CTA and step
 constexpr int kPSpan = 1024;                 // sequences of a step kept in shared memory
 
 // Tokens that one CTA does alone (see launch_policy_loss).
-constexpr int64_t kPSmallTokens = 4608;
-constexpr int64_t kPSmallSeqs = 2048;
-constexpr int kPSmallThreads = 512;
+constexpr int64_t kPSmallTokens = 5120;
+constexpr int64_t kPSmallSeqs = 2048;  // times kPSmallTokens: below 2^24
+constexpr int kPSmallThreads = 1024;
 
 // A sum in fp32 with its rounding errors carried along (the fp64 pipe would
 // take as long as everything else here).
@@ -126,16 +126,45 @@ __device__ __forceinline__ bool below(float d, float e, const Border& b) {
   return d < b.hi || (d == b.hi && e < b.lo);
 }
 
+// e^y - 1, and e^y - 1 - y: y^2 (1/2 + y/6 + ... + y^7/9!), cut off at 2e-9 of
+// it, for |y| <= 1/2; beyond, e^y - 1 keeps its digits but for two bits.
+__device__ __forceinline__ void exp_less(float y, float& em1, float& em1y) {
+  float p = 1.0f / 362880.0f;
+  p = __fmaf_rn(p, y, 1.0f / 40320.0f);
+  p = __fmaf_rn(p, y, 1.0f / 5040.0f);
+  p = __fmaf_rn(p, y, 1.0f / 720.0f);
+  p = __fmaf_rn(p, y, 1.0f / 120.0f);
+  p = __fmaf_rn(p, y, 1.0f / 24.0f);
+  p = __fmaf_rn(p, y, 1.0f / 6.0f);
+  p = __fmaf_rn(p, y, 0.5f);
+  p = __fmul_rn(__fmul_rn(y, y), p);
+  const bool near = fabsf(y) <= 0.5f;
+  const float far_em1 = __fsub_rn(expf(y), 1.0f);
+  em1 = near ? __fadd_rn(y, p) : far_em1;
+  em1y = near ? p : __fsub_rn(far_em1, y);
+}
+
 struct Token {
   float value, slope, ratio, kl;  // l and dl/dx without the weight
+  float rest;                     // EXACT: l is value + rest
   bool held;
 };
-template <bool REF>
+// EXACT: the objective as a sum of two fp32 numbers, A and A (rho - 1) or the
+// parts of a product: advantages that cancel over a batch leave a loss far smaller
+// than its terms.
+template <bool REF, bool EXACT>
 __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, float ref, float adv) {
   Token t;
   float d, e;
   two_diff(x, old, d, e);
-  t.ratio = expf(d);
+  float em1 = 0.0f, unused;
+  if constexpr (EXACT) {
+    exp_less(d, em1, unused);
+    t.ratio = fabsf(d) <= 0.5f ? __fadd_rn(1.0f, em1) : expf(d);
+    if (fabsf(d) <= 0.5f) em1 = __fmaf_rn(e, t.ratio, em1);  // (e is a number there)
+  } else {
+    t.ratio = expf(d);
+  }
   const bool gains = adv > 0.0f, loses = adv < 0.0f;
   const Border top = gains ? a.high : a.dual;
   const bool over = (gains || loses) && above(d, e, top);
@@ -146,25 +175,22 @@ __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, 
   t.slope = t.held ? 0.0f : -obj;
   t.kl = 0.0f;
   t.value = -obj;
+  t.rest = 0.0f;
+  if constexpr (EXACT) {
+    if (t.held) {
+      t.rest = __fmaf_rn(-factor, adv, obj);
+    } else if (fabsf(d) <= 0.5f && adv != 0.0f) {
+      t.value = -adv;
+      t.rest = -__fmul_rn(adv, em1);
+    }
+  }
   if constexpr (REF) {
     const float y = __fsub_rn(ref, x);
-    // y^2 (1/2 + y/6 + ... + y^7/9!): cut off at 2e-9 of it for |y| <= 1/2;
-    // beyond, e^y - 1 keeps its digits but for two bits
-    float p = 1.0f / 362880.0f;
-    p = __fmaf_rn(p, y, 1.0f / 40320.0f);
-    p = __fmaf_rn(p, y, 1.0f / 5040.0f);
-    p = __fmaf_rn(p, y, 1.0f / 720.0f);
-    p = __fmaf_rn(p, y, 1.0f / 120.0f);
-    p = __fmaf_rn(p, y, 1.0f / 24.0f);
-    p = __fmaf_rn(p, y, 1.0f / 6.0f);
-    p = __fmaf_rn(p, y, 0.5f);
-    p = __fmul_rn(__fmul_rn(y, y), p);
-    const bool near = fabsf(y) <= 0.5f;
-    const float far_em1 = __fsub_rn(expf(y), 1.0f);
-    const float em1 = near ? __fadd_rn(y, p) : far_em1;
-    t.kl = near ? p : __fsub_rn(far_em1, y);
-    t.value = __fmaf_rn(a.kl, t.kl, t.value);
-    t.slope = __fmaf_rn(-a.kl, em1, t.slope);
+    float em1y;
+    exp_less(y, em1y, t.kl);
+    if constexpr (EXACT) t.rest = __fmaf_rn(a.kl, t.kl, t.rest);
+    else t.value = __fmaf_rn(a.kl, t.kl, t.value);
+    t.slope = __fmaf_rn(-a.kl, em1y, t.slope);
   }
   return t;
 }
@@ -401,7 +427,7 @@ __global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a)
     unsigned held = 0;
 #pragma unroll
     for (int j = 0; j < kPRun; ++j) {
-      const Token tk = token<REF>(a, x[j], old[j], ref[j], adv[j]);
+      const Token tk = token<REF, false>(a, x[j], old[j], ref[j], adv[j]);
       const bool in = live >> j & 1;
       loss = __fadd_rn(loss, in ? (FIND ? __fmul_rn(tk.value, w[j]) : tk.value) : 0.0f);
       ratio = __fadd_rn(ratio, in ? tk.ratio : 0.0f);
@@ -514,24 +540,34 @@ __global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(Polic
     __syncthreads();
   }
   const unsigned n = totals[0];
-  // whole numbers below 2^24: their product's reciprocal rounds twice
+  // a sequence's weight as the sum of two fp32 numbers, from the rounding error
+  // of its quotient (sequences times tokens is below 2^24, so exact)
   const float seqs = (float)totals[1];
-  const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN ? (n ? __fdiv_rn(1.0f, (float)n) : 0.0f) : 1.0f;
-  float loss = 0.0f, ratio = 0.0f, kl = 0.0f;
+  const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN && n ? __fdiv_rn(1.0f, (float)n) : 1.0f;
+  Pair loss = {0.0f, 0.0f}, ratio = loss, kl = loss;
   unsigned held = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int t = j * kPSmallThreads + tid;
-    const float w = by_seq && in[j] ? __fdiv_rn(1.0f, __fmul_rn(seqs, (float)counts[seq[j]])) : w_token;
-    const Token tk = token<REF>(a, x[j], old[j], ref[j], adv[j]);
-    loss = __fadd_rn(loss, in[j] ? (by_seq ? __fmul_rn(tk.value, w) : tk.value) : 0.0f);
-    ratio = __fadd_rn(ratio, in[j] ? tk.ratio : 0.0f);
-    kl = __fadd_rn(kl, in[j] ? tk.kl : 0.0f);
-    held += in[j] && tk.held;
+    float w = 1.0f, w_lo = 0.0f;  // (of the token mean: the sum's, in fp64)
+    if (by_seq && in[j]) {
+      const float count = __fmul_rn(seqs, (float)counts[seq[j]]);
+      w = __fdiv_rn(1.0f, count);
+      w_lo = __fmul_rn(__fmaf_rn(-w, count, 1.0f), w);
+    }
+    const Token tk = token<REF, true>(a, x[j], old[j], ref[j], adv[j]);
+    if (in[j]) {
+      const float part = __fmul_rn(w, tk.value);
+      loss.add(part);
+      loss.lo = __fadd_rn(loss.lo, __fmaf_rn(w, tk.rest, __fmaf_rn(w_lo, tk.value, __fmaf_rn(w, tk.value, -part))));
+      ratio.add(tk.ratio);
+      kl.add(tk.kl);
+      held += tk.held;
+    }
     if (a.grad && t >= lo && t < hi)
-      a.grad[t] = in[j] ? __fmul_rn(__fmul_rn(up, w), tk.slope) : 0.0f;
+      a.grad[t] = in[j] ? __fmul_rn(__fmul_rn(up, by_seq ? w : w_token), tk.slope) : 0.0f;
   }
-  const Sums s = block_sums<kPSmallThreads>(Pair{loss, 0.0f}, Pair{ratio, 0.0f}, Pair{kl, 0.0f}, held);
+  const Sums s = block_sums<kPSmallThreads>(loss, ratio, kl, held);
   if (tid == 0) finish(a, s, n);
 }
 
@@ -548,7 +584,7 @@ static void launch_large(const PolicyArgs& a, unsigned grid, bool find, cudaStre
 
 cudaError_t launch_policy_loss(PolicyArgs a, cudaStream_t st) {
   if (a.T <= kPSmallTokens && a.S <= kPSmallSeqs) {
-    if (a.T <= 2 * kPSmallThreads) launch_small<2>(a, st);
+    if (a.T <= kPSmallThreads) launch_small<1>(a, st);
     else launch_small<(int)(kPSmallTokens / kPSmallThreads)>(a, st);
     return cudaGetLastError();
   }
