@@ -40,7 +40,6 @@ namespace gs {
 constexpr int kQThreads = 384;      // warps 0-3: loads, MMA, two idle; 4-11 store
 constexpr int kQRow = 128;          // bytes of a row of a stage: 256 elements
 constexpr int kQK = 256;
-constexpr int kQSlots = 3;          // a sum is split in four at most
 
 // One configuration's sizes.
 // SLOTS: sums of other CTAs of a cluster that the leading one takes in.
@@ -57,7 +56,7 @@ struct Q4 {
   // store staging of 8 warps, or the other CTAs' sums
   static constexpr int kOut = SLOTS ? SLOTS * kSlot : 8 * 32 * 128;
   static constexpr int kMost = (232448 - 1024 - 512 - kOut) / kStage;
-  static constexpr int kStages = kMost > 6 ? 6 : kMost;
+  static constexpr int kStages = kMost > 8 ? 8 : kMost;
   static constexpr int kAccs = BN <= 128 ? 2 : 1;
   static constexpr int kSfCol = kAccs * BN;                // columns of the scales
   static constexpr int kSbCol = kSfCol + 4 * kTiles;
@@ -114,15 +113,16 @@ __device__ __forceinline__ void cp_scales(uint32_t tmem, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-// Sums of a tile split along K (TRANS): cluster CTA r takes its part of the
-// stages, CTAs 1 .. split - 1 write their fp32 sums to the leading CTA's shared
-// memory, which adds them in their order.
-template <int CG, int BN, int FMT, int OUT, bool TRANS, bool TMA_STORE>
+// TRANS: 0, or the operands have changed places and TRANS + 1 CTAs of a cluster at
+// most share a tile's sum, split along K: CTA r takes its part of the stages, CTAs
+// 1 .. split - 1 write their fp32 sums to the leading CTA's shared memory, which
+// adds them in their order.
+template <int CG, int BN, int FMT, int OUT, int TRANS, bool TMA_STORE>
 __global__ void __launch_bounds__(kQThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                     const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
                     const __grid_constant__ CUtensorMap map_d, Gemm4Args a) {
-  using S = Q4<CG, BN, FMT, TRANS ? kQSlots : 0>;
+  using S = Q4<CG, BN, FMT, TRANS>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;  // the same offset in both CTAs of a pair
@@ -430,9 +430,9 @@ struct Operand {
   int64_t rows;
 };
 
-template <int CG, int BN, int FMT, int OUT, bool TRANS, bool TMA_STORE>
+template <int CG, int BN, int FMT, int OUT, int TRANS, bool TMA_STORE>
 static cudaError_t gemm4_run(const Operand& x, const Operand& y, Gemm4Args a, cudaStream_t st) {
-  using S = Q4<CG, BN, FMT, TRANS ? kQSlots : 0>;
+  using S = Q4<CG, BN, FMT, TRANS>;
   auto k = gemm_fp4_kernel<CG, BN, FMT, OUT, TRANS, TMA_STORE>;
   int occ = 0;  // also raises the shared-memory limit in this context
   cudaError_t e = kernel_blocks_per_sm((const void*)k, kQThreads, S::kSmem, &occ);
@@ -490,13 +490,15 @@ static cudaError_t gemm4_pick(const Operand& x, const Operand& y, Gemm4Args a, b
       const int64_t cost = div_up(tiles, sm_count() / s) * (div_up(kb, s) + 2);
       if (cost < best) best = cost, a.split = s;
     }
-    return gemm4_run<1, 32, FMT, OUT, true, false>(y, x, a, st);
+    // (room for fewer sums is room for more stages)
+    return a.split <= 2 ? gemm4_run<1, 32, FMT, OUT, 1, false>(y, x, a, st)
+                        : gemm4_run<1, 32, FMT, OUT, 3, false>(y, x, a, st);
   }
   if (rounds(a.M, a.N, a.K, 128, 128, 1, 0.6, 3.0) < rounds(a.M, a.N, a.K, 256, 256, 2, 1.0, 5.0))
-    return tma ? gemm4_run<1, 128, FMT, OUT, false, true>(x, y, a, st)
-               : gemm4_run<1, 128, FMT, OUT, false, false>(x, y, a, st);
-  return tma ? gemm4_run<2, 256, FMT, OUT, false, true>(x, y, a, st)
-             : gemm4_run<2, 256, FMT, OUT, false, false>(x, y, a, st);
+    return tma ? gemm4_run<1, 128, FMT, OUT, 0, true>(x, y, a, st)
+               : gemm4_run<1, 128, FMT, OUT, 0, false>(x, y, a, st);
+  return tma ? gemm4_run<2, 256, FMT, OUT, 0, true>(x, y, a, st)
+             : gemm4_run<2, 256, FMT, OUT, 0, false>(x, y, a, st);
 }
 
 cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* ta, const uint8_t* qb,

@@ -107,12 +107,20 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
   const float clip = clip_of(a);
   float sum = 0.0f;
   int64_t begun = -1;  // this CTA's first chunk of the matrix
+  int64_t chunks = 0;
+  int id = 0;
+  MuonMat mat = {};    // (a copy: what is stored could be the table, to the compiler)
+  bool vec_m = false, vec_g = false;
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
-    const MuonMat& mat = t.mats[id];
+    if (c >= mat.first_chunk + chunks) {
+      id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
+      mat = t.mats[id];
+      chunks = ((int64_t)mat.rows * mat.cols + kMuonChunk - 1) / kMuonChunk;
+      vec_m = (uintptr_t)mat.m % 16 == 0;
+      vec_g = (uintptr_t)mat.g % 16 == 0;
+    }
     const int64_t n = (int64_t)mat.rows * mat.cols, base = (c - mat.first_chunk) * kMuonChunk;
     const int64_t end = min(n, base + kMuonChunk);
-    const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
     if (base == 0 && threadIdx.x == 0) t.done[id] = 0;  // for the products' launch
     // everything is loaded before anything is stored: the loads do not wait for
     // one another
@@ -146,7 +154,6 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
           if (i + e < end) mat.m[i + e] = m[j][e];
       }
     }
-    const int64_t chunks = (n + kMuonChunk - 1) / kMuonChunk;
     if (begun < 0) begun = c;
     if (c + gridDim.x < mat.first_chunk + chunks) continue;
     // this CTA's part of the matrix's sum.  A thread's is a few hundred squares in
@@ -194,14 +201,22 @@ template <int DT>
 __global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, MuonArgs a) {
   if (*a.found_inf) return;
   const float clip = clip_of(a);
+  int64_t chunks = 0;
+  MuonMat mat = {};
+  bool vec_m = false, vec_g = false;
+  float f = 0.0f;
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
-    const MuonMat& mat = t.mats[id];
+    if (c >= mat.first_chunk + chunks) {
+      const int id = mat_of(t.mats, t.n, c, &MuonMat::first_chunk);
+      mat = t.mats[id];
+      chunks = ((int64_t)mat.rows * mat.cols + kMuonChunk - 1) / kMuonChunk;
+      vec_m = (uintptr_t)mat.m % 16 == 0;
+      vec_g = (uintptr_t)mat.g % 16 == 0;
+      f = t.factor[id];
+    }
     const int64_t n = (int64_t)mat.rows * mat.cols, base = (c - mat.first_chunk) * kMuonChunk;
     const int64_t end = min(n, base + kMuonChunk);
-    const bool vec_m = (uintptr_t)mat.m % 16 == 0, vec_g = (uintptr_t)mat.g % 16 == 0;
     const bool rows4 = mat.cols % 4 == 0;  // four elements lie in one row
-    const float f = t.factor[id];
     float g[kMRuns][4], m[kMRuns][4];
 #pragma unroll
     for (int j = 0; j < kMRuns; ++j) {
