@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_elem.cuh"
 #include "gs_fp4.h"
@@ -123,8 +124,10 @@ __device__ __forceinline__ uint32_t block_scale4(float amax, const Tensor4& ts, 
     // the quotient as IEEE division rounds it wherever it is not 0 in e4m3, or
     // far beyond its range (where the residuals could overflow)
     ok = ts.ok && amax < __uint_as_float(0x7F800000u);
-    const float u = __fmul_rn(amax, ts.r6) < 1024.0f ? exact_quotient<2>(amax, ts.t6, ts.r6) : 1024.0f;
-    const uint32_t c = ok ? cvt_f32x2_fp8x2<GS_E4M3>(0.0f, u) & 0x7Fu : kFp8NaN;
+    const float q = exact_quotient<2>(amax, ts.t6, ts.r6);
+    const float u = __fmul_rn(amax, ts.r6) < 1024.0f ? q : 1024.0f;
+    const uint32_t k = cvt_f32x2_fp8x2<GS_E4M3>(0.0f, u) & 0x7Fu;
+    const uint32_t c = ok ? k : kFp8NaN;
     r = ts.table[c];
     return c;
   }
@@ -176,18 +179,19 @@ struct Run16 {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
-  // From element off of x; align: bytes every run begins at a multiple of (32,
-  // 16, or less), the same for all threads.
-  __device__ __forceinline__ void load(const void* x, int64_t off, int align) {
+  // From element off of x, ALIGN: bytes every run begins at a multiple of (32, 16,
+  // or less).
+  template <int ALIGN>
+  __device__ __forceinline__ void load(const void* x, int64_t off) {
     const typename Elem<DT>::type* p = static_cast<const typename Elem<DT>::type*>(x) + off;
-    if (align == 32) {
+    if constexpr (ALIGN == 32) {
 #pragma unroll
       for (int i = 0; i < kWords / 8; ++i) {
         const V8 a = ld_stream8(reinterpret_cast<const uint32_t*>(p) + 8 * i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[8 * i + e] = a.w[e];
       }
-    } else if (align == 16) {
+    } else if constexpr (ALIGN == 16) {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
         const uint4 a = ld_stream(reinterpret_cast<const uint4*>(p) + i);
@@ -200,6 +204,12 @@ struct Run16 {
         else w[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
       }
     }
+  }
+  // The same with the alignment as a number, the same for all threads.
+  __device__ __forceinline__ void load(const void* x, int64_t off, int align) {
+    if (align == 32) load<32>(x, off);
+    else if (align == 16) load<16>(x, off);
+    else load<1>(x, off);
   }
   // Takes the elements into a running maximum of magnitudes (start: 0), in the
   // elements' own type and, of 16 bits, by halves; see mag_of.
@@ -224,7 +234,7 @@ struct Run16 {
           v[i] = pair(__uint_as_float(w[8 * g + 2 * i]), __uint_as_float(w[8 * g + 2 * i + 1]));
         else v[i] = pair(Half<DT>::lo(w[4 * g + i]), Half<DT>::hi(w[4 * g + i]));
       }
-      c[g] = ok ? codes8(v, pair(r, r)) : 0u;
+      c[g] = codes8(v, pair(r, r)) & (ok ? 0xFFFFFFFFu : 0u);
     }
     return make_uint2(c[0], c[1]);
   }
@@ -238,18 +248,18 @@ constexpr int kFScales = kFTile / kFBlk<FMT>;
 template <int FMT>
 constexpr int kFScaleBytes = kFTile * kFScales<FMT>;
 
-// Copies a tile's staged scale tiles to the matrix's; k_tiles: scale tiles per row tile.
+// Copies a tile's staged scale tiles to the matrix's, where they lie together;
+// k_tiles: scale tiles per row tile.
 template <int FMT>
 __device__ __forceinline__ void put_scales(const uint8_t* sc, uint8_t* scales, int64_t row_tile,
                                            int64_t col_tile, int64_t k_tiles) {
   constexpr int kPer = kFScales<FMT> / 4;  // scale tiles side by side
-#pragma unroll
-  for (int i = threadIdx.x; i < kFScaleBytes<FMT> / 4; i += kFThreads) {
-    const int64_t kt = col_tile * kPer + i / 128;
-    if (kt < k_tiles)
-      reinterpret_cast<uint32_t*>(scales)[(row_tile * k_tiles + kt) * 128 + i % 128] =
-          reinterpret_cast<const uint32_t*>(sc)[i];
-  }
+  static_assert(kPer * 32 <= kFThreads, "16 bytes a thread");
+  const int64_t kt = col_tile * kPer;
+  const int n = 32 * (int)min((int64_t)kPer, k_tiles - kt);
+  if ((int)threadIdx.x < n)
+    reinterpret_cast<uint4*>(scales + (row_tile * k_tiles + kt) * 512)[threadIdx.x] =
+        reinterpret_cast<const uint4*>(sc)[threadIdx.x];
 }
 
 struct Quant4Args {
@@ -340,8 +350,8 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
 
   for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
     // last tile first: what L2 holds of a pass over x before is read from there
-    const int64_t at = n_tiles - 1 - i;
-    const int64_t tr = at / a.tiles_c, tc = at % a.tiles_c;
+    const unsigned at = (unsigned)(n_tiles - 1 - i), across = (unsigned)a.tiles_c;
+    const int64_t tr = at / across, tc = at % across;
     const int64_t r0 = tr * kFTile, c0 = tc * kFTile;
     // rows tid / 8 + 32 j: eight lanes to a row, a run of 16 each
     const int blk = tid & 7, row0 = tid >> 3 & 31;
@@ -349,11 +359,16 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
     const int64_t first = (r0 + row0) * a.ldx + c0 + blk * kFBlock;
     uint8_t* const to = ROW ? a.q + (r0 + row0) * (a.C / 2) + (c0 + blk * kFBlock) / 2 : nullptr;
     Run16<DT> v[kRuns];
+    const auto load = [&](auto align) {
 #pragma unroll
-    for (int j = 0; j < kRuns; ++j) {
-      v[j].zero();
-      if (row0 + 32 * j < rows) v[j].load(a.x, first + 32 * j * a.ldx, a.align);
-    }
+      for (int j = 0; j < kRuns; ++j) {
+        v[j].zero();
+        if (row0 + 32 * j < rows) v[j].template load<decltype(align)::value>(a.x, first + 32 * j * a.ldx);
+      }
+    };
+    if (a.align == 32) load(std::integral_constant<int, 32>());
+    else if (a.align == 16) load(std::integral_constant<int, 16>());
+    else load(std::integral_constant<int, 1>());
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
       const int row = 32 * j + row0;
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
               else p[e] = side ? pair(Half<DT>::hi(x0), Half<DT>::hi(x1))
                                : pair(Half<DT>::lo(x0), Half<DT>::lo(x1));
             }
-            c[g] = ok ? codes8(p, pair(r, r)) : 0u;
+            c[g] = codes8(p, pair(r, r)) & (ok ? 0xFFFFFFFFu : 0u);
           }
 #pragma unroll
           for (int g = 0; g < kBlk / 8; g += 2)
