@@ -24,8 +24,9 @@
 // ways.  A thread takes runs of 16 of a row in registers; for the transpose the
 // tile goes through shared memory, a thread taking a block's rows of two columns
 // (of one for fp32), and the codes go through it again so that a column's 64 bytes
-// are stored together.  Both directions read x once; the tensor's scale needs a
-// pass over x before, and the second pass runs from the last tile to the first, so
+// are stored together; the next tile is loaded meanwhile (16384 x 8192 bf16 both
+// ways: 137 us without, 129 with it and three CTAs per SM).  Both directions read x
+// once; the tensor's scale needs a pass over x before, and the second pass runs from the last tile to the first, so
 // that what L2 still holds of the first pass is read from there.  Small tensors
 // are one cluster's, which reads its own part twice.
 #include <cuda_runtime.h>
@@ -295,7 +296,7 @@ __device__ __forceinline__ float scale_of_amax(uint32_t m) {
 // ROW, COL: the directions wanted.  ONE: a single cluster forms the tensor scale
 // too.
 template <int DT, int FMT, bool ROW, bool COL, bool ONE>
-__global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
+__global__ void __launch_bounds__(kFThreads, DT == GS_F32 ? 2 : COL ? 3 : 5) quant4_kernel(Quant4Args a) {
   constexpr int kBlk = kFBlk<FMT>;
   constexpr int kRuns = kFTile * 8 / kFThreads;  // per thread and tile
   static_assert(kFThreads == 256 && kRuns == 4, "a thread's runs are 32 rows apart");
@@ -348,27 +349,45 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
     ts = tensor4(t, table);
   }
 
-  for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-    // last tile first: what L2 holds of a pass over x before is read from there
+  // Tile i, last tile first: what L2 holds of a pass over x before is read from
+  // there.
+  const auto place = [&](int64_t i, int64_t& tr, int64_t& tc) {
     const unsigned at = (unsigned)(n_tiles - 1 - i), across = (unsigned)a.tiles_c;
-    const int64_t tr = at / across, tc = at % across;
-    const int64_t r0 = tr * kFTile, c0 = tc * kFTile;
-    // rows tid / 8 + 32 j: eight lanes to a row, a run of 16 each
-    const int blk = tid & 7, row0 = tid >> 3 & 31;
-    const int rows = c0 + blk * kFBlock < a.C ? (int)min((int64_t)kFTile, a.R - r0) : 0;
-    const int64_t first = (r0 + row0) * a.ldx + c0 + blk * kFBlock;
-    uint8_t* const to = ROW ? a.q + (r0 + row0) * (a.C / 2) + (c0 + blk * kFBlock) / 2 : nullptr;
-    Run16<DT> v[kRuns];
-    const auto load = [&](auto align) {
+    tr = at / across;
+    tc = at % across;
+  };
+  // rows tid / 8 + 32 j: eight lanes to a row, a run of 16 each
+  const int blk = tid & 7, row0 = tid >> 3 & 31;
+  Run16<DT> v[kRuns];
+  const auto load = [&](int64_t tr, int64_t tc) {
+    const int64_t c = tc * kFTile + blk * kFBlock, r = tr * kFTile;
+    const int rows = c < a.C ? (int)min((int64_t)kFTile, a.R - r) : 0;
+    const int64_t first = (r + row0) * a.ldx + c;
+    const auto all = [&](auto align) {
 #pragma unroll
       for (int j = 0; j < kRuns; ++j) {
         v[j].zero();
         if (row0 + 32 * j < rows) v[j].template load<decltype(align)::value>(a.x, first + 32 * j * a.ldx);
       }
     };
-    if (a.align == 32) load(std::integral_constant<int, 32>());
-    else if (a.align == 16) load(std::integral_constant<int, 16>());
-    else load(std::integral_constant<int, 1>());
+    if (a.align == 32) all(std::integral_constant<int, 32>());
+    else if (a.align == 16) all(std::integral_constant<int, 16>());
+    else all(std::integral_constant<int, 1>());
+  };
+  int64_t tr, tc, tr_n = 0, tc_n = 0;
+  if (blockIdx.x < n_tiles) place(blockIdx.x, tr_n, tc_n);
+  if constexpr (COL) {
+    if (blockIdx.x < n_tiles) load(tr_n, tc_n);
+  }
+  for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+    tr = tr_n;
+    tc = tc_n;
+    const bool more = i + gridDim.x < n_tiles;
+    if (more) place(i + gridDim.x, tr_n, tc_n);
+    if constexpr (!COL) load(tr, tc);
+    const int64_t r0 = tr * kFTile, c0 = tc * kFTile;
+    const int rows = c0 + blk * kFBlock < a.C ? (int)min((int64_t)kFTile, a.R - r0) : 0;
+    uint8_t* const to = ROW ? a.q + (r0 + row0) * (a.C / 2) + (c0 + blk * kFBlock) / 2 : nullptr;
 #pragma unroll
     for (int j = 0; j < kRuns; ++j) {
       const int row = 32 * j + row0;
@@ -392,6 +411,7 @@ __global__ void __launch_bounds__(kFThreads) quant4_kernel(Quant4Args a) {
       }
     }
     if constexpr (COL) {
+      if (more) load(tr_n, tc_n);  // while this tile's columns are taken
       __syncthreads();
       // a word's columns (two of 16 bits, one of 32), the rows of a block
       constexpr int kSide = DT == GS_F32 ? kFTile : kFTile / 2;
@@ -513,7 +533,8 @@ static cudaError_t quant4_t(const Quant4Args& a, cudaStream_t st) {
     at.val.clusterDim.x = ctas;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
   } else {
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, (int64_t)sm_count() * 64));
+    // tiles loaded ahead: one wave; else several, which even out the SMs' progress
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(tiles, (int64_t)sm_count() * (COL ? occ : 64)));
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
   }
