@@ -1,7 +1,8 @@
 /*
  * gsfp8.h -- C ABI of the GB300 (sm_103a) mixed-precision cast-and-scale
- * library: dynamic loss scaling of FP16 gradient lists and FP8
- * quantisation with fine-grained (1x128 / 128x128 / per-tensor) scaling.
+ * library: dynamic loss scaling of FP16 gradient lists, FP8 quantisation with
+ * fine-grained (1x128 / 128x128 / per-tensor) scaling, 4-bit tensors, and the
+ * operators of training steps around them.
  *
  * Sources of the definitions (web pages, cited by title and section):
  *   [P1] "Loss scaling, FP8, and the failure that never crashes"
