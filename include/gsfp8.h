@@ -568,8 +568,8 @@ int fp4_dequant(const uint8_t* q, const uint8_t* scales, const float* tensor_sca
  * that depends on the sizes and the device alone: |error| <= 2^-23 (K / 16 +
  * 8) sum of |terms| before the output's rounding (an addition's error for each
  * 16 products, however the tensor cores round it).
- * K % 32 == 0, M, N, K < 2^31 and fewer than 2^30 tiles of 128 x 128 (else
- * GS_ERR_SHAPE); any M and N; K == 0 writes zeros.  Codes and scales 16-byte
+ * K % 32 == 0, K <= 2^24, M, N < 2^31 and fewer than 2^30 tiles of 128 x 128
+ * (else GS_ERR_SHAPE); any M and N; K == 0 writes zeros.  Codes and scales 16-byte
  * aligned.  A wait that runs out records GS_ERR_TIMEOUT (gs_device_status) and
  * leaves d unspecified. */
 int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta, const uint8_t* qb,
@@ -633,7 +633,8 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
  * (master_bf16 or an entry of it may be NULL), gradients of grad_dtype (any of
  * the three) and momentum[i] fp32, each contiguous, element-aligned, of the
  * current device; nothing that is written may overlap anything else.  Fewer
- * than 2^31 elements per matrix; empty ones are left out.  Allocates the list's
+ * than 2^31 elements per matrix, sides of up to 2^18 (fp32 sums of more would
+ * be further off than the operands' roundings); empty ones are left out.  Allocates the list's
  * workspace: 4 bytes per element (rows counted up to a multiple of 8 elements) and
  * 4 per element of a square of the smaller side. */
 typedef struct gs_muon_list gs_muon_list;

@@ -30,6 +30,13 @@ static int cuda_fail(cudaError_t e) {
   return GS_ERR_CUDA;
 }
 
+// The tensor cores add 16 products at a time to an fp32 sum and cut off what it
+// does not hold: a sum of n positive products ends up to n / 16 2^-24 below
+// itself, half of that in the mean.  The momentum's sides are held to where that
+// is two of fp16's roundings (2^24 elements gave a polynomial 8 % off); the 4-bit
+// product's to where the bound it states still says something.
+constexpr int64_t kMostSum = 1LL << 24, kMostSide = 1LL << 18;
+
 static bool valid_fmt4(int f) { return f == GS_MXFP4 || f == GS_NVFP4; }
 
 // Reachable or absent.
@@ -126,7 +133,7 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
                           int fmt, int out_dtype, void* d, int64_t ldd, void* stream) {
   if (!valid_fmt4(fmt) || !(out_dtype == GS_F32 || out_dtype == GS_BF16)) return GS_ERR_DTYPE;
   const size_t esz = dtype_size(out_dtype);
-  if (M < 0 || N < 0 || K < 0 || K % 32 || M >= (1LL << 31) || N >= (1LL << 31) || K >= (1LL << 31) ||
+  if (M < 0 || N < 0 || K < 0 || K % 32 || M >= (1LL << 31) || N >= (1LL << 31) || K > kMostSum ||
       ldd >= (1LL << 36) || !rows_ok(M, N, ldd, esz) || !mul_ok(M, K) || !mul_ok(N, K))
     return GS_ERR_SHAPE;
   if (div_up(M, 128) * div_up(N, 128) >= (1LL << 30)) return GS_ERR_SHAPE;
@@ -245,8 +252,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
   try {
     for (int32_t i = 0; i < n; ++i) {
       const int64_t R = rows[i], C = cols[i];
-      if (R < 0 || C < 0 || !mul_ok(R, C) || R * C >= (1LL << 31) || R >= (1LL << 31) || C >= (1LL << 31))
-        return GS_ERR_SHAPE;
+      if (R < 0 || C < 0 || R > kMostSide || C > kMostSide || R * C >= (1LL << 31)) return GS_ERR_SHAPE;
       if (R == 0 || C == 0) continue;
       uint16_t* wb = master_bf16 ? master_bf16[i] : nullptr;
       if (!master[i] || !grads[i] || !momentum[i]) return GS_ERR_NULL;

@@ -42,7 +42,7 @@ def test_fp4_dequant_and_product_arguments(gs):
         gs._lib.fp4_gemm_block_scaled(qa, sa, ta, qb, sb, tb, M, N, K, fmt, ot, d, ld, None)  # noqa: E731
     assert f(ot=0) == f(fmt=2) == gs.GS_ERR_DTYPE
     assert f(K=48) == f(M=-1) == f(ld=7) == f(M=1 << 31) == f(K=1 << 31) == f(N=1 << 31, ld=1 << 31) == gs.GS_ERR_SHAPE
-    assert f(M=1 << 23, N=1 << 23, ld=1 << 23) == gs.GS_ERR_SHAPE
+    assert f(M=1 << 23, N=1 << 23, ld=1 << 23) == f(K=(1 << 24) + 32) == gs.GS_ERR_SHAPE
     assert f(M=0) == f(N=0, ld=0) == gs.GS_OK
     assert f(qa=None) == f(sb=None) == f(d=None) == f(fmt=1, ta=P) == f(fmt=1, tb=P) == gs.GS_ERR_NULL
     assert f(ta=P) == f(tb=P) == f(qa=ODD) == f(sb=ODD) == gs.GS_ERR_ARG
@@ -108,6 +108,7 @@ def test_muon_arguments(gs):
     assert f(w=none) == f(g=none) == f(m=none) == gs.GS_ERR_NULL
     assert f(gt=4) == gs.GS_ERR_DTYPE
     assert f(n=-1) == f(r=dims(-1)) == f(r=dims(1 << 20), c=dims(1 << 11)) == f(r=dims(1 << 40)) == gs.GS_ERR_SHAPE
+    assert f(r=dims((1 << 18) + 1), c=dims(1)) == f(r=dims(1), c=dims((1 << 18) + 1)) == gs.GS_ERR_SHAPE
     assert f(w=odd) == f(m=odd) == f(g=odd) == gs.GS_ERR_ARG
     assert gs._lib.gs_muon_list_destroy(None) == gs.GS_OK
     g = lambda li=P, lr=1e-3, mu=0.9, wd=0.0, st=5, sc=0, mx=0.0, nrm=None, fi=P: gs._lib.gs_master_update_muon(  # noqa: E731
