@@ -285,24 +285,52 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     std::stable_sort(mats.begin(), mats.end(), [](const MuonMat& x, const MuonMat& y) {
       return std::max(x.rows, x.cols) > std::max(y.rows, y.cols);
     });
-    int64_t sym = 0, app = 0;
+    // tiles of 256 x 256, or of 256 x 128 where so few leave pairs of CTAs without
+    // any: rounds of tiles times a tile's stages or its store, whichever is longer,
+    // and a last store, in units of a stage of the wide ones (a narrow one takes
+    // 0.62, for its loads).  Measured, wide and narrow: one matrix of 4096 x 2048
+    // 694 and 493 us, twelve of 256 x 768 162 and 153, 32 of 512 x 512 342 and 388,
+    // two of 14336 x 4096 5720 and 6870.
+    double cost[2];
+    int64_t tiles[2][2];  // of either width: products of squares, of X
+    for (int k = 0; k < 2; ++k) {
+      const int64_t w = kMuonTile >> k, pairs = std::max(1, sm_count() / 2);
+      double sums[3] = {0, 0, 0};  // stages of G, P and X over all tiles
+      tiles[k][0] = tiles[k][1] = 0;
+      for (const MuonMat& m : mats) {
+        const int64_t ts = div_up(m.s, kMuonTile), syms = (ts * (ts + 1) / 2) << k;
+        const int64_t apps = div_up(m.rows, kMuonTile) * div_up(m.cols, w);
+        tiles[k][0] += syms;
+        tiles[k][1] += apps;
+        sums[0] += (double)syms * (double)div_up(std::max(m.rows, m.cols), 64);
+        sums[1] += (double)syms * (double)div_up(m.s, 64);
+        sums[2] += (double)apps * (double)div_up(m.s, 64);
+      }
+      cost[k] = 0;
+      for (int j = 0; j < 3 && !mats.empty(); ++j) {
+        const int64_t n = tiles[k][j == 2];
+        const double sum = sums[j] / (double)n * (k ? 0.62 : 1.0), store = k ? 10 : 13;
+        cost[k] += (double)div_up(n, pairs) * std::max(sum, store) + store;
+      }
+    }
+    const int half = cost[1] < cost[0];
+    t.tile_n = kMuonTile >> half;
+    if (2 * tiles[half][0] + tiles[half][1] >= (1LL << 25)) return GS_ERR_SHAPE;  // of 20 steps: an int
+    int sym = 0, app = 0;
     for (MuonMat& m : mats) {
       m.first_chunk = t.chunks;
-      m.first_sym = (int)sym;
-      m.first_app = (int)app;
+      m.first_sym = sym;
+      m.first_app = app;
       t.chunks += div_up((int64_t)m.rows * m.cols, kMuonChunk);
       const int64_t ts = div_up(m.s, kMuonTile);
-      const int64_t syms = ts * (ts + 1) / 2;
-      const int64_t apps = div_up(m.rows, kMuonTile) * div_up(m.cols, kMuonTile);
-      sym += syms;
-      app += apps;
-      if (2 * sym + app >= (1LL << 25)) return GS_ERR_SHAPE;  // of 20 steps: an int
-      m.syms = (int)syms;
-      m.apps = (int)apps;
+      m.syms = (int)(ts * (ts + 1) / 2) << half;
+      m.apps = (int)(div_up(m.rows, kMuonTile) * div_up(m.cols, t.tile_n));
+      sym += m.syms;
+      app += m.apps;
     }
     t.n = (int)mats.size();
-    t.sym_tiles = (int)sym;
-    t.app_tiles = (int)app;
+    t.sym_tiles = sym;
+    t.app_tiles = app;
     at_mats = take(mats.size() * sizeof(MuonMat));
     at_maps = take(mats.size() * 8 * sizeof(CUtensorMap));
     at_partials = take((size_t)t.chunks * sizeof(double));

@@ -8,7 +8,7 @@
 
 namespace gs {
 
-constexpr int kMuonTile = 256;               // rows and columns of a product's tile
+constexpr int kMuonTile = 256;               // rows of a product's tile; its columns are these or half
 constexpr int64_t kMuonChunk = 4096;         // elements of an element-wise step's CTA
 
 // One matrix [rows, cols]; s = min, l = max of the two.  The products' operands
@@ -38,6 +38,7 @@ struct MuonTable {
   int n;
   int64_t chunks;
   int sym_tiles, app_tiles;
+  int tile_n;                // columns of a tile
 };
 
 struct MuonArgs {

@@ -51,12 +51,18 @@ constexpr int kMThreads = 384;               // warps 0-3: loads, MMA, two idle;
 constexpr int kMEThreads = 256;              // of the element-wise steps
 constexpr int kMRuns = (int)(kMuonChunk / (4 * kMEThreads));  // of four elements, per thread
 constexpr int kMBox = 64 * 128;              // bytes of a 64 x 64 box
-constexpr int kMStage = 4 * kMBox;           // a CTA's 128 x 64 of either operand
-constexpr int kMStages = 5;
 constexpr int kMPiece = 32 * 128;            // bytes of a warp's 32 rows x 64 columns of fp16
 constexpr int kMKeys = 128;                  // matrices whose first tiles are kept in shared memory
-constexpr int kMSmem = kMStages * kMStage + 16 * kMPiece + 8 * kMKeys + 1024 + 512;
-static_assert(kMSmem <= 232448, "dynamic shared memory above the per-CTA limit");
+// Sizes for tiles of 256 x BN.
+template <int BN>
+struct Mu {
+  static constexpr int kBBoxes = BN / 128;               // a CTA's half of B's columns
+  static constexpr int kStage = (2 + kBBoxes) * kMBox;   // and 128 rows of A
+  static constexpr int kStages = BN == 256 ? 5 : 8;
+  static constexpr int kPieces = BN / 128;               // per storing warp: 64 columns each
+  static constexpr int kSmem = kStages * kStage + 8 * kPieces * kMPiece + 8 * kMKeys + 1024 + 512;
+  static_assert(kSmem <= 232448, "dynamic shared memory above the per-CTA limit");
+};
 
 // The matrix that holds item t: the last one whose first is not above t.
 template <typename T>
@@ -254,10 +260,10 @@ __global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, Muo
 // ---- products -----------------------------------------------------------------
 enum { kGram, kPoly, kApply, kLast };
 
-// Instruction descriptor: fp16 operands, fp32 sums, 256 x 256; t: the operand's
-// sum dimension runs across its rows.
-__device__ __forceinline__ uint32_t idesc16(bool ta, bool tb) {
-  return (1u << 4) | (ta ? 1u << 15 : 0u) | (tb ? 1u << 16 : 0u) | ((uint32_t)(kMuonTile >> 3) << 17) |
+// Instruction descriptor: fp16 operands, fp32 sums, 256 x n; t: the operand's sum
+// dimension runs across its rows.
+__device__ __forceinline__ uint32_t idesc16(int n, bool ta, bool tb) {
+  return (1u << 4) | (ta ? 1u << 15 : 0u) | (tb ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(kMuonTile >> 4) << 24);
 }
 __device__ __forceinline__ void mma16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -289,6 +295,7 @@ struct Product {
 };
 // The step's tiles in their order: every matrix's G, every P, every X.
 // keys: the matrices' first tiles of either kind, or null to read them from memory.
+template <int BN>
 __device__ __forceinline__ Product product(const MuonTable& t, const int* keys, int at, int steps) {
   Product p;
   const int per = 2 * t.sym_tiles + t.app_tiles, step = at / per;
@@ -319,22 +326,24 @@ __device__ __forceinline__ Product product(const MuonTable& t, const int* keys, 
   const int done = step * (2 * mat.syms + mat.apps);
   p.need = 16u * (unsigned)(done + (p.kind == kGram ? 0 : p.kind == kPoly ? mat.syms : 2 * mat.syms));
   int mt, nt;
-  if (sym) {  // row mt of a triangle holds tiles mt (mt + 1) / 2 ...
-    mt = (int)((sqrtf(8.0f * (float)at + 1.0f) - 1.0f) * 0.5f);
-    while ((mt + 1) * (mt + 2) / 2 <= at) ++mt;
-    while (mt * (mt + 1) / 2 > at) --mt;
-    nt = at - mt * (mt + 1) / 2;
+  if (sym) {  // row mt of a triangle holds squares mt (mt + 1) / 2 ..., of one or two tiles
+    constexpr int kW = kMuonTile / BN;
+    const int sq = at / kW;
+    mt = (int)((sqrtf(8.0f * (float)sq + 1.0f) - 1.0f) * 0.5f);
+    while ((mt + 1) * (mt + 2) / 2 <= sq) ++mt;
+    while (mt * (mt + 1) / 2 > sq) --mt;
+    nt = at - kW * (mt * (mt + 1) / 2);
     p.M = p.N = mat.s;
-    p.mirror = mt != nt;
+    p.mirror = nt < kW * mt;
   } else {
-    const int tm = (mat.rows + kMuonTile - 1) / kMuonTile, tn = (mat.cols + kMuonTile - 1) / kMuonTile;
+    const int tm = (mat.rows + kMuonTile - 1) / kMuonTile, tn = (mat.cols + BN - 1) / BN;
     tc_tile(at, 8, tm, tn, mt, nt);
     p.M = mat.rows;
     p.N = mat.cols;
     p.mirror = false;
   }
   p.m0 = mt * kMuonTile;
-  p.n0 = nt * kMuonTile;
+  p.n0 = nt * BN;
   if (p.kind == kGram) {
     p.K = mat.tall ? mat.rows : mat.cols;
     p.ta = p.tb = mat.tall;
@@ -435,14 +444,17 @@ __device__ __forceinline__ void update_weights(const MuonMat& mat, float* buf, c
   }
 }
 
+template <int BN>
 __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     muon_products_kernel(MuonTable t, MuonArgs a) {
+  using S = Mu<BN>;
+  constexpr int kMStages = S::kStages, kMStage = S::kStage;
   if (*a.found_inf) return;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
   uint8_t* pieces = stages + kMStages * kMStage;  // two per storing warp
-  int* key_space = reinterpret_cast<int*>(pieces + 16 * kMPiece);
+  int* key_space = reinterpret_cast<int*>(pieces + 8 * S::kPieces * kMPiece);
   uint64_t* full = reinterpret_cast<uint64_t*>(key_space + 2 * kMKeys);
   uint64_t* empty = full + kMStages;
   uint64_t* tfull = empty + kMStages;
@@ -472,7 +484,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tc_alloc<2>(tmem_slot, 512);
+  if (warp == 1) tc_alloc<2>(tmem_slot, 2 * BN);
   if (keys && threadIdx.x >= 64 && threadIdx.x - 64 < t.n) {
     key_space[threadIdx.x - 64] = t.mats[threadIdx.x - 64].first_sym;
     key_space[kMKeys + threadIdx.x - 64] = t.mats[threadIdx.x - 64].first_app;
@@ -489,13 +501,13 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t s = 0, ph = 0, used = 0;
     bool go = !a.stall;
     for (int tile = first; go && tile < tiles; tile += step) {
-      const Product p = product(t, keys, tile, a.steps);
+      const Product p = product<BN>(t, keys, tile, a.steps);
       const CUtensorMap* maps = t.maps + 8 * p.id;
       if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
       // what other CTAs stored is read by TMA from here on
       asm volatile("fence.proxy.async;" ::: "memory");
       const CUtensorMap *ma = maps + p.map_a, *mb = maps + p.map_b;
-      const int m0 = p.m0 + 128 * (int)rank, n0 = p.n0 + 128 * (int)rank;
+      const int m0 = p.m0 + 128 * (int)rank, n0 = p.n0 + BN / 2 * (int)rank;
       for (int k = 0; k < p.K; k += 64) {
         if (!tc_wait_warp(&empty[s], ph ^ 1u, abort_flag, a.status)) {
           go = false;
@@ -506,8 +518,10 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
           const uint32_t bar = tc_leader<2>(&full[s]);
           if (rank == 0) tc_expect(&full[s], 2 * kMStage);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < 2; ++h)
             tc_load2<2>(ma, bar, st + h * kMBox, p.ta ? m0 + 64 * h : k, p.ta ? k : m0 + 64 * h);
+#pragma unroll
+          for (int h = 0; h < S::kBBoxes; ++h) {
             tc_load2<2>(mb, bar, st + (2 + h) * kMBox, p.tb ? n0 + 64 * h : k, p.tb ? k : n0 + 64 * h);
           }
         }
@@ -526,10 +540,10 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t s = 0, ph = 0, b = 0, tph = 0;
     bool go = true;
     for (int tile = first; go && tile < tiles; tile += step) {
-      const Product p = product(t, keys, tile, a.steps);
+      const Product p = product<BN>(t, keys, tile, a.steps);
       if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
-      const uint32_t idesc = idesc16(p.ta, p.tb);
+      const uint32_t idesc = idesc16(BN, p.ta, p.tb);
       for (int k = 0; k < p.K; k += 64) {
         if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
@@ -540,7 +554,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         if (tc_elect()) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma16(tmem + b * 256, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc,
+            mma16(tmem + b * BN, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc,
                   k > 0 || kk > 0 ? 1u : 0u);
           tc_commit<2>(&empty[s]);
           if (k + 64 >= p.K) tc_commit<2>(&tfull[b]);
@@ -556,11 +570,11 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     tc_drain(drain, 0);
   } else if (warp >= 4) {  // store
     const int q = warp & 3, h = (warp - 4) >> 2;
-    uint8_t* const mine = pieces + (warp - 4) * 2 * kMPiece;
+    uint8_t* const mine = pieces + (warp - 4) * S::kPieces * kMPiece;
     uint64_t* const bar = &loaded[warp - 4];
     uint32_t b = 0, tph = 0, lph = 0;
     for (int tile = first; tile < tiles; tile += step) {
-      const Product p = product(t, keys, tile, a.steps);
+      const Product p = product<BN>(t, keys, tile, a.steps);
       const MuonMat& mat = t.mats[p.id];
       // result = alpha acc + beta old, old in the result's shape
       float alpha, beta = 0.0f, one = 0.0f, decay = 1.0f, to_w = 0.0f;
@@ -588,7 +602,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
           to_w = __fdiv_rn(__fmul_rn(a.lr, scale), mat.sx);
         }
       }
-      const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane, col0 = p.n0 + 128 * h;
+      const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane, col0 = p.n0 + BN / 2 * h;
       const CUtensorMap* maps = t.maps + 8 * p.id + 4;  // boxes of 32 rows
       const bool some = row0 < p.M && col0 < p.N;
       if (p.kind != kGram && some) {
@@ -598,9 +612,10 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
         if (tc_elect()) {
-          tc_expect(bar, 2 * kMPiece);
-          tc_load2<1>(maps + map_old, tc_smem(bar), mine, col0, row0);
-          tc_load2<1>(maps + map_old, tc_smem(bar), mine + kMPiece, col0 + 64, row0);
+          tc_expect(bar, S::kPieces * kMPiece);
+#pragma unroll
+          for (int i = 0; i < S::kPieces; ++i)
+            tc_load2<1>(maps + map_old, tc_smem(bar), mine + i * kMPiece, col0 + 64 * i, row0);
         }
         __syncwarp();
       }
@@ -615,14 +630,14 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
       const bool mirror = p.mirror && row < p.M;
       uint4 later[4] = {};
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < BN / 64; ++c) {
         const int col = col0 + 32 * c;
         uint8_t* const buf = mine + (c >> 1) * kMPiece;
         float o[32];
         uint32_t* const v = reinterpret_cast<uint32_t*>(o);
-        tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * 256 + 128 * h + 32 * c, v);
+        tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * BN + BN / 2 * h + 32 * c, v);
         tc_wait_ld<32>(v);
-        if (c == 3) {
+        if (c == BN / 64 - 1) {
           tc_before();
           __syncwarp();
           if (lane == 0) tc_arrive_at(&tempty[b], 0);
@@ -702,7 +717,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   cluster_barrier();
   tc_after();
-  if (warp == 1) tc_dealloc<2>(tmem, 512);
+  if (warp == 1) tc_dealloc<2>(tmem, 2 * BN);
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -730,17 +745,18 @@ bool muon_encode(CUtensorMap* map, uint16_t* base, int64_t rows, int64_t cols, i
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int BN>
 static cudaError_t launch_products(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
+  auto k = muon_products_kernel<BN>;
   int occ = 0, pairs = 0;  // also raises the shared-memory limit in this context
-  cudaError_t e = kernel_blocks_per_sm((const void*)muon_products_kernel, kMThreads, kMSmem, &occ);
-  if (e == cudaSuccess)
-    e = kernel_clusters((const void*)muon_products_kernel, kMThreads, kMSmem, 2, &pairs);
+  cudaError_t e = kernel_blocks_per_sm((const void*)k, kMThreads, Mu<BN>::kSmem, &occ);
+  if (e == cudaSuccess) e = kernel_clusters((const void*)k, kMThreads, Mu<BN>::kSmem, 2, &pairs);
   if (e != cudaSuccess) return e;
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)std::min(std::max(t.sym_tiles, t.app_tiles), pairs));
   cfg.blockDim = dim3(kMThreads);
-  cfg.dynamicSmemBytes = kMSmem;
+  cfg.dynamicSmemBytes = Mu<BN>::kSmem;
   cfg.stream = st;
   // CTAs wait for one another's tiles: all of them have to be resident
   cudaLaunchAttribute at;
@@ -748,7 +764,7 @@ static cudaError_t launch_products(const MuonTable& t, const MuonArgs& a, cudaSt
   at.val.cooperative = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, muon_products_kernel, t, a);
+  return cudaLaunchKernelEx(&cfg, k, t, a);
 }
 
 template <int DT>
@@ -758,7 +774,9 @@ static cudaError_t muon_dt(const MuonTable& t, const MuonArgs& a, cudaStream_t s
   const unsigned grid = (unsigned)std::min<int64_t>(t.chunks, (int64_t)sm_count() * 32);
   muon_scale_kernel<DT><<<grid, kMEThreads, 0, st>>>(t, a);
   const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? launch_products(t, a, st) : e;
+  if (e != cudaSuccess) return e;
+  return t.tile_n == kMuonTile ? launch_products<kMuonTile>(t, a, st)
+                               : launch_products<kMuonTile / 2>(t, a, st);
 }
 
 cudaError_t launch_master_update_muon(const MuonTable& t, const MuonArgs& a, cudaStream_t st) {
