@@ -238,7 +238,6 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
   const size_t gsz = dtype_size(grad_dtype);
   std::vector<MuonMat> mats;
   std::vector<CUtensorMap> maps;
-  std::vector<int64_t> cost;
   std::vector<Span> written, read;
   MuonTable t = {};
   size_t bytes = 0;
