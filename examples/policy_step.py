@@ -116,7 +116,8 @@ def train(steps: int, tokens: int = 1024, hidden: int = 256, vocab: int = 512, s
     head, rewards = PolicyHead(tokens, hidden, vocab, seqs), []
     offsets = torch.linspace(0, tokens, seqs + 1, device=DEV).long()
     for s in range(steps):
-        x = torch.randn(tokens, hidden, device=DEV, generator=head.gen).bfloat16()
+        # (a mean that is not zero: what a head without biases can learn from)
+        x = (torch.randn(tokens, hidden, device=DEV, generator=head.gen) + 0.5).bfloat16()
         targets, old, advantages, share = sample(head, x, offsets)
         head.step(x, targets, old, old, advantages, offsets)
         rewards.append(float(share.mean()))
