@@ -336,49 +336,59 @@ __global__ void __launch_bounds__(kQThreads, 1)
               else static_cast<uint16_t*>(a.d)[to + c * a.ldd] = Elem<GS_BF16>::put(__uint_as_float(v[c]));
             }
         }
-      } else if constexpr (TMA_STORE) {
-        constexpr int kChunk = OUT == GS_F32 ? 32 : 64;  // columns of 128 bytes
-#pragma unroll
-        for (int c = 0; c < kCols; c += kChunk) {
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {  // 16-byte piece p of row r lies at p ^ (r % 8)
-            uint4 w;
-            if constexpr (OUT == GS_F32) {
-              w = make_uint4(v[c + 4 * p], v[c + 4 * p + 1], v[c + 4 * p + 2], v[c + 4 * p + 3]);
-            } else {
-              const float* f = reinterpret_cast<const float*>(v) + c + 8 * p;
-              w = make_uint4(cvt_f32x2_bf16x2(f[1], f[0]), cvt_f32x2_bf16x2(f[3], f[2]),
-                             cvt_f32x2_bf16x2(f[5], f[4]), cvt_f32x2_bf16x2(f[7], f[6]));
-            }
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = w;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0 && col + c < a.N) {
-            tc_store2(&map_d, buf, (int32_t)(col + c), (int32_t)row);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-        }
-      } else {  // any address: 32 x 32 values through shared memory, rows by turns
-        float* const f = reinterpret_cast<float*>(buf);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
+      } else {
+        // 32 columns at any address: through shared memory, rows by turns
+        const auto by_rows = [&](int c) {
+          float* const f = reinterpret_cast<float*>(buf);
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 32; ++j) f[lane * 32 + ((j + lane) & 31)] = __uint_as_float(v[c + j]);
           __syncwarp();
-          const bool in = col + c + lane < a.N;
           const int rows = (int)min((int64_t)32, a.M - row);
-          for (int r = 0; r < rows; ++r) {
-            const float o = f[r * 32 + ((lane + r) & 31)];
-            const int64_t to = (row + r) * a.ldd + col + c + lane;
-            if (in) {
+          if (col + c + lane < a.N) {
+            for (int r = 0; r < rows; ++r) {
+              const float o = f[r * 32 + ((lane + r) & 31)];
+              const int64_t to = (row + r) * a.ldd + col + c + lane;
               if constexpr (OUT == GS_F32) static_cast<float*>(a.d)[to] = o;
               else static_cast<uint16_t*>(a.d)[to] = Elem<GS_BF16>::put(o);
             }
           }
+        };
+        if constexpr (TMA_STORE) {
+          constexpr int kChunk = OUT == GS_F32 ? 32 : 64;  // columns of 128 bytes
+          // (a TMA store clips a row's end to 16 bytes)
+          const bool whole_end = a.N % (OUT == GS_F32 ? 4 : 8) == 0;
+#pragma unroll
+          for (int c = 0; c < kCols; c += kChunk) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            if (!whole_end && col + c + kChunk > a.N) {
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 32) by_rows(c + i);
+              continue;
+            }
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {  // 16-byte piece p of row r lies at p ^ (r % 8)
+              uint4 w;
+              if constexpr (OUT == GS_F32) {
+                w = make_uint4(v[c + 4 * p], v[c + 4 * p + 1], v[c + 4 * p + 2], v[c + 4 * p + 3]);
+              } else {
+                const float* f = reinterpret_cast<const float*>(v) + c + 8 * p;
+                w = make_uint4(cvt_f32x2_bf16x2(f[1], f[0]), cvt_f32x2_bf16x2(f[3], f[2]),
+                               cvt_f32x2_bf16x2(f[5], f[4]), cvt_f32x2_bf16x2(f[7], f[6]));
+              }
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((p ^ (lane & 7)) << 4)) = w;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && col + c < a.N) {
+              tc_store2(&map_d, buf, (int32_t)(col + c), (int32_t)row);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32) by_rows(c);
         }
       }
     }
@@ -516,8 +526,7 @@ cudaError_t launch_gemm_fp4(const uint8_t* qa, const uint8_t* sa, const float* t
   if (!encode_fn()) return cudaErrorNotSupported;
   const Operand x = {qa, sa, M}, y = {qb, sb, N};
   const Gemm4Args a = {ta, tb, M, N, K, d, ldd, status, 16, 1, test_stall()};
-  // (a TMA store clips a row's end to 16 bytes: N must end there too)
-  const bool tma = (uintptr_t)d % 16 == 0 && ((size_t)ldd * esz) % 16 == 0 && ((size_t)N * esz) % 16 == 0;
+  const bool tma = (uintptr_t)d % 16 == 0 && ((size_t)ldd * esz) % 16 == 0;
   if (fmt == GS_NVFP4)
     return out_dtype == GS_F32 ? gemm4_pick<GS_NVFP4, GS_F32>(x, y, a, tma, st)
                                : gemm4_pick<GS_NVFP4, GS_BF16>(x, y, a, tma, st);
