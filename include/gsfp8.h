@@ -592,7 +592,7 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
  * for GS_LOSS_SEQUENCE_MEAN (n_s tokens that count in the token's sequence, S'
  * sequences that have any); 1 for GS_LOSS_SUM.
  *   logprob, old_logprob, ref_logprob: fp32 [T]; ref_logprob may be NULL with
- *       kl_coef 0;
+ *       kl_coef 0 (given with it, it changes the mean of kl alone);
  *   advantages: fp32, n_advantages = T (one per token) or S (one per sequence;
  *       where T == S, one per token);
  *   targets: int64 [T] as gs_token_logprob takes them: a token with a negative

@@ -188,9 +188,12 @@ __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, 
     const float y = __fsub_rn(ref, x);
     float em1y;
     exp_less(y, em1y, t.kl);
-    if constexpr (EXACT) t.rest = __fmaf_rn(a.kl, t.kl, t.rest);
-    else t.value = __fmaf_rn(a.kl, t.kl, t.value);
-    t.slope = __fmaf_rn(-a.kl, em1y, t.slope);
+    // (a divergence without a coefficient is watched alone: it may be infinite)
+    if (a.kl != 0.0f) {
+      if constexpr (EXACT) t.rest = __fmaf_rn(a.kl, t.kl, t.rest);
+      else t.value = __fmaf_rn(a.kl, t.kl, t.value);
+      t.slope = __fmaf_rn(-a.kl, em1y, t.slope);
+    }
   }
   return t;
 }

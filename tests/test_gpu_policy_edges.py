@@ -1,0 +1,112 @@
+"""The policy loss at the edges of its numbers, against a float64 restatement:
+a divergence that is only watched, ratios and divergences beyond fp32's range, NaN
+under an advantage of zero, advantages that cancel, one advantage per sequence in a
+batch of as many sequences as tokens.
+
+Tolerances, as in test_gpu_policy_loss.py: 2^-20 of the terms' sizes, which include
+(2 + |d|) rho |A| for the rounding of d, and half a step of the result.  A result
+beyond fp32's range is its infinity."""
+import math
+
+import pytest
+import torch
+
+import more_refs as mr
+from gpu_helpers import DEV
+from test_gpu_policy_loss import inputs
+
+pytestmark = pytest.mark.gpu
+
+REDUCTIONS = ["token", "sequence", "sum"]
+LENGTHS = [40, 3000, 9001]                               # one CTA's, by either form; many CTAs'
+
+
+@pytest.fixture(scope="module")
+def gs():
+    import mixed_precision_numerics_gradscaler_gb300 as gs
+    torch.cuda.set_device(0)
+    return gs
+
+
+def f32(v):
+    return float(torch.tensor(v, dtype=torch.float32))
+
+
+def run(gs, i, reduction, dual=0.0, kl=0.0, ref="ref", **k):
+    T = i["lp"].numel()
+    S = 1 if i["offsets"] is None else i["offsets"].numel() - 1
+    ws = torch.full((gs.gs_policy_loss_ws_bytes(T, S),), 0xEE, dtype=torch.uint8, device=DEV)
+    loss, stats, grad = torch.zeros(1, device=DEV), torch.zeros(4, device=DEV), torch.full((T,), 17.0, device=DEV)
+    gs.gs_policy_loss(i["lp"], i["old"], i["adv"], loss, ws, grad, stats, i[ref] if ref else None, i["targets"],
+                      i["offsets"], None, 0.2, 0.28, dual, kl, reduction, **k)
+    return float(loss), stats.cpu().double(), grad.cpu().double()
+
+
+def near(got, want, tol):
+    """got (fp32 values in float64) within tol of want, or the infinity that want
+    rounds to."""
+    got, want, tol = (torch.as_tensor(v, dtype=torch.float64) for v in (got, want, tol))
+    most = torch.finfo(torch.float32).max
+    at_edge = (want.abs() / most - 1).abs() < 2.0 ** -16  # either side of the last finite value
+    ok = torch.where(torch.isinf(want.float()), got == want.float().double(), (got - want).abs() <= tol)
+    ok |= at_edge & (got.sign() == want.sign()) & (got.abs() >= most * (1 - 2.0 ** -15))
+    assert bool(ok.all()), (got[~ok], want[~ok])
+
+
+def sizes(i, weights, dual, kl):
+    """What a token's terms are rounded by: the objective as far as it is not held."""
+    T = i["lp"].numel()
+    d, a = i["lp"].cpu().double() - i["old"].cpu().double(), i["adv"].cpu().double()
+    top = torch.where(a > 0, 1.28, dual if dual else math.inf)
+    size = (2 + d.abs()) * torch.minimum(d.exp(), top) * a.abs() + 1.28 * a.abs()
+    if i["ref"] is not None:
+        size = size + abs(kl) * ((i["ref"].cpu().double() - i["lp"].cpu().double()).exp() + 1)
+    return torch.where(weights > 0, weights * size, torch.zeros(T, dtype=torch.float64))
+
+
+def weights_of(i, reduction):
+    T = i["lp"].numel()
+    live = torch.ones(T, dtype=torch.float64) if i["targets"] is None else (i["targets"].cpu() >= 0).double()
+    if reduction == "sum":
+        return live
+    if reduction == "token":
+        return live / live.sum().clamp(min=1)
+    off = i["offsets"].cpu()
+    seq = torch.searchsorted(off[1:], torch.arange(T), right=True)
+    n = torch.zeros(off.numel() - 1, dtype=torch.float64).index_add_(0, seq, live)
+    return live / n.clamp(min=1)[seq] / (n > 0).sum().clamp(min=1)
+
+
+def check(gs, i, reduction, dual=0.0, kl=0.0, **k):
+    loss, stats, grad = run(gs, i, reduction, dual, kl, "ref" if i["ref"] is not None else None, **k)
+    want, wstats, wgrad, _ = mr.policy_loss(i["lp"], i["old"], i["adv"], i["ref"], i["targets"], i["offsets"],
+                                            f32(0.2), f32(0.28), f32(dual), f32(kl), reduction)
+    size = sizes(i, weights_of(i, reduction), dual, kl)
+    near(grad, wgrad, size * 2.0 ** -20 + wgrad.abs() * 2.0 ** -24)
+    near(loss, want, float(size.sum()) * 2.0 ** -20 + abs(want) * 2.0 ** -23)
+    # the mean ratio's error counts d's rounding: (2 + |d|) rho, as size has it
+    live = torch.ones(i["lp"].numel(), dtype=torch.bool) if i["targets"] is None else i["targets"].cpu() >= 0
+    d = (i["lp"].cpu().double() - i["old"].cpu().double())[live]
+    near(stats[1], wstats[1], float(((2 + d.abs()) * d.exp()).mean()) * 2.0 ** -20 + abs(wstats[1]) * 2.0 ** -24)
+    near(stats[2], wstats[2], 2.0 ** -24)
+    if i["ref"] is not None:
+        y = (i["ref"].cpu().double() - i["lp"].cpu().double())[live]
+        near(stats[3], wstats[3], float(((2 + y.abs()) * (y.exp() + 1)).mean()) * 2.0 ** -20 + abs(wstats[3]) * 2.0 ** -24)
+
+
+def live_places(i, n):
+    return (i["targets"] >= 0).nonzero().flatten()[:n] if i["targets"] is not None else torch.arange(n, device=DEV)
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+def test_a_divergence_that_is_only_watched(gs, T, reduction):
+    """kl_coef 0 with a reference: loss and gradient do not depend on it, however
+    far it is."""
+    i = inputs(T, 3, T + 1)
+    at = live_places(i, 6)
+    i["ref"][at] = i["lp"][at] + torch.tensor([89.0, 120.0, 3e38, 700.0, -math.inf, -200.0], device=DEV)
+    loss, stats, grad = run(gs, i, reduction)
+    loss0, stats0, grad0 = run(gs, i, reduction, ref=None)
+    assert math.isfinite(loss) and bool(torch.isfinite(grad).all())
+    assert loss == loss0 and torch.equal(grad, grad0) and torch.equal(stats[:3], stats0[:3])
