@@ -26,7 +26,8 @@
 // order changes nothing, and leaves a bit per token for the pass over the rest.
 // Sums: eight tokens' terms in fp32, a thread's sums with their rounding errors
 // carried along, everything beyond in fp64, joined in a fixed order by the last
-// CTA to finish.  Short batches are done by one CTA,
+// CTA to finish.  A thread that meets a term of 2^100 or more, Inf or NaN takes its
+// tokens once more in fp64.  Short batches are done by one CTA,
 // which counts and sums in one launch.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -71,6 +72,11 @@ struct Sums {
   double loss, ratio, kl;
   unsigned long long held;
 };
+// Sums from here on (and Inf and NaN) are a thread's in fp64: fp32 pairs of them could
+// leave its range, where the error of an addition would become Inf - Inf.  Below,
+// 2^27 of them fit into a pair.
+constexpr float kPFar = 0x1p100f;
+__device__ __forceinline__ bool is_far(float v) { return !(fabsf(v) < kPFar); }
 // Adds N (a power of two) lanes' sums; the result in lane 0.
 template <int N>
 __device__ __forceinline__ Sums warp_sums(Sums s) {
@@ -198,11 +204,67 @@ __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, 
   return t;
 }
 
+// The same in fp64, for terms that fp32 has no room for (an exponential beyond its
+// range whose mean is inside it, say): what is held, and at which factor, is decided
+// as above.
+struct FarToken {
+  double value, slope, ratio, kl;
+};
+__device__ __noinline__ FarToken far_token(const PolicyArgs& a, float x, float old, float ref, float adv) {
+  FarToken t;
+  float d, e;
+  two_diff(x, old, d, e);
+  const double diff = (double)x - (double)old;
+  t.ratio = exp(diff);
+  const bool gains = adv > 0.0f, loses = adv < 0.0f;
+  const bool over = (gains || loses) && above(d, e, gains ? a.high : a.dual);
+  const bool under = loses && below(d, e, a.low);
+  const double factor = over ? (gains ? a.factor_high : a.factor_dual) : under ? (double)a.factor_low : t.ratio;
+  const double obj = adv == 0.0f ? 0.0 : factor * (double)adv;
+  t.value = -obj;
+  t.slope = over || under ? 0.0 : -obj;
+  t.kl = 0.0;
+  if (a.ref) {
+    const double y = (double)ref - (double)x, em1 = expm1(y);
+    t.kl = em1 - y;
+    if (a.kl != 0.0f) {
+      t.value += (double)a.kl * t.kl;
+      t.slope -= (double)a.kl * em1;
+    }
+  }
+  return t;
+}
+// What a thread sums in fp64 after all, because a part of it was far: all of its
+// tokens' terms, once more from the start (rare, and nothing of it is held in the
+// loops over tokens).  With kFarLoss their gradients are written again too.
+enum { kFarLoss = 1, kFarRatio = 2, kFarKl = 4 };
+struct Far {
+  unsigned which = 0;
+  double loss = 0.0, ratio = 0.0, kl = 0.0;
+  __device__ __forceinline__ void see(float loss, float ratio, float kl) {
+    which |= (is_far(loss) ? kFarLoss : 0u) | (is_far(ratio) ? kFarRatio : 0u) | (is_far(kl) ? kFarKl : 0u);
+  }
+  // Token t, with the weight in the loss and the gradient's factor.
+  __device__ __forceinline__ void add(const PolicyArgs& a, int64_t t, float adv, double w, double up) {
+    const FarToken f = far_token(a, a.logprob[t], a.old[t], a.ref ? a.ref[t] : 0.0f, adv);
+    if (which & kFarLoss) {
+      loss += w * f.value;
+      if (a.grad) a.grad[t] = (float)(up * f.slope);
+    }
+    if (which & kFarRatio) ratio += f.ratio;
+    if (which & kFarKl) kl += f.kl;
+  }
+};
+
 // Adds a block's sums, the threads' as fp32 pairs within a warp (512 threads'
 // additions in fp64 would take 2 us), the warps' in fp64; the result in thread 0.
+// far: sums of this thread that take the place of its pairs.
 template <int NT>
-__device__ __forceinline__ Sums block_sums(Pair loss, Pair ratio, Pair kl, unsigned long long held) {
+__device__ __forceinline__ Sums block_sums(Pair loss, Pair ratio, Pair kl, unsigned long long held, const Far& far) {
   __shared__ Sums red[NT / 32];
+  if (far.which & kFarLoss) loss = Pair{0.0f, 0.0f};
+  if (far.which & kFarRatio) ratio = Pair{0.0f, 0.0f};
+  if (far.which & kFarKl) kl = Pair{0.0f, 0.0f};
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     loss.merge(o);
@@ -210,8 +272,12 @@ __device__ __forceinline__ Sums block_sums(Pair loss, Pair ratio, Pair kl, unsig
     kl.merge(o);
     held += __shfl_down_sync(0xFFFFFFFFu, held, o);
   }
-  if ((threadIdx.x & 31) == 0)
-    red[threadIdx.x >> 5] = Sums{loss.value(), ratio.value(), kl.value(), held};
+  Sums own = {loss.value(), ratio.value(), kl.value(), held};
+  if (__any_sync(0xFFFFFFFFu, far.which != 0)) {
+    const Sums w = warp_sums<32>(Sums{far.loss, far.ratio, far.kl, 0ull});
+    own = Sums{own.loss + w.loss, own.ratio + w.ratio, own.kl + w.kl, held};
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = own;
   __syncthreads();
   Sums s = {0.0, 0.0, 0.0, 0ull};
   if (threadIdx.x < 32) {
@@ -349,10 +415,23 @@ __device__ __forceinline__ void get8(const float* p, float (&v)[8]) {
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
+// This thread's tokens that count, for sums that are far; w_token: the token mean's
+// weight, which the loss gets at the end.
+__device__ __noinline__ void far_tokens(const PolicyArgs& a, Far& far, int64_t lo, int64_t hi, bool by_seq, double w_token) {
+  const double up = a.dloss ? (double)*a.dloss : 1.0;
+  for (int64_t t0 = ((int64_t)blockIdx.x * kPThreads + threadIdx.x) * kPRun; t0 < hi; t0 += (int64_t)gridDim.x * kPTile)
+    for (int64_t t = max(t0, lo); t < min(t0 + kPRun, hi); ++t) {
+      if (a.targets && a.targets[t] < 0) continue;
+      const int64_t s = a.offsets && (by_seq || a.adv_per_seq) ? seq_of(a.offsets + 1, 0, a.S - 1, t) : 0;
+      const double w = by_seq ? 1.0 / ((double)a.head->seqs * (double)a.n[s]) : 1.0;
+      far.add(a, t, a.adv[a.adv_per_seq ? s : t], w, up * w * w_token);
+    }
+}
+
 // VEC: 16-byte aligned arrays; REF: a reference policy; FIND: a token's sequence
 // is needed, for its advantage or its weight.
 template <bool VEC, bool REF, bool FIND>
-__global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a) {
+__global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(const __grid_constant__ PolicyArgs a) {
   __shared__ int64_t range[2];
   __shared__ bool last;
   __shared__ int64_t ends[kPSpan];
@@ -368,6 +447,7 @@ __global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a)
   const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN ? (n ? (float)(1.0 / (double)n) : 0.0f) : 1.0f;
   const float up_token = __fmul_rn(up, w_token);
   Pair loss_sum = {0.0f, 0.0f}, ratio_sum = loss_sum, kl_sum = loss_sum;
+  Far far;
   unsigned long long held_sum = 0;
   const int64_t tiles = (a.T + kPTile - 1) / kPTile;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -439,6 +519,7 @@ __global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a)
       grad[j] = in ? __fmul_rn(FIND ? __fmul_rn(up_token, w[j]) : up_token, tk.slope) : 0.0f;
     }
     held_sum += held;
+    far.see(loss, ratio, kl);
     loss_sum.add(loss);
     ratio_sum.add(ratio);
     kl_sum.add(kl);
@@ -453,7 +534,9 @@ __global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a)
       }
     }
   }
-  const Sums s = block_sums<kPThreads>(loss_sum, ratio_sum, kl_sum, held_sum);
+  if (far.which)
+    far_tokens(a, far, lo, hi, by_seq, a.reduction == GS_LOSS_TOKEN_MEAN && n ? 1.0 / (double)n : 1.0);
+  const Sums s = block_sums<kPThreads>(loss_sum, ratio_sum, kl_sum, held_sum, far);
   if (threadIdx.x == 0) {
     a.part[blockIdx.x] = PolicyPart{s.loss, s.ratio, s.kl, s.held};
     __threadfence();
@@ -475,10 +558,26 @@ __global__ void __launch_bounds__(kPThreads, 4) policy_loss_kernel(PolicyArgs a)
   if (lane == 0) finish(a, all, n);
 }
 
+// The same of a CTA that does everything, with its ends, counts, sequences and tokens.
+__device__ __noinline__ void far_small_tokens(const PolicyArgs& a, Far& far, int lo, int hi, const int* ends,
+                                              const unsigned* counts, unsigned seqs, unsigned n) {
+  const bool by_seq = a.reduction == GS_LOSS_SEQUENCE_MEAN;
+  const double up = a.dloss ? (double)*a.dloss : 1.0;
+  const double w_token = a.reduction == GS_LOSS_TOKEN_MEAN && n ? 1.0 / (double)n : 1.0;
+  for (int t = threadIdx.x; t < hi; t += kPSmallThreads) {
+    if (t < lo || (a.targets && a.targets[t] < 0)) continue;
+    int s = 0;
+    if (by_seq || a.adv_per_seq)
+      while (s < (int)a.S - 1 && ends[s] <= t) ++s;
+    const double w = by_seq ? 1.0 / ((double)seqs * (double)counts[s]) : 1.0;
+    far.add(a, t, a.adv[a.adv_per_seq ? s : t], w, up * w * w_token);
+  }
+}
+
 // Everything by one CTA: offsets, counts and weights in shared memory, the
 // tokens' values loaded once, PER of them a thread.
 template <int PER, bool REF>
-__global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(PolicyArgs a) {
+__global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(const __grid_constant__ PolicyArgs a) {
   __shared__ int ends[kPSmallSeqs];
   __shared__ unsigned counts[kPSmallSeqs];
   __shared__ unsigned totals[2];  // tokens, sequences that have any
@@ -548,6 +647,7 @@ __global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(Polic
   const float seqs = (float)totals[1];
   const float w_token = a.reduction == GS_LOSS_TOKEN_MEAN && n ? __fdiv_rn(1.0f, (float)n) : 1.0f;
   Pair loss = {0.0f, 0.0f}, ratio = loss, kl = loss;
+  Far far;
   unsigned held = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
@@ -561,6 +661,7 @@ __global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(Polic
     const Token tk = token<REF, true>(a, x[j], old[j], ref[j], adv[j]);
     if (in[j]) {
       const float part = __fmul_rn(w, tk.value);
+      far.see(__fadd_rn(fabsf(tk.value), fabsf(tk.rest)), tk.ratio, tk.kl);
       loss.add(part);
       loss.lo = __fadd_rn(loss.lo, __fmaf_rn(w, tk.rest, __fmaf_rn(w_lo, tk.value, __fmaf_rn(w, tk.value, -part))));
       ratio.add(tk.ratio);
@@ -570,7 +671,8 @@ __global__ void __launch_bounds__(kPSmallThreads) policy_loss_small_kernel(Polic
     if (a.grad && t >= lo && t < hi)
       a.grad[t] = in[j] ? __fmul_rn(__fmul_rn(up, by_seq ? w : w_token), tk.slope) : 0.0f;
   }
-  const Sums s = block_sums<kPSmallThreads>(loss, ratio, kl, held);
+  if (far.which) far_small_tokens(a, far, (int)lo, (int)hi, ends, counts, totals[1], n);
+  const Sums s = block_sums<kPSmallThreads>(loss, ratio, kl, held, far);
   if (tid == 0) finish(a, s, n);
 }
 

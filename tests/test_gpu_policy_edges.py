@@ -110,3 +110,58 @@ def test_a_divergence_that_is_only_watched(gs, T, reduction):
     loss0, stats0, grad0 = run(gs, i, reduction, ref=None)
     assert math.isfinite(loss) and bool(torch.isfinite(grad).all())
     assert loss == loss0 and torch.equal(grad, grad0) and torch.equal(stats[:3], stats0[:3])
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+@pytest.mark.parametrize("far", [80.0, 88.7, 89.0, 100.0, 400.0])
+@pytest.mark.parametrize("sign,dual", [(1.0, 0.0), (-1.0, 3.0), (-1.0, 0.0)])
+def test_ratios_beyond_the_range(gs, T, reduction, far, sign, dual):
+    """Counted tokens whose ratio leaves fp32: held where the objective is held,
+    else in the loss and the gradient as far as those reach."""
+    i = inputs(T, 3, T + 2)
+    at = live_places(i, 9)
+    i["old"][at] = i["lp"][at] - far
+    i["adv"][at] = sign
+    check(gs, i, reduction, dual, 0.05)
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+@pytest.mark.parametrize("far", [87.0, 89.0, 95.0, 300.0, -1000.0])
+def test_divergences_beyond_the_range(gs, T, reduction, far):
+    i = inputs(T, 3, T + 3)
+    at = live_places(i, 5)
+    i["ref"][at] = i["lp"][at] + far
+    check(gs, i, reduction, kl=0.05)
+    check(gs, i, reduction, kl=-2.0)
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+def test_sums_beyond_the_range_whose_mean_is_not(gs, T):
+    """Ratios of 1e38 and advantages of 1e30 in every token: their sums leave fp32."""
+    i = inputs(T, 3, T + 4)
+    i["old"] = i["lp"] - 88.0 - 0.5 * torch.rand(T, device=DEV)
+    i["ref"] = i["lp"] + 87.5 + 0.5 * torch.rand(T, device=DEV)
+    i["adv"] = -i["adv"].abs()
+    for reduction in REDUCTIONS:
+        check(gs, i, reduction, kl=0.5)
+    i["adv"] = i["adv"].abs() * 1e37
+    for reduction in REDUCTIONS:
+        check(gs, i, reduction, kl=0.5)
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+def test_infinite_log_probabilities(gs, T, reduction):
+    """log probability -Inf: ratio 0.  Old one -Inf: ratio Inf, held or not."""
+    i = inputs(T, 3, T + 5, ref=False)
+    at = live_places(i, 4)
+    i["lp"][at[:2]] = -math.inf
+    i["old"][at[2:]] = -math.inf
+    i["adv"][at] = torch.tensor([1.0, -1.0, 1.0, 2.0], device=DEV)
+    loss, stats, grad = run(gs, i, reduction)
+    assert math.isfinite(loss) and bool((grad[at.cpu()] == 0.0).all()) and float(stats[1]) == math.inf
+    i["adv"][at[3]] = -2.0                               # l = +Inf, its gradient too
+    loss, _, grad = run(gs, i, reduction)
+    assert loss == math.inf and float(grad[at[3]]) == math.inf and bool((grad[at[:3].cpu()] == 0.0).all())
