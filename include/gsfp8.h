@@ -610,7 +610,8 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
  *       aligned, any contents; calls sharing one must be ordered on one stream.
  * clip_low, clip_high >= 0 (1 or more, Inf: never held there); dual_clip 0 or
  * >= 1.  A ratio or a divergence beyond fp32's range counts as what it is: a result
- * that is inside is finite, one beyond its infinity.  No token that counts: loss,
+ * that is inside is finite, one beyond its infinity.  A log probability that is NaN
+ * shows in the loss and in its token's gradient, an advantage of 0 or not.  No token that counts: loss,
  * statistics and gradient 0.  T, S <= 2^40,
  * S >= 1.  The same inputs give the same bits. */
 typedef enum gs_loss_reduction {

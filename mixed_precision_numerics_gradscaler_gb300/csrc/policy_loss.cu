@@ -177,7 +177,8 @@ __device__ __forceinline__ Token token(const PolicyArgs& a, float x, float old, 
   const bool under = loses && below(d, e, a.low);
   t.held = over || under;
   const float factor = over ? (gains ? a.factor_high : a.factor_dual) : under ? a.factor_low : t.ratio;
-  const float obj = adv == 0.0f ? 0.0f : __fmul_rn(factor, adv);
+  // (a ratio beyond fp32 times 0 is NaN here, and 0 in fp64: see FarToken)
+  const float obj = __fmul_rn(factor, adv);
   t.slope = t.held ? 0.0f : -obj;
   t.kl = 0.0f;
   t.value = -obj;
@@ -220,7 +221,8 @@ __device__ __noinline__ FarToken far_token(const PolicyArgs& a, float x, float o
   const bool over = (gains || loses) && above(d, e, gains ? a.high : a.dual);
   const bool under = loses && below(d, e, a.low);
   const double factor = over ? (gains ? a.factor_high : a.factor_dual) : under ? (double)a.factor_low : t.ratio;
-  const double obj = adv == 0.0f ? 0.0 : factor * (double)adv;
+  // (a finite ratio times 0, whatever exp(diff) makes of it)
+  const double obj = adv == 0.0f && isfinite(diff) ? 0.0 : factor * (double)adv;
   t.value = -obj;
   t.slope = over || under ? 0.0 : -obj;
   t.kl = 0.0;

@@ -165,3 +165,21 @@ def test_infinite_log_probabilities(gs, T, reduction):
     i["adv"][at[3]] = -2.0                               # l = +Inf, its gradient too
     loss, _, grad = run(gs, i, reduction)
     assert loss == math.inf and float(grad[at[3]]) == math.inf and bool((grad[at[:3].cpu()] == 0.0).all())
+
+
+@pytest.mark.parametrize("T", LENGTHS)
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+@pytest.mark.parametrize("name", ["lp", "old"])
+def test_nan_shows_under_an_advantage_of_zero(gs, T, reduction, name):
+    i = inputs(T, 3, T + 6, ref=False)
+    i["adv"].zero_()
+    loss, _, grad = run(gs, i, reduction)
+    assert loss == 0.0 and bool((grad == 0.0).all())
+    at = int(live_places(i, 3)[2])
+    i[name][at] = math.nan
+    loss, stats, grad = run(gs, i, reduction)
+    assert math.isnan(loss) and math.isnan(float(grad[at])) and math.isnan(float(stats[1]))
+    assert int(torch.isnan(grad).sum()) == 1
+    i[name][at] = i["lp" if name == "old" else "old"][at] + (300.0 if name == "lp" else -300.0)
+    loss, _, grad = run(gs, i, reduction)                # a ratio beyond fp32 times 0
+    assert loss == 0.0 and bool((grad == 0.0).all())
