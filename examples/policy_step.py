@@ -83,7 +83,7 @@ class PolicyHead:
         """One update; nothing is read on the host."""
         self.forward(x, targets)
         gs.gs_policy_loss(self.logprob, old, advantages, self.loss, self.loss_ws, self.dlogprob, self.stats, ref,
-                          targets, offsets, None, 0.2, 0.28, 3.0, 0.02, reduction)
+                          targets, offsets, None, 0.2, 0.28, 3.0, 0.02, reduction, per_sequence=True)
         gs.gs_token_logprob_bwd(self.logits, targets, self.lse, self.dlogprob, self.dlogits, loss_scale=self.scale)
         self.d4.quantise(self.dlogits)
         product(self.d4, self.w4, self.dx, b_t=True)                 # dX = dY W

@@ -593,8 +593,8 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
  * sequences that have any); 1 for GS_LOSS_SUM.
  *   logprob, old_logprob, ref_logprob: fp32 [T]; ref_logprob may be NULL with
  *       kl_coef 0 (given with it, it changes the mean of kl alone);
- *   advantages: fp32, n_advantages = T (one per token) or S (one per sequence;
- *       where T == S, one per token);
+ *   advantages: fp32; n_advantages = T: one per token; S or -S: one per sequence
+ *       (-S says so where T == S, which S does not);
  *   targets: int64 [T] as gs_token_logprob takes them: a token with a negative
  *       one does not count, whatever the other arrays hold there; NULL: all do;
  *   seq_offsets: int64 [S + 1], not decreasing: sequence s is the tokens

@@ -754,9 +754,10 @@ def gs_policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages:
                    targets: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
                    dloss: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2,
                    dual_clip: float = 0.0, kl_coef: float = 0.0, reduction: str = "token",
-                   stream=None) -> None:
+                   stream=None, per_sequence: bool | None = None) -> None:
     """logprob, old_logprob, ref_logprob, dlogprob: float32 [T]; advantages:
-    float32 [T] or [S]; targets: int64 [T] (negative: the token does not
+    float32 [T] or [S] (per_sequence says which; unless said their length does,
+    [T] where T == S); targets: int64 [T] (negative: the token does not
     count); seq_offsets: int64 [S + 1]; loss, dloss: float32 [1]; stats:
     float32 [4] (tokens, mean ratio, held fraction, mean divergence); ws:
     gs_policy_loss_ws_bytes(T, S) bytes; reduction: "token", "sequence" or
@@ -764,12 +765,14 @@ def gs_policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages:
     T = logprob.numel()
     S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     n = advantages.numel()
+    if per_sequence is not None and n != (S if per_sequence else T):
+        raise ValueError("advantages must be one per sequence" if per_sequence else "advantages must be one per token")
     if not ws.is_contiguous() or ws.nbytes < _lib.gs_policy_loss_ws_bytes(T, S):
         raise ValueError("ws must be contiguous, of gs_policy_loss_ws_bytes(T, S) bytes at least")
     status = _lib.gs_policy_loss(
         _vector(logprob, "logprob", T, _F32), _vector(old_logprob, "old_logprob", T, _F32),
-        _vector(ref_logprob, "ref_logprob", T, _F32), _vector(advantages, "advantages", n, _F32), n,
-        _vector(targets, "targets", T, _I64), T, _vector(seq_offsets, "seq_offsets", S + 1, _I64), S,
+        _vector(ref_logprob, "ref_logprob", T, _F32), _vector(advantages, "advantages", n, _F32),
+        -n if per_sequence else n, _vector(targets, "targets", T, _I64), T, _vector(seq_offsets, "seq_offsets", S + 1, _I64), S,
         clip_low, clip_high, dual_clip, kl_coef, _REDUCTIONS[reduction], _vector(dloss, "dloss", 1, _F32),
         _vector(loss, "loss", 1, _F32), _vector(stats, "stats", 4, _F32),
         _vector(dlogprob, "dlogprob", T, _F32), ws.data_ptr(), _stream(stream))

@@ -173,7 +173,9 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
                    float* stats, float* dlogprob, void* ws, void* stream) {
   const size_t wsb = gs_policy_loss_ws_bytes(T, S);
   if (!wsb || S < 1 || (!seq_offsets && S != 1)) return GS_ERR_SHAPE;
-  if (n_advantages != T && n_advantages != S) return GS_ERR_SHAPE;
+  if (n_advantages != T && n_advantages != S && n_advantages != -S) return GS_ERR_SHAPE;
+  const bool adv_per_seq = n_advantages != T;
+  if (n_advantages < 0) n_advantages = -n_advantages;
   if (reduction != GS_LOSS_TOKEN_MEAN && reduction != GS_LOSS_SEQUENCE_MEAN && reduction != GS_LOSS_SUM)
     return GS_ERR_ARG;
   if (!(clip_low >= 0.0f) || !(clip_high >= 0.0f) || !std::isfinite(kl_coef)) return GS_ERR_ARG;
@@ -209,7 +211,7 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
   a.T = T;
   a.S = S;
   a.reduction = reduction;
-  a.adv_per_seq = n_advantages != T;
+  a.adv_per_seq = adv_per_seq;
   const double low = 1.0 - (double)clip_low, high = 1.0 + (double)clip_high;
   a.low = border(low > 0.0 ? std::log(low) : -HUGE_VAL);
   a.high = border(std::log(high));

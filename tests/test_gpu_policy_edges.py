@@ -183,3 +183,21 @@ def test_nan_shows_under_an_advantage_of_zero(gs, T, reduction, name):
     i[name][at] = i["lp" if name == "old" else "old"][at] + (300.0 if name == "lp" else -300.0)
     loss, _, grad = run(gs, i, reduction)                # a ratio beyond fp32 times 0
     assert loss == 0.0 and bool((grad == 0.0).all())
+
+
+@pytest.mark.parametrize("reduction", REDUCTIONS)
+@pytest.mark.parametrize("T", [1, 7, 300, 6000])
+def test_as_many_sequences_as_tokens(gs, reduction, T):
+    """Some sequences empty, some longer: the length of the advantages does not tell
+    whether they are the tokens' or the sequences'."""
+    i = inputs(T, T, T + 7)
+    check(gs, i, reduction, kl=0.05)                     # unless said: the tokens'
+    check(gs, i, reduction, kl=0.05, per_sequence=False)
+    loss, stats, grad = run(gs, i, reduction, kl=0.05, per_sequence=True)
+    seq = torch.searchsorted(i["offsets"][1:], torch.arange(T, device=DEV), right=True).clamp(max=T - 1)
+    each = i | {"adv": i["adv"][seq].contiguous()}
+    loss2, stats2, grad2 = run(gs, each, reduction, kl=0.05, per_sequence=False)
+    tol = float(sizes(each, weights_of(each, reduction), 0.0, 0.05).sum()) * 2.0 ** -20
+    assert abs(loss - loss2) <= tol and torch.equal(stats, stats2)
+    assert bool(((grad - grad2).abs() <= grad2.abs() * 2.0 ** -22).all())
+    check(gs, each, reduction, kl=0.05, per_sequence=False)
