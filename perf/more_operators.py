@@ -276,7 +276,7 @@ def _run_own(s):
     if case["op"] == "policy":
         gs.gs_policy_loss(s.logprob, s.old, s.adv, s.loss, s.ws, s.dlogprob, s.stats, s.ref, s.targets,
                           s.offsets, s.dloss, s.clip_low, s.clip_high, case["dual"],
-                          0.0 if s.ref is None else s.kl, case["reduction"])
+                          0.0 if s.ref is None else s.kl, case["reduction"], per_sequence=not case["per_token"])
         return {"loss": s.loss, "stats": s.stats, "dlogprob": s.dlogprob}
     gs.gs_master_update_muon(s.list, s.found_inf, s.lr, s.mu, s.wd, case["nesterov"], case["steps"],
                              "rms", s.max_norm, s.grad_norm)
