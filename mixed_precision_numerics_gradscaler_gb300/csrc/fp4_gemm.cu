@@ -263,8 +263,18 @@ __global__ void __launch_bounds__(kQThreads, 1)
     constexpr int kCols = BN >= 64 ? BN / 2 : BN;  // per warp (the first four alone below 64)
     const bool mine = BN >= 64 || h == 0;
     uint8_t* const buf = out_stage + (warp - 4) * 32 * 128;
-    float alpha = 1.0f;
+    float alpha = 1.0f, beta = 1.0f;
     if (a.ta) alpha = __fmul_rn(*a.ta, *a.tb);
+    // A product of the two that fp32 does not hold is applied a factor at a time: the
+    // larger one first where it is small, the smaller one first where it is large, so
+    // that nothing on the way leaves fp32 but where the result does (a sum is 0 or at
+    // least 2^-20).
+    if (a.ta && !(fabsf(alpha) >= 0x1p-126f && fabsf(alpha) < INFINITY)) {
+      const float x = *a.ta, y = *a.tb;
+      const bool x_first = fabsf(alpha) < 1.0f ? fabsf(x) > fabsf(y) : fabsf(x) < fabsf(y);
+      alpha = x_first ? x : y;
+      beta = x_first ? y : x;
+    }
     uint32_t n = 0;
     for (int t = first; t < n_tiles; t += step, ++n) {
       int mt, nt;
@@ -326,6 +336,10 @@ __global__ void __launch_bounds__(kQThreads, 1)
       if (row >= a.M || col >= a.N) continue;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) v[c] = __float_as_uint(__fmul_rn(__uint_as_float(v[c]), alpha));
+      if (beta != 1.0f) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) v[c] = __float_as_uint(__fmul_rn(__uint_as_float(v[c]), beta));
+      }
       if constexpr (TRANS) {
         const int64_t to = col * a.ldd + row + lane;
         if (row + lane < a.M) {
