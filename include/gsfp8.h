@@ -638,7 +638,7 @@ int gs_policy_loss(const float* logprob, const float* old_logprob, const float* 
  * current device; nothing that is written may overlap anything else.  Fewer
  * than 2^31 elements per matrix, sides of up to 2^18 (fp32 sums of more would
  * be further off than the operands' roundings); empty ones are left out.  Allocates the list's
- * workspace: 4 bytes per element (rows counted up to a multiple of 8 elements) and
+ * workspace: 8 bytes per element (rows counted up to a multiple of 8 elements) and
  * 4 per element of a square of the smaller side. */
 typedef struct gs_muon_list gs_muon_list;
 int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, const void* const* grads,
@@ -659,10 +659,12 @@ typedef enum gs_muon_scale { GS_MUON_SCALE_RMS = 0, GS_MUON_SCALE_ASPECT = 1 } g
  *   w = w (1 - lr weight_decay) - lr scale X;   bf16 copy = w rounded to nearest
  *       even;  scale = 0.2 sqrt(max(rows, cols)) (GS_MUON_SCALE_RMS: an update of
  *       AdamW's size) or sqrt(max(1, rows / cols)) (GS_MUON_SCALE_ASPECT).
- * X, G and the polynomial are held in fp16, scaled by powers of two to its range
- * (11 bits where bf16 would keep 8), sums in fp32: after five steps X is off the
- * exact polynomial by about 1.1e-3 of its norm (2^-11 per rounding, which the
- * polynomial's slope at small singular values carries on).  Sums of squares are fp32 within a thread's elements and fp64
+ * G, the polynomial and X are held in fp16, scaled by powers of two to their ranges,
+ * X up to its last step with what fp16 leaves of it beside it (22 bits; G is formed
+ * from the first 11), sums in fp32.  After five or six steps X is off the exact
+ * polynomial by 4e-4 to 2.5e-3 of its norm, whatever the singular values (flat, or a
+ * few up to 1e5 times the rest).  More steps move singular values about near 1 and
+ * errors with them, by slopes of up to 3.9: twenty end 2e-3 to 2e-2 off.  Sums of squares are fp32 within a thread's elements and fp64
  * beyond: elements of u below 2^-75 count as zero there, and a thread's sum above
  * fp32's range makes the matrix NaN.  Non-finite gradients are for
  * the check before this step to find.

@@ -409,7 +409,8 @@ def gs_master_update_adamw(alist: AdamWList, step: torch.Tensor, found_inf: torc
 class MuonList:
     """Owns a ``gs_muon_list`` handle: fp32 master matrices [rows, cols], their
     gradients (all float32, bfloat16 or float16), fp32 momenta and optional bf16
-    copies, and the workspace of the step (4 to 8 bytes per element)."""
+    copies, and the workspace of the step (8 to 12 bytes per element; rows are
+    counted up to a multiple of 8 elements in it)."""
 
     def __init__(self, master: list[torch.Tensor], grads: list[torch.Tensor],
                  momentum: list[torch.Tensor], master_bf16: list[torch.Tensor] | None = None):

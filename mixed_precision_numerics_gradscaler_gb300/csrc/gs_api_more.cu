@@ -290,8 +290,8 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     // any: rounds of tiles times a tile's stages or its store, whichever is longer,
     // and a last store, in units of a stage of the wide ones (a narrow one takes
     // 0.62, for its loads).  Measured, wide and narrow: one matrix of 4096 x 2048
-    // 694 and 493 us, twelve of 256 x 768 162 and 153, 32 of 512 x 512 342 and 388,
-    // two of 14336 x 4096 5720 and 6870.
+    // 634 and 607 us, one of 2048 x 2048 492 and 413, twelve of 256 x 768 185 and 164,
+    // 32 of 512 x 512 377 and 405, two of 14336 x 4096 8020 and 9660.
     double cost[2];
     int64_t tiles[2][2];  // of either width: products of squares, of X
     for (int k = 0; k < 2; ++k) {
@@ -305,7 +305,7 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
         tiles[k][1] += apps;
         sums[0] += (double)syms * (double)div_up(std::max(m.rows, m.cols), 64);
         sums[1] += (double)syms * (double)div_up(m.s, 64);
-        sums[2] += (double)apps * (double)div_up(m.s, 64);
+        sums[2] += (double)apps * (double)div_up(m.s, 64) * 1.8;  // twice but in the last of five steps
       }
       cost[k] = 0;
       for (int j = 0; j < 3 && !mats.empty(); ++j) {
@@ -333,16 +333,16 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
     t.sym_tiles = sym;
     t.app_tiles = app;
     at_mats = take(mats.size() * sizeof(MuonMat));
-    at_maps = take(mats.size() * 8 * sizeof(CUtensorMap));
+    at_maps = take(mats.size() * 2 * kMuonMaps * sizeof(CUtensorMap));
     at_partials = take((size_t)t.chunks * sizeof(double));
     at_arrived = take(mats.size() * sizeof(unsigned));
     at_done = take(mats.size() * sizeof(unsigned));
     at_factor = take(mats.size() * sizeof(float));
     for (const MuonMat& m : mats) {
       const size_t x = (size_t)m.rows * m.ldx * 2, g = (size_t)m.s * m.lds * 2;
-      for (const size_t b : {x, x, g, g}) at_x.push_back(take(b));
+      for (const size_t b : {x, x, g, g, x, x}) at_x.push_back(take(b));
     }
-    maps.resize(mats.size() * 8);
+    maps.resize(mats.size() * 2 * kMuonMaps);
   } catch (...) {
     return GS_ERR_ARG;
   }
@@ -357,16 +357,19 @@ int gs_muon_list_create(float* const* master, uint16_t* const* master_bf16, cons
   if (e == cudaSuccess) {
     for (size_t i = 0; i < mats.size() && e == cudaSuccess; ++i) {
       MuonMat& m = mats[i];
-      uint16_t* p[4];
-      for (int j = 0; j < 4; ++j) p[j] = reinterpret_cast<uint16_t*>(d + at_x[4 * i + j]);
+      uint16_t* p[kMuonMaps];
+      for (int j = 0; j < kMuonMaps; ++j) p[j] = reinterpret_cast<uint16_t*>(d + at_x[kMuonMaps * i + j]);
       m.x[0] = p[0];
       m.x[1] = p[1];
       m.gram = p[2];
       m.poly = p[3];
-      for (int j = 0; j < 8; ++j) {
-        const int k = j % 4;
-        if (!muon_encode(&maps[8 * i + j], p[k], k < 2 ? m.rows : m.s, k < 2 ? m.cols : m.s,
-                         k < 2 ? m.ldx : m.lds, j < 4 ? 64 : 32))
+      m.x_lo[0] = p[4];
+      m.x_lo[1] = p[5];
+      for (int j = 0; j < 2 * kMuonMaps; ++j) {
+        const int k = j % kMuonMaps;
+        const bool square = k == 2 || k == 3;
+        if (!muon_encode(&maps[2 * kMuonMaps * i + j], p[k], square ? m.s : m.rows, square ? m.s : m.cols,
+                         square ? m.lds : m.ldx, j < kMuonMaps ? 64 : 32))
           e = cudaErrorNotSupported;
       }
     }

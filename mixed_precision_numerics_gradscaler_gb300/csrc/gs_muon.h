@@ -10,6 +10,7 @@ namespace gs {
 
 constexpr int kMuonTile = 256;               // rows of a product's tile; its columns are these or half
 constexpr int64_t kMuonChunk = 4096;         // elements of an element-wise step's CTA
+constexpr int kMuonMaps = 6;                 // tensor maps of a matrix by one box: x, gram, poly, x_lo
 
 // One matrix [rows, cols]; s = min, l = max of the two.  The products' operands
 // are fp16 times a power of two each: x by sx, gram and poly by sa and sa / 4.
@@ -19,6 +20,7 @@ struct MuonMat {
   const void* g;
   float* m;
   uint16_t* x[2];            // [rows, ldx], in turns
+  uint16_t* x_lo[2];         // what fp16 leaves of x, in fp16
   uint16_t *gram, *poly;     // [s, lds]
   int rows, cols, s, ldx, lds;
   int tall;                  // rows > cols
@@ -30,7 +32,7 @@ struct MuonMat {
 
 struct MuonTable {
   const MuonMat* mats;
-  const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly by 64 x 64, then by 32 x 64
+  const CUtensorMap* maps;   // per matrix: x[0], x[1], gram, poly, x_lo[0], x_lo[1] by 64 x 64, then by 32 x 64
   double* partials;          // one per chunk
   unsigned int* arrived;     // per matrix, 0 between calls
   unsigned int* done;        // per matrix: warps' parts of tiles (16 each) stored by the call's products

@@ -8,15 +8,23 @@
 // takes (0, 1] to near 1.
 //
 // The products take s^2 (l + s) operations each way of G and P with their
-// symmetric halves left out, 2 s^2 l for X: all on the tensor cores.  Operands
+// symmetric halves left out, 2 s^2 l for X (twice, see below): all on the tensor cores.  Operands
 // are fp16, not bf16: every value is bounded (singular values of X stay below
 // 1.21, of G below 1.46, of P below 2.45), so that a power of two per matrix
 // keeps them in fp16's normal range with three more bits than bf16 has, at the
 // same rate.  Sums are fp32 in tensor memory and round to fp16 once per product;
 // the last product's go into w unrounded.  One X is left out of P: where singular
 // values are near 1, P is then the small difference between X and the result,
-// and its rounding counts for as much (five steps end 1.1e-3 of |X| from the exact
-// polynomial, 1.5e-3 with X = a X + (b G + c G G) X; with bf16 1e-2).
+// and its rounding counts for as much.
+// X is kept as two fp16 numbers, x and what it leaves, up to the last step, and P is
+// applied to both.  A rounding of X is relative to its strongest directions and lies in
+// all of them, and five steps raise weak ones up to 3.44^5 = 485 times: with x alone X
+// ended 1e-3 of its norm off where its spectrum was flat, 2.7e-2 with one direction
+// 1000 times the rest and 0.13 with one of 1e4, both of them now 1.6e-3 at most.  G and
+// P need no second part: their roundings multiply X and lie in its own directions.
+// The sum of P's product with the second part is another one as long: five steps take
+// 1.4 to 1.5 times the operations (two of 14336 x 4096 5720 us without, 7900 with it).
+// The last step's X is short of it: nothing raises its rounding any more.
 //
 // One cooperative launch takes every product of every step and matrix of the
 // list: persistent pairs of CTAs walk the tiles of 256 x 256, half as wide where a
@@ -26,15 +34,15 @@
 // a launch.  Pairs take their tiles in the common order, so the first tile that
 // is not done never waits for one behind it.  A pair shares an MMA of
 // 256 x 256 x 16, each CTA loading half of either operand (TMA, 64 x 64 boxes, five
-// stages of 64 of the sum, or eight narrow ones); operands lie with the sum along
+// stages of 64 of the sum, or six narrow ones); operands lie with the sum along
 // their rows or across them, which the MMA's descriptors tell.  Two accumulators:
 // eight warps store one while the other is formed, each a quarter's rows of half the
 // columns: what the sum is added to comes and what it becomes goes by TMA (stores
 // by lanes took 13000 cycles a tile, these 4700).  Tiles above the diagonal of G
 // and P are stored transposed from the ones below.
-// Two matrices of 14336 x 4096 (7.9e12 operations): products 4.65 ms, 1.69 PFLOP/s,
-// the tensor cores under the power cap; momentum and scaling 0.37 ms at the copy
-// rate.  Twelve of 256 x 768: 152 us, fifteen products in a chain.
+// Two matrices of 14336 x 4096 (7.9e12 operations, 11.7e12 with X's second part): 7.9
+// ms, 7.4 of them products at 1.6 PFLOP/s, the tensor cores under the power cap.
+// Twelve of 256 x 768: 164 us, fifteen products in a chain.
 // Every wait is bounded and reports GS_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -63,9 +71,9 @@ template <int BN>
 struct Mu {
   static constexpr int kBBoxes = BN / 128;               // a CTA's half of B's columns
   static constexpr int kStage = (2 + kBBoxes) * kMBox;   // and 128 rows of A
-  static constexpr int kStages = BN == 256 ? 5 : 8;
-  static constexpr int kPieces = BN / 128;               // per storing warp: 64 columns each
-  static constexpr int kSmem = kStages * kStage + 8 * kPieces * kMPiece + 8 * kMKeys + 1024 + 512;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kGroups = BN / 128;               // of 64 columns, per storing warp
+  static constexpr int kSmem = kStages * kStage + 8 * 2 * kMPiece + 8 * kMKeys + 1024 + 512;
   static_assert(kSmem <= 232448, "dynamic shared memory above the per-CTA limit");
 };
 
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
   }
 }
 
-// x[0] = fp16(u sx / |u|).
+// x[0] = fp16(u sx / |u|), and what that leaves.
 template <int DT>
 __global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, MuonArgs a) {
   if (*a.found_inf) return;
@@ -241,20 +249,28 @@ __global__ void __launch_bounds__(kMEThreads) muon_scale_kernel(MuonTable t, Muo
     for (int j = 0; j < kMRuns; ++j) {
       const int64_t i = base + (j * kMEThreads + threadIdx.x) * 4;
       if (i >= end) continue;
-      uint16_t h[4];
+      uint16_t h[4], l[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float u = a.nesterov ? __fmaf_rn(a.mu, m[j][e], __fmul_rn(g[j][e], clip)) : m[j][e];
-        h[e] = Elem<GS_F16>::put(__fmul_rn(u, f));
+        const float x = __fmul_rn(u, f);
+        h[e] = Elem<GS_F16>::put(x);
+        l[e] = Elem<GS_F16>::put(__fsub_rn(x, Elem<GS_F16>::get(h[e])));
       }
       unsigned row = (unsigned)i / (unsigned)mat.cols, col = (unsigned)i - row * (unsigned)mat.cols;
       if (rows4) {  // i + 4 <= end: the matrix is a multiple of 4
         *reinterpret_cast<uint2*>(mat.x[0] + (int64_t)row * mat.ldx + col) =
             make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        if (a.steps > 1)
+          *reinterpret_cast<uint2*>(mat.x_lo[0] + (int64_t)row * mat.ldx + col) =
+              make_uint2(l[0] | (uint32_t)l[1] << 16, l[2] | (uint32_t)l[3] << 16);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (i + e < end) mat.x[0][(int64_t)row * mat.ldx + col] = h[e];
+          if (i + e < end) {
+            mat.x[0][(int64_t)row * mat.ldx + col] = h[e];
+            if (a.steps > 1) mat.x_lo[0][(int64_t)row * mat.ldx + col] = l[e];
+          }
           if (++col == (unsigned)mat.cols) col = 0, ++row;
         }
       }
@@ -294,7 +310,9 @@ struct Product {
   int m0, n0;            // first row and column of the result
   int M, N, K;
   bool ta, tb;           // operand with its sum across the rows
-  int map_a, map_b;      // of the matrix's four maps
+  int map_a, map_b;      // of the matrix's maps
+  bool lo_in, lo_out;    // x's low part takes part, is stored
+  int map_a_lo, map_b_lo;  // with lo_in: the operands of the sum's second half
   bool mirror;           // a tile below the diagonal
   unsigned need;         // sixteenths of the matrix's tiles to be stored before
 };
@@ -349,6 +367,8 @@ __device__ __forceinline__ Product product(const MuonTable& t, const int* keys, 
   }
   p.m0 = mt * kMuonTile;
   p.n0 = nt * BN;
+  p.lo_in = p.kind == kApply;
+  p.lo_out = p.lo_in && step + 2 < steps;
   if (p.kind == kGram) {
     p.K = mat.tall ? mat.rows : mat.cols;
     p.ta = p.tb = mat.tall;
@@ -364,6 +384,8 @@ __device__ __forceinline__ Product product(const MuonTable& t, const int* keys, 
     p.map_a = mat.tall ? p.turn : 3;
     p.map_b = mat.tall ? 3 : p.turn;
   }
+  p.map_a_lo = mat.tall ? 4 + p.turn : p.map_a;
+  p.map_b_lo = mat.tall ? p.map_b : 4 + p.turn;
   return p;
 }
 
@@ -459,7 +481,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t pad = (1024u - (tc_smem(smem_raw) & 1023u)) & 1023u;
   uint8_t* stages = smem_raw + pad;
   uint8_t* pieces = stages + kMStages * kMStage;  // two per storing warp
-  int* key_space = reinterpret_cast<int*>(pieces + 8 * S::kPieces * kMPiece);
+  int* key_space = reinterpret_cast<int*>(pieces + 8 * 2 * kMPiece);
   uint64_t* full = reinterpret_cast<uint64_t*>(key_space + 2 * kMKeys);
   uint64_t* empty = full + kMStages;
   uint64_t* tfull = empty + kMStages;
@@ -495,7 +517,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     key_space[kMKeys + threadIdx.x - 64] = t.mats[threadIdx.x - 64].first_app;
   }
   // the tensor maps lie in global memory: once per CTA before their use
-  for (int i = threadIdx.x; i < 8 * t.n; i += kMThreads) map_fence(t.maps + i);
+  for (int i = threadIdx.x; i < 2 * kMuonMaps * t.n; i += kMThreads) map_fence(t.maps + i);
   tc_before();
   __syncthreads();
   cluster_barrier();
@@ -507,17 +529,20 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     bool go = !a.stall;
     for (int tile = first; go && tile < tiles; tile += step) {
       const Product p = product<BN>(t, keys, tile, a.steps);
-      const CUtensorMap* maps = t.maps + 8 * p.id;
+      const CUtensorMap* maps = t.maps + 2 * kMuonMaps * p.id;
       if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
       // what other CTAs stored is read by TMA from here on
       asm volatile("fence.proxy.async;" ::: "memory");
       const CUtensorMap *ma = maps + p.map_a, *mb = maps + p.map_b;
       const int m0 = p.m0 + 128 * (int)rank, n0 = p.n0 + BN / 2 * (int)rank;
-      for (int k = 0; k < p.K; k += 64) {
+      const int parts = (p.K + 63) / 64, all = p.lo_in ? 2 * parts : parts;
+      for (int i = 0; i < all; ++i) {
         if (!tc_wait_warp(&empty[s], ph ^ 1u, abort_flag, a.status)) {
           go = false;
           break;
         }
+        if (i == parts) ma = maps + p.map_a_lo, mb = maps + p.map_b_lo;
+        const int k = 64 * (i < parts ? i : i - parts);
         uint8_t* st = stages + s * kMStage;
         if (tc_elect()) {
           const uint32_t bar = tc_leader<2>(&full[s]);
@@ -549,7 +574,8 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
       if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
       const uint32_t idesc = idesc16(BN, p.ta, p.tb);
-      for (int k = 0; k < p.K; k += 64) {
+      const int all = (p.lo_in ? 2 : 1) * ((p.K + 63) / 64);
+      for (int i = 0; i < all; ++i) {
         if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
           break;
@@ -560,9 +586,9 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma16(tmem + b * BN, desc16(a0, kk, p.ta), desc16(b0, kk, p.tb), idesc,
-                  k > 0 || kk > 0 ? 1u : 0u);
+                  i > 0 || kk > 0 ? 1u : 0u);
           tc_commit<2>(&empty[s]);
-          if (k + 64 >= p.K) tc_commit<2>(&tfull[b]);
+          if (i == all - 1) tc_commit<2>(&tfull[b]);
         }
         __syncwarp();
         if (++s == kMStages) s = 0, ph ^= 1u;
@@ -575,7 +601,7 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
     tc_drain(drain, 0);
   } else if (warp >= 4) {  // store
     const int q = warp & 3, h = (warp - 4) >> 2;
-    uint8_t* const mine = pieces + (warp - 4) * S::kPieces * kMPiece;
+    uint8_t* const mine = pieces + (warp - 4) * 2 * kMPiece;
     uint64_t* const bar = &loaded[warp - 4];
     uint32_t b = 0, tph = 0, lph = 0;
     for (int tile = first; tile < tiles; tile += step) {
@@ -608,8 +634,14 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
       const int row0 = p.m0 + 128 * (int)rank + 32 * q, row = row0 + lane, col0 = p.n0 + BN / 2 * h;
-      const CUtensorMap* maps = t.maps + 8 * p.id + 4;  // boxes of 32 rows
+      const CUtensorMap* maps = t.maps + 2 * kMuonMaps * p.id + kMuonMaps;  // boxes of 32 rows
       const bool some = row0 < p.M && col0 < p.N;
+      // what the sum is added to, of 64 columns and both parts (one lane)
+      const auto old_pair = [&](int g) {
+        tc_expect(bar, 2 * kMPiece);
+        tc_load2<1>(maps + map_old, tc_smem(bar), mine, col0 + 64 * g, row0);
+        tc_load2<1>(maps + map_old + 4, tc_smem(bar), mine + kMPiece, col0 + 64 * g, row0);
+      };
       if (p.kind != kGram && some) {
         if (!wait_done(t.done + p.id, p.need, abort_flag, a.status)) break;
         // what other CTAs stored is read by TMA; this warp's own uses of its
@@ -617,10 +649,14 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
         if (tc_elect()) {
-          tc_expect(bar, S::kPieces * kMPiece);
+          if (p.lo_in) {
+            old_pair(0);
+          } else {
+            tc_expect(bar, S::kGroups * kMPiece);
 #pragma unroll
-          for (int i = 0; i < S::kPieces; ++i)
-            tc_load2<1>(maps + map_old, tc_smem(bar), mine + i * kMPiece, col0 + 64 * i, row0);
+            for (int i = 0; i < S::kGroups; ++i)
+              tc_load2<1>(maps + map_old, tc_smem(bar), mine + i * kMPiece, col0 + 64 * i, row0);
+          }
         }
         __syncwarp();
       }
@@ -637,7 +673,8 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll 1
       for (int c = 0; c < BN / 64; ++c) {
         const int col = col0 + 32 * c;
-        uint8_t* const buf = mine + (c >> 1) * kMPiece;
+        uint8_t* const buf = mine + (p.lo_in ? 0 : c >> 1) * kMPiece;
+        uint8_t* const buf_lo = mine + kMPiece;
         float o[32];
         uint32_t* const v = reinterpret_cast<uint32_t*>(o);
         tc_ld32(tmem + ((uint32_t)(32 * q) << 16) + b * BN + BN / 2 * h + 32 * c, v);
@@ -649,9 +686,21 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         }
         // (the second half of a piece is stored with the first)
         if (row0 >= p.M || col0 + 64 * (c >> 1) >= p.N) continue;
+        if (p.lo_in && c > 0 && (c & 1) == 0) {  // the next 64 columns, where the last are on their way
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          asm volatile("fence.proxy.async;" ::: "memory");
+          __syncwarp();
+          if (tc_elect()) old_pair(c >> 1);
+          __syncwarp();
+          tc_drain(bar, lph);
+          lph ^= 1u;
+        }
         // 16 bytes j of row r lie at j ^ (r % 8)
         const auto place = [&](int j) {
           return reinterpret_cast<uint4*>(buf + lane * 128 + ((j ^ (lane & 7)) << 4));
+        };
+        const auto place_lo = [&](int j) {
+          return reinterpret_cast<uint4*>(buf_lo + lane * 128 + ((j ^ (lane & 7)) << 4));
         };
         uint4 was[4];  // both halves are read before the piece is written
 #pragma unroll
@@ -662,6 +711,18 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = __fmul_rn(o[j], alpha);
+        if (p.lo_in) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 w = *place_lo(4 * (c & 1) + j);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[8 * j + 2 * e] = __fadd_rn(lo_f16(ww[e]), o[8 * j + 2 * e]);
+              o[8 * j + 2 * e + 1] = __fadd_rn(hi_f16(ww[e]), o[8 * j + 2 * e + 1]);
+            }
+          }
+        }
         if (p.kind != kGram) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -685,12 +746,20 @@ __global__ void __launch_bounds__(kMThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = cvt_f32x2_f16x2(o[8 * j + 2 * e + 1], o[8 * j + 2 * e]);
             *place(4 * (c & 1) + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (p.lo_out) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = cvt_f32x2_f16x2(__fsub_rn(o[8 * j + 2 * e + 1], hi_f16(w[e])),
+                                       __fsub_rn(o[8 * j + 2 * e], lo_f16(w[e])));
+              *place_lo(4 * (c & 1) + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
           if (c & 1) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (tc_elect()) {  // clipped at the matrix's edges
               tc_store2(maps + map_out, buf, col - 32, row0);
+              if (p.lo_out) tc_store2(maps + map_out + 4, buf_lo, col - 32, row0);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
             __syncwarp();
