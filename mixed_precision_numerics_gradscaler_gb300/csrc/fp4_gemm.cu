@@ -120,7 +120,9 @@ __device__ __forceinline__ void cp_scales(uint32_t tmem, uint64_t desc) {
 // TRANS: 0, or the operands have changed places and TRANS + 1 CTAs of a cluster at
 // most share a tile's sum, split along K: CTA r takes its part of the stages, CTAs
 // 1 .. split - 1 write their fp32 sums to the leading CTA's shared memory, which
-// adds them in their order.
+// adds them in their order.  There is one tile of columns then (N <= BN): one further
+// on would begin inside its 128 rows' scales, and an MMA takes scales from multiples
+// of four columns of tensor memory alone.
 template <int CG, int BN, int FMT, int OUT, int TRANS, bool TMA_STORE>
 __global__ void __launch_bounds__(kQThreads, 1)
     gemm_fp4_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -215,8 +217,6 @@ __global__ void __launch_bounds__(kQThreads, 1)
       tc_tile(t, a.group, tiles_m, tiles_n, mt, nt);
       if (!tc_wait_warp(&tempty[b], tph ^ 1u, abort_flag, a.status)) break;
       tc_after();
-      // where in its 128 rows' scales a narrow tile of B begins
-      const uint32_t sb_at = BN < 128 ? (uint32_t)(nt * BN % 128) / 32 : 0;
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!tc_wait_warp(&full[s], ph, abort_flag, a.status)) {
           go = false;
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
               const uint32_t sf = FMT == GS_NVFP4 ? 0u : 2u * (kk & 1);
               mma4<CG, FMT>(tmem + b * BN, tc_desc_k(a0 + 32 * kk), tc_desc_k(b0 + 32 * kk),
                             idesc4<FMT>(128 * CG, BN, sf), tmem + S::kSfCol + 4 * j,
-                            tmem + S::kSbCol + 4 * j * S::kBTiles + sb_at, kb > kb0 || kk > 0 ? 1u : 0u);
+                            tmem + S::kSbCol + 4 * j * S::kBTiles, kb > kb0 || kk > 0 ? 1u : 0u);
             }
           }
           tc_commit<CG>(&empty[s]);
@@ -509,7 +509,9 @@ static double rounds(int64_t M, int64_t N, int64_t K, int tm, int tn, int ctas, 
 
 template <int FMT, int OUT>
 static cudaError_t gemm4_pick(const Operand& x, const Operand& y, Gemm4Args a, bool tma, cudaStream_t st) {
-  if (a.M <= 32) {  // few rows of A: they become a tile's columns
+  // few rows of A: they become a tile's columns, one tile of 32.  One to 32 rows by
+  // 4096 x 14336 15 us, 25 in tiles of 128 rows; by 28672 x 8192 30, 33 to 51
+  if (a.M <= 32) {
     std::swap(a.M, a.N);
     // the split that leaves the fewest stages to the busiest SM
     const int64_t tiles = div_up(a.M, 128), kb = div_up(a.K, kQK);
