@@ -45,9 +45,13 @@ constexpr int kPRun = 8;                     // tokens per thread and step
 constexpr int kPTile = kPThreads * kPRun;    // tokens per CTA and step
 constexpr int kPSpan = 1024;                 // sequences of a step kept in shared memory
 
-// Tokens that one CTA does alone (see launch_policy_loss).
+// Tokens that one CTA does alone, and their sequences.  Alone and by many CTAs, in
+// two or three launches, on the device: 1024 tokens 7.0 and 14.4 us, 5120 11.1 and
+// 14.5 (13.4 and 21.5 by sequences), 4608 in 2048 sequences 15.5 and 30.1.  8192 alone
+// take 14.9 where many CTAs take 14.4 (18.5 and 22.6 by sequences), and eight tokens a
+// thread spill: 5120 tokens then take 13.7.
 constexpr int64_t kPSmallTokens = 5120;
-constexpr int64_t kPSmallSeqs = 2048;  // times kPSmallTokens: below 2^24
+constexpr int64_t kPSmallSeqs = 2048;  // times kPSmallTokens: below 2^24, exact in fp32
 constexpr int kPSmallThreads = 1024;
 
 // A sum in fp32 with its rounding errors carried along (the fp64 pipe would
