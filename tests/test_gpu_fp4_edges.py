@@ -48,3 +48,23 @@ def test_scales_whose_product_leaves_fp32(gs, out, M, N, K, pad, ea, eb):
     assert bool((((got - want).abs() <= tol) | over).all())
     assert bool((torch.isinf(got) & (got.sign() == want.sign()))[(want.abs() - tol) > most * (1 + step)].all())
     assert gs.gs_device_status() == gs.GS_OK
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("M,N,ld", [(5, 9, 16), (5, 9, 9), (1, 9, 16), (3, 300, 301), (40, 1, 7)])
+def test_an_empty_sum_writes_its_rows_alone(gs, out, M, N, ld):
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    for fmt, ts in (("mxfp4", None), ("nvfp4", torch.ones(1, device=DEV))):
+        buf = torch.full((M, ld), 77.0, dtype=TYPES[out], device=DEV)
+        gs.fp4_gemm_block_scaled(u8(M, 0), u8(0), u8(N, 0), u8(0), fmt, buf[:, :N], ts, ts)
+        assert bool((buf[:, :N] == 0.0).all()) and bool((buf[:, N:] == 77.0).all())
+
+
+@pytest.mark.parametrize("ld", [(1 << 29) + 8, 1 << 29])
+def test_an_empty_sum_of_long_rows(gs, ld):
+    """Rows of 2 GiB and more, as they lie together and apart."""
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    N = 1 << 29
+    buf = torch.full((3, ld), 77.0, device=DEV)
+    gs.fp4_gemm_block_scaled(u8(3, 0), u8(0), u8(N, 0), u8(0), "mxfp4", buf[:, :N])
+    assert int(torch.count_nonzero(buf[:, :N])) == 0 and bool((buf[:, N:] == 77.0).all())

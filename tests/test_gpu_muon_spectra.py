@@ -119,3 +119,23 @@ def test_strong_rows_and_elements(gs):
     for v in (rows, lone):
         x, want = direction(gs, v, 5)
         assert off(x, want) <= bound((200, 600), 5), off(x, want)
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("shape", [(64, 64), (65, 63), (100, 1000), (1000, 100), (256, 256), (257, 255), (300, 2000),
+                                   (2000, 300), (513, 769), (1024, 2050), (2050, 1030)])
+def test_every_element(gs, shape, offset):
+    ts = make([shape], "f32", 7, offset)
+    w, g, m, _ = views(ts)
+    before = w[0].clone(), m[0].clone()
+    step(gs, w, g, m, None, 0.02, momentum=0.95, weight_decay=0.1)
+    f32 = lambda v: float(torch.tensor(v, dtype=torch.float32))  # noqa: E731
+    want, _ = mr.muon(before[0], g[0], before[1], f32(0.02), f32(0.95), f32(0.1))
+    moved = want - before[0].double() * (1 - f32(0.02) * f32(0.1))
+    unit = bound(shape, 5) * float(torch.linalg.norm(moved)) / math.sqrt(moved.numel())
+    err = w[0].double() - want
+    assert bool((err.abs() <= 8 * unit + want.abs() * 2.0 ** -22).all()), float(err.abs().max()) / unit
+    for dim in (0, 1):
+        n = shape[dim]
+        e, size = torch.linalg.norm(err, dim=dim), torch.linalg.norm(want, dim=dim)
+        assert bool((e <= (math.sqrt(n) + 8) * unit + size * 2.0 ** -22).all())

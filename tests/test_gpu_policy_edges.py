@@ -186,6 +186,30 @@ def test_nan_shows_under_an_advantage_of_zero(gs, T, reduction, name):
 
 
 @pytest.mark.parametrize("reduction", REDUCTIONS)
+@pytest.mark.parametrize("T,S", [(5120, 16), (1024, 2048), (5121, 16), (5120, 2049), (40000, 16)])
+def test_advantages_that_cancel(gs, reduction, T, S):
+    """Advantages less their mean, ratios within 2^-19 of 1: the loss is a small part
+    of its terms.  Up to 5120 tokens and 2048 sequences A and A (rho - 1) are summed
+    apart, the latter to 2^-20 of itself (its series, a product, the sum's steps),
+    the former as pairs of fp32 numbers: 2^-40 of the terms.  Beyond, 2^-20 of the
+    terms as everywhere."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(T + S)
+    off = torch.linspace(0, T, S + 1, device=DEV).long()
+    adv = torch.randn(T, device=DEV, generator=gen)
+    adv -= adv.mean()
+    lp = -torch.exp(torch.randn(T, device=DEV, generator=gen))
+    old = lp + (torch.rand(T, device=DEV, generator=gen) - 0.5) * 2.0 ** -18
+    i = dict(lp=lp, old=old, adv=adv, ref=None, targets=None, offsets=off)
+    loss, _, _ = run(gs, i, reduction, ref=None)
+    want, _, _, size = mr.policy_loss(lp, old, adv, None, None, off, f32(0.2), f32(0.28), 0.0, 0.0, reduction)
+    terms = float(size.sum())
+    moved = float((size.cpu() * torch.expm1(lp.cpu().double() - old.cpu().double()).abs()).sum())
+    tol = moved * 2.0 ** -20 + terms * 2.0 ** -40 if T <= 5120 and S <= 2048 else terms * 2.0 ** -20
+    assert abs(loss - want) <= tol + abs(want) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("reduction", REDUCTIONS)
 @pytest.mark.parametrize("T", [1, 7, 300, 6000])
 def test_as_many_sequences_as_tokens(gs, reduction, T):
     """Some sequences empty, some longer: the length of the advantages does not tell
