@@ -782,8 +782,9 @@ def gs_policy_loss(logprob: torch.Tensor, old_logprob: torch.Tensor, advantages:
 
 
 def gs_test_set_stall(on: bool) -> None:
-    """Test hook: the block-scaled FP8 GEMM issues no TMA loads while on, so
-    its bounded waits run out and it reports GS_ERR_TIMEOUT."""
+    """Test hook: the block-scaled FP8 and 4-bit products and the products of
+    gs_master_update_muon issue no TMA loads while on, so their bounded waits
+    run out and they report GS_ERR_TIMEOUT."""
     _check(_lib.gs_test_set_stall(1 if on else 0), "gs_test_set_stall")
 
 

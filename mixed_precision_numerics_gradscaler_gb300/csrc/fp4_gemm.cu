@@ -21,10 +21,10 @@
 // Few rows of A (TRANS): the operands change places, the weight's rows become
 // the 128 rows of a tile and the few rows its BN columns, and a tile is stored
 // transposed, 32 lanes to 32 neighbours of a row of D.
-// 16384 x 28672 x 8192, NVFP4, bf16 out: 1.19 to 1.31 ms, 5.9 to 6.5 PFLOP/s under
+// 16384 x 28672 x 8192, NVFP4, bf16 out: 1.26 to 1.31 ms, 5.9 to 6.1 PFLOP/s under
 // the power cap (without the copies of scales, twelve a stage in the MMAs' pipe,
 // 1.14 ms; two sets of columns for them change nothing).  One row by 28672 x 8192:
-// 29 us, 26 of them on the device, 19.5 at the copy rate.
+// 29 us, 26 from a graph (30 with cold caches), 19.8 at the copy rate.
 // Every wait is bounded and reports GS_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -103,8 +103,8 @@ __device__ __forceinline__ void tc_arrive_at(uint64_t* bar, uint32_t rank) {
                : "memory");
 }
 
-// The shared::cluster address of p's place in the pair's leading CTA: a CTA's
-// window is told by bit 24 within a pair.
+// The shared::cluster address of p's place in the pair's leading CTA (for one CTA,
+// of its own).
 template <int CG>
 __device__ __forceinline__ uint32_t tc_leader(const void* p) {
   return CG == 2 ? remote(p, cluster_rank() & ~1u) : tc_smem(p);

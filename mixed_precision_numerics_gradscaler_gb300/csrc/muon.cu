@@ -18,12 +18,14 @@
 // and its rounding counts for as much.
 // X is kept as two fp16 numbers, x and what it leaves, up to the last step, and P is
 // applied to both.  A rounding of X is relative to its strongest directions and lies in
-// all of them, and five steps raise weak ones up to 3.44^5 = 485 times: with x alone X
-// ended 1e-3 of its norm off where its spectrum was flat, 2.7e-2 with one direction
-// 1000 times the rest and 0.13 with one of 1e4, both of them now 1.6e-3 at most.  G and
+// all of them, and five steps raise weak ones up to 3.44^5 = 485 times: with x alone
+// a matrix of 256 x 768 ended 9e-4 of its norm off where its spectrum was flat, 2.1e-2
+// with one direction 1000 times the rest and 0.12 with one of 1e4; with both parts
+// 9e-4, 5e-4 and 1.6e-3.  G and
 // P need no second part: their roundings multiply X and lie in its own directions.
 // The sum of P's product with the second part is another one as long: five steps take
-// 1.4 to 1.5 times the operations (two of 14336 x 4096 5720 us without, 7900 with it).
+// 1.4 to 1.5 times the operations (two of 14336 x 4096 5500 to 5850 us without, 7500 to
+// 8300 with it).
 // The last step's X is short of it: nothing raises its rounding any more.
 //
 // One cooperative launch takes every product of every step and matrix of the
@@ -40,9 +42,10 @@
 // columns: what the sum is added to comes and what it becomes goes by TMA (stores
 // by lanes took 13000 cycles a tile, these 4700).  Tiles above the diagonal of G
 // and P are stored transposed from the ones below.
-// Two matrices of 14336 x 4096 (7.9e12 operations, 11.7e12 with X's second part): 7.9
-// ms, 7.4 of them products at 1.6 PFLOP/s, the tensor cores under the power cap.
-// Twelve of 256 x 768: 164 us, fifteen products in a chain.
+// Two matrices of 14336 x 4096 (7.9e12 operations, 11.7e12 with X's second part): the
+// products 6.8 to 7.0 ms by themselves, 1.7 PFLOP/s, the tensor cores under the power
+// cap; momentum and scaling 0.40 ms at the copy rate.  Twelve of 256 x 768: 164 us,
+// fifteen products in a chain.
 // Every wait is bounded and reports GS_ERR_TIMEOUT.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -175,8 +178,9 @@ __global__ void __launch_bounds__(kMEThreads) muon_momentum_kernel(MuonTable t, 
     }
     if (begun < 0) begun = c;
     if (c + gridDim.x < mat.first_chunk + chunks) continue;
-    // this CTA's part of the matrix's sum.  A thread's is a few hundred squares in
-    // fp32, all positive: 2^-24 of it each; fp64 from there
+    // this CTA's part of the matrix's sum.  A thread's is of groups of four squares in
+    // fp32, all positive: 200 additions for 32 M elements and 3400 for 2^31, 2^-24 of
+    // the sum each at most (1.2e-5, 2e-4; half of that in the norm); fp64 from there
     double part = (double)sum;
     sum = 0.0f;
 #pragma unroll
