@@ -616,8 +616,8 @@ int fp4_gemm_block_scaled(const uint8_t* qa, const uint8_t* sa, const float* ta,
  * statistics and gradient 0.  T, S <= 2^40,
  * S >= 1.  The same inputs give the same bits.
  * Gradients and the loss are off by at most 2^-20 of the terms they are made of,
- * |w| ((2 + |x - x'|) rho |A| + kl_coef (exp(x'' - x) + 1)), and half a step of
- * themselves.  In batches of up to 5120 tokens in up to 2048 sequences the loss sums A
+ * |w| ((2 + |x - x'|) rho |A| + kl_coef (2 + |x'' - x|) (exp(x'' - x) + 1)), and half
+ * a step of themselves.  In batches of up to 5120 tokens in up to 2048 sequences the loss sums A
  * and A (rho - 1) apart, so that advantages that cancel leave an objective that is off
  * by 2^-20 of |w A (rho - 1)| and 2^-40 of its terms; longer ones hold to the first
  * bound alone. */

@@ -3,9 +3,11 @@ a divergence that is only watched, ratios and divergences beyond fp32's range, N
 under an advantage of zero, advantages that cancel, one advantage per sequence in a
 batch of as many sequences as tokens.
 
-Tolerances, as in test_gpu_policy_loss.py: 2^-20 of the terms' sizes, which include
-(2 + |d|) rho |A| for the rounding of d, and half a step of the result.  A result
-beyond fp32's range is its infinity."""
+Tolerances, as in test_gpu_policy_loss.py: 2^-20 of the terms' sizes, and half a step
+of the result.  d and y = x'' - x are rounded to fp32, 2^-24 |d| and 2^-24 |y| of which
+their exponentials carry on: sizes are (2 + |d|) rho |A| and (2 + |y|) (e^y + 1).  A
+result beyond fp32's range is its infinity, one below its subnormals within a step of
+them."""
 import math
 
 import pytest
@@ -48,7 +50,7 @@ def near(got, want, tol):
     got, want, tol = (torch.as_tensor(v, dtype=torch.float64) for v in (got, want, tol))
     most = torch.finfo(torch.float32).max
     at_edge = (want.abs() / most - 1).abs() < 2.0 ** -16  # either side of the last finite value
-    ok = torch.where(torch.isinf(want.float()), got == want.float().double(), (got - want).abs() <= tol)
+    ok = torch.where(torch.isinf(want.float()), got == want.float().double(), (got - want).abs() <= tol + 2.0 ** -148)
     ok |= at_edge & (got.sign() == want.sign()) & (got.abs() >= most * (1 - 2.0 ** -15))
     assert bool(ok.all()), (got[~ok], want[~ok])
 
@@ -60,7 +62,8 @@ def sizes(i, weights, dual, kl):
     top = torch.where(a > 0, 1.28, dual if dual else math.inf)
     size = (2 + d.abs()) * torch.minimum(d.exp(), top) * a.abs() + 1.28 * a.abs()
     if i["ref"] is not None:
-        size = size + abs(kl) * ((i["ref"].cpu().double() - i["lp"].cpu().double()).exp() + 1)
+        y = i["ref"].cpu().double() - i["lp"].cpu().double()
+        size = size + abs(kl) * (2 + y.abs()) * (y.exp() + 1)
     return torch.where(weights > 0, weights * size, torch.zeros(T, dtype=torch.float64))
 
 
@@ -87,11 +90,12 @@ def check(gs, i, reduction, dual=0.0, kl=0.0, **k):
     # the mean ratio's error counts d's rounding: (2 + |d|) rho, as size has it
     live = torch.ones(i["lp"].numel(), dtype=torch.bool) if i["targets"] is None else i["targets"].cpu() >= 0
     d = (i["lp"].cpu().double() - i["old"].cpu().double())[live]
-    near(stats[1], wstats[1], float(((2 + d.abs()) * d.exp()).mean()) * 2.0 ** -20 + abs(wstats[1]) * 2.0 ** -24)
+    n = max(1, d.numel())
+    near(stats[1], wstats[1], float(((2 + d.abs()) * d.exp()).sum()) / n * 2.0 ** -20 + abs(wstats[1]) * 2.0 ** -24)
     near(stats[2], wstats[2], 2.0 ** -24)
     if i["ref"] is not None:
         y = (i["ref"].cpu().double() - i["lp"].cpu().double())[live]
-        near(stats[3], wstats[3], float(((2 + y.abs()) * (y.exp() + 1)).mean()) * 2.0 ** -20 + abs(wstats[3]) * 2.0 ** -24)
+        near(stats[3], wstats[3], float(((2 + y.abs()) * (y.exp() + 1)).sum()) / n * 2.0 ** -20 + abs(wstats[3]) * 2.0 ** -24)
 
 
 def live_places(i, n):
@@ -225,3 +229,19 @@ def test_as_many_sequences_as_tokens(gs, reduction, T):
     assert abs(loss - loss2) <= tol and torch.equal(stats, stats2)
     assert bool(((grad - grad2).abs() <= grad2.abs() * 2.0 ** -22).all())
     check(gs, each, reduction, kl=0.05, per_sequence=False)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_far_tokens_among_others(gs, seed):
+    """Lengths from one token on, a few tokens of any distance either way."""
+    gen = torch.Generator()
+    gen.manual_seed(seed)
+    rnd = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=gen))  # noqa: E731
+    T = int(math.exp(torch.rand(1, generator=gen).item() * 9.5))
+    i = inputs(T, rnd(1, max(1, min(T, 3000))), seed, masked=seed % 3 > 0, ref=seed % 4 > 0)
+    for name, other, sign in (("old", "lp", -1), ("ref", "lp", 1)):
+        if i[name] is not None:
+            at = torch.randint(0, T, (rnd(0, 6),), generator=gen).to(DEV)
+            far = (torch.rand(at.numel(), generator=gen) - 0.5) * 600
+            i[name][at] = i[other][at] + sign * far.to(DEV)
+    check(gs, i, REDUCTIONS[seed % 3], 3.0 if seed % 2 else 0.0, 0.05 if i["ref"] is not None else 0.0)
